@@ -74,6 +74,7 @@ typedef enum { CE_DT_F32 = 0, CE_DT_BF16 = 1, CE_DT_F16 = 2 } ce_dtype;
 #define CE_FLAG_TARGET_OUT_OF_RANGE 0x1u /* some target was neither ignore_index nor in [0, vocab) */
 #define CE_FLAG_NO_VALID_ROWS 0x2u       /* mean over zero valid rows: loss and gradient set to 0 */
 #define CE_FLAG_WAIT_TIMEOUT 0x4u        /* a device-side wait gave up (results invalid) */
+#define CE_FLAG_BAD_OFFSETS 0x8u         /* sequence offsets that fall or leave [0, n_rows] */
 
 /* ce_params.variant: which kernels ce_fwd_bwd uses */
 #define CE_VARIANT_AUTO 0   /* the library picks (ce_select_variant) */
@@ -392,6 +393,128 @@ ce_status flce_fwd_bwd(const ce_params *p, int64_t hidden_dim, const void *hidde
                        const float *bias, const void *target, float *loss, const float *grad_output,
                        void *grad_hidden, float *grad_weight, float *grad_bias, int64_t chunk_rows,
                        void *workspace, size_t workspace_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Token log-probabilities and the losses of post-training that are made of
+ * them. With z = x / T (T the temperature), target t and p = softmax(z):
+ *
+ *   logp = z_t - LSE(z),   H = -sum_c p_c log p_c   (0 log 0 = 0)
+ *   d(g logp + h H)/dx_c = (1/T) [ g (1[c = t] - p_c) - h p_c (log p_c + H) ]
+ *
+ * Of ce_params these calls use n_rows, vocab, ld, ignore_index, dtype,
+ * target_is_int32 and, for the two losses, reduction; variant is 0
+ * (CE_ERR_INVALID_ARG otherwise) and the other options are off
+ * (CE_ERR_UNSUPPORTED otherwise). T is in [1e-4, 1e4]. Logits of -inf are
+ * allowed (p_c = 0); a row whose logits are all -inf, or with a NaN or +inf
+ * among them, comes out NaN. Rows that take no part (ignored target, or as
+ * each call says) are not read and have gradient 0.
+ *
+ * The gradient goes to `grad`, device [n_rows, ld_grad] of p->dtype, its
+ * columns < vocab: the logits buffer itself (then ld_grad = p->ld), or a
+ * buffer that shares no element with it (CE_ERR_INVALID_ARG where the two
+ * overlap in any other way).
+ * ------------------------------------------------------------------------ */
+
+/*
+ * Log-probability and entropy of every row's target. One kernel, no workspace.
+ *   logp     device fp32 [n_rows], or NULL.
+ *   entropy  device fp32 [n_rows], or NULL: not formed.
+ *   stats    device fp32 [n_rows][4] (16-byte aligned), or NULL: the row
+ *            statistics ce_token_logprob_backward takes, {M, s, x_t, u}: M = max_c x_c,
+ *            s = sum_{c != t} 2^a_c, u = sum_{c != t} 2^a_c a_c (NaN when the
+ *            entropy was not asked for), a_c = (x_c - M) log2(e) / T.
+ * Ignored rows: 0. Targets outside [0, vocab) other than ignore_index: NaN.
+ */
+ce_status ce_token_logprob(const ce_params *p, float temperature, const void *logits, const void *target, float *logp,
+                           float *entropy, float *stats, void *stream);
+
+/*
+ * The gradient of sum_i g_i logp_i + h_i H_i from the statistics of
+ * ce_token_logprob on the same logits. Rows without a valid target: 0.
+ *   grad_logp, grad_entropy  device fp32 [n_rows], or NULL for 0 (not both).
+ *   grad_entropy needs statistics formed with the entropy (else NaN).
+ */
+ce_status ce_token_logprob_backward(const ce_params *p, float temperature, const void *logits, const void *target,
+                                    const float *stats, const float *grad_logp, const float *grad_entropy, void *grad,
+                                    int64_t ld_grad, void *stream);
+
+typedef struct ce_policy_params {
+    float temperature;
+    float clip_low, clip_high; /* ratio clipped to [1 - clip_low, 1 + clip_high]; clip_low in [0, 1], clip_high >= 0 */
+    float kl_coef;             /* >= 0 */
+    float entropy_coef;        /* finite */
+    int32_t reserved;          /* must be 0 */
+} ce_policy_params; /* 24 bytes */
+
+/*
+ * Clipped policy loss with a KL term and an entropy bonus, and its gradient.
+ * Per row i with a valid target and weight w_i != 0 (others: loss 0):
+ *   r = e^(logp_i - old_i),  kl = e^(ref_i - logp_i) - (ref_i - logp_i) - 1
+ *   l_i = max(-A_i r, -A_i clip(r, 1 - clip_low, 1 + clip_high)) + kl_coef kl - entropy_coef H_i
+ * and the loss is sum w_i l_i / sum w_i (mean), sum w_i l_i (sum) or the
+ * vector w_i l_i (none). The gradient follows the branch that the max takes
+ * (on the border of the clip range: the unclipped one).
+ *   advantage   device fp32 [n_rows] (A).
+ *   old_logp    device fp32 [n_rows], or NULL: old = logp, r = 1 (its gradient
+ *               then is that of A logp).
+ *   ref_logp    device fp32 [n_rows], or NULL (then kl_coef must be 0).
+ *   row_weight  device fp32 [n_rows], or NULL for 1.
+ *   grad_output device fp32 [1] ([n_rows] for none), or NULL for 1.
+ *   loss        device fp32 [1] ([n_rows] for none).
+ *   row_stats   device fp32 [n_rows][4] (16-byte aligned), or NULL: {logp, H, r, kl}
+ *               per row (0 on rows that take no part).
+ *   workspace   ce_workspace_size() bytes; status bits as for ce_fwd_bwd.
+ * A mean over a weight sum of 0 gives loss and gradient 0 (CE_FLAG_NO_VALID_ROWS).
+ */
+ce_status ce_policy_fwd_bwd(const ce_params *p, const ce_policy_params *q, const void *logits, const void *target,
+                            const float *advantage, const float *old_logp, const float *ref_logp,
+                            const float *row_weight, const float *grad_output, float *loss, float *row_stats,
+                            void *grad, int64_t ld_grad, void *workspace, size_t workspace_bytes, void *stream);
+
+/* ce_preference_params.kind */
+#define CE_PREF_SIGMOID 0 /* -(1-eps) log sigmoid(beta h) - eps log sigmoid(-beta h) */
+#define CE_PREF_HINGE 1   /* max(0, 1 - beta h) */
+#define CE_PREF_SQUARED 2 /* (h - 1 / (2 beta))^2 */
+
+typedef struct ce_preference_params {
+    int64_t n_pairs;           /* P >= 0 */
+    int32_t kind;              /* CE_PREF_* */
+    int32_t offsets_are_int32; /* 0: int64 offsets, 1: int32 */
+    int32_t length_normalize;  /* 1: a sequence's value is the mean of its log-probabilities, 0: their sum */
+    float beta;                /* > 0 */
+    float label_smoothing;     /* eps in [0, 0.5], CE_PREF_SIGMOID only (0 otherwise) */
+    int32_t reserved;          /* must be 0 */
+} ce_preference_params; /* 32 bytes */
+
+/* Workspace bytes of ce_preference_fwd_bwd: 20 bytes a row and 8 a pair, plus at most 1 KB. */
+ce_status ce_preference_workspace_size(const ce_params *p, int64_t n_pairs, size_t *bytes);
+
+/*
+ * Paired preference loss over 2 P sequences of rows and its gradient:
+ * sequence j is the rows [offsets[j], offsets[j + 1]); sequences 0..P-1 are
+ * the preferred ones and P..2P-1, in the same order, the others. With v_j
+ * the sum (or mean) of logp over the rows of j with a valid target,
+ *   h_p = (v_p - v_{P+p}) - (ref_p - ref_{P+p}),
+ * and the loss of kind applied to h_p. Pairs in which a side has no valid
+ * target take no part (loss 0, not counted by the mean, which is over the
+ * others). Rows outside of every sequence take no part.
+ *   offsets     device [2 P + 1], never falling, within [0, n_rows]; otherwise
+ *               loss and seq_logp are NaN, the gradient is 0 and
+ *               CE_FLAG_BAD_OFFSETS is set.
+ *   ref_logp    device fp32 [2 P] (ref_j of the same reduction over a
+ *               sequence's rows), or NULL for 0.
+ *   grad_output device fp32 [1] ([P] for none), or NULL for 1.
+ *   loss        device fp32 [1] ([P] for none).
+ *   seq_logp    device fp32 [2 P] (v_j), or NULL.
+ *   workspace   ce_preference_workspace_size() bytes; status bits as for
+ *               ce_fwd_bwd (CE_FLAG_NO_VALID_ROWS: no pair takes part).
+ * The coefficient of a row depends on its whole pair: the logits are read
+ * once for the log-probabilities and once more for the gradient.
+ */
+ce_status ce_preference_fwd_bwd(const ce_params *p, const ce_preference_params *q, const void *logits,
+                                const void *target, const void *offsets, const float *ref_logp,
+                                const float *grad_output, float *loss, float *seq_logp, void *grad, int64_t ld_grad,
+                                void *workspace, size_t workspace_bytes, void *stream);
 
 #ifdef __cplusplus
 }

@@ -13,6 +13,7 @@ Entry points (same names as the C ABI):
   ce_fwd_bwd(logits, target, ...)            -> loss; gradient over logits
   ce_scale_grad(grad, grad_output, ...)      in-place grad_output scaling
   ce_workspace_size / ce_fused_plan / ce_get_status
+the token log-probability, policy and preference operators (logprob.py),
 and ``cross_entropy``: a torch.autograd entry with two modes.
 ``CrossEntropyFunction`` computes the gradient in the forward (in place) and
 scales it by grad_output in the backward, with a device-side skip when
@@ -507,3 +508,7 @@ def flce_fwd_bwd(hidden, weight, target, *, bias=None, class_weight=None, ignore
                              _ptr(ws), ws.numel(), _stream(stream)), "flce_fwd_bwd")
     return loss, grad_hidden, grad_weight, grad_bias
 
+
+from .logprob import (CE_FLAG_BAD_OFFSETS, PREFERENCE_KINDS, TokenLogprobFunction, ce_policy_fwd_bwd,  # noqa: E402
+                      ce_policy_params, ce_preference_fwd_bwd, ce_preference_params, ce_token_logprob,
+                      ce_token_logprob_backward, policy_loss, preference_loss, token_logprob)

@@ -17,14 +17,14 @@
 
 using namespace ce;
 
-namespace {
+static thread_local std::string g_last_cuda_error;
 
-thread_local std::string g_last_cuda_error;
-
-ce_status cuda_fail(cudaError_t e) {
+ce_status ce::cuda_fail(cudaError_t e) {
     g_last_cuda_error = std::string(cudaGetErrorName(e)) + ": " + cudaGetErrorString(e);
     return CE_ERR_CUDA;
 }
+
+namespace {
 
 int64_t elem_bytes(int32_t dtype) { return dtype == CE_DT_F32 ? 4 : 2; }
 

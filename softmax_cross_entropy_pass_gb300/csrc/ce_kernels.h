@@ -11,6 +11,9 @@ namespace ce {
 
 struct WsCtl;
 
+// keeps the error's text for ce_last_cuda_error and returns CE_ERR_CUDA
+ce_status cuda_fail(cudaError_t e);
+
 constexpr int kPrepThreads = 256;
 constexpr int kRowThreads = 256;
 constexpr int kRowpassThreads = 512;

@@ -1,0 +1,282 @@
+// lp_grad.cu -- the gradient of token log-probabilities from saved row
+// statistics, the normalisers of the policy loss, and the sequence-level
+// kernels of the preference loss.
+#include "lp_device.cuh"
+#include "lp_kernels.h"
+
+namespace ce {
+
+// ------------------------------------------------------------------ policy normalisers
+constexpr int kLpPrepThreads = 1024;
+
+// One block: how many rows take part, the sum of their weights (fp64, fixed
+// order), and the target check. It lets the row kernel start at once; that
+// kernel waits for it where it reads the sum.
+__global__ void __launch_bounds__(kLpPrepThreads) lp_prep_kernel(LpArgs a) {
+    pdl_launch_dependents();
+    __shared__ double sh_w[kLpPrepThreads / 32];
+    __shared__ unsigned sh_bad;
+    const int tid = threadIdx.x;
+    if (tid == 0) sh_bad = 0;
+    __syncthreads();
+    double w = 0.0;
+    bool bad = false;
+    for (int64_t i = tid; i < a.n_rows; i += kLpPrepThreads) {
+        const int64_t t = load_target(a.target, a.tgt32, i);
+        if (target_valid(t, a.ignore_index, a.vocab)) w += a.row_weight ? static_cast<double>(__ldg(a.row_weight + i)) : 1.0;
+        else if (t != a.ignore_index) bad = true;
+    }
+    if (bad) atomicOr(&sh_bad, 1u);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) w += __shfl_xor_sync(0xffffffffu, w, off);
+    if ((tid & 31) == 0) sh_w[tid >> 5] = w;
+    __syncthreads();
+    if (tid == 0) {
+        double sum = 0.0;
+        for (int i = 0; i < kLpPrepThreads / 32; ++i) sum += sh_w[i];
+        a.ctl->done = 0u;
+        a.ctl->w_y = static_cast<float>(sum);
+        a.ctl->status = (sh_bad ? CE_FLAG_TARGET_OUT_OF_RANGE : 0u) |
+                        (a.reduction == CE_RED_MEAN && static_cast<float>(sum) == 0.f ? CE_FLAG_NO_VALID_ROWS : 0u);
+    }
+}
+
+// ------------------------------------------------------------------ gradient from statistics
+constexpr int kLpGradThreads = 256;
+constexpr int kLpGradBytes = 65536;  // bytes of a row per block
+
+// The logits once more, the gradient written: a map over (row, 64 KB part)
+// items, last rows first, so that what the forward read last is still in L2.
+// Bound by HBM; 4 vectors in flight per thread.
+template <int DT, bool ENT>
+__global__ void __launch_bounds__(kLpGradThreads) lp_grad_kernel(LpArgs a, int64_t parts) {
+    using F = Fmt<DT>;
+    constexpr int KB = F::kBytes;
+    constexpr int64_t span = kLpGradBytes / KB;
+    const int tid = threadIdx.x;
+    if (a.row_coef) pdl_wait();
+    for (int64_t i = blockIdx.x; i < a.n_rows * parts; i += gridDim.x) {
+        const int64_t row = a.n_rows - 1 - i / parts, c0 = (i % parts) * span;
+        const int64_t c1 = c0 + span < a.vocab ? c0 + span : a.vocab;
+        char *grow = reinterpret_cast<char *>(a.grad) + row * a.ld_grad * KB;
+        const int64_t t = load_target(a.target, a.tgt32, row);
+        const bool valid = target_valid(t, a.ignore_index, a.vocab);
+        const float g = valid && a.g_logp ? __ldg(a.g_logp + row) : 0.f;
+        const float h = valid && ENT && a.g_entropy ? __ldg(a.g_entropy + row) : 0.f;
+        if (!valid || (a.row_coef && g == 0.f)) {
+            lp_zero_span<DT>(grow, c0, c1, tid, kLpGradThreads);
+            continue;
+        }
+        const float4 st = __ldg(a.stats + row);
+        const LpRow r = lp_row(st, a.k, a.inv_t);
+        const LpGrad lg = lp_grad(st, r, a.inv_t, g, h);
+        lp_grad_span<DT, ENT>(reinterpret_cast<const char *>(a.x) + row * a.ld * KB, grow, c0, c1, static_cast<int>(t), lg,
+                              a.k, tid, kLpGradThreads);
+    }
+}
+
+// ------------------------------------------------------------------ preference pairs
+constexpr int kPairThreads = 256;
+
+// fixed-order block sum of two doubles, to every thread
+__device__ inline void block_sum2(double &x, double &y, double (&sh)[kPairThreads / 32][2]) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+        x += __shfl_xor_sync(0xffffffffu, x, off);
+        y += __shfl_xor_sync(0xffffffffu, y, off);
+    }
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) {
+        sh[threadIdx.x >> 5][0] = x;
+        sh[threadIdx.x >> 5][1] = y;
+    }
+    __syncthreads();
+    x = y = 0.0;
+    for (int i = 0; i < kPairThreads / 32; ++i) {
+        x += sh[i][0];
+        y += sh[i][1];
+    }
+}
+
+// One block per pair (p: sequences p and P + p of the 2 P): their log
+// probability sums in fp64, the pair's loss and the coefficient dL/dlogp of
+// each of their rows, written over the row's log-probability (rows whose
+// target takes no part already hold 0). The batch divisor of the mean (pairs
+// with a valid target on both sides) and grad_output are applied by the
+// kernel that finishes the batch, which all coefficients pass through.
+// Offsets that fall, or leave [0, n_rows], make the whole batch void: loss
+// NaN, gradient 0, a status bit. Every block checks all of them itself.
+__global__ void __launch_bounds__(kPairThreads) lp_pair_kernel(PairArgs a) {
+    __shared__ double sh[kPairThreads / 32][2];
+    pdl_wait();
+    const int tid = threadIdx.x;
+    bool bad = false;
+    for (int64_t j = tid; j < 2 * a.n_pairs; j += kPairThreads) {
+        const int64_t b = load_target(a.offsets, a.off32, j), e = load_target(a.offsets, a.off32, j + 1);
+        if (b < 0 || e < b || e > a.n_rows) bad = true;
+    }
+    if (__syncthreads_or(bad)) {
+        for (int64_t i = static_cast<int64_t>(blockIdx.x) * kPairThreads + tid; i < a.n_rows;
+             i += static_cast<int64_t>(gridDim.x) * kPairThreads)
+            a.row[i] = 0.f;
+        for (int64_t p = static_cast<int64_t>(blockIdx.x) * kPairThreads + tid; p < a.n_pairs;
+             p += static_cast<int64_t>(gridDim.x) * kPairThreads) {
+            a.pair_loss[p] = NAN;
+            if (a.reduction == CE_RED_NONE) a.loss[p] = NAN;
+            if (a.seq_logp) a.seq_logp[p] = a.seq_logp[a.n_pairs + p] = NAN;
+        }
+        if (blockIdx.x == 0 && tid == 0) atomicOr(&a.ctl->status, CE_FLAG_BAD_OFFSETS);
+        return;
+    }
+    for (int64_t p = blockIdx.x; p < a.n_pairs; p += gridDim.x) {
+        int64_t b[2], e[2];
+        double sum[2], cnt[2];
+        bool oob = false;
+        for (int side = 0; side < 2; ++side) {
+            const int64_t seq = p + side * a.n_pairs;
+            b[side] = load_target(a.offsets, a.off32, seq);
+            e[side] = load_target(a.offsets, a.off32, seq + 1);
+            double s = 0.0, n = 0.0;
+            for (int64_t i = b[side] + tid; i < e[side]; i += kPairThreads) {
+                const int64_t t = load_target(a.target, a.tgt32, i);
+                if (target_valid(t, a.ignore_index, a.vocab)) {
+                    s += static_cast<double>(a.row[i]);
+                    n += 1.0;
+                } else if (t != a.ignore_index) {
+                    oob = true;
+                }
+            }
+            block_sum2(s, n, sh);
+            sum[side] = s;
+            cnt[side] = n;
+        }
+        if (__syncthreads_or(oob) && tid == 0) atomicOr(&a.ctl->status, CE_FLAG_TARGET_OUT_OF_RANGE);
+        const bool live = cnt[0] > 0.0 && cnt[1] > 0.0;
+        double v[2];
+        for (int side = 0; side < 2; ++side) v[side] = a.normalize && cnt[side] > 0.0 ? sum[side] / cnt[side] : sum[side];
+        double loss = 0.0, slope = 0.0;
+        if (live) {
+            double h = v[0] - v[1];
+            if (a.ref) h -= static_cast<double>(__ldg(a.ref + p)) - static_cast<double>(__ldg(a.ref + a.n_pairs + p));
+            const double be = a.beta, z = be * h, eps = a.smoothing;
+            if (a.kind == CE_PREF_SIGMOID) {
+                // softplus(+-z) and the logistic function through e^-|z|, which cannot overflow
+                const double q = exp(-fabs(z)), l = log1p(q);
+                const double sp_pos = (z > 0.0 ? z : 0.0) + l, sp_neg = (z > 0.0 ? 0.0 : -z) + l;
+                const double big = 1.0 / (1.0 + q), small = q / (1.0 + q);
+                const double s_pos = z > 0.0 ? big : small, s_neg = z > 0.0 ? small : big;
+                loss = (1.0 - eps) * sp_neg + eps * sp_pos;
+                slope = be * (eps * s_pos - (1.0 - eps) * s_neg);
+            } else if (a.kind == CE_PREF_HINGE) {
+                loss = z < 1.0 ? 1.0 - z : (z >= 1.0 ? 0.0 : z);
+                slope = z < 1.0 ? -be : (z >= 1.0 ? 0.0 : z);
+            } else {
+                const double m = h - 0.5 / be;
+                loss = m * m;
+                slope = 2.0 * m;
+            }
+        }
+        if (tid == 0) {
+            a.pair_loss[p] = loss;
+            if (a.reduction == CE_RED_NONE) a.loss[p] = static_cast<float>(loss);
+            if (a.seq_logp) {
+                a.seq_logp[p] = static_cast<float>(v[0]);
+                a.seq_logp[a.n_pairs + p] = static_cast<float>(v[1]);
+            }
+            if (live) atomicAdd(&a.ctl->n_correct, 1u);  // integers: the order does not matter
+        }
+        if (a.reduction == CE_RED_NONE && a.grad_output) slope *= static_cast<double>(__ldg(a.grad_output + p));
+        for (int side = 0; side < 2; ++side) {
+            double c = side == 0 ? slope : -slope;
+            if (a.normalize && live) c /= cnt[side];
+            const float cf = static_cast<float>(c);
+            for (int64_t i = b[side] + tid; i < e[side]; i += kPairThreads) {
+                const int64_t t = load_target(a.target, a.tgt32, i);
+                a.row[i] = target_valid(t, a.ignore_index, a.vocab) ? cf : 0.f;
+            }
+        }
+    }
+}
+
+// The batch: loss = the pair losses' sum (fixed order, fp64) over the number
+// of live pairs for the mean, and the row coefficients times the same divisor
+// and grad_output. One launch, every block scales its share of the rows and
+// the first also forms the loss.
+__global__ void __launch_bounds__(kPairThreads) lp_pair_finish_kernel(PairArgs a) {
+    __shared__ double sh[kPairThreads / 32][2];
+    pdl_wait();
+    const int tid = threadIdx.x;
+    const unsigned live = a.ctl->n_correct;
+    const bool mean = a.reduction == CE_RED_MEAN;
+    if (a.reduction != CE_RED_NONE) {
+        const float up = a.grad_output ? __ldg(a.grad_output) : 1.f;
+        const float scale = mean ? (live ? up / static_cast<float>(live) : 0.f) : up;
+        for (int64_t i = static_cast<int64_t>(blockIdx.x) * kPairThreads + tid; i < a.n_rows;
+             i += static_cast<int64_t>(gridDim.x) * kPairThreads)
+            if (a.row[i] != 0.f) a.row[i] *= scale;
+        if (blockIdx.x == 0) {
+            double s = 0.0, none = 0.0;
+            for (int64_t p = tid; p < a.n_pairs; p += kPairThreads) s += a.pair_loss[p];
+            block_sum2(s, none, sh);
+            if (tid == 0) {
+                if (mean && live) s /= static_cast<double>(live);
+                a.loss[0] = static_cast<float>(s);
+            }
+        }
+    }
+    if (blockIdx.x == 0 && tid == 0 && live == 0u && !(a.ctl->status & CE_FLAG_BAD_OFFSETS))
+        a.ctl->status |= CE_FLAG_NO_VALID_ROWS;
+}
+
+// ------------------------------------------------------------------ launches
+template <typename A>
+static cudaError_t launch_dep(const void *fn, int64_t grid, int threads, A &a, int64_t *extra, bool dependent,
+                              cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid < 1 ? 1 : grid));
+    cfg.blockDim = dim3(threads);
+    cfg.stream = s;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = dependent ? 1 : 0;
+    void *args[] = {&a, extra};
+    return cudaLaunchKernelExC(&cfg, fn, args);
+}
+
+cudaError_t launch_lp_prep(const LpArgs &a0, cudaStream_t s) {
+    LpArgs a = a0;
+    return launch_dep(reinterpret_cast<const void *>(&lp_prep_kernel), 1, kLpPrepThreads, a, nullptr, false, s);
+}
+
+template <int DT>
+static const void *grad_fn(bool ent) {
+    return ent ? reinterpret_cast<const void *>(&lp_grad_kernel<DT, true>)
+               : reinterpret_cast<const void *>(&lp_grad_kernel<DT, false>);
+}
+
+cudaError_t launch_lp_grad(const LpArgs &a0, int dtype, bool entropy, bool dependent, cudaStream_t s) {
+    LpArgs a = a0;
+    const void *fn = dtype == CE_DT_F32 ? grad_fn<CE_DT_F32>(entropy)
+                   : dtype == CE_DT_BF16 ? grad_fn<CE_DT_BF16>(entropy) : grad_fn<CE_DT_F16>(entropy);
+    const int64_t span = kLpGradBytes / (dtype == CE_DT_F32 ? 4 : 2);
+    int64_t parts = (a.vocab + span - 1) / span;
+    const int64_t items = a.n_rows * parts, cap = int64_t(1) << 20;
+    return launch_dep(fn, items < cap ? items : cap, kLpGradThreads, a, &parts, dependent, s);
+}
+
+cudaError_t launch_lp_pairs(const PairArgs &a0, cudaStream_t s) {
+    PairArgs a = a0;
+    return launch_dep(reinterpret_cast<const void *>(&lp_pair_kernel), a.n_pairs < 512 ? a.n_pairs : 512, kPairThreads, a,
+                      nullptr, true, s);
+}
+
+cudaError_t launch_lp_pair_loss(const PairArgs &a0, cudaStream_t s) {
+    PairArgs a = a0;
+    const int64_t want = (a.n_rows + kPairThreads - 1) / kPairThreads;
+    return launch_dep(reinterpret_cast<const void *>(&lp_pair_finish_kernel), want < 64 ? want : 64, kPairThreads, a,
+                      nullptr, true, s);
+}
+
+}  // namespace ce

@@ -1,0 +1,83 @@
+// lp_policy.cuh -- the scalars of one row of the clipped policy loss, shared
+// by the kernels that form it.
+#pragma once
+
+#include "lp_device.cuh"
+#include "lp_kernels.h"
+
+namespace ce {
+
+// e^g - g - 1 >= 0: near 0 by its series (the subtraction would cancel)
+__device__ inline float kl_of_gap(float g) {
+    if (fabsf(g) < 0.25f) {
+        float p = 1.f / 40320.f;  // g^8 / 8!, relative error below 2e-9 there
+        p = fmaf(p, g, 1.f / 5040.f);
+        p = fmaf(p, g, 1.f / 720.f);
+        p = fmaf(p, g, 1.f / 120.f);
+        p = fmaf(p, g, 1.f / 24.f);
+        p = fmaf(p, g, 1.f / 6.f);
+        p = fmaf(p, g, 0.5f);
+        return p * g * g;
+    }
+    return expf(g) - g - 1.f;
+}
+
+// What a policy row reads besides its logits, fetched before its first pass.
+struct PolicyIn {
+    float adv, old_logp, ref_logp, weight;
+};
+// a row without a usable target or with weight 0 takes no part: nothing else of it is read
+__device__ inline bool policy_row_live(const LpArgs &a, int64_t row, int64_t t) {
+    return target_valid(t, a.ignore_index, a.vocab) && !(a.row_weight && __ldg(a.row_weight + row) == 0.f);
+}
+__device__ inline PolicyIn policy_load(const LpArgs &a, int64_t row) {
+    PolicyIn p;
+    p.adv = __ldg(a.adv + row);
+    p.old_logp = a.old_logp ? __ldg(a.old_logp + row) : 0.f;
+    p.ref_logp = a.ref_logp ? __ldg(a.ref_logp + row) : 0.f;
+    p.weight = a.row_weight ? __ldg(a.row_weight + row) : 1.f;
+    return p;
+}
+
+struct PolicyOut {
+    float loss;        // weighted, not divided by the batch's normaliser
+    float g, h;        // d(weighted loss) / dlogp and / dH
+    float ratio, kl;
+};
+// r = e^(logp - old), loss = max(-A r, -A clip(r)) + beta (e^gap - gap - 1) - eta H,
+// gap = ref - logp. On the border of the clip range (the two branches equal)
+// the unclipped branch's slope is taken. NaN inputs come out NaN.
+__device__ inline PolicyOut policy_row(const LpArgs &a, const PolicyIn &in, const LpRow &r, float entropy) {
+    PolicyOut o;
+    o.ratio = a.old_logp ? expf(r.logp - in.old_logp) : 1.f;
+    const float clipped = fminf(fmaxf(o.ratio, a.clip_lo), a.clip_hi);
+    const float u1 = -in.adv * o.ratio, u2 = -in.adv * clipped;
+    float loss = u1 < u2 ? u2 : u1;
+    float g = u1 < u2 ? 0.f : u1;
+    o.kl = 0.f;
+    if (a.ref_logp) {
+        const float gap = in.ref_logp - r.logp;
+        o.kl = kl_of_gap(gap);
+        if (a.kl_coef != 0.f) {
+            loss = fmaf(a.kl_coef, o.kl, loss);
+            g = fmaf(-a.kl_coef, expm1f(gap), g);
+        }
+    }
+    o.h = 0.f;
+    if (a.ent_coef != 0.f) {
+        loss = fmaf(-a.ent_coef, entropy, loss);
+        o.h = -a.ent_coef * in.weight;
+    }
+    o.loss = in.weight * loss;
+    o.g = in.weight * g;
+    return o;
+}
+
+// the gradient scale of the batch: grad_output over the weight sum for mean
+__device__ inline float policy_scale(const LpArgs &a, int64_t row, float w_sum) {
+    const float up = a.grad_output ? __ldg(a.grad_output + (a.reduction == CE_RED_NONE ? row : 0)) : 1.f;
+    if (a.reduction != CE_RED_MEAN) return up;
+    return w_sum != 0.f ? up / w_sum : 0.f;
+}
+
+}  // namespace ce

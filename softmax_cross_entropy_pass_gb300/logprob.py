@@ -1,0 +1,359 @@
+"""Token log-probabilities and the post-training losses made of them.
+
+  ce_token_logprob(logits, target, ...)            -> (logp, entropy, stats)
+  ce_token_logprob_backward(logits, target, stats, grad_logp, ...) -> grad
+  ce_policy_fwd_bwd(logits, target, advantage, ...)    -> (loss, grad)
+  ce_preference_fwd_bwd(logits, target, seq_offsets, ...) -> (loss, seq_logp, grad)
+and their torch.autograd entries ``token_logprob``, ``policy_loss`` and
+``preference_loss``. The formulas, the layouts and what each call does with
+ignored rows are in include/ce.h.
+
+``logits`` is a 2-D CUDA tensor with unit column stride (bf16, fp16 or fp32).
+Per-row and per-sequence inputs are contiguous fp32 tensors on its device.
+``grad`` receives the gradient: a tensor of the logits' shape and dtype with
+unit column stride, or None to write it over the logits. ``stream`` defaults
+to the current stream of the logits' device.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import (CE_DT, CE_RED, CEError, _check, _lib, _ptr, ce_params, ce_scale_grad)
+
+CE_FLAG_BAD_OFFSETS = 8
+PREFERENCE_KINDS = {"sigmoid": 0, "hinge": 1, "squared": 2}
+
+
+class ce_policy_params(ctypes.Structure):
+    _fields_ = [("temperature", ctypes.c_float), ("clip_low", ctypes.c_float), ("clip_high", ctypes.c_float),
+                ("kl_coef", ctypes.c_float), ("entropy_coef", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
+
+class ce_preference_params(ctypes.Structure):
+    _fields_ = [("n_pairs", ctypes.c_int64), ("kind", ctypes.c_int32), ("offsets_are_int32", ctypes.c_int32),
+                ("length_normalize", ctypes.c_int32), ("beta", ctypes.c_float), ("label_smoothing", ctypes.c_float),
+                ("reserved", ctypes.c_int32)]
+
+
+assert ctypes.sizeof(ce_policy_params) == 24 and ctypes.sizeof(ce_preference_params) == 32
+
+
+def _sign():
+    P, vp, f, i64 = ctypes.POINTER(ce_params), ctypes.c_void_p, ctypes.c_float, ctypes.c_int64
+    sz, st = ctypes.c_size_t, ctypes.c_int
+    for name, args in {
+        "ce_token_logprob": [P, f, vp, vp, vp, vp, vp, vp],
+        "ce_token_logprob_backward": [P, f, vp, vp, vp, vp, vp, vp, i64, vp],
+        "ce_policy_fwd_bwd": [P, ctypes.POINTER(ce_policy_params)] + [vp] * 10 + [i64, vp, sz, vp],
+        "ce_preference_workspace_size": [P, i64, ctypes.POINTER(sz)],
+        "ce_preference_fwd_bwd": [P, ctypes.POINTER(ce_preference_params)] + [vp] * 8 + [i64, vp, sz, vp],
+    }.items():
+        fn = getattr(_lib, name)
+        fn.restype, fn.argtypes = st, args
+
+
+_sign()
+
+
+# ---------------------------------------------------------------------- arguments
+def _params(logits, target, ignore_index, reduction="mean") -> ce_params:
+    if logits.dim() != 2 or logits.stride(1) != 1 and logits.shape[1] != 1:
+        raise ValueError("logits must be a 2-D tensor with unit column stride")
+    if logits.dtype not in CE_DT:
+        raise TypeError(f"unsupported logits dtype {logits.dtype}")
+    if target.dtype not in (torch.int64, torch.int32):
+        raise TypeError("target must be int64 or int32")
+    n, v = logits.shape
+    if target.dim() != 1 or target.shape[0] != n or not target.is_contiguous():
+        raise ValueError("target must be a contiguous 1-D tensor with one entry per row")
+    if reduction not in CE_RED:
+        raise ValueError(f"unknown reduction {reduction!r}")
+    p = ce_params()
+    p.n_rows, p.vocab, p.ld = n, v, logits.stride(0) if n > 1 else v
+    p.ignore_index = ignore_index
+    p.dtype, p.reduction = CE_DT[logits.dtype], CE_RED[reduction]
+    p.target_is_int32 = 1 if target.dtype == torch.int32 else 0
+    return p
+
+
+def _vec(name, t, n, device):
+    """A contiguous fp32 vector of n entries on the logits' device (or None)."""
+    if t is not None and (t.dtype != torch.float32 or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous()
+                          or t.device != device):
+        raise ValueError(f"{name} must be a contiguous fp32 tensor of {n} entries on the logits' device")
+    return t
+
+
+def _grad_buffer(logits, grad):
+    if grad is None:
+        return logits, logits.stride(0) if logits.shape[0] > 1 else logits.shape[1]
+    if grad.shape != logits.shape or grad.dtype != logits.dtype or grad.device != logits.device \
+            or (grad.stride(1) != 1 and grad.shape[1] != 1):
+        raise ValueError("grad must have the logits' shape, dtype and device, and unit column stride")
+    return grad, grad.stride(0) if grad.shape[0] > 1 else grad.shape[1]
+
+
+class _Call:
+    """The device and the stream of one call. Memory that the call allocates
+    comes from the current stream's pool: where the kernels run on another
+    stream, that pool is told so before it may hand the memory out again."""
+
+    def __init__(self, tensor, others, stream):
+        if not tensor.is_cuda:
+            raise ValueError("all tensors must live on the GPU")
+        self.device = tensor.device
+        for t in others:
+            if t is not None and t.device != self.device:
+                raise ValueError("all tensors must live on the logits' device")
+        current = torch.cuda.current_stream(self.device)
+        if stream is None:
+            stream = current
+        elif not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream), device=self.device)
+        if stream.device != self.device:
+            raise ValueError("stream must be one of the logits' device")
+        self.stream = stream
+        self.other = current if stream.cuda_stream != current.cuda_stream else None
+        self.handle = ctypes.c_void_p(stream.cuda_stream)
+
+    def empty(self, *shape, dtype=torch.float32):
+        t = torch.empty(*shape, dtype=dtype, device=self.device)
+        if self.other is not None:
+            self.stream.wait_stream(self.other)  # the memory's last user may still be running there
+            t.record_stream(self.stream)
+        return t
+
+    def run(self, name, *args):
+        if torch.cuda.current_device() == self.device.index:
+            _check(getattr(_lib, name)(*args, self.handle), name)
+        else:
+            with torch.cuda.device(self.device):
+                _check(getattr(_lib, name)(*args, self.handle), name)
+
+
+def _workspace(call, ws, nbytes):
+    if ws is None:
+        return call.empty(nbytes, dtype=torch.uint8), nbytes
+    if ws.device != call.device or not ws.is_contiguous():
+        raise ValueError("ws must be a contiguous tensor on the logits' device")
+    return ws, ws.numel() * ws.element_size()
+
+
+def _ws_bytes(p, n_pairs=None) -> int:
+    out = ctypes.c_size_t()
+    if n_pairs is None:
+        _check(_lib.ce_workspace_size(ctypes.byref(p), ctypes.byref(out)), "ce_workspace_size")
+    else:
+        _check(_lib.ce_preference_workspace_size(ctypes.byref(p), n_pairs, ctypes.byref(out)),
+               "ce_preference_workspace_size")
+    return out.value
+
+
+# ---------------------------------------------------------------------- token log-probabilities
+def ce_token_logprob(logits, target, *, temperature=1.0, ignore_index=-100, with_entropy=True, logp=None, entropy=None,
+                     stats=None, stream=None):
+    """(logp [n], entropy [n] or None, stats [n, 4]) of softmax(logits / temperature):
+    the log-probability of every row's target and the entropy of its
+    distribution. Ignored rows give 0, targets outside the vocabulary NaN.
+    One kernel, no workspace."""
+    p = _params(logits, target, ignore_index)
+    n = p.n_rows
+    call = _Call(logits, (target, logp, entropy, stats), stream)
+    logp = call.empty(n) if logp is None else _vec("logp", logp, n, call.device)
+    if with_entropy:
+        entropy = call.empty(n) if entropy is None else _vec("entropy", entropy, n, call.device)
+    elif entropy is not None:
+        raise ValueError("entropy given with with_entropy=False")
+    if stats is None:
+        stats = call.empty(n, 4)
+    elif stats.dtype != torch.float32 or stats.shape != (n, 4) or not stats.is_contiguous():
+        raise ValueError("stats must be a contiguous fp32 [n_rows, 4] tensor")
+    call.run("ce_token_logprob", ctypes.byref(p), float(temperature), _ptr(logits), _ptr(target), _ptr(logp),
+             _ptr(entropy), _ptr(stats))
+    return logp, entropy, stats
+
+
+def ce_token_logprob_backward(logits, target, stats, grad_logp, *, grad_entropy=None, temperature=1.0,
+                              ignore_index=-100, grad=None, stream=None):
+    """The gradient of sum(grad_logp logp + grad_entropy entropy), from the
+    statistics ce_token_logprob returned for the same logits (with the
+    entropy, if grad_entropy is given). Written over the logits unless
+    ``grad`` is given; returned."""
+    p = _params(logits, target, ignore_index)
+    n = p.n_rows
+    grad, ld = _grad_buffer(logits, grad)
+    call = _Call(logits, (target, stats, grad_logp, grad_entropy, grad), stream)
+    _vec("grad_logp", grad_logp, n, call.device)
+    _vec("grad_entropy", grad_entropy, n, call.device)
+    if stats.dtype != torch.float32 or stats.shape != (n, 4) or not stats.is_contiguous():
+        raise ValueError("stats must be a contiguous fp32 [n_rows, 4] tensor")
+    call.run("ce_token_logprob_backward", ctypes.byref(p), float(temperature), _ptr(logits), _ptr(target), _ptr(stats),
+             _ptr(grad_logp), _ptr(grad_entropy), _ptr(grad), ld)
+    return grad
+
+
+# ---------------------------------------------------------------------- policy loss
+def ce_policy_fwd_bwd(logits, target, advantage, *, old_logp=None, ref_logp=None, row_weight=None, clip_low=0.2,
+                      clip_high=0.2, kl_coef=0.0, entropy_coef=0.0, temperature=1.0, ignore_index=-100,
+                      reduction="mean", grad_output=None, grad=None, loss=None, row_stats=None, ws=None, stream=None):
+    """(loss, grad) of the clipped policy loss with a KL term and an entropy
+    bonus; ``grad`` (times grad_output, or 1) is written over the logits
+    unless a buffer is given. ``row_stats``: an fp32 [n, 4] tensor that
+    receives {logp, entropy, ratio, KL} of every row."""
+    p = _params(logits, target, ignore_index, reduction)
+    n = p.n_rows
+    grad, ld = _grad_buffer(logits, grad)
+    call = _Call(logits, (target, grad, loss), stream)
+    for name, t in (("advantage", advantage), ("old_logp", old_logp), ("ref_logp", ref_logp),
+                    ("row_weight", row_weight)):
+        _vec(name, t, n, call.device)
+    m = n if reduction == "none" else 1
+    _vec("grad_output", grad_output, m, call.device)
+    loss = call.empty(m) if loss is None else _vec("loss", loss, m, call.device)
+    if row_stats is not None and (row_stats.dtype != torch.float32 or row_stats.shape != (n, 4)
+                                  or not row_stats.is_contiguous() or row_stats.device != call.device):
+        raise ValueError("row_stats must be a contiguous fp32 [n_rows, 4] tensor on the logits' device")
+    q = ce_policy_params(float(temperature), float(clip_low), float(clip_high), float(kl_coef), float(entropy_coef), 0)
+    ws, nbytes = _workspace(call, ws, _ws_bytes(p))
+    call.run("ce_policy_fwd_bwd", ctypes.byref(p), ctypes.byref(q), _ptr(logits), _ptr(target), _ptr(advantage),
+             _ptr(old_logp), _ptr(ref_logp), _ptr(row_weight), _ptr(grad_output), _ptr(loss), _ptr(row_stats),
+             _ptr(grad), ld, _ptr(ws), nbytes)
+    return loss, grad
+
+
+# ---------------------------------------------------------------------- preference loss
+def ce_preference_fwd_bwd(logits, target, seq_offsets, *, ref_logp=None, loss_kind="sigmoid", beta=0.1,
+                          label_smoothing=0.0, length_normalize=False, ignore_index=-100, reduction="mean",
+                          grad_output=None, grad=None, loss=None, seq_logp=None, ws=None, stream=None):
+    """(loss, seq_logp [2 P], grad) of the paired preference loss. Sequence j
+    is the rows seq_offsets[j] .. seq_offsets[j + 1] (2 P + 1 offsets); the
+    first P sequences are the preferred ones, the last P their counterparts
+    in the same order. ``seq_logp`` holds every sequence's log-probability
+    (its mean per token with ``length_normalize``), ``ref_logp`` the
+    reference model's values of the same kind. ``grad`` (times grad_output,
+    or 1) is written over the logits unless a buffer is given."""
+    p = _params(logits, target, ignore_index, reduction)
+    n = p.n_rows
+    if seq_offsets.dtype not in (torch.int64, torch.int32) or seq_offsets.dim() != 1 \
+            or not seq_offsets.is_contiguous() or seq_offsets.shape[0] % 2 != 1:
+        raise ValueError("seq_offsets must be a contiguous 1-D int64 or int32 tensor of 2 P + 1 entries")
+    if loss_kind not in PREFERENCE_KINDS:
+        raise ValueError(f"unknown loss_kind {loss_kind!r}")
+    pairs = seq_offsets.shape[0] // 2
+    grad, ld = _grad_buffer(logits, grad)
+    call = _Call(logits, (target, seq_offsets, grad), stream)
+    _vec("ref_logp", ref_logp, 2 * pairs, call.device)
+    m = pairs if reduction == "none" else 1
+    _vec("grad_output", grad_output, m, call.device)
+    loss = call.empty(m) if loss is None else _vec("loss", loss, m, call.device)
+    seq_logp = call.empty(2 * pairs) if seq_logp is None else _vec("seq_logp", seq_logp, 2 * pairs, call.device)
+    q = ce_preference_params(pairs, PREFERENCE_KINDS[loss_kind], 1 if seq_offsets.dtype == torch.int32 else 0,
+                             1 if length_normalize else 0, float(beta), float(label_smoothing), 0)
+    ws, nbytes = _workspace(call, ws, _ws_bytes(p, pairs))
+    call.run("ce_preference_fwd_bwd", ctypes.byref(p), ctypes.byref(q), _ptr(logits), _ptr(target), _ptr(seq_offsets),
+             _ptr(ref_logp), _ptr(grad_output), _ptr(loss), _ptr(seq_logp), _ptr(grad), ld, _ptr(ws), nbytes)
+    return loss, seq_logp, grad
+
+
+# ---------------------------------------------------------------------- autograd
+def _once(ctx):
+    """The backward passes here write or scale one buffer in place: a second
+    run over the same graph would use it up again."""
+    if getattr(ctx, "spent", False):
+        raise CEError("the gradient of this call has been used up (its buffer was handed out by an earlier backward)")
+    ctx.spent = True
+
+
+class TokenLogprobFunction(torch.autograd.Function):
+    """Forward reads the logits once and keeps 16 bytes a row; the backward
+    reads them again and writes the gradient (over them with ``inplace``)."""
+
+    @staticmethod
+    def forward(ctx, logits, target, temperature, ignore_index, with_entropy, inplace):
+        x = logits.detach()
+        logp, entropy, stats = ce_token_logprob(x, target, temperature=temperature, ignore_index=ignore_index,
+                                                with_entropy=with_entropy)
+        ctx.save_for_backward(logits, target, stats)
+        ctx.args = temperature, ignore_index, inplace
+        ctx.set_materialize_grads(False)
+        return (logp, entropy) if with_entropy else logp
+
+    @staticmethod
+    def backward(ctx, grad_logp, grad_entropy=None):
+        if grad_logp is None and grad_entropy is None:
+            return None, None, None, None, None, None
+        logits, target, stats = ctx.saved_tensors
+        temperature, ignore_index, inplace = ctx.args
+        x = logits.detach()
+        if inplace:
+            _once(ctx)
+        g = None if grad_logp is None else grad_logp.detach().to(torch.float32).contiguous()
+        h = None if grad_entropy is None else grad_entropy.detach().to(torch.float32).contiguous()
+        out = ce_token_logprob_backward(x, target, stats, g, grad_entropy=h, temperature=temperature,
+                                        ignore_index=ignore_index, grad=None if inplace else torch.empty_like(x))
+        return out, None, None, None, None, None
+
+
+def token_logprob(logits, target, *, temperature=1.0, ignore_index=-100, with_entropy=False, inplace=False):
+    """Differentiable log-probabilities of the targets (and the entropies, as
+    a pair, with ``with_entropy``). ``inplace``: the backward writes the
+    gradient over the logits, which nothing else may use then."""
+    return TokenLogprobFunction.apply(logits, target, temperature, ignore_index, with_entropy, inplace)
+
+
+class _FormedGradientFunction(torch.autograd.Function):
+    """A loss whose gradient the forward forms (one read and one write of the
+    logits); the backward multiplies it by grad_output, skipped on the device
+    where that is 1 (otherwise the product is rounded a second time)."""
+
+    @staticmethod
+    def forward(ctx, logits, inplace, per_row, run):
+        x = logits.detach()
+        loss, grad = run(x, x if inplace else torch.empty_like(x))
+        ctx.save_for_backward(grad)
+        ctx.per_row = per_row
+        return loss if per_row else loss.reshape(())
+
+    @staticmethod
+    def backward(ctx, grad_out):
+        _once(ctx)
+        (grad,) = ctx.saved_tensors
+        if grad.shape[0]:
+            g = grad_out.detach().to(torch.float32).reshape(-1).contiguous()
+            with torch.cuda.device(grad.device):
+                ce_scale_grad(grad, g, reduction="none" if ctx.per_row else "mean")
+        return grad, None, None, None
+
+
+def policy_loss(logits, target, advantage, *, old_logp=None, ref_logp=None, row_weight=None, clip_low=0.2,
+                clip_high=0.2, kl_coef=0.0, entropy_coef=0.0, temperature=1.0, ignore_index=-100, reduction="mean",
+                row_stats=None, inplace=False):
+    """Differentiable ce_policy_fwd_bwd: the loss (a scalar, or [n] for
+    reduction "none"). The gradient reaches the logits only; advantage,
+    old_logp, ref_logp and row_weight are constants. ``inplace``: the
+    gradient is formed over the logits, which nothing else may use then."""
+    def run(x, grad):
+        return ce_policy_fwd_bwd(x, target, advantage, old_logp=old_logp, ref_logp=ref_logp, row_weight=row_weight,
+                                 clip_low=clip_low, clip_high=clip_high, kl_coef=kl_coef, entropy_coef=entropy_coef,
+                                 temperature=temperature, ignore_index=ignore_index, reduction=reduction, grad=grad,
+                                 row_stats=row_stats)
+    return _FormedGradientFunction.apply(logits, inplace, reduction == "none", run)
+
+
+def preference_loss(logits, target, seq_offsets, *, ref_logp=None, loss_kind="sigmoid", beta=0.1, label_smoothing=0.0,
+                    length_normalize=False, ignore_index=-100, reduction="mean", seq_logp=None, inplace=False):
+    """Differentiable ce_preference_fwd_bwd: the scalar loss ("mean" or
+    "sum"). ``seq_logp``, if given, receives the sequences' values. The
+    gradient reaches the logits only. ``inplace`` as in policy_loss."""
+    if reduction not in ("mean", "sum"):
+        raise ValueError("preference_loss takes reduction 'mean' or 'sum'")
+
+    def run(x, grad):
+        loss, _, grad = ce_preference_fwd_bwd(x, target, seq_offsets, ref_logp=ref_logp, loss_kind=loss_kind, beta=beta,
+                                              label_smoothing=label_smoothing, length_normalize=length_normalize,
+                                              ignore_index=ignore_index, reduction=reduction, grad=grad,
+                                              seq_logp=seq_logp)
+        return loss, grad
+    return _FormedGradientFunction.apply(logits, inplace, False, run)
