@@ -516,6 +516,49 @@ ce_status ce_preference_fwd_bwd(const ce_params *p, const ce_preference_params *
                                 const float *grad_output, float *loss, float *seq_logp, void *grad, int64_t ld_grad,
                                 void *workspace, size_t workspace_bytes, void *stream);
 
+/*
+ * Token log-probabilities of a linear head, z = (hidden weight^T + bias) / T,
+ * and their gradient. The logits are formed tile by tile on the tensor cores
+ * (fp32 accumulation) and never stored.
+ *   p       n_rows, vocab, ignore_index, target_is_int32; dtype = CE_DT_BF16
+ *           (hidden and weight); the other fields as for ce_token_logprob,
+ *           ld and reduction are ignored.
+ *   hidden  device bf16 [n_rows, H], weight device bf16 [vocab, H], both
+ *           row-major and 16-byte aligned; H a multiple of 8, any vocab.
+ *   bias    device fp32 [vocab] (16-byte aligned) or NULL.
+ *   target, logp, entropy, stats: as for ce_token_logprob.
+ * Rows whose target is ignored or out of range are skipped on the device
+ * (their hidden states may hold anything).
+ */
+
+/* Workspace bytes: of flce_token_logprob for chunk_rows = 0 (16 bytes per row
+ * and 256-column tile, and over 128 rows a compacted copy of hidden), of
+ * flce_token_logprob_backward for its chunk_rows. */
+ce_status flce_token_logprob_workspace_size(const ce_params *p, int64_t hidden_dim, int64_t chunk_rows, size_t *bytes);
+
+ce_status flce_token_logprob(const ce_params *p, int64_t hidden_dim, float temperature, const void *hidden,
+                             const void *weight, const float *bias, const void *target, float *logp, float *entropy,
+                             float *stats, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * The gradient of sum_i g_i logp_i + h_i H_i with respect to hidden, weight
+ * and bias, from the statistics of flce_token_logprob on the same inputs. Per
+ * chunk of chunk_rows rows the logits are formed again and their gradient dZ
+ * (chunk_rows x vocab, rounded once to bf16) is kept in the workspace;
+ * grad_hidden = dZ weight, grad_weight (+)= dZ^T hidden.
+ *   grad_logp, grad_entropy  device fp32 [n_rows], or NULL for 0 (not both).
+ *   grad_hidden  device bf16 [n_rows, H] (written; 0 on skipped rows).
+ *   grad_weight  device [vocab, H] (written), fp32 or bf16 (grad_weight_dtype);
+ *                bf16 with chunk_rows >= n_rows only (CE_ERR_UNSUPPORTED:
+ *                several chunks add up in fp32). 16-byte aligned.
+ *   grad_bias    device fp32 [vocab], or NULL.
+ */
+ce_status flce_token_logprob_backward(const ce_params *p, int64_t hidden_dim, float temperature, const void *hidden,
+                                      const void *weight, const float *bias, const void *target, const float *stats,
+                                      const float *grad_logp, const float *grad_entropy, void *grad_hidden,
+                                      void *grad_weight, int32_t grad_weight_dtype, float *grad_bias,
+                                      int64_t chunk_rows, void *workspace, size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -509,6 +509,7 @@ def flce_fwd_bwd(hidden, weight, target, *, bias=None, class_weight=None, ignore
     return loss, grad_hidden, grad_weight, grad_bias
 
 
-from .logprob import (CE_FLAG_BAD_OFFSETS, PREFERENCE_KINDS, TokenLogprobFunction, ce_policy_fwd_bwd,  # noqa: E402
-                      ce_policy_params, ce_preference_fwd_bwd, ce_preference_params, ce_token_logprob,
-                      ce_token_logprob_backward, policy_loss, preference_loss, token_logprob)
+from .logprob import (CE_FLAG_BAD_OFFSETS, PREFERENCE_KINDS, LinearTokenLogprobFunction,  # noqa: E402
+                      TokenLogprobFunction, ce_policy_fwd_bwd, ce_policy_params, ce_preference_fwd_bwd,
+                      ce_preference_params, ce_token_logprob, ce_token_logprob_backward, flce_token_logprob,
+                      flce_token_logprob_backward, linear_token_logprob, policy_loss, preference_loss, token_logprob)

@@ -25,6 +25,7 @@
 #include "ce_device.cuh"
 #include "ce_kernels.h"
 #include "flce.h"
+#include "lp_device.cuh"
 #include "tc_device.cuh"
 
 namespace ce {
@@ -72,6 +73,11 @@ struct GemmArgs {
     int st_tgt32;
     int64_t st_ignore;
     const float *st_weight;
+    // log-probability epilogues (GemmLp)
+    const LpMapRow *lp_rows;
+    float lp_k;
+    int lp_ent;
+    int m_static;          // M before a device-side count lowered it
 };
 
 __device__ inline void tile_coords(const GemmArgs &g, int t, int &tm, int &tn) {
@@ -206,8 +212,116 @@ __device__ inline void epilogue_stats(const GemmArgs &g, int row, int col0, cons
     }
 }
 
+// One row's 32 consecutive logits (+ bias); columns past N read as -inf.
+__device__ inline void epilogue_logits(const GemmArgs &g, int col0, const uint32_t (&v)[32], float (&x)[32]) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) x[j] = __uint_as_float(v[j]);
+    if (col0 + 32 <= g.N) {
+        if (g.bias) {
+            const float4 *b4 = reinterpret_cast<const float4 *>(g.bias + col0);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                const float4 bb = __ldg(b4 + q);
+                x[4 * q] += bb.x; x[4 * q + 1] += bb.y; x[4 * q + 2] += bb.z; x[4 * q + 3] += bb.w;
+            }
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            x[j] = col0 + j < g.N ? x[j] + (g.bias ? __ldg(g.bias + col0 + j) : 0.f) : -INFINITY;
+    }
+}
+
+// Log-probability statistics of 32 logits of one row (nothing stored): the
+// target column (position `skip` among them, or -1) is taken out and kept in xy.
+__device__ inline void epilogue_lp_stats(const GemmArgs &g, int col0, const uint32_t (&v)[32], LpState &st, int skip,
+                                         float &xy) {
+    if (col0 >= g.N) return;
+    float x[32];
+    epilogue_logits(g, col0, v, x);
+    if (skip >= 0) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            if (j == skip) {
+                xy = x[j];
+                x[j] = -INFINITY;
+            }
+    }
+    float vmax = x[0];
+#pragma unroll
+    for (int j = 1; j < 32; ++j) vmax = fmaxf(vmax, x[j]);
+    if (g.lp_ent) lp_add<true, 32>(st, x, vmax, g.lp_k);
+    else lp_add<false, 32>(st, x, vmax, g.lp_k);
+}
+
+// The gradient of 32 logits of one row, rounded once to bf16.
+__device__ inline void epilogue_lp_grad(const GemmArgs &g, int row, int col0, const uint32_t (&v)[32], const LpGrad &lg,
+                                        int y) {
+    if (col0 >= g.N) return;
+    float x[32];
+    if (row < g.M) {
+        epilogue_logits(g, col0, v, x);
+        if (g.lp_ent) lp_grad_vec<true, 32>(lg, x, g.lp_k, x);
+        else lp_grad_vec<false, 32>(lg, x, g.lp_k, x);
+        const int rel = y - col0;
+        if (static_cast<unsigned>(rel) < 32u) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) x[j] = j == rel ? lg.dy : x[j];
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) x[j] = 0.f;
+    }
+    __nv_bfloat16 *o = reinterpret_cast<__nv_bfloat16 *>(g.out) + static_cast<int64_t>(row) * g.ldo + col0;
+    if (col0 + 32 <= g.N) {  // the row stride is a multiple of 8
+#pragma unroll
+        for (int q = 0; q < 4; ++q) reinterpret_cast<uint4 *>(o)[q] = Fmt<CE_DT_BF16>::pack(x + 8 * q);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            if (col0 + j < g.N) o[j] = __float2bfloat16_rn(x[j]);
+    }
+}
+
+// The log-probability epilogue of one tile by one warp: this thread's row,
+// its 256 accumulator columns in steps of 32. EPI 4: statistics; 5: gradient.
+template <int EPI>
+__device__ inline void epilogue_lp_tile(const GemmArgs &g, int row, int tn, uint32_t taddr) {
+    LpState st = lp_empty();
+    float xy = 0.f;
+    int y = -(1 << 30);
+    LpGrad lg{};
+    // rows past M whose gradient the products over rows still read, in steps of 64
+    const bool zero_row = EPI == 5 && row >= g.M && row < g.m_static && row < (g.M + 63) / 64 * 64;
+    if (row < g.M) {
+        if (EPI == 4) {
+            const int64_t t = load_target(g.st_target, g.st_tgt32, row);
+            if (target_valid(t, g.st_ignore, g.N)) y = static_cast<int>(t);
+        } else {
+            const float4 *rp = reinterpret_cast<const float4 *>(g.lp_rows + row);
+            const float4 a = __ldg(rp), b = __ldg(rp + 1);
+            lg = LpGrad{a.x, a.y, a.z, a.w, b.x};
+            y = __float_as_int(b.y);
+        }
+    }
+#pragma unroll 1
+    for (int c0 = 0; c0 < GB_N; c0 += 32) {
+        uint32_t v[32];
+        tmem_ld_32x32b_x32(taddr + c0, v);
+        tmem_ld_wait();
+        const int col0 = tn * GB_N + c0;
+        if (EPI == 4) {
+            if (row < g.M) epilogue_lp_stats(g, col0, v, st, static_cast<unsigned>(y - col0) < 32u ? y - col0 : -1, xy);
+        } else if (row < g.M || zero_row) {
+            epilogue_lp_grad(g, row, col0, v, lg, y);
+        }
+    }
+    if (EPI == 4 && row < g.M) g.part[static_cast<int64_t>(row) * g.tiles_n + tn] = make_float4(st.m, st.s, st.u, xy);
+}
+
 // EPI 0: the plain epilogue (epilogue_store); 1..3: fp32 store with row
-// statistics (epilogue_stats, smoothing mode EPI - 1).
+// statistics (epilogue_stats, smoothing mode EPI - 1); 4, 5: log-probability
+// statistics and gradient (epilogue_lp_tile).
 template <int EPI>
 __global__ void __launch_bounds__(GB_THREADS, 1)
 flce_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, GemmArgs g) {
@@ -340,6 +454,9 @@ flce_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             const int row = tm * GB_M + q * 32 + lane;
             const int orow = (g.row_map && row < g.M) ? __ldg(g.row_map + row) : row;
             const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * GB_N;
+            if constexpr (EPI >= 4) {
+                epilogue_lp_tile<EPI>(g, row, tn, taddr);
+            } else {
             RowState st = row_state_empty();
             ArgMax am{-INFINITY, 0x7fffffff};
             int y_rel = -(1 << 30);   // target column relative to the tile (none: far outside)
@@ -362,6 +479,7 @@ flce_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             if (EPI != 0 && row < g.M) {
                 g.part[static_cast<int64_t>(row) * g.tiles_n + tn] = make_float4(st.m, st.s, st.r, st.n);
                 if (g.pam) g.pam[static_cast<int64_t>(row) * g.tiles_n + tn] = make_float2(am.v, __int_as_float(am.i));
+            }
             }
             tc_fence_before();
             __syncwarp();
@@ -529,6 +647,9 @@ flce_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
             const int row = tm * GP_M + static_cast<int>(rank) * 128 + q * 32 + lane;
             const int orow = (g.row_map && row < g.M) ? __ldg(g.row_map + row) : row;
             const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * GP_N;
+            if constexpr (EPI >= 4) {
+                epilogue_lp_tile<EPI>(g, row, tn, taddr);
+            } else {
             RowState stt = row_state_empty();
             ArgMax am{-INFINITY, 0x7fffffff};
             int y_rel = -(1 << 30);
@@ -551,6 +672,7 @@ flce_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
             if (EPI != 0 && row < g.M) {
                 g.part[static_cast<int64_t>(row) * g.tiles_n + tn] = make_float4(stt.m, stt.s, stt.r, stt.n);
                 if (g.pam) g.pam[static_cast<int64_t>(row) * g.tiles_n + tn] = make_float2(am.v, __int_as_float(am.i));
+            }
             }
             tc_fence_before();
             __syncwarp();
@@ -660,7 +782,7 @@ __global__ void __launch_bounds__(256) flce_gather_kernel(const uint4 *hidden, i
         } else {
             for (int64_t j = threadIdx.x; j < row16; j += blockDim.x) dst[j] = zero;
         }
-        if (__ldg(pos + r) < 0) {
+        if (grad_hidden && __ldg(pos + r) < 0) {
             uint4 *gh = grad_hidden + r * row16;
             for (int64_t j = threadIdx.x; j < row16; j += blockDim.x) gh[j] = zero;
         }
@@ -962,8 +1084,8 @@ int gemm_fit_ksplit(int K, int ksplit) {
 
 // Resident CTA pairs of a pair kernel on a device (0 if unknown), asked once.
 static int pair_clusters(const void *fn, int dev) {
-    static const void *fns[8];
-    static int devs[8], vals[8], used = 0;
+    static const void *fns[16];
+    static int devs[16], vals[16], used = 0;
     for (int i = 0; i < used; ++i)
         if (fns[i] == fn && devs[i] == dev) return vals[i];
     cudaLaunchConfig_t cfg = {};
@@ -980,7 +1102,7 @@ static int pair_clusters(const void *fn, int dev) {
     int n = 0;
     if (cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess) n = 0;
     (void)cudaGetLastError();
-    if (used < 8) { fns[used] = fn; devs[used] = dev; vals[used] = n; ++used; }
+    if (used < 16) { fns[used] = fn; devs[used] = dev; vals[used] = n; ++used; }
     return n;
 }
 
@@ -989,7 +1111,7 @@ static int pair_clusters(const void *fn, int dev) {
 cudaError_t gemm_bf16(int M, int N, int K, const void *A, int64_t lda, int a_mn, const void *B, int64_t ldb,
                       int b_mn, int out_kind, void *out, int64_t ldo, const float *bias, unsigned int *status,
                       cudaStream_t s, const GemmDyn *dyn, const GemmStats *stats, int ksplit,
-                      int64_t split_stride, int mode) {
+                      int64_t split_stride, int mode, const GemmLp *lp) {
     if (M <= 0 || N <= 0 || K <= 0) return cudaSuccess;
     if (stats && out_kind != OUT_F32_STORE) return cudaErrorInvalidValue;
     if (ksplit < 1) ksplit = 1;
@@ -997,6 +1119,9 @@ cudaError_t gemm_bf16(int M, int N, int K, const void *A, int64_t lda, int a_mn,
                        gemm_fit_ksplit(K, ksplit) != ksplit))
         return cudaErrorInvalidValue;
     if (mode < GEMM_AUTO || mode > GEMM_PAIR) return cudaErrorInvalidValue;
+    if (lp && (stats || ksplit > 1 || (lp->part != nullptr) == (lp->rows != nullptr) || (dyn && dyn->row_map)))
+        return cudaErrorInvalidValue;
+    if (lp && lp->rows && (out_kind != OUT_BF16_STORE || (ldo % 8))) return cudaErrorInvalidValue;
     // CTA pairs (256 x 256 tiles) when both sides span at least two pair tiles
     const bool pair = mode == GEMM_PAIR || (mode == GEMM_AUTO && M >= 2 * GP_M && N >= 2 * GP_N);
     CUtensorMap ta, tb;
@@ -1037,17 +1162,31 @@ cudaError_t gemm_bf16(int M, int N, int K, const void *A, int64_t lda, int a_mn,
         if (stats->smooth_mode < 0 || stats->smooth_mode > 2 || (stats->smooth_mode == 2 && !stats->weight))
             return cudaErrorInvalidValue;
     }
-    static const void *const kernels[2][4] = {
+    g.m_static = M;
+    if (lp) {
+        g.part = lp->part;
+        g.st_target = lp->target;
+        g.st_tgt32 = lp->tgt32;
+        g.st_ignore = lp->ignore_index;
+        g.lp_rows = lp->rows;
+        g.lp_k = lp->k;
+        g.lp_ent = lp->entropy;
+        epi = lp->part ? 4 : 5;
+    }
+    static const void *const kernels[2][6] = {
         {reinterpret_cast<const void *>(&flce_gemm_kernel<0>), reinterpret_cast<const void *>(&flce_gemm_kernel<1>),
-         reinterpret_cast<const void *>(&flce_gemm_kernel<2>), reinterpret_cast<const void *>(&flce_gemm_kernel<3>)},
+         reinterpret_cast<const void *>(&flce_gemm_kernel<2>), reinterpret_cast<const void *>(&flce_gemm_kernel<3>),
+         reinterpret_cast<const void *>(&flce_gemm_kernel<4>), reinterpret_cast<const void *>(&flce_gemm_kernel<5>)},
         {reinterpret_cast<const void *>(&flce_gemm_pair_kernel<0>),
          reinterpret_cast<const void *>(&flce_gemm_pair_kernel<1>),
          reinterpret_cast<const void *>(&flce_gemm_pair_kernel<2>),
-         reinterpret_cast<const void *>(&flce_gemm_pair_kernel<3>)}};
+         reinterpret_cast<const void *>(&flce_gemm_pair_kernel<3>),
+         reinterpret_cast<const void *>(&flce_gemm_pair_kernel<4>),
+         reinterpret_cast<const void *>(&flce_gemm_pair_kernel<5>)}};
     const void *fn = kernels[pair ? 1 : 0][epi];
     const size_t smem = pair ? GP_SMEM : GB_SMEM;
     // the shared-memory limit is a per-device attribute of each kernel: set it once per device
-    static uint64_t attr_set[2][4] = {};
+    static uint64_t attr_set[2][6] = {};
     int dev = 0;
     if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
     const uint64_t bit = dev < 64 ? (1ull << dev) : 0ull;
@@ -1081,6 +1220,67 @@ cudaError_t gemm_bf16(int M, int N, int K, const void *A, int64_t lda, int a_mn,
     return cudaLaunchKernelExC(&cfg, fn, args);
 }
 
+// Split count of the grad_hidden GEMM: its output has few tiles (chunk x H)
+// and a long K (V), so one product per tile leaves the last of few waves
+// mostly idle; 4 parts below 1024 tiles, 2 below 2048 (host rule, no device
+// query, so the workspace size is a function of the sizes alone).
+int flce_dh_splits(int64_t chunk, int64_t H, int64_t V) {
+    const int64_t tiles = ((chunk + 127) / 128) * ((H + 255) / 256);
+    const int want = tiles >= 2048 ? 1 : (tiles >= 1024 ? 2 : 4);
+    return gemm_fit_ksplit(static_cast<int>(V), want);
+}
+
+cudaError_t flce_compact(const void *target, int tgt32, int64_t n_rows, int64_t vocab, int64_t ignore_index,
+                         const void *hidden, int64_t H, const CompactBufs &b, void *grad_hidden, const float *g_in,
+                         float *g_out, cudaStream_t s) {
+    CompactBufs w = b;
+    void *cargs[] = {&target, &tgt32, &n_rows, &vocab, &ignore_index, &w.idx, &w.pos, &w.tgt, &w.cnt};
+    cudaError_t e = cudaLaunchKernel(reinterpret_cast<const void *>(&flce_compact_kernel), dim3(1),
+                                     dim3(kCompactThreads), cargs, 0, s);
+    if (e != cudaSuccess) return e;
+    const uint4 *hid = reinterpret_cast<const uint4 *>(hidden);
+    int64_t row16 = H * 2 / 16;
+    const int *ci = w.idx, *cp = w.pos, *cc = w.cnt;
+    uint4 *hc = reinterpret_cast<uint4 *>(w.hc), *gh = reinterpret_cast<uint4 *>(grad_hidden);
+    void *args[] = {&hid, &row16, &n_rows, &ci, &cp, &cc, &hc, &gh, &g_in, &g_out};
+    const int64_t want = static_cast<int64_t>(sm_count()) * 8;
+    const int blocks = static_cast<int>(n_rows < want ? n_rows : want);
+    return cudaLaunchKernel(reinterpret_cast<const void *>(&flce_gather_kernel), dim3(blocks), dim3(256), args, 0, s);
+}
+
+cudaError_t flce_grad_hidden(int64_t c, int64_t H, int64_t V, const void *dz, int64_t ldd, const void *weight, int splits,
+                             float *parts, const int *count, int64_t off, const int *row_map, void *out,
+                             unsigned int *status, cudaStream_t s) {
+    const GemmDyn rows_m{count, static_cast<int>(off), 0, nullptr};
+    const GemmDyn rows_out{count, static_cast<int>(off), 0, row_map};
+    if (splits <= 1)
+        return gemm_bf16(static_cast<int>(c), static_cast<int>(H), static_cast<int>(V), dz, ldd, 0, weight, H, 1,
+                         OUT_BF16_STORE, out, H, nullptr, status, s, count ? &rows_out : nullptr);
+    // split-K parts in fp32, then one kernel sums them (fixed order), rounds once
+    // to bf16 and stores each row at its own position
+    int64_t stride = c * H;
+    cudaError_t e = gemm_bf16(static_cast<int>(c), static_cast<int>(H), static_cast<int>(V), dz, ldd, 0, weight, H, 1,
+                              OUT_F32_STORE, parts, H, nullptr, status, s, count ? &rows_m : nullptr, nullptr, splits,
+                              stride);
+    if (e != cudaSuccess) return e;
+    const float *pp = parts;
+    int64_t ldo = H;
+    __nv_bfloat16 *o = reinterpret_cast<__nv_bfloat16 *>(out);
+    void *args[] = {&pp, &splits, &stride, &c, &H, &count, &off, &row_map, &o, &ldo};
+    return cudaLaunchKernel(reinterpret_cast<const void *>(&flce_splitk_sum_kernel),
+                            dim3(static_cast<unsigned>(sm_count() * 8)), dim3(256), args, 0, s);
+}
+
+cudaError_t flce_grad_bias(int64_t c, int64_t V, const void *dz, int64_t ldd, const int *count, int64_t off,
+                           float *grad_bias, int accumulate, cudaStream_t s) {
+    const __nv_bfloat16 *dzc = reinterpret_cast<const __nv_bfloat16 *>(dz);
+    int rows = static_cast<int>(c), o = static_cast<int>(off);
+    const int threads = 256;
+    void *args[] = {&dzc, &ldd, &rows, &V, &grad_bias, &accumulate, &count, &o};
+    return cudaLaunchKernel(reinterpret_cast<const void *>(&flce_colsum_kernel),
+                            dim3(static_cast<unsigned>((V + threads - 1) / threads)), dim3(threads), args, 0, s);
+}
+
 }  // namespace ce
 
 // ------------------------------------------------------------------ C ABI
@@ -1105,16 +1305,6 @@ struct FlceLayout {
     size_t dhp_off;
     int dh_splits;
 };
-
-// Split count of the grad_hidden GEMM: its output has few tiles (chunk x H)
-// and a long K (V), so one product per tile leaves the last of few waves
-// mostly idle; 4 parts below 1024 tiles, 2 below 2048 (host rule, no device
-// query, so the workspace size is a function of the sizes alone).
-int flce_dh_splits(int64_t chunk, int64_t H, int64_t V) {
-    const int64_t tiles = ((chunk + 127) / 128) * ((H + 255) / 256);
-    const int want = tiles >= 2048 ? 1 : (tiles >= 1024 ? 2 : 4);
-    return gemm_fit_ksplit(static_cast<int>(V), want);
-}
 
 FlceLayout flce_layout(int64_t n_rows, int64_t vocab, int64_t chunk, int64_t hidden, bool compact, bool map_ce) {
     FlceLayout L{};
@@ -1270,30 +1460,11 @@ ce_status flce_fwd_bwd(const ce_params *p, int64_t H, const void *hidden, const 
         int64_t *tgt_c = reinterpret_cast<int64_t *>(wsb + L.tgt_off);
         float *g_c = reinterpret_cast<float *>(wsb + L.gc_off);
         int *cnt = reinterpret_cast<int *>(wsb + L.cnt_off);
-        {
-            const void *tg = target;
-            int t32 = p->target_is_int32;
-            int64_t n = BT, vv = V, ign = p->ignore_index;
-            void *args[] = {&tg, &t32, &n, &vv, &ign, &idx_w, &pos_w, &tgt_c, &cnt};
-            e = cudaLaunchKernel(reinterpret_cast<const void *>(&flce_compact_kernel), dim3(1),
-                                 dim3(kCompactThreads), args, 0, s);
-            if (e != cudaSuccess) return flce_cuda_fail(e);
-        }
-        uint4 *hc = reinterpret_cast<uint4 *>(wsb + L.hc_off);
-        {
-            const uint4 *hid = reinterpret_cast<const uint4 *>(hidden);
-            int64_t row16 = H * 2 / 16, n = BT;
-            const int *ci = idx_w, *cp = pos_w, *cc = cnt;
-            uint4 *gh = reinterpret_cast<uint4 *>(grad_hidden);
-            const float *gi = (none && grad_output) ? grad_output : nullptr;
-            float *gc = g_c;
-            void *args[] = {&hid, &row16, &n, &ci, &cp, &cc, &hc, &gh, &gi, &gc};
-            const int64_t want = static_cast<int64_t>(sm_count()) * 8;
-            const int blocks = static_cast<int>(BT < want ? BT : want);
-            e = cudaLaunchKernel(reinterpret_cast<const void *>(&flce_gather_kernel), dim3(blocks), dim3(256), args,
-                                 0, s);
-            if (e != cudaSuccess) return flce_cuda_fail(e);
-        }
+        void *hc = wsb + L.hc_off;
+        e = flce_compact(target, p->target_is_int32, BT, V, p->ignore_index, hidden, H,
+                         CompactBufs{idx_w, pos_w, cnt, tgt_c, hc}, grad_hidden, (none && grad_output) ? grad_output : nullptr,
+                         g_c, s);
+        if (e != cudaSuccess) return flce_cuda_fail(e);
         h_src = hc;
         tgt_src = tgt_c;
         tgt32 = 0;
@@ -1310,7 +1481,6 @@ ce_status flce_fwd_bwd(const ce_params *p, int64_t H, const void *hidden, const 
         const char *h_c = reinterpret_cast<const char *>(h_src) + r0 * H * 2;
         const GemmDyn rows_m{count, static_cast<int>(r0), 0, nullptr};
         const GemmDyn rows_k{count, static_cast<int>(r0), 1, nullptr};
-        const GemmDyn rows_out{count, static_cast<int>(r0), 0, idx ? idx + r0 : nullptr};
         const void *tgt_chunk = reinterpret_cast<const char *>(tgt_src) + r0 * tgt_bytes;
         if (map_ce) {
             // Z = h_c W^T (+ b), fp32, with the per-tile row states; then the
@@ -1370,46 +1540,15 @@ ce_status flce_fwd_bwd(const ce_params *p, int64_t H, const void *hidden, const 
         // grad_hidden rows = dZ W   (A = dZ K-major, B = W stored [V, H] = [K, N]: MN-major);
         // compacted rows are stored back at their own rows
         void *gh = compact ? grad_hidden : reinterpret_cast<char *>(grad_hidden) + r0 * H * 2;
-        if (L.dh_splits > 1) {
-            // split-K parts in fp32, then one kernel sums them (fixed order), rounds once
-            // to bf16 and stores each row at its own position
-            float *dhp = reinterpret_cast<float *>(wsb + L.dhp_off);
-            const int64_t stride = c * H;
-            e = gemm_bf16(static_cast<int>(c), static_cast<int>(H), static_cast<int>(V), dZ, L.ldd, 0, weight, H, 1,
-                          0, dhp, H, nullptr, &ctl->status, s, compact ? &rows_m : nullptr, nullptr, L.dh_splits,
-                          stride);
-            if (e != cudaSuccess) return flce_cuda_fail(e);
-            const float *pp = dhp;
-            int ks = L.dh_splits;
-            int64_t st = stride, nr = c, hh = H, off = r0, ldo = H;
-            const int *cc = count;
-            const int *rm = compact ? idx + r0 : nullptr;
-            __nv_bfloat16 *o = reinterpret_cast<__nv_bfloat16 *>(gh);
-            void *args[] = {&pp, &ks, &st, &nr, &hh, &cc, &off, &rm, &o, &ldo};
-            e = cudaLaunchKernel(reinterpret_cast<const void *>(&flce_splitk_sum_kernel),
-                                 dim3(static_cast<unsigned>(sm_count() * 8)), dim3(256), args, 0, s);
-        } else {
-            e = gemm_bf16(static_cast<int>(c), static_cast<int>(H), static_cast<int>(V), dZ, L.ldd, 0, weight, H, 1,
-                          2, gh, H, nullptr, &ctl->status, s, compact ? &rows_out : nullptr);
-        }
+        e = flce_grad_hidden(c, H, V, dZ, L.ldd, weight, L.dh_splits, reinterpret_cast<float *>(wsb + L.dhp_off), count, r0,
+                             compact ? idx + r0 : nullptr, gh, &ctl->status, s);
         if (e != cudaSuccess) return flce_cuda_fail(e);
         // grad_weight (+)= dZ^T h_c   (A = dZ stored [c, V] = [K, M]: MN-major; B = h_c [K, N]: MN-major)
         e = gemm_bf16(static_cast<int>(V), static_cast<int>(H), static_cast<int>(c), dZ, L.ldd, 1, h_c, H, 1,
                       r0 == 0 ? 0 : 1, grad_weight, H, nullptr, &ctl->status, s, compact ? &rows_k : nullptr);
         if (e != cudaSuccess) return flce_cuda_fail(e);
         if (grad_bias) {
-            const int threads = 256;
-            const int blocks = static_cast<int>((V + threads - 1) / threads);
-            const __nv_bfloat16 *dzc = dZ;
-            int64_t ldd = L.ldd;
-            int rows = static_cast<int>(c);
-            int64_t vv = V;
-            int accum = r0 == 0 ? 0 : 1;
-            const int *cc = count;
-            int off = static_cast<int>(r0);
-            void *args[] = {&dzc, &ldd, &rows, &vv, &grad_bias, &accum, &cc, &off};
-            e = cudaLaunchKernel(reinterpret_cast<const void *>(&flce_colsum_kernel), dim3(blocks), dim3(threads),
-                                 args, 0, s);
+            e = flce_grad_bias(c, V, dZ, L.ldd, count, r0, grad_bias, r0 == 0 ? 0 : 1, s);
             if (e != cudaSuccess) return flce_cuda_fail(e);
         }
     }

@@ -41,6 +41,30 @@ struct GemmStats {
 };
 constexpr int kGemmTileN = 256;
 
+// Log-probability epilogues of the logits product (the product itself is not
+// stored): `part` set: per output row and 256-column tile the state {max m,
+// s = sum 2^a without the row's target column, u = sum 2^a a (with entropy),
+// the target logit where the tile holds it}, a = (x - m) k, x = product +
+// bias. `rows` set: the gradient of every logit, rounded once to bf16 into
+// the output, from the row's scalars; rows from M up to the next multiple of
+// 64 (within the launch's static M) become zeros.
+struct LpMapRow {
+    float m, neg_log2d, A, B;  // (A + B log2 p) p off the target, p = 2^((x - m) k + neg_log2d)
+    float dy;                  // at the target column y
+    int y;
+    float pad0, pad1;
+};
+static_assert(sizeof(LpMapRow) == 32, "two 16-byte loads per row");
+struct GemmLp {
+    float4 *part;
+    const void *target;
+    int tgt32;
+    int64_t ignore_index;
+    const LpMapRow *rows;
+    float k;
+    int entropy;
+};
+
 // `mode`: GEMM_AUTO (CTA pairs on 256 x 256 tiles when M and N both span at
 // least two such tiles, else one CTA per 128 x 256 tile), GEMM_ONE_CTA,
 // GEMM_PAIR.
@@ -50,7 +74,31 @@ cudaError_t gemm_bf16(int M, int N, int K, const void *A, int64_t lda, int a_mn,
                       int64_t ldb, int b_mn, int out_kind, void *out, int64_t ldo, const float *bias,
                       unsigned int *status, cudaStream_t s, const GemmDyn *dyn = nullptr,
                       const GemmStats *stats = nullptr, int ksplit = 1, int64_t split_stride = 0,
-                      int mode = GEMM_AUTO);
+                      int mode = GEMM_AUTO, const GemmLp *lp = nullptr);
+
+// Ignored-row compaction of n_rows targets (flce.cu): valid rows' indices to
+// idx, their positions (or -1) to pos, their targets to tgt, their count to
+// cnt; hidden rows [n_rows, H] gathered to hc in that order (zeros past the
+// count). grad_hidden (or NULL): rows left out are zeroed. g_in (or NULL):
+// gathered to g_out.
+struct CompactBufs {
+    int *idx, *pos, *cnt;
+    int64_t *tgt;
+    void *hc;
+};
+cudaError_t flce_compact(const void *target, int tgt32, int64_t n_rows, int64_t vocab, int64_t ignore_index,
+                         const void *hidden, int64_t H, const CompactBufs &b, void *grad_hidden, const float *g_in,
+                         float *g_out, cudaStream_t s);
+// split count of the grad_hidden product (chunk x H outputs over K = V)
+int flce_dh_splits(int64_t chunk, int64_t H, int64_t V);
+// grad_hidden rows from dZ (bf16 [c, V], stride ldd): dh = dZ W, each row
+// stored at out[row_map[r]] (or r); `parts` holds the split-K partials
+cudaError_t flce_grad_hidden(int64_t c, int64_t H, int64_t V, const void *dz, int64_t ldd, const void *weight, int splits,
+                             float *parts, const int *count, int64_t off, const int *row_map, void *out,
+                             unsigned int *status, cudaStream_t s);
+// grad_bias (+)= column sums of dZ
+cudaError_t flce_grad_bias(int64_t c, int64_t V, const void *dz, int64_t ldd, const int *count, int64_t off,
+                           float *grad_bias, int accumulate, cudaStream_t s);
 
 // K steps of 64 per split-K part: ksplit parts over kiters steps, each
 // non-empty (the split count actually used, <= ksplit).

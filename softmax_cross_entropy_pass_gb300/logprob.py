@@ -4,8 +4,11 @@
   ce_token_logprob_backward(logits, target, stats, grad_logp, ...) -> grad
   ce_policy_fwd_bwd(logits, target, advantage, ...)    -> (loss, grad)
   ce_preference_fwd_bwd(logits, target, seq_offsets, ...) -> (loss, seq_logp, grad)
-and their torch.autograd entries ``token_logprob``, ``policy_loss`` and
-``preference_loss``. The formulas, the layouts and what each call does with
+  flce_token_logprob(hidden, weight, target, ...)  -> (logp, entropy, stats)
+  flce_token_logprob_backward(hidden, weight, target, stats, grad_logp, ...)
+                                                   -> (grad_hidden, grad_weight, grad_bias)
+and their torch.autograd entries ``token_logprob``, ``policy_loss``,
+``preference_loss`` and ``linear_token_logprob``. The formulas, the layouts and what each call does with
 ignored rows are in include/ce.h.
 
 ``logits`` is a 2-D CUDA tensor with unit column stride (bf16, fp16 or fp32).
@@ -49,6 +52,9 @@ def _sign():
         "ce_policy_fwd_bwd": [P, ctypes.POINTER(ce_policy_params)] + [vp] * 10 + [i64, vp, sz, vp],
         "ce_preference_workspace_size": [P, i64, ctypes.POINTER(sz)],
         "ce_preference_fwd_bwd": [P, ctypes.POINTER(ce_preference_params)] + [vp] * 8 + [i64, vp, sz, vp],
+        "flce_token_logprob_workspace_size": [P, i64, i64, ctypes.POINTER(sz)],
+        "flce_token_logprob": [P, i64, f] + [vp] * 8 + [sz, vp],
+        "flce_token_logprob_backward": [P, i64, f] + [vp] * 9 + [ctypes.c_int32, vp, i64, vp, sz, vp],
     }.items():
         fn = getattr(_lib, name)
         fn.restype, fn.argtypes = st, args
@@ -357,3 +363,141 @@ def preference_loss(logits, target, seq_offsets, *, ref_logp=None, loss_kind="si
                                               seq_logp=seq_logp)
         return loss, grad
     return _FormedGradientFunction.apply(logits, inplace, False, run)
+
+
+# ---------------------------------------------------------------------- linear head
+# dZ of all rows at once (bf16) up to this many bytes: grad_weight is then
+# formed by one product, without a sum over chunks
+DZ_BYTES = 16 << 30
+
+
+def _linear_params(hidden, weight, target, bias, ignore_index):
+    if hidden.dim() != 2 or weight.dim() != 2 or not hidden.is_contiguous() or not weight.is_contiguous():
+        raise ValueError("hidden and weight must be contiguous 2-D tensors")
+    if hidden.dtype != torch.bfloat16 or weight.dtype != torch.bfloat16:
+        raise TypeError("hidden and weight must be bf16")
+    if hidden.shape[1] != weight.shape[1]:
+        raise ValueError("hidden and weight must have the same number of columns")
+    if target.dtype not in (torch.int64, torch.int32):
+        raise TypeError("target must be int64 or int32")
+    if target.dim() != 1 or target.shape[0] != hidden.shape[0] or not target.is_contiguous():
+        raise ValueError("target must be a contiguous 1-D tensor with one entry per row")
+    p = ce_params()
+    p.n_rows, p.vocab, p.ld = hidden.shape[0], weight.shape[0], weight.shape[0]
+    p.ignore_index, p.dtype = ignore_index, CE_DT[torch.bfloat16]
+    p.target_is_int32 = 1 if target.dtype == torch.int32 else 0
+    return p
+
+
+def _linear_ws_bytes(p, hidden_dim, chunk_rows) -> int:
+    out = ctypes.c_size_t()
+    _check(_lib.flce_token_logprob_workspace_size(ctypes.byref(p), hidden_dim, chunk_rows, ctypes.byref(out)),
+           "flce_token_logprob_workspace_size")
+    return out.value
+
+
+def flce_token_logprob(hidden, weight, target, *, bias=None, temperature=1.0, ignore_index=-100, with_entropy=True,
+                       logp=None, entropy=None, stats=None, ws=None, stream=None):
+    """(logp [n], entropy [n] or None, stats [n, 4]) of softmax((hidden
+    weight^T + bias) / temperature) without the logits in memory: hidden
+    [n, H] and weight [V, H] bf16, bias [V] fp32."""
+    p = _linear_params(hidden, weight, target, bias, ignore_index)
+    n, H = hidden.shape
+    call = _Call(hidden, (weight, target, bias, logp, entropy, stats), stream)
+    _vec("bias", bias, weight.shape[0], call.device)
+    logp = call.empty(n) if logp is None else _vec("logp", logp, n, call.device)
+    if with_entropy:
+        entropy = call.empty(n) if entropy is None else _vec("entropy", entropy, n, call.device)
+    elif entropy is not None:
+        raise ValueError("entropy given with with_entropy=False")
+    if stats is None:
+        stats = call.empty(n, 4)
+    elif stats.dtype != torch.float32 or stats.shape != (n, 4) or not stats.is_contiguous():
+        raise ValueError("stats must be a contiguous fp32 [n_rows, 4] tensor")
+    ws, nbytes = _workspace(call, ws, _linear_ws_bytes(p, H, 0))
+    call.run("flce_token_logprob", ctypes.byref(p), H, float(temperature), _ptr(hidden), _ptr(weight), _ptr(bias),
+             _ptr(target), _ptr(logp), _ptr(entropy), _ptr(stats), _ptr(ws), nbytes)
+    return logp, entropy, stats
+
+
+def flce_token_logprob_backward(hidden, weight, target, stats, grad_logp, *, grad_entropy=None, bias=None,
+                                temperature=1.0, ignore_index=-100, chunk_rows=None, grad_hidden=None,
+                                grad_weight=None, grad_bias=None, ws=None, stream=None):
+    """(grad_hidden [n, H] bf16, grad_weight [V, H] fp32 or bf16, grad_bias
+    [V] fp32 or None) of sum(grad_logp logp + grad_entropy entropy), from the
+    statistics flce_token_logprob returned. ``chunk_rows`` rows of the logits'
+    gradient (bf16) are held at a time: all of them by default where that
+    takes at most 16 GB. ``grad_weight``: a buffer of either type; by
+    default fp32. bf16 needs all rows in one chunk."""
+    p = _linear_params(hidden, weight, target, bias, ignore_index)
+    (n, H), V = hidden.shape, weight.shape[0]
+    call = _Call(hidden, (weight, target, stats, grad_logp, grad_entropy, bias, grad_hidden, grad_weight, grad_bias), stream)
+    _vec("bias", bias, V, call.device)
+    _vec("grad_logp", grad_logp, n, call.device)
+    _vec("grad_entropy", grad_entropy, n, call.device)
+    if stats.dtype != torch.float32 or stats.shape != (n, 4) or not stats.is_contiguous():
+        raise ValueError("stats must be a contiguous fp32 [n_rows, 4] tensor")
+    if chunk_rows is None:
+        chunk_rows = _chunk_rows(n, V)
+    if grad_hidden is None:
+        grad_hidden = call.empty(n, H, dtype=torch.bfloat16)
+    elif grad_hidden.shape != hidden.shape or grad_hidden.dtype != torch.bfloat16 or not grad_hidden.is_contiguous():
+        raise ValueError("grad_hidden must be a contiguous bf16 tensor of hidden's shape")
+    if grad_weight is None:
+        grad_weight = call.empty(V, H)
+    elif grad_weight.shape != weight.shape or grad_weight.dtype not in (torch.float32, torch.bfloat16) \
+            or not grad_weight.is_contiguous():
+        raise ValueError("grad_weight must be a contiguous fp32 or bf16 tensor of weight's shape")
+    if grad_bias is None and bias is not None:
+        grad_bias = call.empty(V)
+    _vec("grad_bias", grad_bias, V, call.device)
+    ws, nbytes = _workspace(call, ws, _linear_ws_bytes(p, H, chunk_rows))
+    call.run("flce_token_logprob_backward", ctypes.byref(p), H, float(temperature), _ptr(hidden), _ptr(weight), _ptr(bias),
+             _ptr(target), _ptr(stats), _ptr(grad_logp), _ptr(grad_entropy), _ptr(grad_hidden), _ptr(grad_weight),
+             CE_DT[grad_weight.dtype], _ptr(grad_bias), chunk_rows, _ptr(ws), nbytes)
+    return grad_hidden, grad_weight, grad_bias
+
+
+def _chunk_rows(n, V) -> int:
+    fit = max(128, DZ_BYTES // (2 * V) // 128 * 128)
+    return max(1, min(n, fit))
+
+
+class LinearTokenLogprobFunction(torch.autograd.Function):
+    """Forward: one product with the statistics in its epilogue. Backward: the
+    logits formed again, their gradient in bf16, two products. grad_weight
+    and grad_bias come in the parameters' types, as autograd has it."""
+
+    @staticmethod
+    def forward(ctx, hidden, weight, bias, target, temperature, ignore_index, with_entropy):
+        logp, entropy, stats = flce_token_logprob(hidden.detach(), weight.detach(), target,
+                                                  bias=None if bias is None else bias.detach(),
+                                                  temperature=temperature, ignore_index=ignore_index,
+                                                  with_entropy=with_entropy)
+        ctx.save_for_backward(hidden, weight, bias, target, stats)
+        ctx.args = temperature, ignore_index
+        ctx.set_materialize_grads(False)
+        return (logp, entropy) if with_entropy else logp
+
+    @staticmethod
+    def backward(ctx, grad_logp, grad_entropy=None):
+        hidden, weight, bias, target, stats = ctx.saved_tensors
+        if grad_logp is None and grad_entropy is None:
+            return None, None, None, None, None, None, None
+        g = None if grad_logp is None else grad_logp.detach().to(torch.float32).contiguous()
+        h = None if grad_entropy is None else grad_entropy.detach().to(torch.float32).contiguous()
+        temperature, ignore_index = ctx.args
+        n, V = hidden.shape[0], weight.shape[0]
+        chunk = _chunk_rows(n, V)
+        gw = torch.empty(weight.shape, dtype=torch.bfloat16 if chunk >= n else torch.float32, device=weight.device)
+        gh, gw, gb = flce_token_logprob_backward(hidden.detach(), weight.detach(), target, stats, g, grad_entropy=h,
+                                                 bias=None if bias is None else bias.detach(), temperature=temperature,
+                                                 ignore_index=ignore_index, chunk_rows=chunk, grad_weight=gw)
+        return gh, gw.to(weight.dtype), gb, None, None, None, None
+
+
+def linear_token_logprob(hidden, weight, target, *, bias=None, temperature=1.0, ignore_index=-100, with_entropy=False):
+    """Differentiable log-probabilities of a linear head's targets (and the
+    entropies, as a pair, with ``with_entropy``), the logits never in memory:
+    hidden [n, H] and weight [V, H] bf16, bias [V] fp32 or None."""
+    return LinearTokenLogprobFunction.apply(hidden, weight, bias, target, temperature, ignore_index, with_entropy)

@@ -260,3 +260,55 @@ def test_python_refusals(ce):
         ce.ce_preference_fwd_bwd(x, t, torch.zeros(5, dtype=torch.int64), loss_kind="margin")
     with pytest.raises(ValueError, match="mean"):
         ce.preference_loss(x, t, torch.zeros(5, dtype=torch.int64), reduction="none")
+
+
+# ---------------------------------------------------------------------- linear head
+def _linear(ce, p, H=64, t=1.0, h=FAKE, w=FAKE, b=None, tgt=FAKE, logp=FAKE, stats=FAKE, ws=WS, nb=NB):
+    return ce._lib.flce_token_logprob(ctypes.byref(p), H, t, h, w, b, tgt, logp, FAKE, stats, ws, nb, None)
+
+
+def _linear_backward(ce, p, H=64, t=1.0, h=FAKE, w=FAKE, b=None, tgt=FAKE, logp=FAKE, stats=FAKE, gw=FAKE, dtype=0,
+                     gb=None, chunk=4, ws=WS, nb=NB):
+    return ce._lib.flce_token_logprob_backward(ctypes.byref(p), H, t, h, w, b, tgt, stats, logp, None, FAKE, gw, dtype, gb,
+                                               chunk, ws, nb, None)
+
+
+@pytest.mark.parametrize("call", [_linear, _linear_backward])
+def test_linear_refusals_on_host(ce, call):
+    bad, uns = ce.CE_ERR_INVALID_ARG, ce.CE_ERR_UNSUPPORTED
+    for kw in (dict(n_rows=-1), dict(vocab=0), dict(tgt=2), dict(variant=1), dict(reserved=1)):
+        assert call(ce, _p(ce, **kw)) == bad, kw
+    for kw in UNSUPPORTED + [dict(dtype=0), dict(dtype=2), dict(n_rows=1 << 31)]:
+        assert call(ce, _p(ce, **kw)) == uns, kw
+    p = _p(ce)
+    assert call(ce, p, H=0) == bad and call(ce, p, H=60) == uns
+    assert call(ce, p, t=0.0) == bad and call(ce, p, t=math.nan) == bad
+    odd = ctypes.c_void_p(0x100008)
+    for kw in (dict(h=None), dict(w=None), dict(tgt=None), dict(h=odd), dict(w=odd), dict(b=odd), dict(stats=odd)):
+        assert call(ce, p, **kw) == bad, kw
+    assert call(ce, p, ws=None) == ce.CE_ERR_WORKSPACE
+    assert call(ce, p, ws=ctypes.c_void_p(0x4000010)) == ce.CE_ERR_WORKSPACE
+    assert call(ce, p, nb=512) == ce.CE_ERR_WORKSPACE
+
+
+def test_linear_backward_refusals_on_host(ce):
+    p, bad = _p(ce), ce.CE_ERR_INVALID_ARG
+    assert _linear_backward(ce, p, chunk=0) == bad
+    assert _linear_backward(ce, p, dtype=2) == bad
+    assert _linear_backward(ce, p, dtype=1, chunk=3) == ce.CE_ERR_UNSUPPORTED
+    assert _linear_backward(ce, p, gw=None) == bad
+    assert _linear_backward(ce, p, gw=ctypes.c_void_p(0x100008)) == bad
+    assert _linear_backward(ce, p, logp=None) == bad
+    assert _linear_backward(ce, p, stats=None) == bad
+
+
+def test_linear_workspace_sizes(ce):
+    out = ctypes.c_size_t()
+    size = lambda n, V, H, c: (ce._lib.flce_token_logprob_workspace_size(ctypes.byref(_p(ce, n_rows=n, vocab=V)), H, c,  # noqa: E731
+                                                                        ctypes.byref(out)), out.value)[1]
+    tiles = (128256 + 255) // 256
+    assert 16 * tiles * 100 <= size(100, 128256, 4096, 0) <= 16 * tiles * 100 + 4096          # one row tile: no copy
+    assert size(4096, 128256, 4096, 0) <= 4096 * (16 * tiles + 4096 * 2 + 16) + 16384
+    assert size(4096, 128256, 4096, 4096) >= 4096 * 128256 * 2
+    assert size(4096, 128256, 4096, 512) < size(4096, 128256, 4096, 4096)
+    assert ce._lib.flce_token_logprob_workspace_size(ctypes.byref(_p(ce)), 64, -1, ctypes.byref(out)) == ce.CE_ERR_INVALID_ARG
