@@ -36,6 +36,7 @@ struct LpSmem {
     // waits for every warp)
     float4 slot[2][kLpMaxCluster];  // each CTA's {m, s, u, target logit}
     LpState red[2][kLpWarps];
+    LpGrad grad[2];                 // the row's gradient scalars, from warp 0
     float xy[2];
     int abort;
     unsigned last;
@@ -62,11 +63,91 @@ __device__ inline float take_out(uint32_t addr) {
     return Fmt<DT>::load1(&b, 0);
 }
 
+// Add NV vectors of one thread to its statistics: one packed FMA an exponent
+// pair, a' = x k - mu with mu = m k rounded. The FMA rounds a' alone, and what
+// mu's rounding shifted (the same for every term) is taken out of the chunk's
+// sums, so the sums are as exact as those of (x - m) k. With the entropy, a
+// logit that is -inf (or so low that a' overflows) makes 0 * inf = NaN in u:
+// false is returned then, and where mu is not finite, with st moved to the new
+// maximum but nothing added; lp_add takes such vectors.
+template <int DT, bool ENT, int NV>
+__device__ inline bool add_vectors(LpState &st, const uint4 (&raw)[NV], float k) {
+    using F = Fmt<DT>;
+    constexpr int VEC = F::kVec;
+    float cm = F::vmax(raw[0]);
+#pragma unroll
+    for (int i = 1; i < NV; ++i) cm = fmaxf(cm, F::vmax(raw[i]));
+    if (cm > st.m) lp_rebase<ENT>(st, cm, k);
+    const float mu = st.m * k;
+    if (!(fabsf(mu) < 1e38f)) return false;
+    const F2 kk = f2(k, k), nm = f2(-mu, -mu);
+    F2 s2[2] = {f2(0.f, 0.f), f2(0.f, 0.f)}, u2[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        float x[VEC];
+        F::unpack(raw[i], x);
+#pragma unroll
+        for (int p = 0; p < VEC / 2; ++p) {
+            const F2 e = f2_fma(f2(x[2 * p], x[2 * p + 1]), kk, nm);
+            const F2 ex = f2_ex2(e);
+            s2[p & 1] = f2_add(s2[p & 1], ex);
+            if (ENT) u2[p & 1] = f2_fma(ex, e, u2[p & 1]);
+        }
+    }
+    float s0, s1, u0 = 0.f, u1 = 0.f;
+    f2_split(f2_add(s2[0], s2[1]), s0, s1);
+    const float sc = s0 + s1, shift = fmaf(st.m, k, -mu), f = fmaf(-shift, kLn2, 1.f);
+    if (ENT) {
+        f2_split(f2_add(u2[0], u2[1]), u0, u1);
+        const float uc = u0 + u1;
+        if (uc != uc) return false;
+        st.u = fmaf(fmaf(-shift, sc, uc), f, st.u);
+    }
+    st.s = fmaf(sc, f, st.s);
+    return true;
+}
+template <int DT, bool ENT, int NV>
+__device__ inline bool add_or_clamp(LpState &st, const uint4 (&raw)[NV], float k) {
+    if (add_vectors<DT, ENT, NV>(st, raw, k)) return true;
+#pragma unroll 1
+    for (int i = 0; i < NV; ++i) {
+        uint4 r = raw[0];
+#pragma unroll
+        for (int n = 1; n < NV; ++n) r = n == i ? raw[n] : r;
+        float x[Fmt<DT>::kVec];
+        Fmt<DT>::unpack(r, x);
+        lp_add<ENT, Fmt<DT>::kVec>(st, x, Fmt<DT>::vmax(r), k);
+    }
+    return false;
+}
+
+// How the second pass forms its exponents log2 p: from x - M (SLOW: held at
+// kLpMinExp where the entropy's part multiplies them), or on 16-bit rows with
+// one FMA, x k + c with c = log2(1 / d) - M k rounded once: while |c| < 64
+// that moves p by less than 2^-18, against half steps of 2^-9 and 2^-11.
+constexpr float kFoldC = 64.f;
+template <int DT, bool E, bool SLOW>
+__device__ inline void grad_vec(const LpGrad &g, float c, const float *x, float k, float *out) {
+    constexpr int VEC = Fmt<DT>::kVec;
+    if (SLOW) {
+        lp_grad_vec<E, VEC>(g, x, k, out);
+        return;
+    }
+    const F2 kk = f2(k, k), A = f2(g.A, g.A), B = f2(g.B, g.B), cc = f2(c, c), mm = f2(g.M, g.M);
+#pragma unroll
+    for (int p = 0; p < VEC / 2; ++p) {
+        const F2 xx = f2(x[2 * p], x[2 * p + 1]);
+        const F2 e = Fmt<DT>::kBytes == 2 ? f2_fma(xx, kk, cc) : f2_fma(f2_sub(xx, mm), kk, cc);
+        f2_split(f2_mul(f2_ex2(e), E ? f2_fma(B, e, A) : A), out[2 * p], out[2 * p + 1]);
+    }
+}
+
 template <int DT, int MODE, bool ENT>
 __global__ void __launch_bounds__(kLpThreads, kLpCtasPerSm) lp_rows_kernel(LpArgs a) {
     using F = Fmt<DT>;
     constexpr int VEC = F::kVec, KB = F::kBytes, NCT = kLpConsumers;
     constexpr int VPC = kStreamChunk / 16, VPT = VPC / NCT;
+    static_assert(VPC % NCT == 0, "a full chunk gives every consumer the same vectors");
     constexpr bool POLICY = MODE == LP_POLICY;
     extern __shared__ __align__(128) uint8_t smem[];
     LpSmem &S = *reinterpret_cast<LpSmem *>(smem + kLpSlots * kStreamChunk);
@@ -194,9 +275,10 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtasPerSm) lp_rows_kernel(LpArg
             const int nkeep = twice ? min(nch, kLpSlots) : 0;
             const uint32_t rp = j & 1u, it_row = it;
             PolicyIn in{};
-            if (POLICY) in = policy_load(a, row);  // its latency hides under the first pass
+            if (POLICY && warp == 0) in = policy_load(a, row);  // its latency hides under the first pass
             // ------------------------------------------------ pass 1: statistics
             LpState st = lp_empty();
+            uint32_t held = 0;
             for (int c = 0; c < nch; ++c, ++it) {
                 const uint32_t s = it % kLpSlots;
                 mbar_wait_bounded<false, kStreamSleepConsumer>(smem_u32(&S.full[s]), (it / kLpSlots) & 1u, abort);
@@ -208,53 +290,20 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtasPerSm) lp_rows_kernel(LpArg
                     S.xy[rp] = take_out<DT>(base_s + 16u * vy + static_cast<uint32_t>(y % VEC) * KB);
                     fence_async_shared();  // before a copy may overwrite the slot
                 }
-                uint4 raw[VPT];
-                float cm = -INFINITY;
+                bool plain = true;
+                if (nv == VPC) {
+                    uint4 raw[VPT];
 #pragma unroll
-                for (int i = 0; i < VPT; ++i) {
-                    const uint32_t ninf = F::kNegInfWord;
-                    raw[i] = tid + i * NCT < nv ? ld_shared_v4(base_s + 16u * (tid + i * NCT)) : make_uint4(ninf, ninf, ninf, ninf);
-                    cm = fmaxf(cm, F::vmax(raw[i]));
-                }
-                if (cm > st.m) lp_rebase<ENT>(st, cm, k);
-                if (st.m != -INFINITY) {
-                    const F2 mm = f2(st.m, st.m), kk = f2(k, k);
-                    F2 s2[2] = {f2(0.f, 0.f), f2(0.f, 0.f)}, u2[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
-#pragma unroll
-                    for (int i = 0; i < VPT; ++i) {
-                        float x[VEC];
-                        F::unpack(raw[i], x);
-#pragma unroll
-                        for (int p = 0; p < VEC / 2; ++p) {
-                            F2 e2 = f2_mul(f2_sub(f2(x[2 * p], x[2 * p + 1]), mm), kk);
-                            if (ENT) {
-                                float a0, a1;
-                                f2_split(e2, a0, a1);
-                                e2 = f2(lp_clamp(a0), lp_clamp(a1));
-                            }
-                            const F2 ex = f2_ex2(e2);
-                            s2[p & 1] = f2_add(s2[p & 1], ex);
-                            if (ENT) u2[p & 1] = f2_fma(ex, e2, u2[p & 1]);
-                        }
-                    }
-                    float a0, a1;
-                    f2_split(f2_add(s2[0], s2[1]), a0, a1);
-                    st.s += a0 + a1;
-                    if (ENT) {
-                        f2_split(f2_add(u2[0], u2[1]), a0, a1);
-                        st.u += a0 + a1;
-                    }
+                    for (int i = 0; i < VPT; ++i) raw[i] = ld_shared_v4(base_s + 16u * (tid + i * NCT));
+                    plain = add_or_clamp<DT, ENT, VPT>(st, raw, k);
                 } else {
-                    // -inf only so far: a NaN among it (which the maximum drops) is kept
-#pragma unroll
-                    for (int i = 0; i < VPT; ++i) {
-                        float x[VEC];
-                        F::unpack(raw[i], x);
-#pragma unroll
-                        for (int e = 0; e < VEC; ++e)
-                            if (x[e] != x[e]) st.s = x[e];
+                    for (int v = tid; v < nv; v += NCT) {
+                        const uint4 raw[1] = {ld_shared_v4(base_s + 16u * v)};
+                        plain = add_or_clamp<DT, ENT, 1>(st, raw, k) && plain;
                     }
                 }
+                // chunks whose exponents the second pass has to hold as well (31: any later one)
+                if (POLICY && ENT && !plain) held |= 1u << min(c, 31);
                 __syncwarp();
                 if (lane == 0 && c < nch - nkeep) mbar_arrive(smem_u32(&S.empty[s]));
             }
@@ -266,54 +315,59 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtasPerSm) lp_rows_kernel(LpArg
                 else lp_add1<ENT>(st, x, k);
             }
             // ------------------------------------------------ merge and row scalars
-            // every warp merges the CTA's partials itself, in the same order: one
-            // barrier per row, and every thread holds the same values
+            // warp 0 merges the CTA's partials (and the cluster's), forms the row's
+            // scalars and hands the gradient's to the others
             st = lp_warp_merge<ENT>(st, k);
             if (lane == 0) S.red[rp][warp] = st;
             lp_consumer_sync();
-            st = lp_warp_merge<ENT, kLpWarps>(S.red[rp][lane & (kLpWarps - 1)], k);
-            float xy = yc >= 0 && yc < L ? S.xy[rp] : 0.f;
-            if (cl > 1) {
-                const uint32_t my_bar = smem_u32(&S.xbar[rp]);
-                if (tid < static_cast<int>(cl)) {
-                    st_cluster_v4(mapa_shared(smem_u32(&S.slot[rp][rank]), tid), st.m, st.s, st.u, xy);
-                    mbar_arrive_remote(mapa_shared(my_bar, tid));
+            if (warp == 0) {
+                st = lp_warp_merge<ENT, kLpWarps>(S.red[rp][lane & (kLpWarps - 1)], k);
+                float xy = yc >= 0 && yc < L ? S.xy[rp] : 0.f;
+                if (cl > 1) {
+                    const uint32_t my_bar = smem_u32(&S.xbar[rp]);
+                    if (lane < static_cast<int>(cl)) {
+                        st_cluster_v4(mapa_shared(smem_u32(&S.slot[rp][rank]), lane), st.m, st.s, st.u, xy);
+                        mbar_arrive_remote(mapa_shared(my_bar, lane));
+                    }
+                    mbar_wait_bounded<true, kStreamSleepConsumer>(my_bar, (j >> 1) & 1u, abort);
+                    st = lp_empty();
+                    for (uint32_t d = 0; d < cl; ++d) {
+                        const float4 q = S.slot[rp][d];
+                        st = lp_merge<ENT>(st, LpState{q.x, q.y, q.z}, k);
+                    }
+                    xy = S.slot[rp][t / part].w;
                 }
-                mbar_wait_bounded<true, kStreamSleepConsumer>(my_bar, (j >> 1) & 1u, abort);
-                st = lp_empty();
-                for (uint32_t d = 0; d < cl; ++d) {
-                    const float4 q = S.slot[rp][d];
-                    st = lp_merge<ENT>(st, LpState{q.x, q.y, q.z}, k);
+                float4 stats = lp_row_stats(st, xy, k);
+                const LpRow r = lp_row(stats, k, a.inv_t);
+                if (!POLICY) {
+                    if (writer) {
+                        const bool gone = *abort != 0;  // a wait gave up: no workspace to flag it in
+                        if (a.logp) a.logp[row] = gone ? NAN : r.logp;
+                        if (ENT && a.entropy) a.entropy[row] = gone ? NAN : r.entropy;
+                        if (!ENT || gone) stats.w = NAN;
+                        if (gone) stats.x = NAN;
+                        if (a.stats) a.stats[row] = stats;
+                    }
+                } else {
+                    const PolicyOut o = policy_row(a, in, r, r.entropy);
+                    if (!have_norm) {
+                        pdl_wait();
+                        w_sum = a.ctl->w_y;
+                        have_norm = true;
+                    }
+                    if (writer) {
+                        if (a.reduction == CE_RED_NONE) a.loss[row] = o.loss;
+                        else S.cta_sum += static_cast<double>(o.loss);
+                        if (a.row_stats) a.row_stats[row] = make_float4(r.logp, ENT ? r.entropy : 0.f, o.ratio, o.kl);
+                    }
+                    const float scale = policy_scale(a, row, w_sum);
+                    if (lane == 0) S.grad[rp] = lp_grad(stats, r, a.inv_t, o.g * scale, o.h * scale);
                 }
-                xy = S.slot[rp][t / part].w;
             }
             ++j;
-            float4 stats = lp_row_stats(st, xy, k);
-            const LpRow r = lp_row(stats, k, a.inv_t);
-            if (!POLICY) {
-                if (writer) {
-                    const bool gone = *abort != 0;  // a wait gave up: no workspace to flag it in
-                    if (a.logp) a.logp[row] = gone ? NAN : r.logp;
-                    if (ENT && a.entropy) a.entropy[row] = gone ? NAN : r.entropy;
-                    if (!ENT || gone) stats.w = NAN;
-                    if (gone) stats.x = NAN;
-                    if (a.stats) a.stats[row] = stats;
-                }
-                continue;
-            }
-            const PolicyOut o = policy_row(a, in, r, r.entropy);
-            if (!have_norm) {
-                pdl_wait();
-                w_sum = a.ctl->w_y;
-                have_norm = true;
-            }
-            if (writer) {
-                if (a.reduction == CE_RED_NONE) a.loss[row] = o.loss;
-                else S.cta_sum += static_cast<double>(o.loss);
-                if (a.row_stats) a.row_stats[row] = make_float4(r.logp, ENT ? r.entropy : 0.f, o.ratio, o.kl);
-            }
-            const float scale = policy_scale(a, row, w_sum);
-            const LpGrad g = lp_grad(stats, r, a.inv_t, o.g * scale, o.h * scale);
+            if (!POLICY) continue;
+            lp_consumer_sync();
+            const LpGrad g = S.grad[rp];
             // ------------------------------------------------ pass 2: gradient
             char *grow = gbase + row * gstep;
             if (!twice) {
@@ -321,6 +375,11 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtasPerSm) lp_rows_kernel(LpArg
                 continue;
             }
             uint4 *vp = reinterpret_cast<uint4 *>(grow + static_cast<int64_t>(vlo) * KB);
+            const float fold = fmaf(-g.M, k, g.neg_log2d);
+            const float cexp = KB == 2 ? fold : g.neg_log2d;
+            // the whole row takes the slow form where the folded constant is too large,
+            // and on fp32 rows where M might carry x - M out of range
+            if (!(fabsf(KB == 2 ? fold : g.M) < (KB == 2 ? kFoldC : 1e30f))) held = ~0u;
             auto pass2 = [&](auto ent_tag) {
                 constexpr bool E = decltype(ent_tag)::value;
                 for (int i = 0; i < nch; ++i) {
@@ -334,17 +393,26 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtasPerSm) lp_rows_kernel(LpArg
                     }
                     const uint32_t base_s = ring + s * kStreamChunk;
                     const int v0 = c * VPC, nv = min(VPC, nvec - v0);
-                    for (int v = tid; v < nv; v += NCT) {
-                        float x[VEC], og[VEC];
-                        F::unpack(ld_shared_v4(base_s + 16u * v), x);
-                        lp_grad_vec<E, VEC>(g, x, k, og);
-                        st_stream(vp + v0 + v, F::pack(og));
+                    if (!((held >> min(c, 31)) & 1u)) {
+                        for (int v = tid; v < nv; v += NCT) {
+                            float x[VEC], og[VEC];
+                            F::unpack(ld_shared_v4(base_s + 16u * v), x);
+                            grad_vec<DT, E, false>(g, cexp, x, k, og);
+                            st_stream(vp + v0 + v, F::pack(og));
+                        }
+                    } else {
+                        for (int v = tid; v < nv; v += NCT) {
+                            float x[VEC], og[VEC];
+                            F::unpack(ld_shared_v4(base_s + 16u * v), x);
+                            grad_vec<DT, E, true>(g, cexp, x, k, og);
+                            st_stream(vp + v0 + v, F::pack(og));
+                        }
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_u32(&S.empty[s]));
                 }
             };
-            if (ENT && g.B != 0.f) pass2(std::integral_constant<bool, true>{});
+            if (ENT && g.B != 0.f) pass2(std::integral_constant<bool, ENT>{});
             else pass2(std::integral_constant<bool, false>{});
             // the target column of the interior, by the thread that stored its vector, after that store
             if (y >= 0 && (y / VEC) % NCT == tid) F::store1(grow, vlo + y, g.dy);
