@@ -53,16 +53,18 @@ __device__ inline LpState lp_merge(LpState a, LpState b, float k) {
     return LpState{M, a.s + b.s, ENT ? a.u + b.u : 0.f};
 }
 
-// merge over groups of W lanes, in the same order in every group
+// merge over groups of W lanes (in the same order in every group): the
+// maximum first, then one move of each lane's sums to it
 template <bool ENT, int W = 32>
 __device__ inline LpState lp_warp_merge(LpState st, float k) {
+    float M = st.m;
+#pragma unroll
+    for (int off = W / 2; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+    if (M != -INFINITY) lp_rebase<ENT>(st, M, k);
 #pragma unroll
     for (int off = W / 2; off > 0; off >>= 1) {
-        LpState o;
-        o.m = __shfl_xor_sync(0xffffffffu, st.m, off);
-        o.s = __shfl_xor_sync(0xffffffffu, st.s, off);
-        o.u = ENT ? __shfl_xor_sync(0xffffffffu, st.u, off) : 0.f;
-        st = lp_merge<ENT>(st, o, k);
+        st.s += __shfl_xor_sync(0xffffffffu, st.s, off);
+        if (ENT) st.u += __shfl_xor_sync(0xffffffffu, st.u, off);
     }
     return st;
 }
@@ -128,16 +130,17 @@ __device__ inline LpRow lp_row(const float4 st, float k, float inv_t) {
     LpRow r;
     const float a_y = lp_clamp((xy - M) * k);
     const float e_y = exp2f(a_y);
-    const float d = s + e_y;
+    const float d = s + e_y, inv_d = 1.f / d;
     const float log2d = log2f(d);
     r.neg_log2d = -log2d;
-    r.p_y = e_y / d;
-    r.q_y = s / d;
-    // -log p_t = log(1 + s e^((M - x_t) / T)); s = 0 leaves M = x_t
-    const float nll = s <= 0.f ? (M - xy) * 0.f : softplus_f(logf(s) + (M - xy) * inv_t);
+    r.p_y = e_y * inv_d;
+    r.q_y = s * inv_d;
+    // -log p_t = log d + (M - x_t) / T, a sum of two parts >= 0; near p_t = 1,
+    // where both are small, log(1 + s / e_y)
+    const float nll = r.p_y < 0.5f ? fmaf(M - xy, inv_t, kLn2 * log2d) : log1pf(s / e_y);
     r.logp = -nll;
     // H = log d - (1/d) sum 2^a a ln 2: both terms >= 0
-    r.entropy = kLn2 * (log2d - (u + e_y * a_y) / d);
+    r.entropy = kLn2 * (log2d - fmaf(e_y, a_y, u) * inv_d);
     return r;
 }
 
@@ -186,20 +189,31 @@ __device__ inline void lp_grad_vec(const LpGrad &g, const float *x, float k, flo
     }
 }
 
-// 16 bytes at any address that is a multiple of the element size (2 or 4): the
-// five aligned words that cover them (the outer two only where they hold some
-// of the bytes), shifted together.
+// The 16 bytes from byte sh on (0 < sh < 16, a multiple of the element size)
+// of two consecutive vectors.
+template <int KB>
+__device__ inline uint4 shift16(const uint4 &a, const uint4 &b, uint32_t sh) {
+    uint32_t w[7] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z};
+    uint32_t last = b.w;
+    if (sh & 8u) {
+        w[0] = w[2]; w[1] = w[3]; w[2] = w[4]; w[3] = w[5]; w[4] = w[6]; w[5] = last;
+    }
+    if (sh & 4u) {
+        w[0] = w[1]; w[1] = w[2]; w[2] = w[3]; w[3] = w[4]; w[4] = w[5];
+    }
+    if (KB == 2 && (sh & 2u))
+        return make_uint4(__funnelshift_r(w[0], w[1], 16), __funnelshift_r(w[1], w[2], 16), __funnelshift_r(w[2], w[3], 16),
+                          __funnelshift_r(w[3], w[4], 16));
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+// 16 bytes at any address that is a multiple of the element size: from the two
+// aligned vectors that hold them (each of them holds some).
 template <int KB>
 __device__ inline uint4 ld_unaligned16(const char *p) {
-    const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p)) & 3u;
-    const uint32_t *w = reinterpret_cast<const uint32_t *>(p - off);
-    uint4 v = make_uint4(w[0], w[1], w[2], w[3]);
-    if (KB == 2 && off) {
-        const uint32_t w4 = w[4];
-        v = make_uint4(__funnelshift_r(v.x, v.y, 16), __funnelshift_r(v.y, v.z, 16), __funnelshift_r(v.z, v.w, 16),
-                       __funnelshift_r(v.w, w4, 16));
-    }
-    return v;
+    const uint32_t sh = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p)) & 15u;
+    if (sh == 0) return ld_stream(p);
+    const uint4 *v = reinterpret_cast<const uint4 *>(p - sh);
+    return shift16<KB>(v[0], v[1], sh);
 }
 
 // Columns [c0, c1) of one row's gradient, by nt threads (this one is tid):

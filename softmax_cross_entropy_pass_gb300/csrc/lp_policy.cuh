@@ -60,7 +60,7 @@ __device__ inline PolicyOut policy_row(const LpArgs &a, const PolicyIn &in, cons
         o.kl = kl_of_gap(gap);
         if (a.kl_coef != 0.f) {
             loss = fmaf(a.kl_coef, o.kl, loss);
-            g = fmaf(-a.kl_coef, expm1f(gap), g);
+            g = fmaf(-a.kl_coef, gap + o.kl, g);  // e^gap - 1
         }
     }
     o.h = 0.f;

@@ -19,33 +19,26 @@
 
 namespace ce {
 
-constexpr int kLpWarps = 8;
+constexpr int kLpWarps = 8;                    // consumers
 constexpr int kLpConsumers = kLpWarps * 32;
-constexpr int kLpThreads = kLpConsumers + 32;
-constexpr int kLpSlots = 4;
-constexpr int kLpCtasPerSm = 3;
+constexpr int kLpThreads = kLpConsumers + 64;  // and the producer and the scalar warp
+constexpr int kLpSlots = 6;
+constexpr int kLpCtasPerSm = 2;
 constexpr int kLpMaxCluster = 8;
 constexpr int kLpCtlBytes = 1024;
-constexpr int kLpSmemBytes = kLpSlots * kStreamChunk + kLpCtlBytes;
+constexpr int kLpSmemBytes = kLpSlots * kStreamChunk + 2 * kLpConsumers * 16 + kLpCtlBytes;
 
 struct LpSmem {
     uint64_t full[kLpSlots], empty[kLpSlots];
     uint64_t xbar[2];
-    // per row parity: a warp may write the next row's values while a slower
-    // warp still reads this row's (never further ahead: the row's barrier
-    // waits for every warp)
+    uint64_t done[2], taken[2];     // per row parity: the consumers' statistics are there; they have been used
     float4 slot[2][kLpMaxCluster];  // each CTA's {m, s, u, target logit}
-    LpState red[2][kLpWarps];
-    LpGrad grad[2];                 // the row's gradient scalars, from warp 0
+    LpGrad grad[2];                 // the row's gradient scalars
     float xy[2];
     int abort;
-    unsigned last;
-    double cta_sum;                 // this cluster's row losses (thread 0 of its first CTA)
-    double sum[kLpWarps];
 };
 static_assert(sizeof(LpSmem) <= kLpCtlBytes, "control block too large");
 
-__device__ inline void lp_consumer_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kLpConsumers) : "memory"); }
 __device__ inline void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // one element of a 16-byte aligned shared-memory chunk: read, and set to -inf
@@ -150,7 +143,8 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtasPerSm) lp_rows_kernel(LpArg
     static_assert(VPC % NCT == 0, "a full chunk gives every consumer the same vectors");
     constexpr bool POLICY = MODE == LP_POLICY;
     extern __shared__ __align__(128) uint8_t smem[];
-    LpSmem &S = *reinterpret_cast<LpSmem *>(smem + kLpSlots * kStreamChunk);
+    float4 *const parts = reinterpret_cast<float4 *>(smem + kLpSlots * kStreamChunk);  // [2][NCT] {m, s, u, -}
+    LpSmem &S = *reinterpret_cast<LpSmem *>(parts + 2 * NCT);
     const uint32_t ring = smem_u32(smem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int V = static_cast<int>(a.vocab);
@@ -170,10 +164,12 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtasPerSm) lp_rows_kernel(LpArg
             mbar_init(smem_u32(&S.full[s]), 1);
             mbar_init(smem_u32(&S.empty[s]), kLpWarps);
         }
-        mbar_init(smem_u32(&S.xbar[0]), cl);
-        mbar_init(smem_u32(&S.xbar[1]), cl);
+        for (int p = 0; p < 2; ++p) {
+            mbar_init(smem_u32(&S.xbar[p]), cl);
+            mbar_init(smem_u32(&S.done[p]), kLpWarps);
+            mbar_init(smem_u32(&S.taken[p]), 1);
+        }
         S.abort = 0;
-        S.cta_sum = 0.0;
         fence_mbar_init_cluster();
     }
     __syncthreads();
@@ -194,13 +190,6 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtasPerSm) lp_rows_kernel(LpArg
         if (POLICY) return policy_row_live(a, row, t);
         return target_valid(t, a.ignore_index, V) && row >= row_lo && row < row_hi;
     };
-    // The gradient's vectors lie where the logits' do only when both rows
-    // start at the same offset from a 16-byte boundary.
-    auto same_align = [&](int64_t row) {
-        return (((reinterpret_cast<uintptr_t>(xbase) + row * xstep) ^ (reinterpret_cast<uintptr_t>(gbase) + row * gstep)) &
-                15u) == 0;
-    };
-
     if (warp == kLpWarps) {
         // -------------------------------------------------------------- producer
         if (lane == 0) {
@@ -214,9 +203,8 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtasPerSm) lp_rows_kernel(LpArg
                 const char *slice = xbase + row * xstep;
                 const RowGeom gm = row_geom<KB>(slice, lo, L);
                 const char *src = slice + gm.nhead * KB;
-                const bool twice = POLICY && same_align(row);
-                const int nkeep = twice ? min(gm.nch, kLpSlots) : 0;
-                for (int pass = 0; pass < (twice ? 2 : 1); ++pass) {
+                const int nkeep = POLICY ? min(gm.nch, kLpSlots) : 0;
+                for (int pass = 0; pass < (POLICY ? 2 : 1); ++pass) {
                     const int nc = pass == 0 ? gm.nch : gm.nch - nkeep;
                     for (int i = 0; i < nc; ++i, ++it) {
                         const int c = pass == 0 ? i : nc - 1 - i;
@@ -238,18 +226,119 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtasPerSm) lp_rows_kernel(LpArg
             }
         }
         __syncwarp();
-    } else {
-        // -------------------------------------------------------------- consumers
+    } else if (warp == kLpWarps + 1) {
+        // -------------------------------------------------------------- scalar warp
+        // Merges the consumers' statistics of each row (and the cluster's), forms the
+        // row's scalars, writes its results and hands the gradient's scalars back,
+        // so that in the forward the consumers go on with the next row meanwhile.
         const float k = a.k;
         bool have_norm = false;
         float w_sum = 0.f;
+        double cta_sum = 0.0;  // this cluster's row losses (lane 0 of its first CTA)
+        uint32_t j = 0;
+        int64_t t_next = q0 < a.n_rows ? load_target(a.target, a.tgt32, q0) : 0;
+        for (int64_t row = q0; row < a.n_rows; row += nq) {
+            const int64_t t = t_next;
+            if (row + nq < a.n_rows) t_next = load_target(a.target, a.tgt32, row + nq);
+            if (!row_live(row, t)) continue;
+            PolicyIn in{};
+            if (POLICY) in = policy_load(a, row);
+            const uint32_t rp = j & 1u, ph = (j >> 1) & 1u;
+            ++j;
+            const bool writer = lane == 0 && rank == 0;
+            mbar_wait_bounded<false, kStreamSleepConsumer>(smem_u32(&S.done[rp]), ph, abort);
+            const float4 *const pp = parts + rp * NCT;
+            float M = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < kLpWarps; ++i) M = fmaxf(M, pp[lane + 32 * i].x);
+            LpState st{M, 0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < kLpWarps; ++i) {
+                const float4 q = pp[lane + 32 * i];
+                LpState o{q.x, q.y, q.z};
+                if (M != -INFINITY) lp_rebase<ENT>(o, M, k);
+                st.s += o.s;
+                if (ENT) st.u += o.u;
+            }
+            st = lp_warp_merge<ENT>(st, k);
+            float xy = S.xy[rp];
+            if (cl > 1) {
+                const uint32_t my_bar = smem_u32(&S.xbar[rp]);
+                if (lane < static_cast<int>(cl)) {
+                    st_cluster_v4(mapa_shared(smem_u32(&S.slot[rp][rank]), lane), st.m, st.s, st.u, xy);
+                    mbar_arrive_remote(mapa_shared(my_bar, lane));
+                }
+                mbar_wait_bounded<true, kStreamSleepConsumer>(my_bar, ph, abort);
+                // lanes from cl on repeat its last CTA's entry as an empty state
+                const float4 q = S.slot[rp][lane < static_cast<int>(cl) ? lane : 0];
+                st = lane < static_cast<int>(cl) ? LpState{q.x, q.y, q.z} : lp_empty();
+                st = lp_warp_merge<ENT>(st, k);
+                xy = S.slot[rp][t / part].w;
+            }
+            float4 stats = lp_row_stats(st, xy, k);
+            const LpRow r = lp_row(stats, k, a.inv_t);
+            if (!POLICY) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&S.taken[rp]));
+                if (writer) {
+                    const bool gone = *abort != 0;  // a wait gave up: no workspace to flag it in
+                    if (a.logp) a.logp[row] = gone ? NAN : r.logp;
+                    if (ENT && a.entropy) a.entropy[row] = gone ? NAN : r.entropy;
+                    if (!ENT || gone) stats.w = NAN;
+                    if (gone) stats.x = NAN;
+                    if (a.stats) a.stats[row] = stats;
+                }
+                continue;
+            }
+            const PolicyOut o = policy_row(a, in, r, r.entropy);
+            if (!have_norm) {
+                pdl_wait();
+                w_sum = a.ctl->w_y;
+                have_norm = true;
+            }
+            const float scale = policy_scale(a, row, w_sum);
+            if (lane == 0) {
+                S.grad[rp] = lp_grad(stats, r, a.inv_t, o.g * scale, o.h * scale);
+                mbar_arrive(smem_u32(&S.taken[rp]));
+            }
+            if (writer) {
+                if (a.reduction == CE_RED_NONE) a.loss[row] = o.loss;
+                else cta_sum += static_cast<double>(o.loss);
+                if (a.row_stats) a.row_stats[row] = make_float4(r.logp, ENT ? r.entropy : 0.f, o.ratio, o.kl);
+            }
+        }
+        // ---------------------------------------------------- batch loss (last cluster)
+        if (POLICY && a.reduction != CE_RED_NONE && rank == 0) {
+            if (!have_norm) pdl_wait();
+            unsigned last = 0;
+            if (lane == 0) {
+                a.part[q0] = cta_sum;
+                __threadfence();
+                last = atomicAdd(&a.ctl->done, 1u) == static_cast<unsigned>(nq) - 1u ? 1u : 0u;
+            }
+            if (__shfl_sync(0xffffffffu, last, 0)) {
+                __threadfence();
+                double sum = 0.0;  // in cluster order, then a fixed tree
+                for (int64_t i = lane; i < nq; i += 32) sum += __ldcg(a.part + i);
+#pragma unroll
+                for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+                if (a.reduction == CE_RED_MEAN) {
+                    const float w_all = a.ctl->w_y;
+                    sum = w_all != 0.f ? sum / static_cast<double>(w_all) : 0.0;
+                }
+                if (lane == 0) a.loss[0] = static_cast<float>(sum);
+            }
+        }
+    } else {
+        // -------------------------------------------------------------- consumers
+        const float k = a.k;
         uint32_t it = 0, j = 0;  // ring position; live rows done (parities)
         int64_t t_next = q0 < a.n_rows ? load_target(a.target, a.tgt32, q0) : 0;
         for (int64_t row = q0; row < a.n_rows; row += nq) {
             const int64_t t = t_next;
             if (row + nq < a.n_rows) t_next = load_target(a.target, a.tgt32, row + nq);
-            const bool writer = tid == 0 && rank == 0;
             if (!row_live(row, t)) {
+                const bool writer = tid == 0 && rank == 0;
                 if (POLICY) {
                     lp_zero_span<DT>(gbase + row * gstep, 0, L, tid, NCT);
                     if (writer) {
@@ -271,11 +360,11 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtasPerSm) lp_rows_kernel(LpArg
             const int vlo = static_cast<int>(gm.vlo) - lo, tail0 = static_cast<int>(gm.tail0) - lo;
             const int yc = static_cast<int>(t) - lo;  // target column of the slice (it may lie outside)
             const int y = yc >= vlo && yc < tail0 ? yc - vlo : -1;
-            const bool twice = POLICY && same_align(row);
-            const int nkeep = twice ? min(nch, kLpSlots) : 0;
+            const int nkeep = POLICY ? min(nch, kLpSlots) : 0;
             const uint32_t rp = j & 1u, it_row = it;
-            PolicyIn in{};
-            if (POLICY && warp == 0) in = policy_load(a, row);  // its latency hides under the first pass
+            // (the policy loss's wait for its gradient scalars has covered this)
+            if (!POLICY && j > 1)
+                mbar_wait_bounded<false, kStreamSleepConsumer>(smem_u32(&S.taken[rp]), ((j >> 1) - 1u) & 1u, abort);
             // ------------------------------------------------ pass 1: statistics
             LpState st = lp_empty();
             uint32_t held = 0;
@@ -314,67 +403,21 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtasPerSm) lp_rows_kernel(LpArg
                 if (edge_c == yc) S.xy[rp] = x;
                 else lp_add1<ENT>(st, x, k);
             }
-            // ------------------------------------------------ merge and row scalars
-            // warp 0 merges the CTA's partials (and the cluster's), forms the row's
-            // scalars and hands the gradient's to the others
-            st = lp_warp_merge<ENT>(st, k);
-            if (lane == 0) S.red[rp][warp] = st;
-            lp_consumer_sync();
-            if (warp == 0) {
-                st = lp_warp_merge<ENT, kLpWarps>(S.red[rp][lane & (kLpWarps - 1)], k);
-                float xy = yc >= 0 && yc < L ? S.xy[rp] : 0.f;
-                if (cl > 1) {
-                    const uint32_t my_bar = smem_u32(&S.xbar[rp]);
-                    if (lane < static_cast<int>(cl)) {
-                        st_cluster_v4(mapa_shared(smem_u32(&S.slot[rp][rank]), lane), st.m, st.s, st.u, xy);
-                        mbar_arrive_remote(mapa_shared(my_bar, lane));
-                    }
-                    mbar_wait_bounded<true, kStreamSleepConsumer>(my_bar, (j >> 1) & 1u, abort);
-                    st = lp_empty();
-                    for (uint32_t d = 0; d < cl; ++d) {
-                        const float4 q = S.slot[rp][d];
-                        st = lp_merge<ENT>(st, LpState{q.x, q.y, q.z}, k);
-                    }
-                    xy = S.slot[rp][t / part].w;
-                }
-                float4 stats = lp_row_stats(st, xy, k);
-                const LpRow r = lp_row(stats, k, a.inv_t);
-                if (!POLICY) {
-                    if (writer) {
-                        const bool gone = *abort != 0;  // a wait gave up: no workspace to flag it in
-                        if (a.logp) a.logp[row] = gone ? NAN : r.logp;
-                        if (ENT && a.entropy) a.entropy[row] = gone ? NAN : r.entropy;
-                        if (!ENT || gone) stats.w = NAN;
-                        if (gone) stats.x = NAN;
-                        if (a.stats) a.stats[row] = stats;
-                    }
-                } else {
-                    const PolicyOut o = policy_row(a, in, r, r.entropy);
-                    if (!have_norm) {
-                        pdl_wait();
-                        w_sum = a.ctl->w_y;
-                        have_norm = true;
-                    }
-                    if (writer) {
-                        if (a.reduction == CE_RED_NONE) a.loss[row] = o.loss;
-                        else S.cta_sum += static_cast<double>(o.loss);
-                        if (a.row_stats) a.row_stats[row] = make_float4(r.logp, ENT ? r.entropy : 0.f, o.ratio, o.kl);
-                    }
-                    const float scale = policy_scale(a, row, w_sum);
-                    if (lane == 0) S.grad[rp] = lp_grad(stats, r, a.inv_t, o.g * scale, o.h * scale);
-                }
-            }
+            // ------------------------------------------------ to the scalar warp
+            parts[rp * NCT + tid] = make_float4(st.m, st.s, st.u, 0.f);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&S.done[rp]));
+            const uint32_t ph = (j >> 1) & 1u;
             ++j;
             if (!POLICY) continue;
-            lp_consumer_sync();
+            mbar_wait_bounded<false, kStreamSleepConsumer>(smem_u32(&S.taken[rp]), ph, abort);
             const LpGrad g = S.grad[rp];
             // ------------------------------------------------ pass 2: gradient
             char *grow = gbase + row * gstep;
-            if (!twice) {
-                lp_grad_span<DT, ENT>(xrow, grow, 0, L, yc, g, k, tid, NCT);
-                continue;
-            }
-            uint4 *vp = reinterpret_cast<uint4 *>(grow + static_cast<int64_t>(vlo) * KB);
+            char *const gv = grow + static_cast<int64_t>(vlo) * KB;
+            uint4 *vp = reinterpret_cast<uint4 *>(gv);
+            // gradient rows at another offset from a 16-byte boundary than the logits'
+            const uint32_t mis = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(gv)) & 15u;
             const float fold = fmaf(-g.M, k, g.neg_log2d);
             const float cexp = KB == 2 ? fold : g.neg_log2d;
             // the whole row takes the slow form where the folded constant is too large,
@@ -393,7 +436,19 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtasPerSm) lp_rows_kernel(LpArg
                     }
                     const uint32_t base_s = ring + s * kStreamChunk;
                     const int v0 = c * VPC, nv = min(VPC, nvec - v0);
-                    if (!((held >> min(c, 31)) & 1u)) {
+                    if (mis != 0) {
+                        // vector o of the gradient is the last mis bytes of the logits' vector o and
+                        // the first 16 - mis of o + 1 (past the chunk's end read from L2)
+                        for (int v = tid; v < nv && v0 + v + 1 < nvec; v += NCT) {
+                            const uint4 r0 = ld_shared_v4(base_s + 16u * v);
+                            const uint4 r1 = v + 1 < nv ? ld_shared_v4(base_s + 16u * (v + 1))
+                                                        : ld_stream(xrow + vlo * KB + 16 * static_cast<int64_t>(v0 + v + 1));
+                            float x[VEC], og[VEC];
+                            F::unpack(shift16<KB>(r0, r1, 16u - mis), x);
+                            grad_vec<DT, E, true>(g, cexp, x, k, og);
+                            st_stream(gv + 16 * static_cast<int64_t>(v0 + v) + (16u - mis), F::pack(og));
+                        }
+                    } else if (!((held >> min(c, 31)) & 1u)) {
                         for (int v = tid; v < nv; v += NCT) {
                             float x[VEC], og[VEC];
                             F::unpack(ld_shared_v4(base_s + 16u * v), x);
@@ -414,37 +469,17 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtasPerSm) lp_rows_kernel(LpArg
             };
             if (ENT && g.B != 0.f) pass2(std::integral_constant<bool, ENT>{});
             else pass2(std::integral_constant<bool, false>{});
-            // the target column of the interior, by the thread that stored its vector, after that store
-            if (y >= 0 && (y / VEC) % NCT == tid) F::store1(grow, vlo + y, g.dy);
-            if (tid < nedge)
-                F::store1(grow, edge_c, edge_c == yc ? g.dy : lp_grad_elem<ENT>(g, F::load1(xrow, edge_c), k));
-        }
-        // ---------------------------------------------------- batch loss (last cluster)
-        if (POLICY && a.reduction != CE_RED_NONE && rank == 0) {
-            if (!have_norm) pdl_wait();
-            if (tid == 0) {
-                a.part[q0] = S.cta_sum;
-                __threadfence();
-                S.last = atomicAdd(&a.ctl->done, 1u) == static_cast<unsigned>(nq) - 1u ? 1u : 0u;
-            }
-            lp_consumer_sync();
-            if (S.last) {
-                __threadfence();
-                double sum = 0.0;  // in cluster order, then a fixed tree
-                for (int64_t i = tid; i < nq; i += NCT) sum += __ldcg(a.part + i);
-#pragma unroll
-                for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-                if (lane == 0) S.sum[warp] = sum;
-                lp_consumer_sync();
-                if (tid == 0) {
-                    double tot = 0.0;
-                    for (int w = 0; w < kLpWarps; ++w) tot += S.sum[w];
-                    if (a.reduction == CE_RED_MEAN) {
-                        const float w_all = a.ctl->w_y;
-                        tot = w_all != 0.f ? tot / static_cast<double>(w_all) : 0.0;
-                    }
-                    a.loss[0] = static_cast<float>(tot);
-                }
+            // The target column of the vectors, by the thread that stored its vector,
+            // after that store; the columns outside of them. Shifted vectors leave the
+            // first 16 - mis bytes of the interior and its last mis out as well.
+            const int lead = mis != 0 && nvec > 0 ? static_cast<int>(16u - mis) / KB : 0;
+            const int trail = mis != 0 && nvec > 0 ? static_cast<int>(mis) / KB : 0;
+            const int yo = y - lead;
+            if (y >= 0 && yo >= 0 && y < nvec * VEC - trail && (yo / VEC) % NCT == tid) F::store1(grow, vlo + y, g.dy);
+            const int nh = gm.nhead + lead, ne = nh + trail + gm.ntail;
+            if (tid < ne) {
+                const int c = tid < nh ? tid : tail0 - trail + (tid - nh);
+                F::store1(grow, c, c == yc ? g.dy : lp_grad_elem<ENT>(g, F::load1(xrow, c), k));
             }
         }
     }
@@ -517,12 +552,17 @@ cudaError_t launch_lp_rows(const LpArgs &a0, int dtype, int mode, bool entropy, 
     cudaError_t e = rows_ready(fn, 1, &clusters, &sms);
     if (e != cudaSuccess) return e;
     const int64_t slots = static_cast<int64_t>(sms) * kLpCtasPerSm;
-    // With two passes the parts that wait in L2 for their second one (three
-    // CTAs per SM) stay well inside it: 176 KB a CTA.
     int cl = 1;
-    if (mode == LP_POLICY)
-        while (cl < kLpMaxCluster && row_bytes > cl * (int64_t(176) << 10)) cl *= 2;
-    // Few rows: split them over more CTAs, down to one chunk each.
+    // Two passes over many rows: the rows in flight, whose first chunks wait in
+    // L2 for the second pass, kept to 60 MB (GB300, L2 flushed, with the
+    // entropy: 8192 x 128256 bf16 one CTA a row 709 us, pairs 686, quads 781;
+    // 4096 x 256000 891, 769, 773; 2048 x 128256 fp32 438, 389, 354; below the
+    // limit 8192 x 64000 364, 467, 647 and 8192 x 32000 220, 324, 481).
+    if (mode == LP_POLICY && a.n_rows > slots)
+        while (cl < kLpMaxCluster && slots / cl * row_bytes > (int64_t(60) << 20)) cl *= 2;
+    // Few rows: split over more CTAs while all rows still run at once, down to
+    // one chunk each (8 x 128256 bf16, with the gradient: one CTA a row 25.6 us,
+    // 2 19.5, 4 15.4, 8 15.0; 64 x 32000 fp16 the same for 1 to 4, 8 slower).
     while (cl < kLpMaxCluster && a.n_rows * cl * 2 <= slots && row_bytes >= cl * 2 * kStreamChunk) cl *= 2;
     if (cl > 1 && (e = rows_ready(fn, cl, &clusters, &sms)) != cudaSuccess) return e;
     if (clusters > a.n_rows) clusters = static_cast<int>(a.n_rows);
