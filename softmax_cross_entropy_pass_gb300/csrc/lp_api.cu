@@ -221,12 +221,14 @@ ce_status ce_preference_fwd_bwd(const ce_params *p, const ce_preference_params *
     cudaError_t e = n > 0 ? launch_lp_rows(a, p->dtype, LP_FWD, false, false, s)
                           : cudaMemsetAsync(ws, 0, kWsCtlBytes, s);  // the row kernel clears the control block otherwise
     if (e == cudaSuccess) e = launch_lp_pairs(pa, s);
-    if (e == cudaSuccess) e = launch_lp_pair_loss(pa, s);
-    if (e == cudaSuccess && n > 0) {
+    if (e == cudaSuccess) {
         a.g_logp = pa.row;
         a.row_coef = 1;
         a.grad = grad;
         a.ld_grad = ld_grad;
+        a.part = pa.pair_loss;
+        a.loss = loss;
+        a.grad_output = grad_output;
         e = launch_lp_grad(a, p->dtype, false, true, s);
     }
     return e == cudaSuccess ? CE_OK : cuda_fail(e);

@@ -43,40 +43,8 @@ __global__ void __launch_bounds__(kLpPrepThreads) lp_prep_kernel(LpArgs a) {
 
 // ------------------------------------------------------------------ gradient from statistics
 constexpr int kLpGradThreads = 256;
-constexpr int kLpGradBytes = 65536;  // bytes of a row per block
-
-// The logits once more, the gradient written: a map over (row, 64 KB part)
-// items, last rows first, so that what the forward read last is still in L2.
-// Bound by HBM; 4 vectors in flight per thread.
-template <int DT, bool ENT>
-__global__ void __launch_bounds__(kLpGradThreads) lp_grad_kernel(LpArgs a, int64_t parts) {
-    using F = Fmt<DT>;
-    constexpr int KB = F::kBytes;
-    constexpr int64_t span = kLpGradBytes / KB;
-    const int tid = threadIdx.x;
-    if (a.row_coef) pdl_wait();
-    for (int64_t i = blockIdx.x; i < a.n_rows * parts; i += gridDim.x) {
-        const int64_t row = a.n_rows - 1 - i / parts, c0 = (i % parts) * span;
-        const int64_t c1 = c0 + span < a.vocab ? c0 + span : a.vocab;
-        char *grow = reinterpret_cast<char *>(a.grad) + row * a.ld_grad * KB;
-        const int64_t t = load_target(a.target, a.tgt32, row);
-        const bool valid = target_valid(t, a.ignore_index, a.vocab);
-        const float g = valid && a.g_logp ? __ldg(a.g_logp + row) : 0.f;
-        const float h = valid && ENT && a.g_entropy ? __ldg(a.g_entropy + row) : 0.f;
-        if (!valid || (a.row_coef && g == 0.f)) {
-            lp_zero_span<DT>(grow, c0, c1, tid, kLpGradThreads);
-            continue;
-        }
-        const float4 st = __ldg(a.stats + row);
-        const LpRow r = lp_row(st, a.k, a.inv_t);
-        const LpGrad lg = lp_grad(st, r, a.inv_t, g, h);
-        lp_grad_span<DT, ENT>(reinterpret_cast<const char *>(a.x) + row * a.ld * KB, grow, c0, c1, static_cast<int>(t), lg,
-                              a.k, tid, kLpGradThreads);
-    }
-}
-
-// ------------------------------------------------------------------ preference pairs
 constexpr int kPairThreads = 256;
+constexpr int kLpGradBytes = 65536;  // bytes of a row per block
 
 // fixed-order block sum of two doubles, to every thread
 __device__ inline void block_sum2(double &x, double &y, double (&sh)[kPairThreads / 32][2]) {
@@ -98,12 +66,74 @@ __device__ inline void block_sum2(double &x, double &y, double (&sh)[kPairThread
     }
 }
 
+// The batch's part of a preference coefficient: grad_output (for reduction
+// none it is in the coefficients already) over the number of live pairs.
+__device__ inline float lp_pair_scale(const LpArgs &a) {
+    if (a.reduction == CE_RED_NONE) return 1.f;
+    const float up = a.grad_output ? __ldg(a.grad_output) : 1.f;
+    if (a.reduction != CE_RED_MEAN) return up;
+    const unsigned live = __ldcg(&a.ctl->n_correct);
+    return live ? up / static_cast<float>(live) : 0.f;
+}
+
+// The batch loss from the pair losses, by one block (fixed order, fp64).
+__device__ inline void lp_pair_loss(const LpArgs &a) {
+    __shared__ double sh[kPairThreads / 32][2];
+    const unsigned live = __ldcg(&a.ctl->n_correct);
+    if (a.reduction != CE_RED_NONE) {
+        double s = 0.0, none = 0.0;
+        for (int64_t p = threadIdx.x; p < a.n_seqs / 2; p += kPairThreads) s += __ldcg(a.part + p);
+        block_sum2(s, none, sh);
+        if (a.reduction == CE_RED_MEAN && live) s /= static_cast<double>(live);
+        if (threadIdx.x == 0) a.loss[0] = static_cast<float>(s);
+    }
+    if (threadIdx.x == 0 && live == 0u && !(__ldcg(&a.ctl->status) & CE_FLAG_BAD_OFFSETS))
+        atomicOr(&a.ctl->status, CE_FLAG_NO_VALID_ROWS);
+}
+static_assert(kPairThreads == kLpGradThreads, "the gradient kernel's first block forms the batch loss");
+
+// The logits once more, the gradient written: a map over (row, 64 KB part)
+// items, last rows first, so that what the forward read last is still in L2.
+// Bound by HBM; 4 vectors in flight per thread.
+template <int DT, bool ENT>
+__global__ void __launch_bounds__(kLpGradThreads) lp_grad_kernel(LpArgs a, int64_t parts) {
+    using F = Fmt<DT>;
+    constexpr int KB = F::kBytes;
+    constexpr int64_t span = kLpGradBytes / KB;
+    const int tid = threadIdx.x;
+    float batch = 1.f;  // preference: what every row's coefficient is still to be multiplied by
+    if (a.row_coef) {
+        pdl_wait();
+        batch = lp_pair_scale(a);
+        if (blockIdx.x == 0) lp_pair_loss(a);
+    }
+    for (int64_t i = blockIdx.x; i < a.n_rows * parts; i += gridDim.x) {
+        const int64_t row = a.n_rows - 1 - i / parts, c0 = (i % parts) * span;
+        const int64_t c1 = c0 + span < a.vocab ? c0 + span : a.vocab;
+        char *grow = reinterpret_cast<char *>(a.grad) + row * a.ld_grad * KB;
+        const int64_t t = load_target(a.target, a.tgt32, row);
+        const bool valid = target_valid(t, a.ignore_index, a.vocab);
+        const float g = valid && a.g_logp ? __ldg(a.g_logp + row) * batch : 0.f;
+        const float h = valid && ENT && a.g_entropy ? __ldg(a.g_entropy + row) : 0.f;
+        if (!valid || (a.row_coef && g == 0.f)) {
+            lp_zero_span<DT>(grow, c0, c1, tid, kLpGradThreads);
+            continue;
+        }
+        const float4 st = __ldg(a.stats + row);
+        const LpRow r = lp_row(st, a.k, a.inv_t);
+        const LpGrad lg = lp_grad(st, r, a.inv_t, g, h);
+        lp_grad_span<DT, ENT>(reinterpret_cast<const char *>(a.x) + row * a.ld * KB, grow, c0, c1, static_cast<int>(t), lg,
+                              a.k, tid, kLpGradThreads);
+    }
+}
+
+// ------------------------------------------------------------------ preference pairs
 // One block per pair (p: sequences p and P + p of the 2 P): their log
 // probability sums in fp64, the pair's loss and the coefficient dL/dlogp of
 // each of their rows, written over the row's log-probability (rows whose
-// target takes no part already hold 0). The batch divisor of the mean (pairs
-// with a valid target on both sides) and grad_output are applied by the
-// kernel that finishes the batch, which all coefficients pass through.
+// target takes no part already hold 0). The divisor of the mean (pairs with a
+// valid target on both sides, counted here) and grad_output are left to the
+// gradient kernel (lp_pair_scale).
 // Offsets that fall, or leave [0, n_rows], make the whole batch void: loss
 // NaN, gradient 0, a status bit. Every block checks all of them itself.
 __global__ void __launch_bounds__(kPairThreads) lp_pair_kernel(PairArgs a) {
@@ -198,36 +228,6 @@ __global__ void __launch_bounds__(kPairThreads) lp_pair_kernel(PairArgs a) {
     }
 }
 
-// The batch: loss = the pair losses' sum (fixed order, fp64) over the number
-// of live pairs for the mean, and the row coefficients times the same divisor
-// and grad_output. One launch, every block scales its share of the rows and
-// the first also forms the loss.
-__global__ void __launch_bounds__(kPairThreads) lp_pair_finish_kernel(PairArgs a) {
-    __shared__ double sh[kPairThreads / 32][2];
-    pdl_wait();
-    const int tid = threadIdx.x;
-    const unsigned live = a.ctl->n_correct;
-    const bool mean = a.reduction == CE_RED_MEAN;
-    if (a.reduction != CE_RED_NONE) {
-        const float up = a.grad_output ? __ldg(a.grad_output) : 1.f;
-        const float scale = mean ? (live ? up / static_cast<float>(live) : 0.f) : up;
-        for (int64_t i = static_cast<int64_t>(blockIdx.x) * kPairThreads + tid; i < a.n_rows;
-             i += static_cast<int64_t>(gridDim.x) * kPairThreads)
-            if (a.row[i] != 0.f) a.row[i] *= scale;
-        if (blockIdx.x == 0) {
-            double s = 0.0, none = 0.0;
-            for (int64_t p = tid; p < a.n_pairs; p += kPairThreads) s += a.pair_loss[p];
-            block_sum2(s, none, sh);
-            if (tid == 0) {
-                if (mean && live) s /= static_cast<double>(live);
-                a.loss[0] = static_cast<float>(s);
-            }
-        }
-    }
-    if (blockIdx.x == 0 && tid == 0 && live == 0u && !(a.ctl->status & CE_FLAG_BAD_OFFSETS))
-        a.ctl->status |= CE_FLAG_NO_VALID_ROWS;
-}
-
 // ------------------------------------------------------------------ launches
 template <typename A>
 static cudaError_t launch_dep(const void *fn, int64_t grid, int threads, A &a, int64_t *extra, bool dependent,
@@ -269,13 +269,6 @@ cudaError_t launch_lp_grad(const LpArgs &a0, int dtype, bool entropy, bool depen
 cudaError_t launch_lp_pairs(const PairArgs &a0, cudaStream_t s) {
     PairArgs a = a0;
     return launch_dep(reinterpret_cast<const void *>(&lp_pair_kernel), a.n_pairs < 512 ? a.n_pairs : 512, kPairThreads, a,
-                      nullptr, true, s);
-}
-
-cudaError_t launch_lp_pair_loss(const PairArgs &a0, cudaStream_t s) {
-    PairArgs a = a0;
-    const int64_t want = (a.n_rows + kPairThreads - 1) / kPairThreads;
-    return launch_dep(reinterpret_cast<const void *>(&lp_pair_finish_kernel), want < 64 ? want : 64, kPairThreads, a,
                       nullptr, true, s);
 }
 

@@ -34,12 +34,12 @@ struct LpArgs {
     int reduction;
     const float *grad_output;  // NULL = 1.0
     float *loss;
-    double *part;              // workspace: one loss sum per CTA (cluster)
+    double *part;              // workspace: one loss sum per CTA (cluster); preference: one loss per pair
     float4 *row_stats;         // {log p, entropy, ratio, KL}
     // gradient from statistics: dL/dlogp and dL/dH (NULL: 0)
     const float *g_logp, *g_entropy;
-    int row_coef;              // 1: g_logp is the workspace's row coefficients (preference):
-                               // rows with coefficient 0 are not read
+    int row_coef;              // 1: g_logp is the workspace's row coefficients (preference): rows
+                               // with coefficient 0 are not read, and the batch loss is formed
 };
 
 struct PairArgs {
@@ -66,11 +66,8 @@ enum { LP_FWD = 0, LP_POLICY = 1 };
 cudaError_t launch_lp_prep(const LpArgs &a, cudaStream_t s);
 // one pass over every row: log-probabilities, entropies and statistics (LP_FWD), or the policy loss and its gradient
 cudaError_t launch_lp_rows(const LpArgs &a, int dtype, int mode, bool entropy, bool after_prep, cudaStream_t s);
-// the gradient of every row from its statistics
+// the gradient of every row from its statistics (preference: and the batch loss)
 cudaError_t launch_lp_grad(const LpArgs &a, int dtype, bool entropy, bool dependent, cudaStream_t s);
 // sequence sums, pair losses and row coefficients of the preference loss
 cudaError_t launch_lp_pairs(const PairArgs &a, cudaStream_t s);
-// the last kernel of the preference loss: the batch loss from the pair losses
-cudaError_t launch_lp_pair_loss(const PairArgs &a, cudaStream_t s);
-
 }  // namespace ce

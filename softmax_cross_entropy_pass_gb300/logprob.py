@@ -23,7 +23,10 @@ import ctypes
 
 import torch
 
-from . import (CE_DT, CE_RED, CEError, _check, _lib, _ptr, ce_params, ce_scale_grad)
+from . import CE_DT, CE_RED, CEError, _check, _lib, ce_params, ce_scale_grad
+
+_raw_stream = torch._C._cuda_getCurrentRawStream  # the current stream of a device as an integer
+_byref = ctypes.byref
 
 CE_FLAG_BAD_OFFSETS = 8
 PREFERENCE_KINDS = {"sigmoid": 0, "hinge": 1, "squared": 2}
@@ -64,6 +67,10 @@ _sign()
 
 
 # ---------------------------------------------------------------------- arguments
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
 def _params(logits, target, ignore_index, reduction="mean") -> ce_params:
     if logits.dim() != 2 or logits.stride(1) != 1 and logits.shape[1] != 1:
         raise ValueError("logits must be a 2-D tensor with unit column stride")
@@ -76,12 +83,9 @@ def _params(logits, target, ignore_index, reduction="mean") -> ce_params:
         raise ValueError("target must be a contiguous 1-D tensor with one entry per row")
     if reduction not in CE_RED:
         raise ValueError(f"unknown reduction {reduction!r}")
-    p = ce_params()
-    p.n_rows, p.vocab, p.ld = n, v, logits.stride(0) if n > 1 else v
-    p.ignore_index = ignore_index
-    p.dtype, p.reduction = CE_DT[logits.dtype], CE_RED[reduction]
-    p.target_is_int32 = 1 if target.dtype == torch.int32 else 0
-    return p
+    # n_rows, vocab, ld, ignore_index, class_weight, label_smoothing, dtype, reduction, target_is_int32
+    return ce_params(n, v, logits.stride(0) if n > 1 else v, ignore_index, None, 0.0, CE_DT[logits.dtype],
+                     CE_RED[reduction], 1 if target.dtype == torch.int32 else 0)
 
 
 def _vec(name, t, n, device):
@@ -105,38 +109,56 @@ class _Call:
     """The device and the stream of one call. Memory that the call allocates
     comes from the current stream's pool: where the kernels run on another
     stream, that pool is told so before it may hand the memory out again."""
+    __slots__ = ("device", "stream", "other", "handle")
 
     def __init__(self, tensor, others, stream):
         if not tensor.is_cuda:
             raise ValueError("all tensors must live on the GPU")
-        self.device = tensor.device
+        device = self.device = tensor.device
         for t in others:
-            if t is not None and t.device != self.device:
+            if t is not None and t.device != device:
                 raise ValueError("all tensors must live on the logits' device")
-        current = torch.cuda.current_stream(self.device)
-        if stream is None:
-            stream = current
-        elif not hasattr(stream, "cuda_stream"):
-            stream = torch.cuda.ExternalStream(int(stream), device=self.device)
-        if stream.device != self.device:
-            raise ValueError("stream must be one of the logits' device")
-        self.stream = stream
-        self.other = current if stream.cuda_stream != current.cuda_stream else None
-        self.handle = ctypes.c_void_p(stream.cuda_stream)
+        self.other = None
+        self.handle = _raw_stream(device.index)
+        if stream is not None:
+            if not hasattr(stream, "cuda_stream"):
+                stream = torch.cuda.ExternalStream(int(stream), device=device)
+            if stream.device != device:
+                raise ValueError("stream must be one of the logits' device")
+            if stream.cuda_stream != self.handle:
+                self.stream, self.other, self.handle = stream, torch.cuda.current_stream(device), stream.cuda_stream
 
     def empty(self, *shape, dtype=torch.float32):
-        t = torch.empty(*shape, dtype=dtype, device=self.device)
+        t = torch.empty(shape, dtype=dtype, device=self.device)
         if self.other is not None:
             self.stream.wait_stream(self.other)  # the memory's last user may still be running there
             t.record_stream(self.stream)
         return t
 
-    def run(self, name, *args):
+    def run(self, name, fn, *args):
         if torch.cuda.current_device() == self.device.index:
-            _check(getattr(_lib, name)(*args, self.handle), name)
+            status = fn(*args, self.handle)
         else:
             with torch.cuda.device(self.device):
-                _check(getattr(_lib, name)(*args, self.handle), name)
+                status = fn(*args, self.handle)
+        if status:
+            _check(status, name)
+
+
+def _outputs(call, n, logp, entropy, stats, with_entropy):
+    """The three outputs of a forward: those given, or new ones."""
+    if not with_entropy and entropy is not None:
+        raise ValueError("entropy given with with_entropy=False")
+    logp = call.empty(n) if logp is None else _vec("logp", logp, n, call.device)
+    if with_entropy:
+        entropy = call.empty(n) if entropy is None else _vec("entropy", entropy, n, call.device)
+    return logp, entropy, call.empty(n, 4) if stats is None else _stats(stats, n)
+
+
+def _stats(stats, n):
+    if stats.dtype != torch.float32 or stats.shape != (n, 4) or not stats.is_contiguous():
+        raise ValueError("stats must be a contiguous fp32 [n_rows, 4] tensor")
+    return stats
 
 
 def _workspace(call, ws, nbytes):
@@ -150,9 +172,9 @@ def _workspace(call, ws, nbytes):
 def _ws_bytes(p, n_pairs=None) -> int:
     out = ctypes.c_size_t()
     if n_pairs is None:
-        _check(_lib.ce_workspace_size(ctypes.byref(p), ctypes.byref(out)), "ce_workspace_size")
+        _check(_lib.ce_workspace_size(_byref(p), _byref(out)), "ce_workspace_size")
     else:
-        _check(_lib.ce_preference_workspace_size(ctypes.byref(p), n_pairs, ctypes.byref(out)),
+        _check(_lib.ce_preference_workspace_size(_byref(p), n_pairs, _byref(out)),
                "ce_preference_workspace_size")
     return out.value
 
@@ -167,16 +189,8 @@ def ce_token_logprob(logits, target, *, temperature=1.0, ignore_index=-100, with
     p = _params(logits, target, ignore_index)
     n = p.n_rows
     call = _Call(logits, (target, logp, entropy, stats), stream)
-    logp = call.empty(n) if logp is None else _vec("logp", logp, n, call.device)
-    if with_entropy:
-        entropy = call.empty(n) if entropy is None else _vec("entropy", entropy, n, call.device)
-    elif entropy is not None:
-        raise ValueError("entropy given with with_entropy=False")
-    if stats is None:
-        stats = call.empty(n, 4)
-    elif stats.dtype != torch.float32 or stats.shape != (n, 4) or not stats.is_contiguous():
-        raise ValueError("stats must be a contiguous fp32 [n_rows, 4] tensor")
-    call.run("ce_token_logprob", ctypes.byref(p), float(temperature), _ptr(logits), _ptr(target), _ptr(logp),
+    logp, entropy, stats = _outputs(call, n, logp, entropy, stats, with_entropy)
+    call.run("ce_token_logprob", _lib.ce_token_logprob, _byref(p), float(temperature), _ptr(logits), _ptr(target), _ptr(logp),
              _ptr(entropy), _ptr(stats))
     return logp, entropy, stats
 
@@ -193,9 +207,8 @@ def ce_token_logprob_backward(logits, target, stats, grad_logp, *, grad_entropy=
     call = _Call(logits, (target, stats, grad_logp, grad_entropy, grad), stream)
     _vec("grad_logp", grad_logp, n, call.device)
     _vec("grad_entropy", grad_entropy, n, call.device)
-    if stats.dtype != torch.float32 or stats.shape != (n, 4) or not stats.is_contiguous():
-        raise ValueError("stats must be a contiguous fp32 [n_rows, 4] tensor")
-    call.run("ce_token_logprob_backward", ctypes.byref(p), float(temperature), _ptr(logits), _ptr(target), _ptr(stats),
+    _stats(stats, n)
+    call.run("ce_token_logprob_backward", _lib.ce_token_logprob_backward, _byref(p), float(temperature), _ptr(logits), _ptr(target), _ptr(stats),
              _ptr(grad_logp), _ptr(grad_entropy), _ptr(grad), ld)
     return grad
 
@@ -223,7 +236,7 @@ def ce_policy_fwd_bwd(logits, target, advantage, *, old_logp=None, ref_logp=None
         raise ValueError("row_stats must be a contiguous fp32 [n_rows, 4] tensor on the logits' device")
     q = ce_policy_params(float(temperature), float(clip_low), float(clip_high), float(kl_coef), float(entropy_coef), 0)
     ws, nbytes = _workspace(call, ws, _ws_bytes(p))
-    call.run("ce_policy_fwd_bwd", ctypes.byref(p), ctypes.byref(q), _ptr(logits), _ptr(target), _ptr(advantage),
+    call.run("ce_policy_fwd_bwd", _lib.ce_policy_fwd_bwd, _byref(p), _byref(q), _ptr(logits), _ptr(target), _ptr(advantage),
              _ptr(old_logp), _ptr(ref_logp), _ptr(row_weight), _ptr(grad_output), _ptr(loss), _ptr(row_stats),
              _ptr(grad), ld, _ptr(ws), nbytes)
     return loss, grad
@@ -258,7 +271,7 @@ def ce_preference_fwd_bwd(logits, target, seq_offsets, *, ref_logp=None, loss_ki
     q = ce_preference_params(pairs, PREFERENCE_KINDS[loss_kind], 1 if seq_offsets.dtype == torch.int32 else 0,
                              1 if length_normalize else 0, float(beta), float(label_smoothing), 0)
     ws, nbytes = _workspace(call, ws, _ws_bytes(p, pairs))
-    call.run("ce_preference_fwd_bwd", ctypes.byref(p), ctypes.byref(q), _ptr(logits), _ptr(target), _ptr(seq_offsets),
+    call.run("ce_preference_fwd_bwd", _lib.ce_preference_fwd_bwd, _byref(p), _byref(q), _ptr(logits), _ptr(target), _ptr(seq_offsets),
              _ptr(ref_logp), _ptr(grad_output), _ptr(loss), _ptr(seq_logp), _ptr(grad), ld, _ptr(ws), nbytes)
     return loss, seq_logp, grad
 
@@ -382,16 +395,14 @@ def _linear_params(hidden, weight, target, bias, ignore_index):
         raise TypeError("target must be int64 or int32")
     if target.dim() != 1 or target.shape[0] != hidden.shape[0] or not target.is_contiguous():
         raise ValueError("target must be a contiguous 1-D tensor with one entry per row")
-    p = ce_params()
-    p.n_rows, p.vocab, p.ld = hidden.shape[0], weight.shape[0], weight.shape[0]
-    p.ignore_index, p.dtype = ignore_index, CE_DT[torch.bfloat16]
-    p.target_is_int32 = 1 if target.dtype == torch.int32 else 0
-    return p
+    V = weight.shape[0]
+    return ce_params(hidden.shape[0], V, V, ignore_index, None, 0.0, CE_DT[torch.bfloat16], 0,
+                     1 if target.dtype == torch.int32 else 0)
 
 
 def _linear_ws_bytes(p, hidden_dim, chunk_rows) -> int:
     out = ctypes.c_size_t()
-    _check(_lib.flce_token_logprob_workspace_size(ctypes.byref(p), hidden_dim, chunk_rows, ctypes.byref(out)),
+    _check(_lib.flce_token_logprob_workspace_size(_byref(p), hidden_dim, chunk_rows, _byref(out)),
            "flce_token_logprob_workspace_size")
     return out.value
 
@@ -405,17 +416,9 @@ def flce_token_logprob(hidden, weight, target, *, bias=None, temperature=1.0, ig
     n, H = hidden.shape
     call = _Call(hidden, (weight, target, bias, logp, entropy, stats), stream)
     _vec("bias", bias, weight.shape[0], call.device)
-    logp = call.empty(n) if logp is None else _vec("logp", logp, n, call.device)
-    if with_entropy:
-        entropy = call.empty(n) if entropy is None else _vec("entropy", entropy, n, call.device)
-    elif entropy is not None:
-        raise ValueError("entropy given with with_entropy=False")
-    if stats is None:
-        stats = call.empty(n, 4)
-    elif stats.dtype != torch.float32 or stats.shape != (n, 4) or not stats.is_contiguous():
-        raise ValueError("stats must be a contiguous fp32 [n_rows, 4] tensor")
+    logp, entropy, stats = _outputs(call, n, logp, entropy, stats, with_entropy)
     ws, nbytes = _workspace(call, ws, _linear_ws_bytes(p, H, 0))
-    call.run("flce_token_logprob", ctypes.byref(p), H, float(temperature), _ptr(hidden), _ptr(weight), _ptr(bias),
+    call.run("flce_token_logprob", _lib.flce_token_logprob, _byref(p), H, float(temperature), _ptr(hidden), _ptr(weight), _ptr(bias),
              _ptr(target), _ptr(logp), _ptr(entropy), _ptr(stats), _ptr(ws), nbytes)
     return logp, entropy, stats
 
@@ -435,8 +438,7 @@ def flce_token_logprob_backward(hidden, weight, target, stats, grad_logp, *, gra
     _vec("bias", bias, V, call.device)
     _vec("grad_logp", grad_logp, n, call.device)
     _vec("grad_entropy", grad_entropy, n, call.device)
-    if stats.dtype != torch.float32 or stats.shape != (n, 4) or not stats.is_contiguous():
-        raise ValueError("stats must be a contiguous fp32 [n_rows, 4] tensor")
+    _stats(stats, n)
     if chunk_rows is None:
         chunk_rows = _chunk_rows(n, V)
     if grad_hidden is None:
@@ -452,7 +454,7 @@ def flce_token_logprob_backward(hidden, weight, target, stats, grad_logp, *, gra
         grad_bias = call.empty(V)
     _vec("grad_bias", grad_bias, V, call.device)
     ws, nbytes = _workspace(call, ws, _linear_ws_bytes(p, H, chunk_rows))
-    call.run("flce_token_logprob_backward", ctypes.byref(p), H, float(temperature), _ptr(hidden), _ptr(weight), _ptr(bias),
+    call.run("flce_token_logprob_backward", _lib.flce_token_logprob_backward, _byref(p), H, float(temperature), _ptr(hidden), _ptr(weight), _ptr(bias),
              _ptr(target), _ptr(stats), _ptr(grad_logp), _ptr(grad_entropy), _ptr(grad_hidden), _ptr(grad_weight),
              CE_DT[grad_weight.dtype], _ptr(grad_bias), chunk_rows, _ptr(ws), nbytes)
     return grad_hidden, grad_weight, grad_bias
