@@ -532,8 +532,8 @@ ce_status ce_preference_fwd_bwd(const ce_params *p, const ce_preference_params *
  */
 
 /* Workspace bytes: of flce_token_logprob for chunk_rows = 0 (16 bytes per row
- * and 256-column tile, and over 128 rows a compacted copy of hidden), of
- * flce_token_logprob_backward for its chunk_rows. */
+ * and 128 columns, and over 128 rows a compacted copy of hidden; up to 64 rows
+ * at most 10 KB a row), of flce_token_logprob_backward for its chunk_rows. */
 ce_status flce_token_logprob_workspace_size(const ce_params *p, int64_t hidden_dim, int64_t chunk_rows, size_t *bytes);
 
 ce_status flce_token_logprob(const ce_params *p, int64_t hidden_dim, float temperature, const void *hidden,

@@ -34,9 +34,22 @@ constexpr int GB_M = 128, GB_N = 256, GB_K = 64, GB_STAGES = 4;
 static_assert(GB_N == kGemmTileN, "the row statistics are kept per 256-column tile");
 constexpr int GB_A_BYTES = GB_M * GB_K * 2;  // 16 KB
 constexpr int GB_B_BYTES = GB_N * GB_K * 2;  // 32 KB
-constexpr int GB_THREADS = 192;
+constexpr int GB_THREADS = 192;  // 320 with the log-probability statistics (GemmEpi)
 constexpr int GB_TMEM_COLS = 512;
 constexpr size_t GB_SMEM = 1024 + GB_STAGES * (GB_A_BYTES + GB_B_BYTES) + 256;
+
+// The log-probability statistics (EPI 4) add the product up in two steps: the
+// tensor core over lp_kpart K steps (its fp32 additions truncate, one after the
+// other, which shifts a long sum by a relative 2^-24 a step), the epilogue warps
+// over the parts, in registers and rounded to nearest. Eight epilogue warps
+// instead of four, so that a row's 256 running sums are two threads' 128. Parts
+// of 1024 (GB300, 4096 x 4096 x 128256): 2270 us and log p off by 1.7e-7
+// (2-norm); of 512 2425 us and 0.7e-7; the whole K at once 2214 us and 6.5e-7.
+constexpr int kLpPartSteps = 16;  // of 64
+template <int EPI> struct GemmEpi {
+    static constexpr int kWarps = EPI == 4 ? 8 : 4;
+    static constexpr int kThreads = 64 + 32 * kWarps;
+};
 
 enum { OUT_F32_STORE = 0, OUT_F32_ACCUM = 1, OUT_BF16_STORE = 2 };
 
@@ -212,36 +225,35 @@ __device__ inline void epilogue_stats(const GemmArgs &g, int row, int col0, cons
     }
 }
 
-// One row's 32 consecutive logits (+ bias); columns past N read as -inf.
-__device__ inline void epilogue_logits(const GemmArgs &g, int col0, const uint32_t (&v)[32], float (&x)[32]) {
-#pragma unroll
-    for (int j = 0; j < 32; ++j) x[j] = __uint_as_float(v[j]);
-    if (col0 + 32 <= g.N) {
+// Bias added to one row's N consecutive logits; columns past the last one
+// become -inf.
+template <int N>
+__device__ inline void epilogue_logits(const GemmArgs &g, int col0, float (&x)[N]) {
+    if (col0 + N <= g.N) {
         if (g.bias) {
             const float4 *b4 = reinterpret_cast<const float4 *>(g.bias + col0);
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
+            for (int q = 0; q < N / 4; ++q) {
                 const float4 bb = __ldg(b4 + q);
                 x[4 * q] += bb.x; x[4 * q + 1] += bb.y; x[4 * q + 2] += bb.z; x[4 * q + 3] += bb.w;
             }
         }
     } else {
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
+        for (int j = 0; j < N; ++j)
             x[j] = col0 + j < g.N ? x[j] + (g.bias ? __ldg(g.bias + col0 + j) : 0.f) : -INFINITY;
     }
 }
 
-// Log-probability statistics of 32 logits of one row (nothing stored): the
-// target column (position `skip` among them, or -1) is taken out and kept in xy.
-__device__ inline void epilogue_lp_stats(const GemmArgs &g, int col0, const uint32_t (&v)[32], LpState &st, int skip,
-                                         float &xy) {
+// Log-probability statistics of N logits of one row (nothing stored): the
+// target column (position `skip` among them, or outside) is taken out and kept in xy.
+template <int N>
+__device__ inline void epilogue_lp_stats(const GemmArgs &g, int col0, float (&x)[N], LpState &st, int skip, float &xy) {
     if (col0 >= g.N) return;
-    float x[32];
-    epilogue_logits(g, col0, v, x);
-    if (skip >= 0) {
+    epilogue_logits<N>(g, col0, x);
+    if (static_cast<unsigned>(skip) < static_cast<unsigned>(N)) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
+        for (int j = 0; j < N; ++j)
             if (j == skip) {
                 xy = x[j];
                 x[j] = -INFINITY;
@@ -249,9 +261,9 @@ __device__ inline void epilogue_lp_stats(const GemmArgs &g, int col0, const uint
     }
     float vmax = x[0];
 #pragma unroll
-    for (int j = 1; j < 32; ++j) vmax = fmaxf(vmax, x[j]);
-    if (g.lp_ent) lp_add<true, 32>(st, x, vmax, g.lp_k);
-    else lp_add<false, 32>(st, x, vmax, g.lp_k);
+    for (int j = 1; j < N; ++j) vmax = fmaxf(vmax, x[j]);
+    if (g.lp_ent) lp_add<true, N>(st, x, vmax, g.lp_k);
+    else lp_add<false, N>(st, x, vmax, g.lp_k);
 }
 
 // The gradient of 32 logits of one row, rounded once to bf16.
@@ -260,7 +272,9 @@ __device__ inline void epilogue_lp_grad(const GemmArgs &g, int row, int col0, co
     if (col0 >= g.N) return;
     float x[32];
     if (row < g.M) {
-        epilogue_logits(g, col0, v, x);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) x[j] = __uint_as_float(v[j]);
+        epilogue_logits<32>(g, col0, x);
         if (g.lp_ent) lp_grad_vec<true, 32>(lg, x, g.lp_k, x);
         else lp_grad_vec<false, 32>(lg, x, g.lp_k, x);
         const int rel = y - col0;
@@ -283,47 +297,68 @@ __device__ inline void epilogue_lp_grad(const GemmArgs &g, int row, int col0, co
     }
 }
 
-// The log-probability epilogue of one tile by one warp: this thread's row,
-// its 256 accumulator columns in steps of 32. EPI 4: statistics; 5: gradient.
-template <int EPI>
-__device__ inline void epilogue_lp_tile(const GemmArgs &g, int row, int tn, uint32_t taddr) {
-    LpState st = lp_empty();
-    float xy = 0.f;
+// The gradient epilogue (EPI 5) of one tile by one warp: this thread's row, its
+// 256 accumulator columns in steps of 32.
+__device__ inline void epilogue_lp_grad_tile(const GemmArgs &g, int row, int tn, uint32_t taddr) {
+    // rows past M whose gradient the products over rows still read, in steps of 64
+    const bool zero_row = row >= g.M && row < g.m_static && row < (g.M + 63) / 64 * 64;
     int y = -(1 << 30);
     LpGrad lg{};
-    // rows past M whose gradient the products over rows still read, in steps of 64
-    const bool zero_row = EPI == 5 && row >= g.M && row < g.m_static && row < (g.M + 63) / 64 * 64;
     if (row < g.M) {
-        if (EPI == 4) {
-            const int64_t t = load_target(g.st_target, g.st_tgt32, row);
-            if (target_valid(t, g.st_ignore, g.N)) y = static_cast<int>(t);
-        } else {
-            const float4 *rp = reinterpret_cast<const float4 *>(g.lp_rows + row);
-            const float4 a = __ldg(rp), b = __ldg(rp + 1);
-            lg = LpGrad{a.x, a.y, a.z, a.w, b.x};
-            y = __float_as_int(b.y);
-        }
+        const float4 *rp = reinterpret_cast<const float4 *>(g.lp_rows + row);
+        const float4 a = __ldg(rp), b = __ldg(rp + 1);
+        lg = LpGrad{a.x, a.y, a.z, a.w, b.x};
+        y = __float_as_int(b.y);
     }
 #pragma unroll 1
     for (int c0 = 0; c0 < GB_N; c0 += 32) {
         uint32_t v[32];
         tmem_ld_32x32b_x32(taddr + c0, v);
         tmem_ld_wait();
-        const int col0 = tn * GB_N + c0;
-        if (EPI == 4) {
-            if (row < g.M) epilogue_lp_stats(g, col0, v, st, static_cast<unsigned>(y - col0) < 32u ? y - col0 : -1, xy);
-        } else if (row < g.M || zero_row) {
-            epilogue_lp_grad(g, row, col0, v, lg, y);
-        }
+        if (row < g.M || zero_row) epilogue_lp_grad(g, row, tn * GB_N + c0, v, lg, y);
     }
-    if (EPI == 4 && row < g.M) g.part[static_cast<int64_t>(row) * g.tiles_n + tn] = make_float4(st.m, st.s, st.u, xy);
+}
+
+// The statistics epilogue (EPI 4) of one tile by one of eight warps: this
+// thread's row and half of its columns. `hand_over(unit)` gives a part's
+// accumulator back, `wait(unit)` waits for the next; unit counts the parts.
+template <typename Wait, typename HandOver>
+__device__ inline void epilogue_lp_stats_tile(const GemmArgs &g, int row, int tn, int half, uint32_t lane_addr, int nparts,
+                                              uint32_t &unit, Wait wait, HandOver hand_over) {
+    constexpr int C = 16;  // columns at a time: the 128 running sums leave few registers beside them
+    float acc[128 / C][C];
+    for (int pt = 0; pt < nparts; ++pt, ++unit) {
+        wait(unit);
+        const uint32_t taddr = lane_addr + (unit & 1u) * GB_N + half * 128;
+#pragma unroll
+        for (int c = 0; c < 128 / C; ++c) {
+            uint32_t v[C];
+            tmem_ld_32x32b_x16(taddr + C * c, v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < C; ++j) acc[c][j] = pt == 0 ? __uint_as_float(v[j]) : acc[c][j] + __uint_as_float(v[j]);
+        }
+        hand_over(unit);
+    }
+    if (row >= g.M) return;
+    int y = -(1 << 30);
+    const int64_t t = load_target(g.st_target, g.st_tgt32, row);
+    if (target_valid(t, g.st_ignore, g.N)) y = static_cast<int>(t);
+    LpState st = lp_empty();
+    float xy = 0.f;
+#pragma unroll
+    for (int c = 0; c < 128 / C; ++c) {
+        const int col0 = tn * GB_N + half * 128 + C * c;
+        epilogue_lp_stats<C>(g, col0, acc[c], st, y - col0, xy);
+    }
+    g.part[(static_cast<int64_t>(row) * g.tiles_n + tn) * 2 + half] = make_float4(st.m, st.s, st.u, xy);
 }
 
 // EPI 0: the plain epilogue (epilogue_store); 1..3: fp32 store with row
 // statistics (epilogue_stats, smoothing mode EPI - 1); 4, 5: log-probability
-// statistics and gradient (epilogue_lp_tile).
+// statistics and gradient.
 template <int EPI>
-__global__ void __launch_bounds__(GB_THREADS, 1)
+__global__ void __launch_bounds__(GemmEpi<EPI>::kThreads, 1)
 flce_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, GemmArgs g) {
     if (g.dyn_count) {
         int n = __ldg(g.dyn_count) - g.dyn_off;
@@ -340,7 +375,9 @@ flce_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     const int mn_tiles = g.tiles_m * g.tiles_n;
     const int num_tiles = mn_tiles * ksplit;
     const int kiters = (g.K + GB_K - 1) / GB_K;
-    const int kper = (kiters + ksplit - 1) / ksplit;   // K steps of one split (the last may have fewer)
+    // K steps of one split (the last may have fewer); EPI 4: of one part, every part of a tile by one CTA
+    const int kper = EPI == 4 ? kLpPartSteps : (kiters + ksplit - 1) / ksplit;
+    const int nparts = EPI == 4 ? (kiters + kper - 1) / kper : 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (num_tiles == 0) return;
     if (kiters == 0) {
@@ -373,7 +410,7 @@ flce_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < GB_STAGES; ++s) { mbar_init(smem_u32(&full[s]), 1); mbar_init(smem_u32(&empty[s]), 1); }
-        for (int a = 0; a < 2; ++a) { mbar_init(smem_u32(&tfull[a]), 1); mbar_init(smem_u32(&tempty[a]), 4); }
+        for (int a = 0; a < 2; ++a) { mbar_init(smem_u32(&tfull[a]), 1); mbar_init(smem_u32(&tempty[a]), GemmEpi<EPI>::kWarps); }
         *abort_flag = 0;
         fence_mbar_init_cluster();
         tma_prefetch_desc(&tmA);
@@ -395,7 +432,7 @@ flce_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             for (int t = blockIdx.x; t < num_tiles; t += gridDim.x) {
                 int tm, tn;
                 tile_coords(g, t % mn_tiles, tm, tn);
-                const int kb = (t / mn_tiles) * kper, ke = min(kiters, kb + kper);
+                const int kb = EPI == 4 ? 0 : (t / mn_tiles) * kper, ke = EPI == 4 ? kiters : min(kiters, kb + kper);
                 for (int k = kb; k < ke; ++k, ++it) {
                     const uint32_t s = it % GB_STAGES, r = it / GB_STAGES;
                     if (r > 0) mbar_wait_bounded<false>(smem_u32(&empty[s]), (r - 1) & 1u, abort);
@@ -419,12 +456,13 @@ flce_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             const uint32_t a_kstep = g.a_mn ? 2048u : 32u, b_kstep = g.b_mn ? 2048u : 32u;
             const uint32_t a_lbo = g.a_mn ? 8192u : 16u, b_lbo = g.b_mn ? 8192u : 16u;
             uint32_t it = 0, lt = 0;
-            for (int t = blockIdx.x; t < num_tiles; t += gridDim.x, ++lt) {
+            for (int t = blockIdx.x; t < num_tiles; t += gridDim.x)
+            for (int pt = 0; pt < nparts; ++pt, ++lt) {
                 const uint32_t acc = lt & 1u, u = lt >> 1;
                 if (u > 0) mbar_wait_bounded<false>(smem_u32(&tempty[acc]), (u - 1) & 1u, abort);
                 tc_fence_after();
                 const uint32_t d = tmem + acc * GB_N;
-                const int kb = (t / mn_tiles) * kper, ke = min(kiters, kb + kper);
+                const int kb = (EPI == 4 ? pt : t / mn_tiles) * kper, ke = min(kiters, kb + kper);
                 for (int k = kb; k < ke; ++k, ++it) {
                     const uint32_t s = it % GB_STAGES, r = it / GB_STAGES;
                     mbar_wait_bounded<false>(smem_u32(&full[s]), r & 1u, abort);
@@ -440,6 +478,26 @@ flce_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                 mma_commit(smem_u32(&tfull[acc]));
             }
         }
+    } else if constexpr (EPI == 4) {
+        // ---------------------------------------------------- statistics epilogue (warps 2..9)
+        const int q = warp & 3, half = (warp - 2) >> 2;
+        const uint32_t lane_addr = tmem + (static_cast<uint32_t>(q * 32) << 16);
+        uint32_t unit = 0;
+        for (int t = blockIdx.x; t < num_tiles; t += gridDim.x) {
+            int tm, tn;
+            tile_coords(g, t, tm, tn);
+            epilogue_lp_stats_tile(
+                g, tm * GB_M + q * 32 + lane, tn, half, lane_addr, nparts, unit,
+                [&](uint32_t u) {
+                    mbar_wait_bounded<false>(smem_u32(&tfull[u & 1u]), (u >> 1) & 1u, abort);
+                    tc_fence_after();
+                },
+                [&](uint32_t u) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&tempty[u & 1u]));
+                });
+        }
     } else {
         // ---------------------------------------------------- epilogue (warps 2..5)
         const int q = warp & 3;  // TMEM lane quarter this warp may access
@@ -454,8 +512,8 @@ flce_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             const int row = tm * GB_M + q * 32 + lane;
             const int orow = (g.row_map && row < g.M) ? __ldg(g.row_map + row) : row;
             const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * GB_N;
-            if constexpr (EPI >= 4) {
-                epilogue_lp_tile<EPI>(g, row, tn, taddr);
+            if constexpr (EPI == 5) {
+                epilogue_lp_grad_tile(g, row, tn, taddr);
             } else {
             RowState st = row_state_empty();
             ArgMax am{-INFINITY, 0x7fffffff};
@@ -509,7 +567,7 @@ constexpr int GP_B_BYTES = 128 * GB_K * 2;   // 16 KB: this CTA's half of B
 constexpr size_t GP_SMEM = 1024 + GP_STAGES * (GP_A_BYTES + GP_B_BYTES) + 256;
 
 template <int EPI>
-__global__ void __launch_bounds__(GB_THREADS, 1)
+__global__ void __launch_bounds__(GemmEpi<EPI>::kThreads, 1)
 flce_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, GemmArgs g) {
     if (g.dyn_count) {
         int n = __ldg(g.dyn_count) - g.dyn_off;
@@ -524,7 +582,8 @@ flce_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
     const int mn_tiles = g.tiles_m * g.tiles_n;
     const int num_tiles = mn_tiles * ksplit;
     const int kiters = (g.K + GB_K - 1) / GB_K;
-    const int kper = (kiters + ksplit - 1) / ksplit;
+    const int kper = EPI == 4 ? kLpPartSteps : (kiters + ksplit - 1) / ksplit;
+    const int nparts = EPI == 4 ? (kiters + kper - 1) / kper : 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
     const int cid = static_cast<int>(cluster_id_x()), ncl = static_cast<int>(nclusters_x());
@@ -564,7 +623,7 @@ flce_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(smem_u32(&tfull[a]), 1);
-            mbar_init(smem_u32(&tempty[a]), 8);
+            mbar_init(smem_u32(&tempty[a]), 2 * GemmEpi<EPI>::kWarps);
         }
         *abort_flag = 0;
         fence_mbar_init_cluster();
@@ -589,7 +648,7 @@ flce_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
             for (int t = cid; t < num_tiles; t += ncl) {
                 int tm, tn;
                 tile_coords(g, t % mn_tiles, tm, tn);
-                const int kb = (t / mn_tiles) * kper, ke = min(kiters, kb + kper);
+                const int kb = EPI == 4 ? 0 : (t / mn_tiles) * kper, ke = EPI == 4 ? kiters : min(kiters, kb + kper);
                 const int row0 = tm * GP_M + static_cast<int>(rank) * 128, col0 = tn * GP_N + static_cast<int>(rank) * 128;
                 for (int k = kb; k < ke; ++k, ++it) {
                     const uint32_t st = it % GP_STAGES, r = it / GP_STAGES;
@@ -611,12 +670,13 @@ flce_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
             const uint32_t a_kstep = g.a_mn ? 2048u : 32u, b_kstep = g.b_mn ? 2048u : 32u;
             const uint32_t a_lbo = g.a_mn ? 8192u : 16u, b_lbo = g.b_mn ? 8192u : 16u;
             uint32_t it = 0, lt = 0;
-            for (int t = cid; t < num_tiles; t += ncl, ++lt) {
+            for (int t = cid; t < num_tiles; t += ncl)
+            for (int pt = 0; pt < nparts; ++pt, ++lt) {
                 const uint32_t acc = lt & 1u, u = lt >> 1;
                 if (u > 0) mbar_wait_bounded<false>(smem_u32(&tempty[acc]), (u - 1) & 1u, abort);
                 tc_fence_after();
                 const uint32_t d = tmem + acc * GP_N;
-                const int kb = (t / mn_tiles) * kper, ke = min(kiters, kb + kper);
+                const int kb = (EPI == 4 ? pt : t / mn_tiles) * kper, ke = min(kiters, kb + kper);
                 for (int k = kb; k < ke; ++k, ++it) {
                     const uint32_t st = it % GP_STAGES, r = it / GP_STAGES;
                     mbar_wait_bounded<false>(smem_u32(&full[st]), r & 1u, abort);
@@ -631,6 +691,30 @@ flce_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
                 }
                 mma_commit_pair_mc(smem_u32(&tfull[acc]), 0x3);
             }
+        }
+    } else if constexpr (EPI == 4) {
+        // ---------------------------------------------------- statistics epilogue (warps 2..9, both CTAs)
+        const int q = warp & 3, half = (warp - 2) >> 2;
+        const uint32_t lane_addr = tmem + (static_cast<uint32_t>(q * 32) << 16);
+        const uint32_t tempty0 = mapa_shared(smem_u32(&tempty[0]), 0);
+        uint32_t unit = 0;
+        for (int t = cid; t < num_tiles; t += ncl) {
+            int tm, tn;
+            tile_coords(g, t, tm, tn);
+            epilogue_lp_stats_tile(
+                g, tm * GP_M + static_cast<int>(rank) * 128 + q * 32 + lane, tn, half, lane_addr, nparts, unit,
+                [&](uint32_t u) {
+                    mbar_wait_bounded<false>(smem_u32(&tfull[u & 1u]), (u >> 1) & 1u, abort);
+                    tc_fence_after();
+                },
+                [&](uint32_t u) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (rank == 0) mbar_arrive(smem_u32(&tempty[u & 1u]));
+                        else mbar_arrive_remote(tempty0 + (u & 1u) * 8u);
+                    }
+                });
         }
     } else {
         // ---------------------------------------------------- epilogue (warps 2..5, both CTAs)
@@ -647,8 +731,8 @@ flce_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_cons
             const int row = tm * GP_M + static_cast<int>(rank) * 128 + q * 32 + lane;
             const int orow = (g.row_map && row < g.M) ? __ldg(g.row_map + row) : row;
             const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * GP_N;
-            if constexpr (EPI >= 4) {
-                epilogue_lp_tile<EPI>(g, row, tn, taddr);
+            if constexpr (EPI == 5) {
+                epilogue_lp_grad_tile(g, row, tn, taddr);
             } else {
             RowState stt = row_state_empty();
             ArgMax am{-INFINITY, 0x7fffffff};
@@ -1046,7 +1130,7 @@ static PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 
 // 2-D bf16 row-major matrix [rows, cols] with row stride ld (elements), box
 // of box_cols x box_rows, 128-byte swizzle, zero fill out of bounds.
-static cudaError_t make_tmap(CUtensorMap *m, const void *ptr, uint64_t rows, uint64_t cols, uint64_t ld,
+cudaError_t make_tmap(CUtensorMap *m, const void *ptr, uint64_t rows, uint64_t cols, uint64_t ld,
                              uint32_t box_cols, uint32_t box_rows) {
     auto fn = encode_fn();
     if (!fn) return cudaErrorNotSupported;
@@ -1083,14 +1167,14 @@ int gemm_fit_ksplit(int K, int ksplit) {
 }
 
 // Resident CTA pairs of a pair kernel on a device (0 if unknown), asked once.
-static int pair_clusters(const void *fn, int dev) {
+static int pair_clusters(const void *fn, int dev, int threads) {
     static const void *fns[16];
     static int devs[16], vals[16], used = 0;
     for (int i = 0; i < used; ++i)
         if (fns[i] == fn && devs[i] == dev) return vals[i];
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * 128);
-    cfg.blockDim = dim3(GB_THREADS);
+    cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = GP_SMEM;
     cudaLaunchAttribute at;
     at.id = cudaLaunchAttributeClusterDimension;
@@ -1196,18 +1280,19 @@ cudaError_t gemm_bf16(int M, int N, int K, const void *A, int64_t lda, int a_mn,
         attr_set[pair ? 1 : 0][epi] |= bit;
     }
     const int tiles = g.tiles_m * g.tiles_n * ksplit;
+    const int threads = epi == 4 ? GemmEpi<4>::kThreads : GB_THREADS;
     void *args[] = {&ta, &tb, &g};
     if (!pair) {
         const int grid = tiles < sm_count() ? tiles : sm_count();
-        return cudaLaunchKernel(fn, dim3(grid), dim3(GB_THREADS), args, GB_SMEM, s);
+        return cudaLaunchKernel(fn, dim3(grid), dim3(threads), args, GB_SMEM, s);
     }
     // persistent pairs: no more clusters than can be resident at once
-    int clusters = pair_clusters(fn, dev);
+    int clusters = pair_clusters(fn, dev, threads);
     if (clusters < 1) clusters = sm_count() / 2 > 0 ? sm_count() / 2 : 1;
     if (clusters > tiles) clusters = tiles;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(2 * clusters));
-    cfg.blockDim = dim3(GB_THREADS);
+    cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = GP_SMEM;
     cfg.stream = s;
     cudaLaunchAttribute at;
@@ -1271,7 +1356,8 @@ cudaError_t flce_grad_hidden(int64_t c, int64_t H, int64_t V, const void *dz, in
                             dim3(static_cast<unsigned>(sm_count() * 8)), dim3(256), args, 0, s);
 }
 
-cudaError_t flce_grad_bias(int64_t c, int64_t V, const void *dz, int64_t ldd, const int *count, int64_t off,
+// grad_bias (+)= column sums of dZ
+static cudaError_t flce_grad_bias(int64_t c, int64_t V, const void *dz, int64_t ldd, const int *count, int64_t off,
                            float *grad_bias, int accumulate, cudaStream_t s) {
     const __nv_bfloat16 *dzc = reinterpret_cast<const __nv_bfloat16 *>(dz);
     int rows = static_cast<int>(c), o = static_cast<int>(off);

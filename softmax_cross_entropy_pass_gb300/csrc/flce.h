@@ -2,6 +2,7 @@
 // fused-linear cross-entropy.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -42,12 +43,13 @@ struct GemmStats {
 constexpr int kGemmTileN = 256;
 
 // Log-probability epilogues of the logits product (the product itself is not
-// stored): `part` set: per output row and 256-column tile the state {max m,
+// stored): `part` set: per output row and kLpTileN columns the state {max m,
 // s = sum 2^a without the row's target column, u = sum 2^a a (with entropy),
-// the target logit where the tile holds it}, a = (x - m) k, x = product +
-// bias. `rows` set: the gradient of every logit, rounded once to bf16 into
+// the target logit where they hold it} at part[row * 2 ceil(N / 256) + column /
+// kLpTileN], a = (x - m) k, x = product + bias. `rows` set: the gradient of every logit, rounded once to bf16 into
 // the output, from the row's scalars; rows from M up to the next multiple of
 // 64 (within the launch's static M) become zeros.
+constexpr int kLpTileN = 128;
 struct LpMapRow {
     float m, neg_log2d, A, B;  // (A + B log2 p) p off the target, p = 2^((x - m) k + neg_log2d)
     float dy;                  // at the target column y
@@ -96,9 +98,19 @@ int flce_dh_splits(int64_t chunk, int64_t H, int64_t V);
 cudaError_t flce_grad_hidden(int64_t c, int64_t H, int64_t V, const void *dz, int64_t ldd, const void *weight, int splits,
                              float *parts, const int *count, int64_t off, const int *row_map, void *out,
                              unsigned int *status, cudaStream_t s);
-// grad_bias (+)= column sums of dZ
-cudaError_t flce_grad_bias(int64_t c, int64_t V, const void *dz, int64_t ldd, const int *count, int64_t off,
-                           float *grad_bias, int accumulate, cudaStream_t s);
+// 2-D bf16 row-major matrix [rows, cols] with row stride ld (elements), box
+// of box_cols x box_rows, 128-byte swizzle, zero fill out of bounds.
+cudaError_t make_tmap(CUtensorMap *m, const void *ptr, uint64_t rows, uint64_t cols, uint64_t ld, uint32_t box_cols,
+                      uint32_t box_rows);
+
+// Log-probability statistics of few rows (flce_few.cu): the states of
+// flce_few_parts(V) column sets to part[row * flce_few_parts(V) + set] and the
+// target logits to xy[row]. n <= kFewMaxRows; arguments as GemmLp's.
+constexpr int kFewMaxRows = 64;
+int flce_few_parts(int64_t V);
+cudaError_t flce_few(int n, int V, int H, const void *hidden, const void *weight, const float *bias, const void *target,
+                     int tgt32, int64_t ignore_index, float k, int entropy, float4 *part, float *xy, unsigned int *status,
+                     cudaStream_t s);
 
 // K steps of 64 per split-K part: ksplit parts over kiters steps, each
 // non-empty (the split count actually used, <= ksplit).

@@ -1,7 +1,7 @@
 // flce_logprob.cu -- token log-probabilities of a linear head and their
 // gradient: the logits (hidden W^T + b) / T are formed tile by tile in tensor
 // memory and never stored. The forward's product keeps the softmax statistics
-// of every 256-column tile (16 bytes a row and tile), which one kernel merges
+// of every 128 columns (16 bytes a row), which one kernel merges
 // per row. The backward forms the logits once more and its product's epilogue
 // writes their gradient dZ (bf16), from which the two gradient products run.
 #include <cmath>
@@ -17,6 +17,7 @@ namespace ce {
 // compacted rows, -1 for rows left out.
 struct LpFinishArgs {
     const float4 *part;
+    const float *xy;         // the rows' target logits, or NULL: in their part's w
     int tiles;
     int64_t n_rows, vocab;
     const void *target;
@@ -50,7 +51,7 @@ __global__ void __launch_bounds__(256) flce_logprob_finish_kernel(LpFinishArgs a
         }
         st = lp_warp_merge<ENT>(st, a.k);
         if (lane != 0) continue;
-        const float xy = __ldg(&pp[t / kGemmTileN].w);
+        const float xy = a.xy ? __ldg(a.xy + row) : __ldg(&pp[t / kLpTileN].w);
         float4 stats = lp_row_stats(st, xy, a.k);
         const LpRow r = lp_row(stats, a.k, a.inv_t);
         if (!ENT) stats.w = NAN;
@@ -75,6 +76,40 @@ __global__ void __launch_bounds__(256) flce_logprob_rows_kernel(const float4 *st
     }
 }
 
+// grad_bias (+)= the column sums of dZ: a block takes 256 columns, 8 to a lane,
+// its 16 warps every 16th row each, and adds the warps up in order. Bound by
+// reading dZ once.
+constexpr int kColsumWarps = 16;
+__global__ void __launch_bounds__(kColsumWarps * 32) flce_logprob_colsum_kernel(const uint4 *dz, int64_t ld8, int rows,
+                                                                                int64_t V, float *gb, int accumulate,
+                                                                                const int *count, int off) {
+    __shared__ float sh[kColsumWarps][256];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t v = static_cast<int64_t>(blockIdx.x) * 32 + lane;  // this lane's vector of a row
+    int n = __ldg(count) - off;
+    n = n < rows ? n : rows;
+    float s[8] = {};
+    if (v * 8 < V) {
+        const uint4 *p = dz + v;
+#pragma unroll 4
+        for (int r = warp; r < n; r += kColsumWarps) {
+            float x[8];
+            Fmt<CE_DT_BF16>::unpack(__ldg(p + r * ld8), x);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s[e] += x[e];
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sh[warp][lane * 8 + e] = s[e];
+    __syncthreads();
+    const int64_t c = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (threadIdx.x < 256 && c < V) {
+        float t = 0.f;
+        for (int w = 0; w < kColsumWarps; ++w) t += sh[w][threadIdx.x];
+        gb[c] = accumulate ? gb[c] + t : t;
+    }
+}
+
 }  // namespace ce
 
 using namespace ce;
@@ -89,7 +124,7 @@ size_t up(size_t a, size_t b) { return (a + b - 1) / b * b; }
 
 struct LpLayout {
     size_t idx, pos, cnt, tgt, hc;       // compaction
-    size_t part;                         // forward
+    size_t part, xy;                     // forward
     size_t rows, dz, dh;                 // backward
     size_t total;
     int64_t ldd;
@@ -111,8 +146,12 @@ LpLayout lp_layout(int64_t n, int64_t V, int64_t H, int64_t chunk, bool backward
         L.tgt = take(n * 8);
         L.hc = take(static_cast<size_t>(n) * H * 2);
     }
-    L.tiles = static_cast<int>((V + kGemmTileN - 1) / kGemmTileN);
+    L.tiles = static_cast<int>((V + kGemmTileN - 1) / kGemmTileN) * (kGemmTileN / kLpTileN);
     if (!backward) {
+        if (n <= kFewMaxRows) {
+            L.tiles = flce_few_parts(V);
+            L.xy = take(n * 4);
+        }
         L.part = take(static_cast<size_t>(n) * L.tiles * 16);
     } else {
         L.ldd = (V + 7) / 8 * 8;
@@ -186,13 +225,21 @@ ce_status flce_token_logprob(const ce_params *p, int64_t H, float temperature, c
     lp.ignore_index = p->ignore_index;
     lp.k = base2(temperature);
     lp.entropy = entropy != nullptr;
-    const GemmDyn rows{cnt, 0, 0, nullptr};
-    e = gemm_bf16(static_cast<int>(n), static_cast<int>(V), static_cast<int>(H), compact ? w + L.hc : hidden, H, 0, weight, H,
-                  0, CE_GEMM_F32_STORE, nullptr, V, bias, &ctl->status, s, compact ? &rows : nullptr, nullptr, 1, 0, GEMM_AUTO,
-                  &lp);
+    const bool few = n <= kFewMaxRows;
+    if (few) {
+        e = flce_few(static_cast<int>(n), static_cast<int>(V), static_cast<int>(H), hidden, weight, bias, target,
+                     p->target_is_int32, p->ignore_index, lp.k, lp.entropy, lp.part, reinterpret_cast<float *>(w + L.xy),
+                     &ctl->status, s);
+    } else {
+        const GemmDyn rows{cnt, 0, 0, nullptr};
+        e = gemm_bf16(static_cast<int>(n), static_cast<int>(V), static_cast<int>(H), compact ? w + L.hc : hidden, H, 0,
+                      weight, H, 0, CE_GEMM_F32_STORE, nullptr, V, bias, &ctl->status, s, compact ? &rows : nullptr, nullptr,
+                      1, 0, GEMM_AUTO, &lp);
+    }
     if (e != cudaSuccess) return cuda_fail(e);
     LpFinishArgs a{};
     a.part = lp.part;
+    a.xy = few ? reinterpret_cast<float *>(w + L.xy) : nullptr;
     a.tiles = L.tiles;
     a.n_rows = n;
     a.vocab = V;
@@ -279,8 +326,16 @@ ce_status flce_token_logprob_backward(const ce_params *p, int64_t H, float tempe
         e = gemm_bf16(static_cast<int>(V), static_cast<int>(H), static_cast<int>(c), dz, L.ldd, 1, h_c, H, 1, out_kind,
                       grad_weight, H, nullptr, &ctl->status, s, &rows_k);
         if (e != cudaSuccess) return cuda_fail(e);
-        if (grad_bias && (e = flce_grad_bias(c, V, dz, L.ldd, cnt, r0, grad_bias, r0 == 0 ? 0 : 1, s)) != cudaSuccess)
-            return cuda_fail(e);
+        if (grad_bias) {
+            const uint4 *dz8 = reinterpret_cast<const uint4 *>(dz);
+            int64_t ld8 = L.ldd / 8, v = V;
+            int nr = static_cast<int>(c), accumulate = r0 == 0 ? 0 : 1, off = static_cast<int>(r0);
+            const int *cc = cnt;
+            void *args[] = {&dz8, &ld8, &nr, &v, &grad_bias, &accumulate, &cc, &off};
+            e = cudaLaunchKernel(reinterpret_cast<const void *>(&flce_logprob_colsum_kernel),
+                                 dim3(static_cast<unsigned>((V + 255) / 256)), dim3(kColsumWarps * 32), args, 0, s);
+            if (e != cudaSuccess) return cuda_fail(e);
+        }
     }
     return CE_OK;
 }

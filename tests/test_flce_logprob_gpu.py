@@ -77,7 +77,8 @@ def reference(h, w, t, b, temperature, gl, gh):
 SHAPES = [
     # rows, H, V
     (1, 64, 256), (1, 8, 1), (3, 72, 1001), (16, 128, 50257), (127, 64, 513), (128, 256, 300), (129, 256, 1000),
-    (200, 136, 4099), (600, 128, 2051), (1100, 192, 777), (65, 64, 70000),
+    (200, 136, 4099), (600, 128, 2051), (1100, 192, 777), (65, 64, 70000), (33, 72, 3001), (64, 200, 4097),
+    (2, 1000, 999), (17, 2056, 33), (300, 2048, 520),
 ]
 
 

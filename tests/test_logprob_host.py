@@ -306,8 +306,9 @@ def test_linear_workspace_sizes(ce):
     out = ctypes.c_size_t()
     size = lambda n, V, H, c: (ce._lib.flce_token_logprob_workspace_size(ctypes.byref(_p(ce, n_rows=n, vocab=V)), H, c,  # noqa: E731
                                                                         ctypes.byref(out)), out.value)[1]
-    tiles = (128256 + 255) // 256
+    tiles = (128256 + 255) // 256 * 2
     assert 16 * tiles * 100 <= size(100, 128256, 4096, 0) <= 16 * tiles * 100 + 4096          # one row tile: no copy
+    assert size(1, 128256, 4096, 0) <= 16384 and size(64, 128256, 4096, 0) <= 64 * 10240
     assert size(4096, 128256, 4096, 0) <= 4096 * (16 * tiles + 4096 * 2 + 16) + 16384
     assert size(4096, 128256, 4096, 4096) >= 4096 * 128256 * 2
     assert size(4096, 128256, 4096, 512) < size(4096, 128256, 4096, 4096)
