@@ -4,10 +4,10 @@
 //
 // The vocabulary is the tensor core's M side: a CTA multiplies tiles of 128
 // weight rows with all hidden rows (N = 16, 32 or 64) and owns a contiguous
-// share of the vocabulary cut at multiples of 32 rows, so that one CTA per SM
+// share of the vocabulary cut at multiples of 16 rows, so that one CTA per SM
 // ends with the others (whole 256-column tiles leave the last of four waves a
-// third full). Weights go through a ring of 16 KB stages by TMA, 32 rows a box,
-// so a share's last tile loads only what it has. Partial products of 256 K
+// third full). Weights go through a ring of 16 KB stages by TMA; a share's last
+// tile loads only the rows it has. Partial products of 256 K
 // columns go to their own accumulator in tensor memory and are added up by the
 // epilogue in registers (the tensor core's long sums truncate). Every epilogue
 // thread keeps the running statistics of its weight rows for 16 hidden rows;
@@ -21,11 +21,12 @@ namespace ce {
 
 constexpr int kFewM = 128, kFewK = 64;
 constexpr int kFewWBytes = kFewM * kFewK * 2;   // 16 KB of weights a stage
-constexpr int kFewBoxRows = 32;
+constexpr int kFewBoxRows = 16;                 // the unit of the shares
+constexpr int kFewBoxBytes = kFewBoxRows * kFewK * 2;
 constexpr int kFewPartSteps = 4;                // K steps of one accumulator
 constexpr int kFewAcc = 8;                      // accumulators in flight
 constexpr int kFewMaxStages = 12;
-constexpr int kFewSmem = 226 * 1024;
+constexpr int kFewSmem = 222 * 1024;
 
 struct FewArgs {
     int n, V, H, N;          // N: hidden rows of a tile (16, 32 or 64)
@@ -55,18 +56,20 @@ __device__ inline void few_add(LpState &st, float x, float k) {
 }
 
 __global__ void __launch_bounds__(64 + 128 * 4, 1)
-flce_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmH, FewArgs g) {
+flce_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmWs,
+                const __grid_constant__ CUtensorMap tmH, FewArgs g) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t full[kFewMaxStages], empty[kFewMaxStages], tfull[kFewAcc], tempty[kFewAcc];
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
     __shared__ int tgt[kFewMaxRows];
+    __shared__ float red_mem[kFewMaxRows * 4 * 3];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int nsets = g.N / 16;
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;  // 128-byte swizzle atoms
     const uint32_t stage_bytes = kFewWBytes + g.N * kFewK * 2;
     volatile int *abort = &abort_flag;
-    // this CTA's share of the vocabulary, in units of 32 rows
+    // this CTA's share of the vocabulary, in units of kFewBoxRows rows
     const int64_t units = (g.V + kFewBoxRows - 1) / kFewBoxRows;
     const int v_lo = static_cast<int>(units * blockIdx.x / gridDim.x) * kFewBoxRows;
     const int v_end = static_cast<int>(units * (blockIdx.x + 1) / gridDim.x) * kFewBoxRows;
@@ -86,8 +89,10 @@ flce_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
             mbar_init(smem_u32(&tempty[a]), 4 * nsets);
         }
         abort_flag = 0;
+        if (blockIdx.x == 0) *g.status = 0u;  // no wait can have given up yet (they run for 2 s)
         fence_mbar_init_cluster();
         tma_prefetch_desc(&tmW);
+        tma_prefetch_desc(&tmWs);
         tma_prefetch_desc(&tmH);
     }
     for (int r = tid; r < kFewMaxRows; r += blockDim.x) {
@@ -106,18 +111,27 @@ flce_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
     if (warp == 0) {
         if (lane == 0) {
             // ------------------------------------------------ TMA producer
-            uint32_t it = 0;
+            // (stage and round are counted, not divided out: one thread issues every copy)
+            uint32_t s = 0, round = 0;
             for (int tile = 0; tile < ntiles; ++tile) {
                 const int v0 = v_lo + tile * kFewM;
                 const int boxes = (min(kFewM, v_hi - v0) + kFewBoxRows - 1) / kFewBoxRows;
-                for (int ks = 0; ks < ksteps; ++ks, ++it) {
-                    const uint32_t s = it % g.stages, r = it / g.stages;
-                    if (r > 0) mbar_wait_bounded<false>(smem_u32(&empty[s]), (r - 1) & 1u, abort);
+                const uint32_t bytes = boxes * kFewBoxBytes + g.N * kFewK * 2;
+                for (int ks = 0; ks < ksteps; ++ks) {
                     const uint32_t fb = smem_u32(&full[s]), dst = base + s * stage_bytes;
-                    mbar_expect_tx(fb, boxes * (kFewWBytes / 4) + g.N * kFewK * 2);
-                    for (int b = 0; b < boxes; ++b)
-                        tma_load_2d(dst + b * (kFewWBytes / 4), &tmW, ks * kFewK, v0 + b * kFewBoxRows, fb);
+                    if (round > 0) mbar_wait_bounded<false>(smem_u32(&empty[s]), (round - 1) & 1u, abort);
+                    mbar_expect_tx(fb, bytes);
+                    if (boxes == kFewM / kFewBoxRows) {
+                        tma_load_2d(dst, &tmW, ks * kFewK, v0, fb);
+                    } else {
+                        for (int b = 0; b < boxes; ++b)
+                            tma_load_2d(dst + b * kFewBoxBytes, &tmWs, ks * kFewK, v0 + b * kFewBoxRows, fb);
+                    }
                     tma_load_2d(dst + kFewWBytes, &tmH, ks * kFewK, 0, fb);
+                    if (++s == static_cast<uint32_t>(g.stages)) {
+                        s = 0;
+                        ++round;
+                    }
                 }
             }
         }
@@ -125,16 +139,15 @@ flce_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
         if (lane == 0) {
             // ------------------------------------------------ MMA issuer
             const uint32_t idesc = idesc_bf16_f32(kFewM, g.N, 0, 0);
-            uint32_t it = 0, unit = 0;
+            uint32_t s = 0, phase = 0, unit = 0;
             for (int tile = 0; tile < ntiles; ++tile)
                 for (int pt = 0; pt < nparts; ++pt, ++unit) {
                     const uint32_t acc = unit % kFewAcc, u = unit / kFewAcc;
                     if (u > 0) mbar_wait_bounded<false>(smem_u32(&tempty[acc]), (u - 1) & 1u, abort);
                     tc_fence_after();
                     const int kb = pt * kFewPartSteps, ke = min(ksteps, kb + kFewPartSteps);
-                    for (int ks = kb; ks < ke; ++ks, ++it) {
-                        const uint32_t s = it % g.stages, r = it / g.stages;
-                        mbar_wait_bounded<false>(smem_u32(&full[s]), r & 1u, abort);
+                    for (int ks = kb; ks < ke; ++ks) {
+                        mbar_wait_bounded<false>(smem_u32(&full[s]), phase, abort);
                         tc_fence_after();
                         const uint32_t a = base + s * stage_bytes, b = a + kFewWBytes;
 #pragma unroll
@@ -142,6 +155,10 @@ flce_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
                             mma_bf16(tmem + acc * g.N, smem_desc_sw128(a + kk * 32, 16, 1024),
                                      smem_desc_sw128(b + kk * 32, 16, 1024), idesc, (ks > kb || kk > 0) ? 1u : 0u);
                         mma_commit(smem_u32(&empty[s]));
+                        if (++s == static_cast<uint32_t>(g.stages)) {
+                            s = 0;
+                            phase ^= 1u;
+                        }
                     }
                     mma_commit(smem_u32(&tfull[acc]));
                 }
@@ -184,17 +201,22 @@ flce_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
                 }
             }
         }
-        // the lanes' statistics, row by row
-        const int parts = gridDim.x * 4;
+        // the lanes' statistics, row by row, then those of the four warps of a row set
+        LpState(*red)[4] = reinterpret_cast<LpState(*)[4]>(red_mem);
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
-            const int row = set * 16 + j;
-            if (row < g.n) {
-                const LpState m = lp_warp_merge<true>(st[j], k);
-                if (lane == 0) g.part[static_cast<int64_t>(row) * parts + blockIdx.x * 4 + q] = make_float4(m.m, m.s, m.u, 0.f);
-            }
+            const LpState m = lp_warp_merge<true>(st[j], k);
+            if (lane == 0) red[set * 16 + j][q] = m;
+        }
+        asm volatile("bar.sync 1, %0;" ::"r"(128 * nsets) : "memory");
+        const int row = tid - 64;
+        if (row < g.n) {
+            LpState m = red[row][0];
+            for (int i = 1; i < 4; ++i) m = lp_merge<true>(m, red[row][i], k);
+            g.part[static_cast<int64_t>(row) * gridDim.x + blockIdx.x] = make_float4(m.m, m.s, m.u, 0.f);
         }
     }
+    pdl_launch_dependents();  // the kernel that merges the parts may be set up meanwhile
     __syncthreads();
     if (warp == 1) {
         tc_fence_after();
@@ -204,12 +226,12 @@ flce_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
 }
 
 // One CTA per SM of a full GB300, fixed so that the workspace is a function of
-// the sizes alone; fewer where the vocabulary has fewer units of 32 rows.
+// the sizes alone; fewer where the vocabulary has fewer units of 16 rows.
 static int few_blocks(int64_t V) {
     const int64_t units = (V + kFewBoxRows - 1) / kFewBoxRows;
     return static_cast<int>(units < 152 ? units : 152);
 }
-int flce_few_parts(int64_t V) { return 4 * few_blocks(V); }
+int flce_few_parts(int64_t V) { return few_blocks(V); }
 
 cudaError_t flce_few(int n, int V, int H, const void *hidden, const void *weight, const float *bias, const void *target,
                      int tgt32, int64_t ignore_index, float k, int entropy, float4 *part, float *xy, unsigned int *status,
@@ -222,8 +244,9 @@ cudaError_t flce_few(int n, int V, int H, const void *hidden, const void *weight
     if (g.stages > kFewMaxStages) g.stages = kFewMaxStages;
     g.bias = bias; g.target = target; g.tgt32 = tgt32; g.ignore_index = ignore_index;
     g.k = k; g.entropy = entropy; g.part = part; g.xy = xy; g.status = status;
-    CUtensorMap tw, th;
-    cudaError_t e = make_tmap(&tw, weight, V, H, H, kFewK, kFewBoxRows);
+    CUtensorMap tw, tws, th;  // weight boxes of a whole tile, and of 16 rows for a share's last one
+    cudaError_t e = make_tmap(&tw, weight, V, H, H, kFewK, kFewM);
+    if (e == cudaSuccess) e = make_tmap(&tws, weight, V, H, H, kFewK, kFewBoxRows);
     if (e == cudaSuccess) e = make_tmap(&th, hidden, n, H, H, kFewK, g.N);
     if (e != cudaSuccess) return e;
     // the shared-memory limit is a per-device attribute: set once per device
@@ -236,7 +259,7 @@ cudaError_t flce_few(int n, int V, int H, const void *hidden, const void *weight
         if (e != cudaSuccess) return e;
         attr_set |= bit;
     }
-    void *args[] = {&tw, &th, &g};
+    void *args[] = {&tw, &tws, &th, &g};
     return cudaLaunchKernel(reinterpret_cast<const void *>(&flce_few_kernel), dim3(few_blocks(V)),
                             dim3(64 + 128 * (g.N / 16)), args, 1024 + g.stages * stage, s);
 }

@@ -31,6 +31,7 @@ struct LpFinishArgs {
 template <bool ENT>
 __global__ void __launch_bounds__(256) flce_logprob_finish_kernel(LpFinishArgs a) {
     const int lane = threadIdx.x & 31;
+    pdl_wait();
     for (int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); row < a.n_rows;
          row += static_cast<int64_t>(gridDim.x) * 8) {
         const int64_t t = load_target(a.target, a.tgt32, row);
@@ -44,10 +45,18 @@ __global__ void __launch_bounds__(256) flce_logprob_finish_kernel(LpFinishArgs a
             continue;
         }
         const float4 *pp = a.part + (a.pos ? static_cast<int64_t>(__ldg(a.pos + row)) : row) * a.tiles;
-        LpState st = lp_empty();
+        // the maximum first, so that the parts' sums are moved to it independently
+        float M = -INFINITY;
+#pragma unroll 4
+        for (int j = lane; j < a.tiles; j += 32) M = fmaxf(M, __ldg(&pp[j].x));
+        LpState st{M, 0.f, 0.f};
+#pragma unroll 4
         for (int j = lane; j < a.tiles; j += 32) {
             const float4 q = __ldg(pp + j);
-            st = lp_merge<ENT>(st, LpState{q.x, q.y, q.z}, a.k);
+            LpState o{q.x, q.y, q.z};
+            if (M != -INFINITY) lp_rebase<ENT>(o, M, a.k);
+            st.s += o.s;
+            if (ENT) st.u += o.u;
         }
         st = lp_warp_merge<ENT>(st, a.k);
         if (lane != 0) continue;
@@ -207,9 +216,9 @@ ce_status flce_token_logprob(const ce_params *p, int64_t H, float temperature, c
     char *w = reinterpret_cast<char *>(ws);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     WsCtl *ctl = reinterpret_cast<WsCtl *>(ws);
-    cudaError_t e = cudaMemsetAsync(ws, 0, 256, s);
+    const bool few = n <= kFewMaxRows, compact = n > kCompactAbove;
+    cudaError_t e = few ? cudaSuccess : cudaMemsetAsync(ws, 0, 256, s);  // the few-rows kernel clears its status word itself
     if (e != cudaSuccess) return cuda_fail(e);
-    const bool compact = n > kCompactAbove;
     int *idx = reinterpret_cast<int *>(w + L.idx), *pos = reinterpret_cast<int *>(w + L.pos);
     int *cnt = reinterpret_cast<int *>(w + L.cnt);
     int64_t *tgt = reinterpret_cast<int64_t *>(w + L.tgt);
@@ -225,7 +234,6 @@ ce_status flce_token_logprob(const ce_params *p, int64_t H, float temperature, c
     lp.ignore_index = p->ignore_index;
     lp.k = base2(temperature);
     lp.entropy = entropy != nullptr;
-    const bool few = n <= kFewMaxRows;
     if (few) {
         e = flce_few(static_cast<int>(n), static_cast<int>(V), static_cast<int>(H), hidden, weight, bias, target,
                      p->target_is_int32, p->ignore_index, lp.k, lp.entropy, lp.part, reinterpret_cast<float *>(w + L.xy),
@@ -254,9 +262,19 @@ ce_status flce_token_logprob(const ce_params *p, int64_t H, float temperature, c
     a.stats = reinterpret_cast<float4 *>(stats);
     void *args[] = {&a};
     const int64_t blocks = (n + 7) / 8;
-    e = cudaLaunchKernel(entropy ? reinterpret_cast<const void *>(&flce_logprob_finish_kernel<true>)
-                                 : reinterpret_cast<const void *>(&flce_logprob_finish_kernel<false>),
-                         dim3(static_cast<unsigned>(blocks < 2048 ? blocks : 2048)), dim3(256), args, 0, s);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(blocks < 2048 ? blocks : 2048));
+    cfg.blockDim = dim3(256);
+    cfg.stream = s;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelExC(&cfg,
+                            entropy ? reinterpret_cast<const void *>(&flce_logprob_finish_kernel<true>)
+                                    : reinterpret_cast<const void *>(&flce_logprob_finish_kernel<false>),
+                            args);
     return e == cudaSuccess ? CE_OK : cuda_fail(e);
 }
 
