@@ -25,7 +25,10 @@ constexpr int kLpThreads = kLpConsumers + 64;  // and the producer and the scala
 constexpr int kLpSlots = 6;
 constexpr int kLpCtasPerSm = 2;
 constexpr int kLpMaxCluster = 8;
-constexpr int kLpCtlBytes = 1024;
+// Rows are shared out per window of at most kLpWindow rows and kLpList rows a cluster
+constexpr int kLpWindow = 8192;
+constexpr int kLpList = 256;
+constexpr int kLpCtlBytes = 6144;
 constexpr int kLpSmemBytes = kLpSlots * kStreamChunk + 2 * kLpConsumers * 16 + kLpCtlBytes;
 
 struct LpSmem {
@@ -36,6 +39,10 @@ struct LpSmem {
     LpGrad grad[2];                 // the row's gradient scalars
     float xy[2];
     int abort;
+    int n_live, n_dead;               // this cluster's rows of the window
+    int live[kLpList + 1], dead[kLpList + 1];
+    uint32_t mask[kLpWindow / 32];    // which rows of the window take part
+    int before[kLpWindow / 32];       // how many of them lie before each 32
 };
 static_assert(sizeof(LpSmem) <= kLpCtlBytes, "control block too large");
 
@@ -190,16 +197,112 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtasPerSm) lp_rows_kernel(LpArg
         if (POLICY) return policy_row_live(a, row, t);
         return target_valid(t, a.ignore_index, V) && row >= row_lo && row < row_hi;
     };
+    // Which rows this cluster takes. Up to one row a cluster: its own number.
+    // Otherwise the rows that take part and those that do not are dealt out
+    // separately, window by window, every cluster getting the same number of each
+    // (dealt together, a cluster's share of the former varies: 8192 x 128256
+    // with 30% left out ran as long as 12% more rows would). A window's lists are
+    // built by the whole CTA from one read of the targets.
+    const bool single = a.n_rows <= nq;
+    const int64_t window = single ? a.n_rows : (kLpList * nq < kLpWindow ? kLpList * nq : kLpWindow);
+    uint32_t it = 0, j = 0;  // ring position (producer and consumers); live rows done (their parities)
+    bool have_norm = false;  // scalar warp: the batch's weight sum, this cluster's row losses (lane 0 of its first CTA)
+    float w_sum = 0.f;
+    double cta_sum = 0.0;
+    const auto dead_outputs = [&](int64_t row, int64_t t) {
+        if (POLICY) {
+            if (a.reduction == CE_RED_NONE) a.loss[row] = 0.f;
+            if (a.row_stats) a.row_stats[row] = make_float4(0.f, 0.f, 0.f, 0.f);
+        } else {
+            // ignored: 0; a target outside [0, vocab): NaN (0 inside the preference loss, which flags it)
+            const float none = t == a.ignore_index || a.offsets ? 0.f : NAN;
+            if (a.logp) a.logp[row] = none;
+            if (a.entropy) a.entropy[row] = none;
+            if (a.stats) a.stats[row] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+    };
+    const auto zero_row = [&](int64_t row) {
+        if (POLICY) lp_zero_span<DT>(gbase + row * gstep, 0, L, tid, NCT);
+    };
+    for (int64_t w0 = 0; w0 < a.n_rows; w0 += window) {
+    int n_live, n_dead;
+    if (single) {
+        const int64_t t = load_target(a.target, a.tgt32, q0);  // at most one cluster a row is launched
+        n_live = row_live(q0, t) ? 1 : 0;
+        n_dead = POLICY ? 1 - n_live : 0;
+        if (n_live == 0 && tid == 0 && rank == 0) dead_outputs(q0, t);
+    } else {
+        const int cnt = static_cast<int>(a.n_rows - w0 < window ? a.n_rows - w0 : window);
+        const int words = (cnt + 31) / 32;
+        // the targets of several words at once: their latency is the window's start-up
+        constexpr int NWARP = kLpThreads / 32, U = 13;
+        for (int base = warp; base < words; base += U * NWARP) {
+            int64_t t[U];
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                const int at = (base + i * NWARP) * 32 + lane;
+                t[i] = at < cnt ? load_target(a.target, a.tgt32, w0 + at) : -1;
+            }
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                const int wd = base + i * NWARP;
+                if (wd < words) {
+                    const uint32_t m = __ballot_sync(0xffffffffu, wd * 32 + lane < cnt && row_live(w0 + wd * 32 + lane, t[i]));
+                    if (lane == 0) S.mask[wd] = m;
+                }
+            }
+        }
+        __syncthreads();
+        if (warp == 0) {
+            constexpr int PER = kLpWindow / 32 / 32;  // words of a lane
+            int c[PER], sum = 0;
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                const int wd = lane * PER + i;
+                c[i] = sum;
+                sum += wd < words ? __popc(S.mask[wd]) : 0;
+            }
+            int incl = sum;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const int o = __shfl_up_sync(0xffffffffu, incl, off);
+                if (lane >= off) incl += o;
+            }
+#pragma unroll
+            for (int i = 0; i < PER; ++i) S.before[lane * PER + i] = incl - sum + c[i];
+            if (lane == 31) {
+                // this cluster's rows have the ranks q0, q0 + nq, ... among each kind
+                const int q = static_cast<int>(q0), n = static_cast<int>(nq), live = incl, dead = cnt - incl;
+                S.n_live = q < live ? (live - q - 1) / n + 1 : 0;
+                S.n_dead = q < dead ? (dead - q - 1) / n + 1 : 0;
+            }
+        }
+        __syncthreads();
+        for (int wd = warp; wd < words; wd += kLpThreads / 32) {
+            const int i = wd * 32 + lane;
+            const uint32_t m = S.mask[wd];
+            const int lr = S.before[wd] + __popc(m & ((1u << lane) - 1u));
+            const bool live = (m >> lane) & 1u;
+            const uint32_t r = live ? lr : i - lr;
+            const uint32_t at = r / static_cast<uint32_t>(nq);
+            if (i < cnt && r - at * static_cast<uint32_t>(nq) == static_cast<uint32_t>(q0)) {
+                (live ? S.live : S.dead)[at] = static_cast<int>(w0) + i;
+                if (!live && rank == 0) dead_outputs(w0 + i, load_target(a.target, a.tgt32, w0 + i));
+            }
+        }
+        __syncthreads();
+        n_live = S.n_live;
+        n_dead = POLICY ? S.n_dead : 0;
+    }
+    const auto live_row = [&](int i) { return single ? q0 : static_cast<int64_t>(S.live[i]); };
+    const auto dead_row = [&](int i) { return single ? q0 : static_cast<int64_t>(S.dead[i]); };
+
     if (warp == kLpWarps) {
         // -------------------------------------------------------------- producer
         if (lane == 0) {
             const uint64_t drop = policy_evict_first(), hold = policy_keep(), normal = createpolicy_normal();
-            uint32_t it = 0;
-            int64_t t_next = q0 < a.n_rows ? load_target(a.target, a.tgt32, q0) : 0;
-            for (int64_t row = q0; row < a.n_rows; row += nq) {
-                const int64_t t = t_next;
-                if (row + nq < a.n_rows) t_next = load_target(a.target, a.tgt32, row + nq);
-                if (!row_live(row, t)) continue;
+            for (int li = 0; li < n_live; ++li) {
+                const int64_t row = live_row(li);
                 const char *slice = xbase + row * xstep;
                 const RowGeom gm = row_geom<KB>(slice, lo, L);
                 const char *src = slice + gm.nhead * KB;
@@ -219,11 +322,6 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtasPerSm) lp_rows_kernel(LpArg
                     }
                 }
             }
-            // drain: every issued copy has landed before the CTA may exit
-            for (uint32_t i = 0; i < kLpSlots && i < it; ++i) {
-                const uint32_t c = it - 1 - i;
-                mbar_wait_bounded<false, kStreamSleepP>(smem_u32(&S.full[c % kLpSlots]), (c / kLpSlots) & 1u, abort);
-            }
         }
         __syncwarp();
     } else if (warp == kLpWarps + 1) {
@@ -232,15 +330,9 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtasPerSm) lp_rows_kernel(LpArg
         // row's scalars, writes its results and hands the gradient's scalars back,
         // so that in the forward the consumers go on with the next row meanwhile.
         const float k = a.k;
-        bool have_norm = false;
-        float w_sum = 0.f;
-        double cta_sum = 0.0;  // this cluster's row losses (lane 0 of its first CTA)
-        uint32_t j = 0;
-        int64_t t_next = q0 < a.n_rows ? load_target(a.target, a.tgt32, q0) : 0;
-        for (int64_t row = q0; row < a.n_rows; row += nq) {
-            const int64_t t = t_next;
-            if (row + nq < a.n_rows) t_next = load_target(a.target, a.tgt32, row + nq);
-            if (!row_live(row, t)) continue;
+        for (int li = 0; li < n_live; ++li) {
+            const int64_t row = live_row(li);
+            const int64_t t = load_target(a.target, a.tgt32, row);
             PolicyIn in{};
             if (POLICY) in = policy_load(a, row);
             const uint32_t rp = j & 1u, ph = (j >> 1) & 1u;
@@ -307,53 +399,13 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtasPerSm) lp_rows_kernel(LpArg
                 if (a.row_stats) a.row_stats[row] = make_float4(r.logp, ENT ? r.entropy : 0.f, o.ratio, o.kl);
             }
         }
-        // ---------------------------------------------------- batch loss (last cluster)
-        if (POLICY && a.reduction != CE_RED_NONE && rank == 0) {
-            if (!have_norm) pdl_wait();
-            unsigned last = 0;
-            if (lane == 0) {
-                a.part[q0] = cta_sum;
-                __threadfence();
-                last = atomicAdd(&a.ctl->done, 1u) == static_cast<unsigned>(nq) - 1u ? 1u : 0u;
-            }
-            if (__shfl_sync(0xffffffffu, last, 0)) {
-                __threadfence();
-                double sum = 0.0;  // in cluster order, then a fixed tree
-                for (int64_t i = lane; i < nq; i += 32) sum += __ldcg(a.part + i);
-#pragma unroll
-                for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-                if (a.reduction == CE_RED_MEAN) {
-                    const float w_all = a.ctl->w_y;
-                    sum = w_all != 0.f ? sum / static_cast<double>(w_all) : 0.0;
-                }
-                if (lane == 0) a.loss[0] = static_cast<float>(sum);
-            }
-        }
     } else {
         // -------------------------------------------------------------- consumers
         const float k = a.k;
-        uint32_t it = 0, j = 0;  // ring position; live rows done (parities)
-        int64_t t_next = q0 < a.n_rows ? load_target(a.target, a.tgt32, q0) : 0;
-        for (int64_t row = q0; row < a.n_rows; row += nq) {
-            const int64_t t = t_next;
-            if (row + nq < a.n_rows) t_next = load_target(a.target, a.tgt32, row + nq);
-            if (!row_live(row, t)) {
-                const bool writer = tid == 0 && rank == 0;
-                if (POLICY) {
-                    lp_zero_span<DT>(gbase + row * gstep, 0, L, tid, NCT);
-                    if (writer) {
-                        if (a.reduction == CE_RED_NONE) a.loss[row] = 0.f;
-                        if (a.row_stats) a.row_stats[row] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    }
-                } else if (writer) {
-                    // ignored: 0; a target outside [0, vocab): NaN (0 inside the preference loss, which flags it)
-                    const float none = t == a.ignore_index || a.offsets ? 0.f : NAN;
-                    if (a.logp) a.logp[row] = none;
-                    if (a.entropy) a.entropy[row] = none;
-                    if (a.stats) a.stats[row] = make_float4(0.f, 0.f, 0.f, 0.f);
-                }
-                continue;
-            }
+        int64_t t_next = n_live > 0 ? load_target(a.target, a.tgt32, live_row(0)) : 0;
+        for (int li = 0; li < n_live; ++li) {
+            const int64_t row = live_row(li), t = t_next;
+            if (li + 1 < n_live) t_next = load_target(a.target, a.tgt32, live_row(li + 1));
             const char *xrow = xbase + row * xstep;
             const RowGeom gm = row_geom<KB>(xrow, lo, L);
             const int nvec = gm.nvec, nch = gm.nch, nedge = gm.nhead + gm.ntail;
@@ -481,6 +533,41 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtasPerSm) lp_rows_kernel(LpArg
                 const int c = tid < nh ? tid : tail0 - trail + (tid - nh);
                 F::store1(grow, c, c == yc ? g.dy : lp_grad_elem<ENT>(g, F::load1(xrow, c), k));
             }
+            // one of the rows that take no part, between two that do
+            if (li < n_dead) zero_row(dead_row(li));
+        }
+        if (POLICY)
+            for (int di = n_live; di < n_dead; ++di) zero_row(dead_row(di));
+    }
+    if (!single && w0 + window < a.n_rows) __syncthreads();  // the lists are rebuilt
+    }
+    if (warp == kLpWarps && lane == 0) {
+        // drain: every issued copy has landed before the CTA may exit
+        for (uint32_t i = 0; i < kLpSlots && i < it; ++i) {
+            const uint32_t c = it - 1 - i;
+            mbar_wait_bounded<false, kStreamSleepP>(smem_u32(&S.full[c % kLpSlots]), (c / kLpSlots) & 1u, abort);
+        }
+    }
+    // ---------------------------------------------------- batch loss (last cluster)
+    if (POLICY && warp == kLpWarps + 1 && a.reduction != CE_RED_NONE && rank == 0) {
+        if (!have_norm) pdl_wait();
+        unsigned last = 0;
+        if (lane == 0) {
+            a.part[q0] = cta_sum;
+            __threadfence();
+            last = atomicAdd(&a.ctl->done, 1u) == static_cast<unsigned>(nq) - 1u ? 1u : 0u;
+        }
+        if (__shfl_sync(0xffffffffu, last, 0)) {
+            __threadfence();
+            double sum = 0.0;  // in cluster order, then a fixed tree
+            for (int64_t i = lane; i < nq; i += 32) sum += __ldcg(a.part + i);
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+            if (a.reduction == CE_RED_MEAN) {
+                const float w_all = a.ctl->w_y;
+                sum = w_all != 0.f ? sum / static_cast<double>(w_all) : 0.0;
+            }
+            if (lane == 0) a.loss[0] = static_cast<float>(sum);
         }
     }
     __syncthreads();
