@@ -142,6 +142,34 @@ __device__ inline void grad_vec(const LpGrad &g, float c, const float *x, float 
     }
 }
 
+// Where one row's slice of L columns sits against 16-byte boundaries, in 32-bit
+// arithmetic (it is formed once a row by every thread): columns before the
+// first, vectors from there, columns after the last.
+struct LpGeom {
+    int head, nvec, tail0, nch;
+};
+template <int KB>
+__device__ inline LpGeom lp_geom(const char *slice, int L) {
+    LpGeom g;
+    g.head = min(static_cast<int>((16u - (static_cast<uint32_t>(reinterpret_cast<uintptr_t>(slice)) & 15u)) & 15u) / KB, L);
+    g.nvec = (L - g.head) / (16 / KB);
+    g.tail0 = g.head + g.nvec * (16 / KB);
+    g.nch = (g.nvec + kStreamChunk / 16 - 1) / (kStreamChunk / 16);
+    return g;
+}
+
+// A position in the ring: slots are used one after the other, phase changes
+// with every round.
+struct RingPos {
+    uint32_t slot, phase;
+    __device__ inline void next() {
+        if (++slot == kLpSlots) {
+            slot = 0;
+            phase ^= 1u;
+        }
+    }
+};
+
 template <int DT, int MODE, bool ENT>
 __global__ void __launch_bounds__(kLpThreads, kLpCtasPerSm) lp_rows_kernel(LpArgs a) {
     using F = Fmt<DT>;
@@ -205,7 +233,9 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtasPerSm) lp_rows_kernel(LpArg
     // built by the whole CTA from one read of the targets.
     const bool single = a.n_rows <= nq;
     const int64_t window = single ? a.n_rows : (kLpList * nq < kLpWindow ? kLpList * nq : kLpWindow);
-    uint32_t it = 0, j = 0;  // ring position (producer and consumers); live rows done (their parities)
+    RingPos pos{0u, 0u};     // producer and consumers
+    uint32_t issued = 0;     // producer: copies so far
+    uint32_t j = 0;          // live rows done (their parities)
     bool have_norm = false;  // scalar warp: the batch's weight sum, this cluster's row losses (lane 0 of its first CTA)
     float w_sum = 0.f;
     double cta_sum = 0.0;
@@ -304,21 +334,23 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtasPerSm) lp_rows_kernel(LpArg
             for (int li = 0; li < n_live; ++li) {
                 const int64_t row = live_row(li);
                 const char *slice = xbase + row * xstep;
-                const RowGeom gm = row_geom<KB>(slice, lo, L);
-                const char *src = slice + gm.nhead * KB;
+                const LpGeom gm = lp_geom<KB>(slice, L);
+                const char *src = slice + gm.head * KB;
                 const int nkeep = POLICY ? min(gm.nch, kLpSlots) : 0;
                 for (int pass = 0; pass < (POLICY ? 2 : 1); ++pass) {
                     const int nc = pass == 0 ? gm.nch : gm.nch - nkeep;
-                    for (int i = 0; i < nc; ++i, ++it) {
+                    for (int i = 0; i < nc; ++i) {
                         const int c = pass == 0 ? i : nc - 1 - i;
                         const uint64_t pol = pass == 1 ? drop : (c < gm.nch - nkeep && POLICY ? hold : normal);
-                        const uint32_t s = it % kLpSlots, r = it / kLpSlots;
-                        if (r > 0) mbar_wait_bounded<false, kStreamSleepP>(smem_u32(&S.empty[s]), (r - 1) & 1u, abort);
-                        const int64_t off = static_cast<int64_t>(c) * kStreamChunk;
-                        const uint32_t bytes =
-                            static_cast<uint32_t>(gm.bytes - off < kStreamChunk ? gm.bytes - off : kStreamChunk);
-                        mbar_expect_tx(smem_u32(&S.full[s]), bytes);
-                        bulk_g2s_hint(ring + s * kStreamChunk, src + off, bytes, smem_u32(&S.full[s]), pol);
+                        const uint32_t full = smem_u32(&S.full[pos.slot]);
+                        if (issued >= kLpSlots)
+                            mbar_wait_bounded<false, kStreamSleepP>(smem_u32(&S.empty[pos.slot]), pos.phase ^ 1u, abort);
+                        const uint32_t bytes = 16u * static_cast<uint32_t>(min(VPC, gm.nvec - c * VPC));
+                        mbar_expect_tx(full, bytes);
+                        bulk_g2s_hint(ring + pos.slot * kStreamChunk, src + static_cast<int64_t>(c) * kStreamChunk, bytes, full,
+                                      pol);
+                        pos.next();
+                        ++issued;
                     }
                 }
             }
@@ -407,49 +439,56 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtasPerSm) lp_rows_kernel(LpArg
             const int64_t row = live_row(li), t = t_next;
             if (li + 1 < n_live) t_next = load_target(a.target, a.tgt32, live_row(li + 1));
             const char *xrow = xbase + row * xstep;
-            const RowGeom gm = row_geom<KB>(xrow, lo, L);
-            const int nvec = gm.nvec, nch = gm.nch, nedge = gm.nhead + gm.ntail;
-            const int vlo = static_cast<int>(gm.vlo) - lo, tail0 = static_cast<int>(gm.tail0) - lo;
+            const LpGeom gm = lp_geom<KB>(xrow, L);
+            const int nvec = gm.nvec, nch = gm.nch, vlo = gm.head, tail0 = gm.tail0, nedge = vlo + L - tail0;
             const int yc = static_cast<int>(t) - lo;  // target column of the slice (it may lie outside)
             const int y = yc >= vlo && yc < tail0 ? yc - vlo : -1;
+            // the chunk in which this thread holds the target's vector
+            const int y_chunk = y >= 0 && (y / VEC) % NCT == tid ? y / VEC / VPC : -1;
             const int nkeep = POLICY ? min(nch, kLpSlots) : 0;
-            const uint32_t rp = j & 1u, it_row = it;
+            const uint32_t rp = j & 1u;
             // (the policy loss's wait for its gradient scalars has covered this)
             if (!POLICY && j > 1)
                 mbar_wait_bounded<false, kStreamSleepConsumer>(smem_u32(&S.taken[rp]), ((j >> 1) - 1u) & 1u, abort);
             // ------------------------------------------------ pass 1: statistics
             LpState st = lp_empty();
-            uint32_t held = 0;
-            for (int c = 0; c < nch; ++c, ++it) {
-                const uint32_t s = it % kLpSlots;
-                mbar_wait_bounded<false, kStreamSleepConsumer>(smem_u32(&S.full[s]), (it / kLpSlots) & 1u, abort);
-                const uint32_t base_s = ring + s * kStreamChunk;
-                const int v0 = c * VPC, nv = min(VPC, nvec - v0);
-                const int vy = y >= 0 ? y / VEC - v0 : -1;
-                if (vy >= 0 && vy < nv && vy % NCT == tid) {
+            uint32_t held = 0, keep_slot = 0;  // the first kept chunk's slot
+            for (int c = 0; c < nch; ++c) {
+                if (c == nch - nkeep) keep_slot = pos.slot;
+                mbar_wait_bounded<false, kStreamSleepConsumer>(smem_u32(&S.full[pos.slot]), pos.phase, abort);
+                const uint32_t base_s = ring + pos.slot * kStreamChunk, mine = base_s + 16u * tid;
+                const int nv = min(VPC, nvec - c * VPC);
+                if (c == y_chunk) {
                     // the target's column leaves the chunk: this thread alone reads its vector
-                    S.xy[rp] = take_out<DT>(base_s + 16u * vy + static_cast<uint32_t>(y % VEC) * KB);
+                    S.xy[rp] = take_out<DT>(base_s + static_cast<uint32_t>(y - c * VPC * VEC) * KB);
                     fence_async_shared();  // before a copy may overwrite the slot
                 }
                 bool plain = true;
                 if (nv == VPC) {
                     uint4 raw[VPT];
 #pragma unroll
-                    for (int i = 0; i < VPT; ++i) raw[i] = ld_shared_v4(base_s + 16u * (tid + i * NCT));
+                    for (int i = 0; i < VPT; ++i) raw[i] = ld_shared_v4(mine + 16u * i * NCT);
                     plain = add_or_clamp<DT, ENT, VPT>(st, raw, k);
                 } else {
-                    for (int v = tid; v < nv; v += NCT) {
-                        const uint4 raw[1] = {ld_shared_v4(base_s + 16u * v)};
+                    // the row's last chunk: vectors that every thread has in pairs, then the others
+                    int v = 0;
+                    for (; v + 2 * NCT <= nv; v += 2 * NCT) {
+                        const uint4 raw[2] = {ld_shared_v4(mine + 16u * v), ld_shared_v4(mine + 16u * (v + NCT))};
+                        plain = add_or_clamp<DT, ENT, 2>(st, raw, k) && plain;
+                    }
+                    for (; v + tid < nv; v += NCT) {
+                        const uint4 raw[1] = {ld_shared_v4(mine + 16u * v)};
                         plain = add_or_clamp<DT, ENT, 1>(st, raw, k) && plain;
                     }
                 }
                 // chunks whose exponents the second pass has to hold as well (31: any later one)
                 if (POLICY && ENT && !plain) held |= 1u << min(c, 31);
                 __syncwarp();
-                if (lane == 0 && c < nch - nkeep) mbar_arrive(smem_u32(&S.empty[s]));
+                if (lane == 0 && c < nch - nkeep) mbar_arrive(smem_u32(&S.empty[pos.slot]));
+                pos.next();
             }
             // columns before the first and after the last 16-byte boundary
-            const int edge_c = tid < gm.nhead ? tid : tail0 + (tid - gm.nhead);
+            const int edge_c = tid < vlo ? tid : tail0 + (tid - vlo);
             if (tid < nedge) {
                 const float x = F::load1(xrow, edge_c);
                 if (edge_c == yc) S.xy[rp] = x;
@@ -481,16 +520,19 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtasPerSm) lp_rows_kernel(LpArg
                     // the kept chunks, from the slots the first pass filled, then the earlier ones
                     const bool in_ring = i < nkeep;
                     const int c = in_ring ? nch - nkeep + i : nch - 1 - i;
-                    const uint32_t s = (in_ring ? it_row + static_cast<uint32_t>(c) : it) % kLpSlots;
-                    if (!in_ring) {
-                        mbar_wait_bounded<false, kStreamSleepConsumer>(smem_u32(&S.full[s]), (it / kLpSlots) & 1u, abort);
-                        ++it;
+                    const uint32_t s = in_ring ? keep_slot : pos.slot;
+                    if (in_ring) {
+                        if (++keep_slot == kLpSlots) keep_slot = 0;
+                    } else {
+                        mbar_wait_bounded<false, kStreamSleepConsumer>(smem_u32(&S.full[s]), pos.phase, abort);
+                        pos.next();
                     }
                     const uint32_t base_s = ring + s * kStreamChunk;
                     const int v0 = c * VPC, nv = min(VPC, nvec - v0);
                     if (mis != 0) {
                         // vector o of the gradient is the last mis bytes of the logits' vector o and
                         // the first 16 - mis of o + 1 (past the chunk's end read from L2)
+#pragma unroll 2
                         for (int v = tid; v < nv && v0 + v + 1 < nvec; v += NCT) {
                             const uint4 r0 = ld_shared_v4(base_s + 16u * v);
                             const uint4 r1 = v + 1 < nv ? ld_shared_v4(base_s + 16u * (v + 1))
@@ -501,13 +543,26 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtasPerSm) lp_rows_kernel(LpArg
                             st_stream(gv + 16 * static_cast<int64_t>(v0 + v) + (16u - mis), F::pack(og));
                         }
                     } else if (!((held >> min(c, 31)) & 1u)) {
-                        for (int v = tid; v < nv; v += NCT) {
-                            float x[VEC], og[VEC];
-                            F::unpack(ld_shared_v4(base_s + 16u * v), x);
-                            grad_vec<DT, E, false>(g, cexp, x, k, og);
-                            st_stream(vp + v0 + v, F::pack(og));
+                        uint4 *const out = vp + v0 + tid;
+                        if (nv == VPC) {
+#pragma unroll
+                            for (int i = 0; i < VPT; ++i) {
+                                float x[VEC], og[VEC];
+                                F::unpack(ld_shared_v4(base_s + 16u * tid + 16u * i * NCT), x);
+                                grad_vec<DT, E, false>(g, cexp, x, k, og);
+                                st_stream(out + i * NCT, F::pack(og));
+                            }
+                        } else {
+#pragma unroll 1
+                            for (int v = 0; v + tid < nv; v += NCT) {
+                                float x[VEC], og[VEC];
+                                F::unpack(ld_shared_v4(base_s + 16u * (tid + v)), x);
+                                grad_vec<DT, E, false>(g, cexp, x, k, og);
+                                st_stream(out + v, F::pack(og));
+                            }
                         }
                     } else {
+#pragma unroll 1
                         for (int v = tid; v < nv; v += NCT) {
                             float x[VEC], og[VEC];
                             F::unpack(ld_shared_v4(base_s + 16u * v), x);
@@ -528,7 +583,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtasPerSm) lp_rows_kernel(LpArg
             const int trail = mis != 0 && nvec > 0 ? static_cast<int>(mis) / KB : 0;
             const int yo = y - lead;
             if (y >= 0 && yo >= 0 && y < nvec * VEC - trail && (yo / VEC) % NCT == tid) F::store1(grow, vlo + y, g.dy);
-            const int nh = gm.nhead + lead, ne = nh + trail + gm.ntail;
+            const int nh = vlo + lead, ne = nh + trail + L - tail0;
             if (tid < ne) {
                 const int c = tid < nh ? tid : tail0 - trail + (tid - nh);
                 F::store1(grow, c, c == yc ? g.dy : lp_grad_elem<ENT>(g, F::load1(xrow, c), k));
@@ -543,9 +598,14 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtasPerSm) lp_rows_kernel(LpArg
     }
     if (warp == kLpWarps && lane == 0) {
         // drain: every issued copy has landed before the CTA may exit
-        for (uint32_t i = 0; i < kLpSlots && i < it; ++i) {
-            const uint32_t c = it - 1 - i;
-            mbar_wait_bounded<false, kStreamSleepP>(smem_u32(&S.full[c % kLpSlots]), (c / kLpSlots) & 1u, abort);
+        for (uint32_t i = 0; i < kLpSlots && i < issued; ++i) {
+            // the last copy of each used slot, latest first
+            if (pos.slot == 0) {
+                pos.slot = kLpSlots;
+                pos.phase ^= 1u;
+            }
+            --pos.slot;
+            mbar_wait_bounded<false, kStreamSleepP>(smem_u32(&S.full[pos.slot]), pos.phase, abort);
         }
     }
     // ---------------------------------------------------- batch loss (last cluster)
