@@ -68,10 +68,11 @@ __device__ inline float take_out(uint32_t addr) {
 // mu's rounding shifted (the same for every term) is taken out of the chunk's
 // sums, so the sums are as exact as those of (x - m) k. With the entropy, a
 // logit that is -inf (or so low that a' overflows) makes 0 * inf = NaN in u:
-// false is returned then, and where mu is not finite, with st moved to the new
-// maximum but nothing added; lp_add takes such vectors.
-template <int DT, bool ENT, int NV>
-__device__ inline bool add_vectors(LpState &st, const uint4 (&raw)[NV], float k) {
+// without CLAMP false is returned then, with st moved to the new maximum but
+// nothing added; with it exponents are held at kLpMinExp, and `low` counts
+// them. Either returns false where mu is not finite.
+template <int DT, bool ENT, int NV, bool CLAMP>
+__device__ inline bool add_vectors(LpState &st, const uint4 (&raw)[NV], float k, int &low) {
     using F = Fmt<DT>;
     constexpr int VEC = F::kVec;
     float cm = F::vmax(raw[0]);
@@ -88,7 +89,15 @@ __device__ inline bool add_vectors(LpState &st, const uint4 (&raw)[NV], float k)
         F::unpack(raw[i], x);
 #pragma unroll
         for (int p = 0; p < VEC / 2; ++p) {
-            const F2 e = f2_fma(f2(x[2 * p], x[2 * p + 1]), kk, nm);
+            F2 e = f2_fma(f2(x[2 * p], x[2 * p + 1]), kk, nm);
+            if (CLAMP) {
+                float a0, a1;
+                f2_split(e, a0, a1);
+                a0 = lp_clamp(a0);
+                a1 = lp_clamp(a1);
+                low += (a0 == kLpMinExp ? 1 : 0) + (a1 == kLpMinExp ? 1 : 0);
+                e = f2(a0, a1);
+            }
             const F2 ex = f2_ex2(e);
             s2[p & 1] = f2_add(s2[p & 1], ex);
             if (ENT) u2[p & 1] = f2_fma(ex, e, u2[p & 1]);
@@ -100,15 +109,25 @@ __device__ inline bool add_vectors(LpState &st, const uint4 (&raw)[NV], float k)
     if (ENT) {
         f2_split(f2_add(u2[0], u2[1]), u0, u1);
         const float uc = u0 + u1;
-        if (uc != uc) return false;
+        if (!CLAMP && uc != uc) return false;
         st.u = fmaf(fmaf(-shift, sc, uc), f, st.u);
     }
     st.s = fmaf(sc, f, st.s);
     return true;
 }
+
+// The same for any vectors. y_warp: one of the warp's lanes holds the row's
+// target column among them, set to -inf (own: this one), so that the warp takes
+// the held exponents at once instead of one lane after the others. Returns
+// whether the second pass needs no held exponents for these vectors (the
+// target's column it writes apart).
 template <int DT, bool ENT, int NV>
-__device__ inline bool add_or_clamp(LpState &st, const uint4 (&raw)[NV], float k) {
-    if (add_vectors<DT, ENT, NV>(st, raw, k)) return true;
+__device__ inline bool add_any(LpState &st, const uint4 (&raw)[NV], float k, bool y_warp, bool own) {
+    int low = 0;
+    if (!(ENT && y_warp) && add_vectors<DT, ENT, NV, false>(st, raw, k, low)) return true;
+    if constexpr (ENT) {
+        if (add_vectors<DT, ENT, NV, true>(st, raw, k, low)) return low <= (own ? 1 : 0);
+    }
 #pragma unroll 1
     for (int i = 0; i < NV; ++i) {
         uint4 r = raw[0];
@@ -443,8 +462,9 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtasPerSm) lp_rows_kernel(LpArg
             const int nvec = gm.nvec, nch = gm.nch, vlo = gm.head, tail0 = gm.tail0, nedge = vlo + L - tail0;
             const int yc = static_cast<int>(t) - lo;  // target column of the slice (it may lie outside)
             const int y = yc >= vlo && yc < tail0 ? yc - vlo : -1;
-            // the chunk in which this thread holds the target's vector
-            const int y_chunk = y >= 0 && (y / VEC) % NCT == tid ? y / VEC / VPC : -1;
+            // the chunk with the target's column, for the warp that reads its vector
+            const int y_thread = y >= 0 ? (y / VEC) % NCT : -32;
+            const int y_chunk = y_thread / 32 == warp ? y / VEC / VPC : -1;
             const int nkeep = POLICY ? min(nch, kLpSlots) : 0;
             const uint32_t rp = j & 1u;
             // (the policy loss's wait for its gradient scalars has covered this)
@@ -458,7 +478,8 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtasPerSm) lp_rows_kernel(LpArg
                 mbar_wait_bounded<false, kStreamSleepConsumer>(smem_u32(&S.full[pos.slot]), pos.phase, abort);
                 const uint32_t base_s = ring + pos.slot * kStreamChunk, mine = base_s + 16u * tid;
                 const int nv = min(VPC, nvec - c * VPC);
-                if (c == y_chunk) {
+                const bool y_warp = c == y_chunk, own = y_warp && y_thread == tid;
+                if (own) {
                     // the target's column leaves the chunk: this thread alone reads its vector
                     S.xy[rp] = take_out<DT>(base_s + static_cast<uint32_t>(y - c * VPC * VEC) * KB);
                     fence_async_shared();  // before a copy may overwrite the slot
@@ -468,17 +489,18 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtasPerSm) lp_rows_kernel(LpArg
                     uint4 raw[VPT];
 #pragma unroll
                     for (int i = 0; i < VPT; ++i) raw[i] = ld_shared_v4(mine + 16u * i * NCT);
-                    plain = add_or_clamp<DT, ENT, VPT>(st, raw, k);
+                    plain = add_any<DT, ENT, VPT>(st, raw, k, y_warp, own);
                 } else {
                     // the row's last chunk: vectors that every thread has in pairs, then the others
+                    const int yv = own ? y / VEC - c * VPC - tid : -1;  // which of this thread's vectors
                     int v = 0;
                     for (; v + 2 * NCT <= nv; v += 2 * NCT) {
                         const uint4 raw[2] = {ld_shared_v4(mine + 16u * v), ld_shared_v4(mine + 16u * (v + NCT))};
-                        plain = add_or_clamp<DT, ENT, 2>(st, raw, k) && plain;
+                        plain = add_any<DT, ENT, 2>(st, raw, k, y_warp, yv == v || yv == v + NCT) && plain;
                     }
                     for (; v + tid < nv; v += NCT) {
                         const uint4 raw[1] = {ld_shared_v4(mine + 16u * v)};
-                        plain = add_or_clamp<DT, ENT, 1>(st, raw, k) && plain;
+                        plain = add_any<DT, ENT, 1>(st, raw, k, y_warp, yv == v) && plain;
                     }
                 }
                 // chunks whose exponents the second pass has to hold as well (31: any later one)

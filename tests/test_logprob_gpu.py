@@ -148,6 +148,38 @@ def test_token_logprob_special_rows(ce, dtype):
     assert grad[nan].isnan().any(1).all()
 
 
+@pytest.mark.parametrize("v", [5003, 8192, 32000, 50257])
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("share", [0.0005, 0.3])
+def test_scattered_masked_columns(ce, v, dtype, share):
+    """-inf anywhere in the rows, beside the target's vector as well: probability
+    and gradient exactly 0 there, everything else as the fp64 form has it."""
+    n, dt = 24, DT[dtype]
+    g, _, x, t = make(n, v, dtype, v + int(share * 1e4), ignored=0.1)
+    off = torch.rand(n, v, generator=g, device="cuda") < share
+    rows = torch.arange(n, device="cuda")
+    for d in range(1, 9):       # some of the target's neighbours
+        off[rows[d % 3::3], (t[d % 3::3].long().clamp_min(0) + d) % v] = True
+    off[rows, t.long().clamp_min(0)] = False
+    x[off] = -math.inf
+    valid, logq, want, want_h = L.rows_ref(x, t)
+    d = L.delta(x)
+    logp, ent, stats = ce.ce_token_logprob(x, t)
+    L.check(logp, want, L.tol_logp(d, want) * valid, "logp")
+    L.check(ent, want_h, L.tol_entropy(d, want_h) * valid, "entropy")
+    gl, gh, z = rnd(g, n), rnd(g, n), torch.zeros(n, device="cuda")
+    ref = L.grad_ref(logq, valid, t, gl, gh)
+    tol = L.tol_grad(x, ref, logq, valid, t, gl, gh, z, z, dt)
+    grad = ce.ce_token_logprob_backward(x, t, stats, gl, grad_entropy=gh, grad=torch.empty_like(x))
+    L.check(grad, ref, tol, "gradient from statistics")
+    adv = rnd(g, n)
+    want = L.policy_ref(x, t, adv, None, None, None, 0.2, 0.2, 0.0, f32(0.05), 1.0, "sum", None)
+    for grad in (torch.empty_like(x), torch.empty(n, v + 1, dtype=dt, device="cuda")[:, 1:]):
+        _, grad = ce.ce_policy_fwd_bwd(x, t, adv, entropy_coef=f32(0.05), reduction="sum", grad=grad)
+        L.check(grad, want["grad"], want["tol_grad"], "policy gradient")
+        assert (grad[off & valid[:, None]] == 0).all()
+
+
 def test_token_logprob_statistics_without_entropy_refuse_its_gradient(ce):
     x, t = torch.randn(3, 100, device="cuda"), torch.zeros(3, dtype=torch.int64, device="cuda")
     _, _, stats = ce.ce_token_logprob(x, t, with_entropy=False)
