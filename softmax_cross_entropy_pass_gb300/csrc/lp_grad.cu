@@ -9,35 +9,48 @@ namespace ce {
 // ------------------------------------------------------------------ policy normalisers
 constexpr int kLpPrepThreads = 1024;
 
-// One block: how many rows take part, the sum of their weights (fp64, fixed
-// order), and the target check. It lets the row kernel start at once; that
-// kernel waits for it where it reads the sum.
+// Up to kPrepParts blocks, each over its share of the rows: the sum of the
+// weights of those that take part (fp64, fixed order) and the target check, to
+// the control block; the row kernel adds the blocks up. It may start at once
+// and waits for this kernel where it reads the sums. Eight rows in flight a
+// thread: with one, 60000 rows took longer here than their 1000-column rows.
 __global__ void __launch_bounds__(kLpPrepThreads) lp_prep_kernel(LpArgs a) {
     pdl_launch_dependents();
     __shared__ double sh_w[kLpPrepThreads / 32];
-    __shared__ unsigned sh_bad;
+    constexpr int U = 8;
     const int tid = threadIdx.x;
-    if (tid == 0) sh_bad = 0;
-    __syncthreads();
     double w = 0.0;
     bool bad = false;
-    for (int64_t i = tid; i < a.n_rows; i += kLpPrepThreads) {
-        const int64_t t = load_target(a.target, a.tgt32, i);
-        if (target_valid(t, a.ignore_index, a.vocab)) w += a.row_weight ? static_cast<double>(__ldg(a.row_weight + i)) : 1.0;
-        else if (t != a.ignore_index) bad = true;
+    for (int64_t base = static_cast<int64_t>(blockIdx.x) * kLpPrepThreads + tid; base < a.n_rows;
+         base += static_cast<int64_t>(U) * gridDim.x * kLpPrepThreads) {
+        int64_t t[U];
+        float wt[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int64_t r = base + static_cast<int64_t>(i) * gridDim.x * kLpPrepThreads;
+            t[i] = r < a.n_rows ? load_target(a.target, a.tgt32, r) : a.ignore_index;
+            wt[i] = a.row_weight && r < a.n_rows ? __ldg(a.row_weight + r) : 1.f;
+        }
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            if (target_valid(t[i], a.ignore_index, a.vocab)) w += static_cast<double>(wt[i]);
+            else if (t[i] != a.ignore_index) bad = true;
+        }
     }
-    if (bad) atomicOr(&sh_bad, 1u);
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) w += __shfl_xor_sync(0xffffffffu, w, off);
     if ((tid & 31) == 0) sh_w[tid >> 5] = w;
-    __syncthreads();
+    const int any_bad = __syncthreads_or(bad);
     if (tid == 0) {
         double sum = 0.0;
         for (int i = 0; i < kLpPrepThreads / 32; ++i) sum += sh_w[i];
-        a.ctl->done = 0u;
-        a.ctl->w_y = static_cast<float>(sum);
-        a.ctl->status = (sh_bad ? CE_FLAG_TARGET_OUT_OF_RANGE : 0u) |
-                        (a.reduction == CE_RED_MEAN && static_cast<float>(sum) == 0.f ? CE_FLAG_NO_VALID_ROWS : 0u);
+        a.ctl->prep_part[blockIdx.x][0] = sum;
+        a.ctl->prep_bad[blockIdx.x] = any_bad ? 1u : 0u;
+        if (blockIdx.x == 0) {
+            a.ctl->done = 0u;
+            // without rows no row kernel follows to set the bits
+            a.ctl->status = a.n_rows == 0 && a.reduction == CE_RED_MEAN ? CE_FLAG_NO_VALID_ROWS : 0u;
+        }
     }
 }
 
@@ -245,9 +258,10 @@ static cudaError_t launch_dep(const void *fn, int64_t grid, int threads, A &a, i
     return cudaLaunchKernelExC(&cfg, fn, args);
 }
 
-cudaError_t launch_lp_prep(const LpArgs &a0, cudaStream_t s) {
-    LpArgs a = a0;
-    return launch_dep(reinterpret_cast<const void *>(&lp_prep_kernel), 1, kLpPrepThreads, a, nullptr, false, s);
+cudaError_t launch_lp_prep(LpArgs &a, cudaStream_t s) {
+    const int64_t want = (a.n_rows + kLpPrepThreads - 1) / kLpPrepThreads;
+    a.n_prep = static_cast<int>(want < 1 ? 1 : (want < kPrepParts ? want : kPrepParts));
+    return launch_dep(reinterpret_cast<const void *>(&lp_prep_kernel), a.n_prep, kLpPrepThreads, a, nullptr, false, s);
 }
 
 template <int DT>

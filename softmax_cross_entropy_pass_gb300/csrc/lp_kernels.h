@@ -35,6 +35,7 @@ struct LpArgs {
     const float *grad_output;  // NULL = 1.0
     float *loss;
     double *part;              // workspace: one loss sum per CTA (cluster); preference: one loss per pair
+    int n_prep;                // blocks of the normaliser kernel
     float4 *row_stats;         // {log p, entropy, ratio, KL}
     // gradient from statistics: dL/dlogp and dL/dH (NULL: 0)
     const float *g_logp, *g_entropy;
@@ -63,9 +64,12 @@ struct PairArgs {
 enum { LP_FWD = 0, LP_POLICY = 1 };
 
 // the normalisers of the policy loss (valid rows, their weight sum) and the target check
-cudaError_t launch_lp_prep(const LpArgs &a, cudaStream_t s);
+cudaError_t launch_lp_prep(LpArgs &a, cudaStream_t s);
 // one pass over every row: log-probabilities, entropies and statistics (LP_FWD), or the policy loss and its gradient
 cudaError_t launch_lp_rows(const LpArgs &a, int dtype, int mode, bool entropy, bool after_prep, cudaStream_t s);
+// the same for rows that a group of warps holds in registers (launch_lp_rows picks it)
+bool lp_short_takes(int64_t vocab, int dtype);
+cudaError_t launch_lp_short(const LpArgs &a, int dtype, int mode, bool entropy, bool after_prep, int sms, cudaStream_t s);
 // the gradient of every row from its statistics (preference: and the batch loss)
 cudaError_t launch_lp_grad(const LpArgs &a, int dtype, bool entropy, bool dependent, cudaStream_t s);
 // sequence sums, pair losses and row coefficients of the preference loss

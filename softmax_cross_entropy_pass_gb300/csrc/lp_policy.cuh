@@ -73,6 +73,21 @@ __device__ inline PolicyOut policy_row(const LpArgs &a, const PolicyIn &in, cons
     return o;
 }
 
+// What the normaliser kernel's blocks found (after a pdl_wait): the sum of the
+// weights, added up in block order, and the status bits, which the first block
+// of the row kernel sets.
+__device__ inline float policy_weight_sum(const LpArgs &a) {
+    double s = 0.0;
+    for (int b = 0; b < a.n_prep; ++b) s += __ldcg(&a.ctl->prep_part[b][0]);
+    return static_cast<float>(s);
+}
+__device__ inline void policy_flags(const LpArgs &a) {
+    unsigned bad = 0;
+    for (int b = 0; b < a.n_prep; ++b) bad |= __ldcg(&a.ctl->prep_bad[b]);
+    const bool none = a.reduction == CE_RED_MEAN && policy_weight_sum(a) == 0.f;
+    if (bad || none) atomicOr(&a.ctl->status, (bad ? CE_FLAG_TARGET_OUT_OF_RANGE : 0u) | (none ? CE_FLAG_NO_VALID_ROWS : 0u));
+}
+
 // the gradient scale of the batch: grad_output over the weight sum for mean
 __device__ inline float policy_scale(const LpArgs &a, int64_t row, float w_sum) {
     const float up = a.grad_output ? __ldg(a.grad_output + (a.reduction == CE_RED_NONE ? row : 0)) : 1.f;

@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtasPerSm) lp_rows_kernel(LpArg
     // Otherwise the rows that take part and those that do not are dealt out
     // separately, window by window, every cluster getting the same number of each
     // (dealt together, a cluster's share of the former varies: 8192 x 128256
-    // with 30% left out ran as long as 12% more rows would). A window's lists are
+    // bf16 with 30% left out 658 us against 636). A window's lists are
     // built by the whole CTA from one read of the targets.
     const bool single = a.n_rows <= nq;
     const int64_t window = single ? a.n_rows : (kLpList * nq < kLpWindow ? kLpList * nq : kLpWindow);
@@ -436,7 +436,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtasPerSm) lp_rows_kernel(LpArg
             const PolicyOut o = policy_row(a, in, r, r.entropy);
             if (!have_norm) {
                 pdl_wait();
-                w_sum = a.ctl->w_y;
+                w_sum = policy_weight_sum(a);
                 have_norm = true;
             }
             const float scale = policy_scale(a, row, w_sum);
@@ -646,11 +646,15 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtasPerSm) lp_rows_kernel(LpArg
 #pragma unroll
             for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
             if (a.reduction == CE_RED_MEAN) {
-                const float w_all = a.ctl->w_y;
+                const float w_all = policy_weight_sum(a);
                 sum = w_all != 0.f ? sum / static_cast<double>(w_all) : 0.0;
             }
             if (lane == 0) a.loss[0] = static_cast<float>(sum);
         }
+    }
+    if (POLICY && blockIdx.x == 0 && tid == 0) {
+        pdl_wait();
+        policy_flags(a);
     }
     __syncthreads();
     if (tid == 0 && S.abort && a.ctl) {
@@ -720,13 +724,19 @@ cudaError_t launch_lp_rows(const LpArgs &a0, int dtype, int mode, bool entropy, 
     int clusters = 0, sms = 0;
     cudaError_t e = rows_ready(fn, 1, &clusters, &sms);
     if (e != cudaSuccess) return e;
+    // Rows of up to 16 KB: a group of warps a row (GB300, 8192 rows with the
+    // entropy, forward / policy: 2 KB rows 17 / 39 us against 39 / 91 here, 8 KB
+    // 27 / 58 against 46 / 108, 16 KB 48 / 95 against 57 / 137; at 32 KB, with
+    // groups of eight warps, 80 / 192 against 74 / 166).
+    if (lp_short_takes(a.vocab, dtype)) return launch_lp_short(a, dtype, mode, entropy, after_prep, sms, s);
     const int64_t slots = static_cast<int64_t>(sms) * kLpCtasPerSm;
     int cl = 1;
     // Two passes over many rows: the rows in flight, whose first chunks wait in
     // L2 for the second pass, kept to 60 MB (GB300, L2 flushed, with the
-    // entropy: 8192 x 128256 bf16 one CTA a row 709 us, pairs 686, quads 781;
-    // 4096 x 256000 891, 769, 773; 2048 x 128256 fp32 438, 389, 354; below the
-    // limit 8192 x 64000 364, 467, 647 and 8192 x 32000 220, 324, 481).
+    // entropy, 30% of the first's rows left out: 8192 x 128256 bf16 one CTA a
+    // row 709 us, pairs 686, quads 781; 4096 x 256000 891, 769, 773; 2048 x
+    // 128256 fp32 438, 389, 354; below the limit 8192 x 64000 364, 467, 647 and
+    // 8192 x 32000 220, 324, 481).
     if (mode == LP_POLICY && a.n_rows > slots)
         while (cl < kLpMaxCluster && slots / cl * row_bytes > (int64_t(60) << 20)) cl *= 2;
     // Few rows: split over more CTAs while all rows still run at once, down to
