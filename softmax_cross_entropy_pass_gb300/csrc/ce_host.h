@@ -9,6 +9,7 @@
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <mutex>
 
 namespace ce {
@@ -37,6 +38,18 @@ inline unsigned long long current_context_id() {
     if (get_current(&ctx) != CUDA_SUCCESS || ctx == nullptr) return 0;
     if (get_id(ctx, &id) != CUDA_SUCCESS) return 0;
     return id;
+}
+
+// SM count of the current device, asked once per device (1 if unknown).
+inline int64_t device_sms() {
+    constexpr int kMaxDev = 64;
+    static std::atomic<int> cache[kMaxDev];
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return 1;
+    if (dev < kMaxDev && (n = cache[dev].load(std::memory_order_relaxed)) > 0) return n;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) return 1;
+    if (dev < kMaxDev) cache[dev].store(n, std::memory_order_relaxed);
+    return n;
 }
 
 }  // namespace ce

@@ -206,20 +206,11 @@ __device__ inline uint4 shift16(const uint4 &a, const uint4 &b, uint32_t sh) {
                           __funnelshift_r(w[3], w[4], 16));
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
-// 16 bytes at any address that is a multiple of the element size: from the two
-// aligned vectors that hold them (each of them holds some).
-template <int KB>
-__device__ inline uint4 ld_unaligned16(const char *p) {
-    const uint32_t sh = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p)) & 15u;
-    if (sh == 0) return ld_stream(p);
-    const uint4 *v = reinterpret_cast<const uint4 *>(p - sh);
-    return shift16<KB>(v[0], v[1], sh);
-}
-
-// Columns [c0, c1) of one row's gradient, by nt threads (this one is tid):
-// the interior in 16-byte vectors placed by the gradient's alignment, the
-// logits read as they lie (another alignment costs five word loads a vector).
-// x and grad may be the same row.
+// Columns [c0, c1) of one row's gradient, by nt threads (whole warps; this one
+// is tid): the interior in 16-byte vectors placed by the gradient's alignment.
+// Where the logits lie otherwise, each lane loads the aligned vector that its
+// columns start in and takes the rest from the next lane. x and grad may be the
+// same row.
 template <int DT, bool ENT>
 __device__ inline void lp_grad_span(const char *xrow, char *grow, int64_t c0, int64_t c1, int y, const LpGrad &g, float k,
                                     int tid, int nt) {
@@ -229,30 +220,44 @@ __device__ inline void lp_grad_span(const char *xrow, char *grow, int64_t c0, in
     const int64_t v0 = c0 + head < c1 ? c0 + head : c1;
     const int64_t nvec = (c1 - v0) / VEC;
     const int64_t tail = v0 + nvec * VEC;
-    const bool same = ((reinterpret_cast<uintptr_t>(xrow + v0 * KB)) & 15u) == 0;
-    auto put = [&](int64_t v, const uint4 &raw) {
-        float xv[VEC], o[VEC];
-        F::unpack(raw, xv);
-        lp_grad_vec<ENT, VEC>(g, xv, k, o);
-        const int64_t rel = y - (v0 + v * VEC);
-        if (rel >= 0 && rel < VEC) {
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) o[e] = e == rel ? g.dy : o[e];
-        }
-        st_stream(grow + (v0 + v * VEC) * KB, F::pack(o));
-    };
+    const uint32_t sh = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(xrow + v0 * KB)) & 15u;
+    const char *const xa = xrow + v0 * KB - sh;  // 16-byte aligned; each vector read holds some of the columns
+    const int lane = tid & 31;
     constexpr int U = 4;  // vectors in flight per thread
-    for (int64_t v = tid; v < nvec; v += static_cast<int64_t>(U) * nt) {
+    for (int64_t vb = tid - lane; vb < nvec; vb += static_cast<int64_t>(U) * nt) {
         uint4 raw[U];
 #pragma unroll
-        for (int j = 0; j < U; ++j)
-            if (v + static_cast<int64_t>(j) * nt < nvec) {
-                const char *p = xrow + (v0 + (v + static_cast<int64_t>(j) * nt) * VEC) * KB;
-                raw[j] = same ? ld_stream(p) : ld_unaligned16<KB>(p);
-            }
+        for (int j = 0; j < U; ++j) {
+            const int64_t v = vb + lane + static_cast<int64_t>(j) * nt;
+            raw[j] = v < nvec ? ld_stream(xa + 16 * v) : make_uint4(0u, 0u, 0u, 0u);
+        }
+        if (sh != 0) {
 #pragma unroll
-        for (int j = 0; j < U; ++j)
-            if (v + static_cast<int64_t>(j) * nt < nvec) put(v + static_cast<int64_t>(j) * nt, raw[j]);
+            for (int j = 0; j < U; ++j) {
+                const int64_t v = vb + lane + static_cast<int64_t>(j) * nt;
+                uint4 next;
+                next.x = __shfl_down_sync(0xffffffffu, raw[j].x, 1);
+                next.y = __shfl_down_sync(0xffffffffu, raw[j].y, 1);
+                next.z = __shfl_down_sync(0xffffffffu, raw[j].z, 1);
+                next.w = __shfl_down_sync(0xffffffffu, raw[j].w, 1);
+                if (v < nvec && (lane == 31 || v + 1 == nvec)) next = ld_stream(xa + 16 * (v + 1));
+                raw[j] = shift16<KB>(raw[j], next, sh);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            const int64_t v = vb + lane + static_cast<int64_t>(j) * nt;
+            if (v >= nvec) continue;
+            float xv[VEC], o[VEC];
+            F::unpack(raw[j], xv);
+            lp_grad_vec<ENT, VEC>(g, xv, k, o);
+            const int64_t rel = y - (v0 + v * VEC);
+            if (rel >= 0 && rel < VEC) {
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) o[e] = e == rel ? g.dy : o[e];
+            }
+            st_stream(grow + (v0 + v * VEC) * KB, F::pack(o));
+        }
     }
     // the columns before the first and after the last vector (fewer than VEC each)
     const int nh = static_cast<int>(v0 - c0), ne = nh + static_cast<int>(c1 - tail);

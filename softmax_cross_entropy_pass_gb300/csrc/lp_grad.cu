@@ -1,6 +1,7 @@
 // lp_grad.cu -- the gradient of token log-probabilities from saved row
 // statistics, the normalisers of the policy loss, and the sequence-level
 // kernels of the preference loss.
+#include "ce_host.h"
 #include "lp_device.cuh"
 #include "lp_kernels.h"
 
@@ -57,7 +58,12 @@ __global__ void __launch_bounds__(kLpPrepThreads) lp_prep_kernel(LpArgs a) {
 // ------------------------------------------------------------------ gradient from statistics
 constexpr int kLpGradThreads = 256;
 constexpr int kPairThreads = 256;
-constexpr int kLpGradBytes = 65536;  // bytes of a row per block
+// A row goes to one item in equal parts of at most 128 KB; with few rows in as
+// many parts as give every resident block one, of at least 8 KB (GB300, both
+// gradients: 8192 x 128256 bf16 645 us, with parts of 64 KB 655 and of 32 KB
+// 815; 8 x 128256 8 us against 17 with 128 KB parts).
+constexpr int64_t kLpGradMaxBytes = 131072, kLpGradMinBytes = 8192;
+constexpr int kLpGradCtasPerSm = 5;
 
 // fixed-order block sum of two doubles, to every thread
 __device__ inline void block_sum2(double &x, double &y, double (&sh)[kPairThreads / 32][2]) {
@@ -105,14 +111,12 @@ __device__ inline void lp_pair_loss(const LpArgs &a) {
 }
 static_assert(kPairThreads == kLpGradThreads, "the gradient kernel's first block forms the batch loss");
 
-// The logits once more, the gradient written: a map over (row, 64 KB part)
-// items, last rows first, so that what the forward read last is still in L2.
+// The logits once more, the gradient written: a map over (row, part) items, last rows first, so that what the forward read last is still in L2.
 // Bound by HBM; 4 vectors in flight per thread.
 template <int DT, bool ENT>
-__global__ void __launch_bounds__(kLpGradThreads) lp_grad_kernel(LpArgs a, int64_t parts) {
+__global__ void __launch_bounds__(kLpGradThreads, kLpGradCtasPerSm) lp_grad_kernel(LpArgs a, int64_t parts, int64_t span) {
     using F = Fmt<DT>;
     constexpr int KB = F::kBytes;
-    constexpr int64_t span = kLpGradBytes / KB;
     const int tid = threadIdx.x;
     float batch = 1.f;  // preference: what every row's coefficient is still to be multiplied by
     if (a.row_coef) {
@@ -242,26 +246,27 @@ __global__ void __launch_bounds__(kPairThreads) lp_pair_kernel(PairArgs a) {
 }
 
 // ------------------------------------------------------------------ launches
-template <typename A>
-static cudaError_t launch_dep(const void *fn, int64_t grid, int threads, A &a, int64_t *extra, bool dependent,
-                              cudaStream_t s) {
+static cudaLaunchConfig_t dep_config(int64_t grid, int threads, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(grid < 1 ? 1 : grid));
     cfg.blockDim = dim3(threads);
     cfg.stream = s;
+    return cfg;
+}
+// may start before the kernel in front of it has ended (it waits inside)
+static cudaLaunchAttribute dep_attribute() {
     cudaLaunchAttribute at;
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = dependent ? 1 : 0;
-    void *args[] = {&a, extra};
-    return cudaLaunchKernelExC(&cfg, fn, args);
+    return at;
 }
 
 cudaError_t launch_lp_prep(LpArgs &a, cudaStream_t s) {
     const int64_t want = (a.n_rows + kLpPrepThreads - 1) / kLpPrepThreads;
     a.n_prep = static_cast<int>(want < 1 ? 1 : (want < kPrepParts ? want : kPrepParts));
-    return launch_dep(reinterpret_cast<const void *>(&lp_prep_kernel), a.n_prep, kLpPrepThreads, a, nullptr, false, s);
+    cudaLaunchConfig_t cfg = dep_config(a.n_prep, kLpPrepThreads, s);
+    void *args[] = {&a};
+    return cudaLaunchKernelExC(&cfg, reinterpret_cast<const void *>(&lp_prep_kernel), args);
 }
 
 template <int DT>
@@ -274,16 +279,29 @@ cudaError_t launch_lp_grad(const LpArgs &a0, int dtype, bool entropy, bool depen
     LpArgs a = a0;
     const void *fn = dtype == CE_DT_F32 ? grad_fn<CE_DT_F32>(entropy)
                    : dtype == CE_DT_BF16 ? grad_fn<CE_DT_BF16>(entropy) : grad_fn<CE_DT_F16>(entropy);
-    const int64_t span = kLpGradBytes / (dtype == CE_DT_F32 ? 4 : 2);
-    int64_t parts = (a.vocab + span - 1) / span;
+    const int64_t esz = dtype == CE_DT_F32 ? 4 : 2, row = a.vocab * esz;
+    int64_t want = a.n_rows > 0 ? (device_sms() * kLpGradCtasPerSm + a.n_rows - 1) / a.n_rows : 1;
+    if (want > row / kLpGradMinBytes) want = row / kLpGradMinBytes;
+    const int64_t least = (row + kLpGradMaxBytes - 1) / kLpGradMaxBytes;
+    int64_t parts = want > least ? want : least;
+    int64_t span = ((row + parts - 1) / parts + 127) / 128 * 128 / esz;  // columns of a part
     const int64_t items = a.n_rows * parts, cap = int64_t(1) << 20;
-    return launch_dep(fn, items < cap ? items : cap, kLpGradThreads, a, &parts, dependent, s);
+    cudaLaunchConfig_t cfg = dep_config(items < cap ? items : cap, kLpGradThreads, s);
+    cudaLaunchAttribute at = dep_attribute();
+    cfg.attrs = &at;
+    cfg.numAttrs = dependent ? 1 : 0;
+    void *args[] = {&a, &parts, &span};
+    return cudaLaunchKernelExC(&cfg, fn, args);
 }
 
 cudaError_t launch_lp_pairs(const PairArgs &a0, cudaStream_t s) {
     PairArgs a = a0;
-    return launch_dep(reinterpret_cast<const void *>(&lp_pair_kernel), a.n_pairs < 512 ? a.n_pairs : 512, kPairThreads, a,
-                      nullptr, true, s);
+    cudaLaunchConfig_t cfg = dep_config(a.n_pairs < 512 ? a.n_pairs : 512, kPairThreads, s);
+    cudaLaunchAttribute at = dep_attribute();
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    void *args[] = {&a};
+    return cudaLaunchKernelExC(&cfg, reinterpret_cast<const void *>(&lp_pair_kernel), args);
 }
 
 }  // namespace ce
