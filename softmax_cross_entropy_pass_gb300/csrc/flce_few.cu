@@ -12,6 +12,8 @@
 // epilogue in registers (the tensor core's long sums truncate). Every epilogue
 // thread keeps the running statistics of its weight rows for 16 hidden rows;
 // they meet across lanes once, at the end.
+#include <atomic>
+
 #include "ce_device.cuh"
 #include "flce.h"
 #include "lp_device.cuh"
@@ -250,14 +252,14 @@ cudaError_t flce_few(int n, int V, int H, const void *hidden, const void *weight
     if (e == cudaSuccess) e = make_tmap(&th, hidden, n, H, H, kFewK, g.N);
     if (e != cudaSuccess) return e;
     // the shared-memory limit is a per-device attribute: set once per device
-    static uint64_t attr_set = 0;
+    static std::atomic<uint64_t> attr_set{0};
     int dev = 0;
     if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
     const uint64_t bit = dev < 64 ? (1ull << dev) : 0ull;
-    if (!bit || !(attr_set & bit)) {
+    if (!bit || !(attr_set.load() & bit)) {
         e = cudaFuncSetAttribute(flce_few_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewSmem);
         if (e != cudaSuccess) return e;
-        attr_set |= bit;
+        attr_set.fetch_or(bit);
     }
     void *args[] = {&tw, &tws, &th, &g};
     return cudaLaunchKernel(reinterpret_cast<const void *>(&flce_few_kernel), dim3(few_blocks(V)),

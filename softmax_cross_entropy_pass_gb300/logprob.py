@@ -169,14 +169,14 @@ def _workspace(call, ws, nbytes):
     return ws, ws.numel() * ws.element_size()
 
 
-def _ws_bytes(p, n_pairs=None) -> int:
-    out = ctypes.c_size_t()
-    if n_pairs is None:
-        _check(_lib.ce_workspace_size(_byref(p), _byref(out)), "ce_workspace_size")
-    else:
-        _check(_lib.ce_preference_workspace_size(_byref(p), n_pairs, _byref(out)),
-               "ce_preference_workspace_size")
-    return out.value
+# The sizes that ce_workspace_size and ce_preference_workspace_size stay within
+# (include/ce.h), without the calls.
+def _policy_ws_bytes(n) -> int:
+    return 20 * n + 512
+
+
+def _preference_ws_bytes(n, pairs) -> int:
+    return 20 * n + 8 * pairs + 1024
 
 
 # ---------------------------------------------------------------------- token log-probabilities
@@ -235,7 +235,7 @@ def ce_policy_fwd_bwd(logits, target, advantage, *, old_logp=None, ref_logp=None
                                   or not row_stats.is_contiguous() or row_stats.device != call.device):
         raise ValueError("row_stats must be a contiguous fp32 [n_rows, 4] tensor on the logits' device")
     q = ce_policy_params(float(temperature), float(clip_low), float(clip_high), float(kl_coef), float(entropy_coef), 0)
-    ws, nbytes = _workspace(call, ws, _ws_bytes(p))
+    ws, nbytes = _workspace(call, ws, _policy_ws_bytes(n))
     call.run("ce_policy_fwd_bwd", _lib.ce_policy_fwd_bwd, _byref(p), _byref(q), _ptr(logits), _ptr(target), _ptr(advantage),
              _ptr(old_logp), _ptr(ref_logp), _ptr(row_weight), _ptr(grad_output), _ptr(loss), _ptr(row_stats),
              _ptr(grad), ld, _ptr(ws), nbytes)
@@ -270,7 +270,7 @@ def ce_preference_fwd_bwd(logits, target, seq_offsets, *, ref_logp=None, loss_ki
     seq_logp = call.empty(2 * pairs) if seq_logp is None else _vec("seq_logp", seq_logp, 2 * pairs, call.device)
     q = ce_preference_params(pairs, PREFERENCE_KINDS[loss_kind], 1 if seq_offsets.dtype == torch.int32 else 0,
                              1 if length_normalize else 0, float(beta), float(label_smoothing), 0)
-    ws, nbytes = _workspace(call, ws, _ws_bytes(p, pairs))
+    ws, nbytes = _workspace(call, ws, _preference_ws_bytes(n, pairs))
     call.run("ce_preference_fwd_bwd", _lib.ce_preference_fwd_bwd, _byref(p), _byref(q), _ptr(logits), _ptr(target), _ptr(seq_offsets),
              _ptr(ref_logp), _ptr(grad_output), _ptr(loss), _ptr(seq_logp), _ptr(grad), ld, _ptr(ws), nbytes)
     return loss, seq_logp, grad

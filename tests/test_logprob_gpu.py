@@ -180,6 +180,72 @@ def test_scattered_masked_columns(ce, v, dtype, share):
         assert (grad[off & valid[:, None]] == 0).all()
 
 
+@pytest.mark.parametrize("temperature", [1e-4, 0.02, 50.0, 1e4])
+@pytest.mark.parametrize("v", [900, 40000])
+def test_far_temperatures(ce, temperature, v):
+    temperature = f32(temperature)
+    g, _, x, t = make(12, v, "f32", 3, ignored=0.1)
+    logp, ent, stats = ce.ce_token_logprob(x, t, temperature=temperature)
+    valid, logq, want, want_h = L.rows_ref(x, t, temperature)
+    d = L.delta(x, temperature)
+    L.check(logp, want, L.tol_logp(d, want) * valid, "logp")
+    L.check(ent, want_h, L.tol_entropy(d, want_h) * valid, "entropy")
+    gl, gh, z = rnd(g, 12), rnd(g, 12), torch.zeros(12, device="cuda")
+    ref = L.grad_ref(logq, valid, t, gl, gh, temperature)
+    grad = ce.ce_token_logprob_backward(x, t, stats, gl, grad_entropy=gh, temperature=temperature, grad=torch.empty_like(x))
+    L.check(grad, ref, L.tol_grad(x, ref, logq, valid, t, gl, gh, z, z, torch.float32, temperature), "gradient")
+
+
+@pytest.mark.parametrize("shape", [(21000, 110001), (300000, 8000)])
+def test_offsets_past_32_bits(ce, shape):
+    """Elements past 2^31 and bytes past 2^32: the last rows as the first ones."""
+    n, v = shape
+    x = torch.empty(n, v, dtype=torch.bfloat16, device="cuda").normal_(0, 2)
+    t = torch.randint(0, v, (n,), device="cuda")
+    t[5:-5] = -100
+    adv, pick = torch.randn(n, device="cuda"), torch.cat([torch.arange(5), torch.arange(n - 5, n)]).cuda()
+    xs, ts = x[pick].clone(), t[pick].clone()
+    want = L.policy_ref(xs, ts, adv[pick], None, None, None, 0.2, 0.2, 0.0, f32(0.01), 1.0, "sum", None)
+    stats = torch.empty(n, 4, device="cuda")
+    logp, ent, st = ce.ce_token_logprob(x, t)
+    gl = torch.randn(n, device="cuda")
+    loss, grad = ce.ce_policy_fwd_bwd(x, t, adv, entropy_coef=f32(0.01), reduction="sum", row_stats=stats, grad=torch.empty_like(x))
+    L.check(loss, want["loss"], want["tol_loss"], "loss")
+    L.check(grad[pick], want["grad"], want["tol_grad"], "policy gradient")
+    L.check(stats[pick], want["stats"], want["tol_stats"], "row statistics")
+    L.check(logp[pick], want["stats"][:, 0], want["tol_stats"][:, 0], "logp")
+    L.check(ent[pick], want["stats"][:, 1], want["tol_stats"][:, 1], "entropy")
+    assert (grad[n // 2] == 0).all() and (logp[5:-5] == 0).all()
+    ce.ce_token_logprob_backward(x, t, st, gl, grad=grad)
+    valid, logq, _, _ = L.rows_ref(xs, ts)
+    z = torch.zeros(10, device="cuda")
+    ref = L.grad_ref(logq, valid, ts, gl[pick], z)
+    L.check(grad[pick], ref, L.tol_grad(xs, ref, logq, valid, ts, gl[pick], z, z, z, torch.bfloat16), "gradient")
+    off = torch.tensor([0, 5, n], device="cuda")
+    loss, seq, grad = ce.ce_preference_fwd_bwd(x, t, off, grad=grad)
+    assert abs(seq[1].item() - logp[-5:].double().sum().item()) < 1e-3 and loss.isfinite().all()
+    assert (grad[n - 1] != 0).any() and (grad[n // 2] == 0).all()
+
+
+@pytest.mark.parametrize("n,v", [(9001, 3000), (20000, 300), (17000, 9000)])
+def test_many_rows(ce, n, v):
+    """More rows than one window of the row kernel deals out, most of them without a target, at random."""
+    g, _, x, t = make(n, v, "bf16", n, ignored=0.6)
+    adv = rnd(g, n)
+    stats = torch.full((n, 4), 9.0, device="cuda")
+    loss, grad = ce.ce_policy_fwd_bwd(x, t, adv, entropy_coef=f32(0.01), row_stats=stats, grad=torch.empty_like(x))
+    want = L.policy_ref(x, t, adv, None, None, None, 0.2, 0.2, 0.0, f32(0.01), 1.0, "mean", None)
+    L.check(loss, want["loss"], want["tol_loss"], "loss")
+    L.check(grad, want["grad"], want["tol_grad"], "gradient")
+    L.check(stats, want["stats"], want["tol_stats"], "row statistics")
+    logp, ent, _ = ce.ce_token_logprob(x, t)
+    L.check(logp, want["stats"][:, 0], want["tol_stats"][:, 0], "logp")
+    L.check(ent, want["stats"][:, 1], want["tol_stats"][:, 1], "entropy")
+    rows, _ = ce.ce_policy_fwd_bwd(x, t, adv, entropy_coef=f32(0.01), reduction="none", grad=torch.empty_like(x))
+    assert (rows[t < 0] == 0).all()
+    assert abs(rows.double().sum().item() / int((t >= 0).sum()) - loss.item()) < 1e-6 * (1 + rows.double().abs().mean().item())
+
+
 def test_token_logprob_statistics_without_entropy_refuse_its_gradient(ce):
     x, t = torch.randn(3, 100, device="cuda"), torch.zeros(3, dtype=torch.int64, device="cuda")
     _, _, stats = ce.ce_token_logprob(x, t, with_entropy=False)

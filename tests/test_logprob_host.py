@@ -228,6 +228,17 @@ def test_preference_workspace_size(ce):
     assert ce._lib.ce_preference_workspace_size(ctypes.byref(_p(ce)), -1, ctypes.byref(out)) == ce.CE_ERR_INVALID_ARG
 
 
+@pytest.mark.parametrize("n", [0, 1, 3, 63, 64, 65, 1000, 8191, 65536, 10 ** 7 + 1])
+def test_python_workspaces_are_large_enough(ce, n):
+    out = ctypes.c_size_t()
+    p = _p(ce, n_rows=n)
+    assert ce._lib.ce_workspace_size(ctypes.byref(p), ctypes.byref(out)) == 0
+    assert out.value <= ce.logprob._policy_ws_bytes(n)
+    for pairs in (0, 1, 31, 500):
+        assert ce._lib.ce_preference_workspace_size(ctypes.byref(p), pairs, ctypes.byref(out)) == 0
+        assert out.value <= ce.logprob._preference_ws_bytes(n, pairs)
+
+
 def test_parameter_blocks(ce):
     assert ctypes.sizeof(ce.ce_policy_params) == 24 and ce.ce_policy_params.entropy_coef.offset == 16
     assert ctypes.sizeof(ce.ce_preference_params) == 32 and ce.ce_preference_params.beta.offset == 20
