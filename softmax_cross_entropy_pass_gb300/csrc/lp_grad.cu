@@ -42,9 +42,13 @@ __global__ void __launch_bounds__(kLpPrepThreads) lp_prep_kernel(LpArgs a) {
     for (int off = 16; off > 0; off >>= 1) w += __shfl_xor_sync(0xffffffffu, w, off);
     if ((tid & 31) == 0) sh_w[tid >> 5] = w;
     const int any_bad = __syncthreads_or(bad);
+    static_assert(kLpPrepThreads == 1024, "one warp adds the warps up");
+    double sum = tid < 32 ? sh_w[tid] : 0.0;
+    if (tid < 32) {
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    }
     if (tid == 0) {
-        double sum = 0.0;
-        for (int i = 0; i < kLpPrepThreads / 32; ++i) sum += sh_w[i];
         a.ctl->prep_part[blockIdx.x][0] = sum;
         a.ctl->prep_bad[blockIdx.x] = any_bad ? 1u : 0u;
         if (blockIdx.x == 0) {
@@ -154,15 +158,18 @@ __global__ void __launch_bounds__(kLpGradThreads, kLpGradCtasPerSm) lp_grad_kern
 // Offsets that fall, or leave [0, n_rows], make the whole batch void: loss
 // NaN, gradient 0, a status bit. Every block checks all of them itself.
 __global__ void __launch_bounds__(kPairThreads) lp_pair_kernel(PairArgs a) {
-    __shared__ double sh[kPairThreads / 32][2];
-    pdl_wait();
+    constexpr int HALF = kPairThreads / 2, W = HALF / 32;
+    __shared__ double sh[2][W][2];  // per side and warp: log-probabilities, valid targets
     const int tid = threadIdx.x;
+    const int side_t = tid / HALF, ht = tid - side_t * HALF;  // half of the block a sequence
     bool bad = false;
     for (int64_t j = tid; j < 2 * a.n_pairs; j += kPairThreads) {
         const int64_t b = load_target(a.offsets, a.off32, j), e = load_target(a.offsets, a.off32, j + 1);
         if (b < 0 || e < b || e > a.n_rows) bad = true;
     }
-    if (__syncthreads_or(bad)) {
+    const bool void_batch = __syncthreads_or(bad);
+    pdl_wait();  // the log-probabilities
+    if (void_batch) {
         for (int64_t i = static_cast<int64_t>(blockIdx.x) * kPairThreads + tid; i < a.n_rows;
              i += static_cast<int64_t>(gridDim.x) * kPairThreads)
             a.row[i] = 0.f;
@@ -176,72 +183,79 @@ __global__ void __launch_bounds__(kPairThreads) lp_pair_kernel(PairArgs a) {
         return;
     }
     for (int64_t p = blockIdx.x; p < a.n_pairs; p += gridDim.x) {
-        int64_t b[2], e[2];
-        double sum[2], cnt[2];
+        const int64_t seq = p + side_t * a.n_pairs;
+        const int64_t b = load_target(a.offsets, a.off32, seq), e = load_target(a.offsets, a.off32, seq + 1);
         bool oob = false;
-        for (int side = 0; side < 2; ++side) {
-            const int64_t seq = p + side * a.n_pairs;
-            b[side] = load_target(a.offsets, a.off32, seq);
-            e[side] = load_target(a.offsets, a.off32, seq + 1);
-            double s = 0.0, n = 0.0;
-            for (int64_t i = b[side] + tid; i < e[side]; i += kPairThreads) {
-                const int64_t t = load_target(a.target, a.tgt32, i);
-                if (target_valid(t, a.ignore_index, a.vocab)) {
-                    s += static_cast<double>(a.row[i]);
-                    n += 1.0;
-                } else if (t != a.ignore_index) {
-                    oob = true;
-                }
+        double s = 0.0, n = 0.0;
+        for (int64_t i = b + ht; i < e; i += HALF) {
+            const int64_t t = load_target(a.target, a.tgt32, i);
+            const float lp = a.row[i];  // 0 where the target takes no part
+            if (target_valid(t, a.ignore_index, a.vocab)) {
+                s += static_cast<double>(lp);
+                n += 1.0;
+            } else if (t != a.ignore_index) {
+                oob = true;
             }
-            block_sum2(s, n, sh);
-            sum[side] = s;
-            cnt[side] = n;
+        }
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) {
+            s += __shfl_xor_sync(0xffffffffu, s, off);
+            n += __shfl_xor_sync(0xffffffffu, n, off);
+        }
+        if ((tid & 31) == 0) {
+            sh[side_t][ht / 32][0] = s;
+            sh[side_t][ht / 32][1] = n;
         }
         if (__syncthreads_or(oob) && tid == 0) atomicOr(&a.ctl->status, CE_FLAG_TARGET_OUT_OF_RANGE);
+        double sum[2] = {}, cnt[2] = {};
+        for (int side = 0; side < 2; ++side)
+            for (int w = 0; w < W; ++w) {
+                sum[side] += sh[side][w][0];
+                cnt[side] += sh[side][w][1];
+            }
         const bool live = cnt[0] > 0.0 && cnt[1] > 0.0;
         double v[2];
         for (int side = 0; side < 2; ++side) v[side] = a.normalize && cnt[side] > 0.0 ? sum[side] / cnt[side] : sum[side];
-        double loss = 0.0, slope = 0.0;
+        // h in fp64 (a difference of long sums), what follows from it in fp32 (every
+        // thread forms it, and fp64 exponentials are slow here)
+        float loss = 0.f, slope = 0.f;
         if (live) {
             double h = v[0] - v[1];
             if (a.ref) h -= static_cast<double>(__ldg(a.ref + p)) - static_cast<double>(__ldg(a.ref + a.n_pairs + p));
-            const double be = a.beta, z = be * h, eps = a.smoothing;
+            const float be = a.beta, z = static_cast<float>(static_cast<double>(be) * h), eps = a.smoothing;
             if (a.kind == CE_PREF_SIGMOID) {
                 // softplus(+-z) and the logistic function through e^-|z|, which cannot overflow
-                const double q = exp(-fabs(z)), l = log1p(q);
-                const double sp_pos = (z > 0.0 ? z : 0.0) + l, sp_neg = (z > 0.0 ? 0.0 : -z) + l;
-                const double big = 1.0 / (1.0 + q), small = q / (1.0 + q);
-                const double s_pos = z > 0.0 ? big : small, s_neg = z > 0.0 ? small : big;
-                loss = (1.0 - eps) * sp_neg + eps * sp_pos;
-                slope = be * (eps * s_pos - (1.0 - eps) * s_neg);
+                const float q = expf(-fabsf(z)), l = log1pf(q), inv = 1.f / (1.f + q);
+                const float sp_pos = (z > 0.f ? z : 0.f) + l, sp_neg = (z > 0.f ? 0.f : -z) + l;
+                const float s_pos = z > 0.f ? inv : q * inv, s_neg = z > 0.f ? q * inv : inv;
+                loss = (1.f - eps) * sp_neg + eps * sp_pos;
+                slope = be * (eps * s_pos - (1.f - eps) * s_neg);
             } else if (a.kind == CE_PREF_HINGE) {
-                loss = z < 1.0 ? 1.0 - z : (z >= 1.0 ? 0.0 : z);
-                slope = z < 1.0 ? -be : (z >= 1.0 ? 0.0 : z);
+                loss = z < 1.f ? 1.f - z : (z >= 1.f ? 0.f : z);  // NaN stays
+                slope = z < 1.f ? -be : (z >= 1.f ? 0.f : z);
             } else {
-                const double m = h - 0.5 / be;
+                const float m = static_cast<float>(h - 0.5 / static_cast<double>(be));
                 loss = m * m;
-                slope = 2.0 * m;
+                slope = 2.f * m;
             }
         }
         if (tid == 0) {
             a.pair_loss[p] = loss;
-            if (a.reduction == CE_RED_NONE) a.loss[p] = static_cast<float>(loss);
+            if (a.reduction == CE_RED_NONE) a.loss[p] = loss;
             if (a.seq_logp) {
                 a.seq_logp[p] = static_cast<float>(v[0]);
                 a.seq_logp[a.n_pairs + p] = static_cast<float>(v[1]);
             }
             if (live) atomicAdd(&a.ctl->n_correct, 1u);  // integers: the order does not matter
         }
-        if (a.reduction == CE_RED_NONE && a.grad_output) slope *= static_cast<double>(__ldg(a.grad_output + p));
-        for (int side = 0; side < 2; ++side) {
-            double c = side == 0 ? slope : -slope;
-            if (a.normalize && live) c /= cnt[side];
-            const float cf = static_cast<float>(c);
-            for (int64_t i = b[side] + tid; i < e[side]; i += kPairThreads) {
-                const int64_t t = load_target(a.target, a.tgt32, i);
-                a.row[i] = target_valid(t, a.ignore_index, a.vocab) ? cf : 0.f;
-            }
+        if (a.reduction == CE_RED_NONE && a.grad_output) slope *= __ldg(a.grad_output + p);
+        float c = side_t == 0 ? slope : -slope;
+        if (a.normalize && live) c /= static_cast<float>(cnt[side_t]);
+        for (int64_t i = b + ht; i < e; i += HALF) {
+            const int64_t t = load_target(a.target, a.tgt32, i);
+            a.row[i] = target_valid(t, a.ignore_index, a.vocab) ? c : 0.f;
         }
+        __syncthreads();  // the sums are used up
     }
 }
 
