@@ -26,7 +26,8 @@ import torch
 from . import CE_DT, CE_RED, CEError, _check, _lib, ce_params, ce_scale_grad
 
 _raw_stream = torch._C._cuda_getCurrentRawStream  # the current stream of a device as an integer
-_byref = ctypes.byref
+_current_device = torch._C._cuda_getDevice
+_byref, _F32, _I64, _I32 = ctypes.byref, torch.float32, torch.int64, torch.int32
 
 CE_FLAG_BAD_OFFSETS = 8
 PREFERENCE_KINDS = {"sigmoid": 0, "hinge": 1, "squared": 2}
@@ -71,72 +72,88 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _params(logits, target, ignore_index, reduction="mean") -> ce_params:
-    if logits.dim() != 2 or logits.stride(1) != 1 and logits.shape[1] != 1:
-        raise ValueError("logits must be a 2-D tensor with unit column stride")
-    if logits.dtype not in CE_DT:
-        raise TypeError(f"unsupported logits dtype {logits.dtype}")
-    if target.dtype not in (torch.int64, torch.int32):
+def _check_target(target, n):
+    dtype = target.dtype
+    if dtype is not _I64 and dtype is not _I32:
         raise TypeError("target must be int64 or int32")
-    n, v = logits.shape
-    if target.dim() != 1 or target.shape[0] != n or not target.is_contiguous():
+    if target.dim() != 1 or target.numel() != n or not target.is_contiguous():
         raise ValueError("target must be a contiguous 1-D tensor with one entry per row")
+    return 1 if dtype is _I32 else 0
+
+
+def _params(logits, target, ignore_index, reduction="mean") -> ce_params:
+    if logits.dim() != 2:
+        raise ValueError("logits must be a 2-D tensor with unit column stride")
+    n, v = logits.shape
+    ld, step = logits.stride()
+    if step != 1 and v != 1:
+        raise ValueError("logits must be a 2-D tensor with unit column stride")
+    dtype = CE_DT.get(logits.dtype)
+    if dtype is None:
+        raise TypeError(f"unsupported logits dtype {logits.dtype}")
     if reduction not in CE_RED:
         raise ValueError(f"unknown reduction {reduction!r}")
     # n_rows, vocab, ld, ignore_index, class_weight, label_smoothing, dtype, reduction, target_is_int32
-    return ce_params(n, v, logits.stride(0) if n > 1 else v, ignore_index, None, 0.0, CE_DT[logits.dtype],
-                     CE_RED[reduction], 1 if target.dtype == torch.int32 else 0)
+    return ce_params(n, v, ld if n > 1 else v, ignore_index, None, 0.0, dtype, CE_RED[reduction], _check_target(target, n))
 
 
-def _vec(name, t, n, device):
-    """A contiguous fp32 vector of n entries on the logits' device (or None)."""
-    if t is not None and (t.dtype != torch.float32 or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous()
-                          or t.device != device):
+def _vec(name, t, n, call):
+    """A contiguous fp32 vector of n entries on the call's device (or None)."""
+    if t is not None and (t.dtype is not _F32 or t.dim() != 1 or t.numel() != n or not t.is_contiguous()
+                          or t.get_device() != call.index):
         raise ValueError(f"{name} must be a contiguous fp32 tensor of {n} entries on the logits' device")
     return t
 
 
-def _grad_buffer(logits, grad):
+def _rows4(name, t, n, call):
+    if t is not None and (t.dtype is not _F32 or t.dim() != 2 or t.shape[1] != 4 or t.shape[0] != n
+                          or not t.is_contiguous() or t.get_device() != call.index):
+        raise ValueError(f"{name} must be a contiguous fp32 [n_rows, 4] tensor on the logits' device")
+    return t
+
+
+def _grad_buffer(logits, grad, p):
+    """(the gradient's buffer, its row stride)."""
     if grad is None:
-        return logits, logits.stride(0) if logits.shape[0] > 1 else logits.shape[1]
-    if grad.shape != logits.shape or grad.dtype != logits.dtype or grad.device != logits.device \
-            or (grad.stride(1) != 1 and grad.shape[1] != 1):
+        return logits, p.ld
+    if grad.shape != logits.shape or grad.dtype is not logits.dtype or grad.get_device() != logits.get_device() \
+            or (grad.stride(1) != 1 and p.vocab != 1):
         raise ValueError("grad must have the logits' shape, dtype and device, and unit column stride")
-    return grad, grad.stride(0) if grad.shape[0] > 1 else grad.shape[1]
+    return grad, grad.stride(0) if p.n_rows > 1 else p.vocab
 
 
 class _Call:
     """The device and the stream of one call. Memory that the call allocates
     comes from the current stream's pool: where the kernels run on another
     stream, that pool is told so before it may hand the memory out again."""
-    __slots__ = ("device", "stream", "other", "handle")
+    __slots__ = ("device", "index", "stream", "other", "handle")
 
     def __init__(self, tensor, others, stream):
-        if not tensor.is_cuda:
+        index = self.index = tensor.get_device()
+        if index < 0:
             raise ValueError("all tensors must live on the GPU")
-        device = self.device = tensor.device
         for t in others:
-            if t is not None and t.device != device:
+            if t is not None and t.get_device() != index:
                 raise ValueError("all tensors must live on the logits' device")
-        self.other = None
-        self.handle = _raw_stream(device.index)
+        self.device, self.other, self.handle = tensor.device, None, _raw_stream(index)
         if stream is not None:
             if not hasattr(stream, "cuda_stream"):
-                stream = torch.cuda.ExternalStream(int(stream), device=device)
-            if stream.device != device:
+                stream = torch.cuda.ExternalStream(int(stream), device=self.device)
+            if stream.device != self.device:
                 raise ValueError("stream must be one of the logits' device")
             if stream.cuda_stream != self.handle:
-                self.stream, self.other, self.handle = stream, torch.cuda.current_stream(device), stream.cuda_stream
+                self.stream, self.other, self.handle = stream, torch.cuda.current_stream(self.device), stream.cuda_stream
 
-    def empty(self, *shape, dtype=torch.float32):
+    def empty(self, *shape, dtype=_F32):
         t = torch.empty(shape, dtype=dtype, device=self.device)
         if self.other is not None:
             self.stream.wait_stream(self.other)  # the memory's last user may still be running there
             t.record_stream(self.stream)
         return t
 
-    def run(self, name, fn, *args):
-        if torch.cuda.current_device() == self.device.index:
+    def run(self, name, *args):
+        fn = getattr(_lib, name)
+        if _current_device() == self.index:
             status = fn(*args, self.handle)
         else:
             with torch.cuda.device(self.device):
@@ -149,22 +166,16 @@ def _outputs(call, n, logp, entropy, stats, with_entropy):
     """The three outputs of a forward: those given, or new ones."""
     if not with_entropy and entropy is not None:
         raise ValueError("entropy given with with_entropy=False")
-    logp = call.empty(n) if logp is None else _vec("logp", logp, n, call.device)
+    logp = call.empty(n) if logp is None else _vec("logp", logp, n, call)
     if with_entropy:
-        entropy = call.empty(n) if entropy is None else _vec("entropy", entropy, n, call.device)
-    return logp, entropy, call.empty(n, 4) if stats is None else _stats(stats, n)
-
-
-def _stats(stats, n):
-    if stats.dtype != torch.float32 or stats.shape != (n, 4) or not stats.is_contiguous():
-        raise ValueError("stats must be a contiguous fp32 [n_rows, 4] tensor")
-    return stats
+        entropy = call.empty(n) if entropy is None else _vec("entropy", entropy, n, call)
+    return logp, entropy, call.empty(n, 4) if stats is None else _rows4("stats", stats, n, call)
 
 
 def _workspace(call, ws, nbytes):
     if ws is None:
         return call.empty(nbytes, dtype=torch.uint8), nbytes
-    if ws.device != call.device or not ws.is_contiguous():
+    if ws.get_device() != call.index or not ws.is_contiguous():
         raise ValueError("ws must be a contiguous tensor on the logits' device")
     return ws, ws.numel() * ws.element_size()
 
@@ -190,7 +201,7 @@ def ce_token_logprob(logits, target, *, temperature=1.0, ignore_index=-100, with
     n = p.n_rows
     call = _Call(logits, (target, logp, entropy, stats), stream)
     logp, entropy, stats = _outputs(call, n, logp, entropy, stats, with_entropy)
-    call.run("ce_token_logprob", _lib.ce_token_logprob, _byref(p), float(temperature), _ptr(logits), _ptr(target), _ptr(logp),
+    call.run("ce_token_logprob", _byref(p), float(temperature), _ptr(logits), _ptr(target), _ptr(logp),
              _ptr(entropy), _ptr(stats))
     return logp, entropy, stats
 
@@ -203,12 +214,12 @@ def ce_token_logprob_backward(logits, target, stats, grad_logp, *, grad_entropy=
     ``grad`` is given; returned."""
     p = _params(logits, target, ignore_index)
     n = p.n_rows
-    grad, ld = _grad_buffer(logits, grad)
+    grad, ld = _grad_buffer(logits, grad, p)
     call = _Call(logits, (target, stats, grad_logp, grad_entropy, grad), stream)
-    _vec("grad_logp", grad_logp, n, call.device)
-    _vec("grad_entropy", grad_entropy, n, call.device)
-    _stats(stats, n)
-    call.run("ce_token_logprob_backward", _lib.ce_token_logprob_backward, _byref(p), float(temperature), _ptr(logits), _ptr(target), _ptr(stats),
+    _vec("grad_logp", grad_logp, n, call)
+    _vec("grad_entropy", grad_entropy, n, call)
+    _rows4("stats", stats, n, call)
+    call.run("ce_token_logprob_backward", _byref(p), float(temperature), _ptr(logits), _ptr(target), _ptr(stats),
              _ptr(grad_logp), _ptr(grad_entropy), _ptr(grad), ld)
     return grad
 
@@ -223,20 +234,19 @@ def ce_policy_fwd_bwd(logits, target, advantage, *, old_logp=None, ref_logp=None
     receives {logp, entropy, ratio, KL} of every row."""
     p = _params(logits, target, ignore_index, reduction)
     n = p.n_rows
-    grad, ld = _grad_buffer(logits, grad)
+    grad, ld = _grad_buffer(logits, grad, p)
     call = _Call(logits, (target, grad, loss), stream)
-    for name, t in (("advantage", advantage), ("old_logp", old_logp), ("ref_logp", ref_logp),
-                    ("row_weight", row_weight)):
-        _vec(name, t, n, call.device)
+    _vec("advantage", advantage, n, call)
+    _vec("old_logp", old_logp, n, call)
+    _vec("ref_logp", ref_logp, n, call)
+    _vec("row_weight", row_weight, n, call)
+    _rows4("row_stats", row_stats, n, call)
     m = n if reduction == "none" else 1
-    _vec("grad_output", grad_output, m, call.device)
-    loss = call.empty(m) if loss is None else _vec("loss", loss, m, call.device)
-    if row_stats is not None and (row_stats.dtype != torch.float32 or row_stats.shape != (n, 4)
-                                  or not row_stats.is_contiguous() or row_stats.device != call.device):
-        raise ValueError("row_stats must be a contiguous fp32 [n_rows, 4] tensor on the logits' device")
+    _vec("grad_output", grad_output, m, call)
+    loss = call.empty(m) if loss is None else _vec("loss", loss, m, call)
     q = ce_policy_params(float(temperature), float(clip_low), float(clip_high), float(kl_coef), float(entropy_coef), 0)
     ws, nbytes = _workspace(call, ws, _policy_ws_bytes(n))
-    call.run("ce_policy_fwd_bwd", _lib.ce_policy_fwd_bwd, _byref(p), _byref(q), _ptr(logits), _ptr(target), _ptr(advantage),
+    call.run("ce_policy_fwd_bwd", _byref(p), _byref(q), _ptr(logits), _ptr(target), _ptr(advantage),
              _ptr(old_logp), _ptr(ref_logp), _ptr(row_weight), _ptr(grad_output), _ptr(loss), _ptr(row_stats),
              _ptr(grad), ld, _ptr(ws), nbytes)
     return loss, grad
@@ -261,17 +271,17 @@ def ce_preference_fwd_bwd(logits, target, seq_offsets, *, ref_logp=None, loss_ki
     if loss_kind not in PREFERENCE_KINDS:
         raise ValueError(f"unknown loss_kind {loss_kind!r}")
     pairs = seq_offsets.shape[0] // 2
-    grad, ld = _grad_buffer(logits, grad)
+    grad, ld = _grad_buffer(logits, grad, p)
     call = _Call(logits, (target, seq_offsets, grad), stream)
-    _vec("ref_logp", ref_logp, 2 * pairs, call.device)
+    _vec("ref_logp", ref_logp, 2 * pairs, call)
     m = pairs if reduction == "none" else 1
-    _vec("grad_output", grad_output, m, call.device)
-    loss = call.empty(m) if loss is None else _vec("loss", loss, m, call.device)
-    seq_logp = call.empty(2 * pairs) if seq_logp is None else _vec("seq_logp", seq_logp, 2 * pairs, call.device)
+    _vec("grad_output", grad_output, m, call)
+    loss = call.empty(m) if loss is None else _vec("loss", loss, m, call)
+    seq_logp = call.empty(2 * pairs) if seq_logp is None else _vec("seq_logp", seq_logp, 2 * pairs, call)
     q = ce_preference_params(pairs, PREFERENCE_KINDS[loss_kind], 1 if seq_offsets.dtype == torch.int32 else 0,
                              1 if length_normalize else 0, float(beta), float(label_smoothing), 0)
     ws, nbytes = _workspace(call, ws, _preference_ws_bytes(n, pairs))
-    call.run("ce_preference_fwd_bwd", _lib.ce_preference_fwd_bwd, _byref(p), _byref(q), _ptr(logits), _ptr(target), _ptr(seq_offsets),
+    call.run("ce_preference_fwd_bwd", _byref(p), _byref(q), _ptr(logits), _ptr(target), _ptr(seq_offsets),
              _ptr(ref_logp), _ptr(grad_output), _ptr(loss), _ptr(seq_logp), _ptr(grad), ld, _ptr(ws), nbytes)
     return loss, seq_logp, grad
 
@@ -384,20 +394,15 @@ def preference_loss(logits, target, seq_offsets, *, ref_logp=None, loss_kind="si
 DZ_BYTES = 16 << 30
 
 
-def _linear_params(hidden, weight, target, bias, ignore_index):
+def _linear_params(hidden, weight, target, ignore_index):
     if hidden.dim() != 2 or weight.dim() != 2 or not hidden.is_contiguous() or not weight.is_contiguous():
         raise ValueError("hidden and weight must be contiguous 2-D tensors")
     if hidden.dtype != torch.bfloat16 or weight.dtype != torch.bfloat16:
         raise TypeError("hidden and weight must be bf16")
     if hidden.shape[1] != weight.shape[1]:
         raise ValueError("hidden and weight must have the same number of columns")
-    if target.dtype not in (torch.int64, torch.int32):
-        raise TypeError("target must be int64 or int32")
-    if target.dim() != 1 or target.shape[0] != hidden.shape[0] or not target.is_contiguous():
-        raise ValueError("target must be a contiguous 1-D tensor with one entry per row")
-    V = weight.shape[0]
-    return ce_params(hidden.shape[0], V, V, ignore_index, None, 0.0, CE_DT[torch.bfloat16], 0,
-                     1 if target.dtype == torch.int32 else 0)
+    n, V = hidden.shape[0], weight.shape[0]
+    return ce_params(n, V, V, ignore_index, None, 0.0, CE_DT[torch.bfloat16], 0, _check_target(target, n))
 
 
 def _linear_ws_bytes(p, hidden_dim, chunk_rows) -> int:
@@ -412,13 +417,13 @@ def flce_token_logprob(hidden, weight, target, *, bias=None, temperature=1.0, ig
     """(logp [n], entropy [n] or None, stats [n, 4]) of softmax((hidden
     weight^T + bias) / temperature) without the logits in memory: hidden
     [n, H] and weight [V, H] bf16, bias [V] fp32."""
-    p = _linear_params(hidden, weight, target, bias, ignore_index)
+    p = _linear_params(hidden, weight, target, ignore_index)
     n, H = hidden.shape
     call = _Call(hidden, (weight, target, bias, logp, entropy, stats), stream)
-    _vec("bias", bias, weight.shape[0], call.device)
+    _vec("bias", bias, weight.shape[0], call)
     logp, entropy, stats = _outputs(call, n, logp, entropy, stats, with_entropy)
     ws, nbytes = _workspace(call, ws, _linear_ws_bytes(p, H, 0))
-    call.run("flce_token_logprob", _lib.flce_token_logprob, _byref(p), H, float(temperature), _ptr(hidden), _ptr(weight), _ptr(bias),
+    call.run("flce_token_logprob", _byref(p), H, float(temperature), _ptr(hidden), _ptr(weight), _ptr(bias),
              _ptr(target), _ptr(logp), _ptr(entropy), _ptr(stats), _ptr(ws), nbytes)
     return logp, entropy, stats
 
@@ -432,13 +437,13 @@ def flce_token_logprob_backward(hidden, weight, target, stats, grad_logp, *, gra
     gradient (bf16) are held at a time: all of them by default where that
     takes at most 16 GB. ``grad_weight``: a buffer of either type; by
     default fp32. bf16 needs all rows in one chunk."""
-    p = _linear_params(hidden, weight, target, bias, ignore_index)
+    p = _linear_params(hidden, weight, target, ignore_index)
     (n, H), V = hidden.shape, weight.shape[0]
     call = _Call(hidden, (weight, target, stats, grad_logp, grad_entropy, bias, grad_hidden, grad_weight, grad_bias), stream)
-    _vec("bias", bias, V, call.device)
-    _vec("grad_logp", grad_logp, n, call.device)
-    _vec("grad_entropy", grad_entropy, n, call.device)
-    _stats(stats, n)
+    _vec("bias", bias, V, call)
+    _vec("grad_logp", grad_logp, n, call)
+    _vec("grad_entropy", grad_entropy, n, call)
+    _rows4("stats", stats, n, call)
     if chunk_rows is None:
         chunk_rows = _chunk_rows(n, V)
     if grad_hidden is None:
@@ -452,9 +457,9 @@ def flce_token_logprob_backward(hidden, weight, target, stats, grad_logp, *, gra
         raise ValueError("grad_weight must be a contiguous fp32 or bf16 tensor of weight's shape")
     if grad_bias is None and bias is not None:
         grad_bias = call.empty(V)
-    _vec("grad_bias", grad_bias, V, call.device)
+    _vec("grad_bias", grad_bias, V, call)
     ws, nbytes = _workspace(call, ws, _linear_ws_bytes(p, H, chunk_rows))
-    call.run("flce_token_logprob_backward", _lib.flce_token_logprob_backward, _byref(p), H, float(temperature), _ptr(hidden), _ptr(weight), _ptr(bias),
+    call.run("flce_token_logprob_backward", _byref(p), H, float(temperature), _ptr(hidden), _ptr(weight), _ptr(bias),
              _ptr(target), _ptr(stats), _ptr(grad_logp), _ptr(grad_entropy), _ptr(grad_hidden), _ptr(grad_weight),
              CE_DT[grad_weight.dtype], _ptr(grad_bias), chunk_rows, _ptr(ws), nbytes)
     return grad_hidden, grad_weight, grad_bias
