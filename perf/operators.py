@@ -369,7 +369,8 @@ def _own_preference(s, c):
     grad = torch.empty(s["logits"].shape, dtype=s["logits"].dtype, device="cuda")
     loss, seq_logp, grad = ce.ce_preference_fwd_bwd(s["logits"], s["target"], s["offsets"], ref_logp=s["ref_logp"],
                                                     loss_kind=c["kind"], beta=c["beta"],
-                                                    label_smoothing=c["smoothing"], length_normalize=c["normalize"],
+                                                    label_smoothing=c["smoothing"] if c["kind"] == "sigmoid" else 0.0,
+                                                    length_normalize=c["normalize"],
                                                     grad_output=s["grad_output"], grad=grad)
     return {"loss": loss, "seq_logp": seq_logp, "grad": grad}
 
