@@ -98,6 +98,17 @@ __device__ inline void tile_coords(const GemmArgs &g, int t, int &tm, int &tn) {
     else { tn = t % g.tiles_n; tm = t / g.tiles_n; }
 }
 
+// 32 bytes to a 32-byte aligned address: one whole sector a lane (rows of a tile
+// lie apart, so two 16-byte stores would send each sector to L2 twice).
+__device__ inline void st_sector(void *p, const uint4 &a, const uint4 &b) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+                 :: "l"(p), "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w) : "memory");
+}
+// rows of `ld` elements of `bytes` each from p on all start on a 32-byte boundary
+__device__ inline bool sector_rows(const void *p, int64_t ld, int bytes) {
+    return (((reinterpret_cast<uintptr_t>(p)) | static_cast<uintptr_t>(ld * bytes)) & 31u) == 0;
+}
+
 // One thread's 32 consecutive accumulator columns of one output row.
 // `orow` is the row of the output the tile row `row` is stored at.
 __device__ inline void epilogue_store(const GemmArgs &g, int row, int orow, int col0, const uint32_t (&v)[32],
@@ -108,6 +119,8 @@ __device__ inline void epilogue_store(const GemmArgs &g, int row, int orow, int 
         __nv_bfloat16 *o = reinterpret_cast<__nv_bfloat16 *>(g.out) + base + static_cast<int64_t>(orow) * g.ldo + col0;
         if (full && (g.ldo % 8) == 0) {
             uint4 *o4 = reinterpret_cast<uint4 *>(o);
+            const bool sectors = sector_rows(g.out, g.ldo, 2) && (base & 15) == 0;
+            uint4 held = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 uint4 w;
@@ -115,7 +128,9 @@ __device__ inline void epilogue_store(const GemmArgs &g, int row, int orow, int 
                 w.y = Fmt<CE_DT_BF16>::pack2(__uint_as_float(v[8 * q + 2]), __uint_as_float(v[8 * q + 3]));
                 w.z = Fmt<CE_DT_BF16>::pack2(__uint_as_float(v[8 * q + 4]), __uint_as_float(v[8 * q + 5]));
                 w.w = Fmt<CE_DT_BF16>::pack2(__uint_as_float(v[8 * q + 6]), __uint_as_float(v[8 * q + 7]));
-                o4[q] = w;
+                if (!sectors) o4[q] = w;
+                else if (q & 1) st_sector(o4 + q - 1, held, w);
+                held = w;
             }
         } else {
 #pragma unroll
@@ -288,8 +303,13 @@ __device__ inline void epilogue_lp_grad(const GemmArgs &g, int row, int col0, co
     }
     __nv_bfloat16 *o = reinterpret_cast<__nv_bfloat16 *>(g.out) + static_cast<int64_t>(row) * g.ldo + col0;
     if (col0 + 32 <= g.N) {  // the row stride is a multiple of 8
+        if (sector_rows(g.out, g.ldo, 2)) {
+            st_sector(o, Fmt<CE_DT_BF16>::pack(x), Fmt<CE_DT_BF16>::pack(x + 8));
+            st_sector(o + 16, Fmt<CE_DT_BF16>::pack(x + 16), Fmt<CE_DT_BF16>::pack(x + 24));
+        } else {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) reinterpret_cast<uint4 *>(o)[q] = Fmt<CE_DT_BF16>::pack(x + 8 * q);
+            for (int q = 0; q < 4; ++q) reinterpret_cast<uint4 *>(o)[q] = Fmt<CE_DT_BF16>::pack(x + 8 * q);
+        }
     } else {
 #pragma unroll
         for (int j = 0; j < 32; ++j)

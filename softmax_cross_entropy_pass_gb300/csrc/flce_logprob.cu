@@ -163,7 +163,7 @@ LpLayout lp_layout(int64_t n, int64_t V, int64_t H, int64_t chunk, bool backward
         }
         L.part = take(static_cast<size_t>(n) * L.tiles * 16);
     } else {
-        L.ldd = (V + 7) / 8 * 8;
+        L.ldd = (V + 15) / 16 * 16;  // rows on 32-byte boundaries
         L.splits = flce_dh_splits(chunk, H, V);
         L.rows = take(n * sizeof(LpMapRow));
         L.dz = take(static_cast<size_t>(chunk) * L.ldd * 2);
