@@ -131,6 +131,17 @@ constexpr int64_t kCompactAbove = 128;
 bool on(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 size_t up(size_t a, size_t b) { return (a + b - 1) / b * b; }
 
+// Split count of grad_hidden = dZ W: with few output tiles (128 x 256) as many
+// parts of K = V as give every SM of a full GB300 a tile (GB300, 16 x 4096 x
+// 128256, 16 tiles: the whole backward 662 us with 4 parts, 618 with 9),
+// otherwise the fused-linear path's rule. A function of the sizes alone.
+int lp_dh_splits(int64_t chunk, int64_t H, int64_t V) {
+    const int64_t tiles = ((chunk + 127) / 128) * ((H + 255) / 256);
+    const int least = flce_dh_splits(chunk, H, V);
+    const int want = static_cast<int>(152 / tiles);
+    return want > least ? gemm_fit_ksplit(static_cast<int>(V), want) : least;
+}
+
 struct LpLayout {
     size_t idx, pos, cnt, tgt, hc;       // compaction
     size_t part, xy;                     // forward
@@ -164,7 +175,7 @@ LpLayout lp_layout(int64_t n, int64_t V, int64_t H, int64_t chunk, bool backward
         L.part = take(static_cast<size_t>(n) * L.tiles * 16);
     } else {
         L.ldd = (V + 15) / 16 * 16;  // rows on 32-byte boundaries
-        L.splits = flce_dh_splits(chunk, H, V);
+        L.splits = lp_dh_splits(chunk, H, V);
         L.rows = take(n * sizeof(LpMapRow));
         L.dz = take(static_cast<size_t>(chunk) * L.ldd * 2);
         L.dh = take(L.splits > 1 ? static_cast<size_t>(L.splits) * chunk * H * 4 : 0);
