@@ -63,7 +63,7 @@ flce_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t full[kFewMaxStages], empty[kFewMaxStages], tfull[kFewAcc], tempty[kFewAcc];
     __shared__ uint32_t tmem_slot;
-    __shared__ int abort_flag;
+    __shared__ int abort_flag, drain_abort;
     __shared__ int tgt[kFewMaxRows];
     __shared__ float red_mem[kFewMaxRows * 4 * 3];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -90,7 +90,7 @@ flce_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
             mbar_init(smem_u32(&tfull[a]), 1);
             mbar_init(smem_u32(&tempty[a]), 4 * nsets);
         }
-        abort_flag = 0;
+        abort_flag = drain_abort = 0;
         if (blockIdx.x == 0) *g.status = 0u;  // no wait can have given up yet (they run for 2 s)
         fence_mbar_init_cluster();
         tma_prefetch_desc(&tmW);
@@ -135,6 +135,12 @@ flce_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
                         ++round;
                     }
                 }
+            }
+            // the copies in flight, with a limit of their own where another wait gave up
+            const uint32_t used = round > 0 ? static_cast<uint32_t>(g.stages) : s;
+            for (uint32_t i = 0; i < used; ++i) {
+                const uint32_t uses = round + (i < s ? 1u : 0u);  // of stage i
+                mbar_wait_bounded<false>(smem_u32(&full[i]), (uses - 1) & 1u, &drain_abort);
             }
         }
     } else if (warp == 1) {

@@ -220,6 +220,7 @@ ce_status flce_token_logprob(const ce_params *p, int64_t H, float temperature, c
     const int64_t n = p->n_rows, V = p->vocab;
     if (n == 0) return CE_OK;
     if (!hidden || !weight || !target || (!logp && !entropy && !stats)) return CE_ERR_INVALID_ARG;
+    if (!on(target, p->target_is_int32 ? 4 : 8)) return CE_ERR_INVALID_ARG;
     if (!on(hidden, 16) || !on(weight, 16) || !on(bias, 16) || !on(logp, 4) || !on(entropy, 4) || !on(stats, 16))
         return CE_ERR_INVALID_ARG;
     const LpLayout L = lp_layout(n, V, H, 0, false);
@@ -303,6 +304,7 @@ ce_status flce_token_logprob_backward(const ce_params *p, int64_t H, float tempe
     if (!grad_weight || !on(grad_weight, 16) || (grad_bias && !on(grad_bias, 4)) || !on(bias, 16)) return CE_ERR_INVALID_ARG;
     if (n > 0 && (!hidden || !weight || !target || !stats || !grad_hidden || (!grad_logp && !grad_entropy)))
         return CE_ERR_INVALID_ARG;
+    if (!on(target, p->target_is_int32 ? 4 : 8)) return CE_ERR_INVALID_ARG;
     if (!on(hidden, 16) || !on(weight, 16) || !on(grad_hidden, 16) || !on(stats, 16) || !on(grad_logp, 4) ||
         !on(grad_entropy, 4))
         return CE_ERR_INVALID_ARG;

@@ -52,6 +52,8 @@ ce_status lp_check_grad(const ce_params *p, const void *x, const void *grad, int
     return (b - a) % esz == 0 && col >= p->vocab && col <= p->ld - p->vocab ? CE_OK : CE_ERR_INVALID_ARG;
 }
 
+bool target_ok(const ce_params *p, const void *target) { return target && on(target, p->target_is_int32 ? 4 : 8); }
+
 LpArgs lp_args(const ce_params *p, float temperature, const void *logits, const void *target) {
     LpArgs a{};
     a.x = logits;
@@ -81,7 +83,7 @@ ce_status ce_token_logprob(const ce_params *p, float temperature, const void *lo
     if (st != CE_OK) return st;
     if (p->n_rows == 0) return CE_OK;
     if (!logp && !entropy && !stats) return CE_ERR_INVALID_ARG;
-    if (!logits || !target || !on(logits, lp_elem_bytes(p))) return CE_ERR_INVALID_ARG;
+    if (!logits || !target_ok(p, target) || !on(logits, lp_elem_bytes(p))) return CE_ERR_INVALID_ARG;
     if (!on(logp, 4) || !on(entropy, 4) || !on(stats, 16)) return CE_ERR_INVALID_ARG;
     LpArgs a = lp_args(p, temperature, logits, target);
     a.logp = logp;
@@ -99,7 +101,7 @@ ce_status ce_token_logprob_backward(const ce_params *p, float temperature, const
     if ((st = lp_check_grad(p, logits, grad, ld_grad)) != CE_OK) return st;
     if (p->n_rows == 0) return CE_OK;
     if (!grad_logp && !grad_entropy) return CE_ERR_INVALID_ARG;
-    if (!logits || !target || !stats || !grad || !on(logits, lp_elem_bytes(p))) return CE_ERR_INVALID_ARG;
+    if (!logits || !target_ok(p, target) || !stats || !grad || !on(logits, lp_elem_bytes(p))) return CE_ERR_INVALID_ARG;
     if (!on(stats, 16) || !on(grad_logp, 4) || !on(grad_entropy, 4)) return CE_ERR_INVALID_ARG;
     LpArgs a = lp_args(p, temperature, logits, target);
     a.stats = reinterpret_cast<float4 *>(const_cast<float *>(stats));
@@ -125,7 +127,7 @@ ce_status ce_policy_fwd_bwd(const ce_params *p, const ce_policy_params *q, const
     if ((st = lp_check_ws(ws, ws_size, ws_bytes(p->n_rows))) != CE_OK) return st;
     if ((st = lp_check_grad(p, logits, grad, ld_grad)) != CE_OK) return st;
     if (!loss && (p->n_rows > 0 || p->reduction != CE_RED_NONE)) return CE_ERR_INVALID_ARG;
-    if (p->n_rows > 0 && (!logits || !target || !advantage || !grad || !on(logits, lp_elem_bytes(p))))
+    if (p->n_rows > 0 && (!logits || !target_ok(p, target) || !advantage || !grad || !on(logits, lp_elem_bytes(p))))
         return CE_ERR_INVALID_ARG;
     if (!on(advantage, 4) || !on(old_logp, 4) || !on(ref_logp, 4) || !on(row_weight, 4) || !on(grad_output, 4) ||
         !on(loss, 4) || !on(row_stats, 16))
@@ -184,7 +186,7 @@ ce_status ce_preference_fwd_bwd(const ce_params *p, const ce_preference_params *
     if ((st = lp_check_ws(ws, ws_size, preference_ws(p->n_rows, q->n_pairs))) != CE_OK) return st;
     if ((st = lp_check_grad(p, logits, grad, ld_grad)) != CE_OK) return st;
     if (!offsets || (!loss && (q->n_pairs > 0 || p->reduction != CE_RED_NONE))) return CE_ERR_INVALID_ARG;
-    if (p->n_rows > 0 && (!logits || !target || !grad || !on(logits, lp_elem_bytes(p)))) return CE_ERR_INVALID_ARG;
+    if (p->n_rows > 0 && (!logits || !target_ok(p, target) || !grad || !on(logits, lp_elem_bytes(p)))) return CE_ERR_INVALID_ARG;
     if (!on(offsets, q->offsets_are_int32 ? 4 : 8) || !on(ref_logp, 4) || !on(grad_output, 4) || !on(loss, 4) ||
         !on(seq_logp, 4))
         return CE_ERR_INVALID_ARG;

@@ -38,7 +38,7 @@ struct LpSmem {
     float4 slot[2][kLpMaxCluster];  // each CTA's {m, s, u, target logit}
     LpGrad grad[2];                 // the row's gradient scalars
     float xy[2];
-    int abort;
+    int abort, drain_abort;           // a wait gave up; the wait for copies in flight did
     int n_live, n_dead;               // this cluster's rows of the window
     int live[kLpList + 1], dead[kLpList + 1];
     uint32_t mask[kLpWindow / 32];    // which rows of the window take part
@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtasPerSm) lp_rows_kernel(LpArg
             mbar_init(smem_u32(&S.done[p]), kLpWarps);
             mbar_init(smem_u32(&S.taken[p]), 1);
         }
-        S.abort = 0;
+        S.abort = S.drain_abort = 0;
         fence_mbar_init_cluster();
     }
     __syncthreads();
@@ -619,7 +619,8 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtasPerSm) lp_rows_kernel(LpArg
     if (!single && w0 + window < a.n_rows) __syncthreads();  // the lists are rebuilt
     }
     if (warp == kLpWarps && lane == 0) {
-        // drain: every issued copy has landed before the CTA may exit
+        // drain: every issued copy has landed before the CTA may exit (waited for
+        // with a limit of its own where another wait gave up)
         for (uint32_t i = 0; i < kLpSlots && i < issued; ++i) {
             // the last copy of each used slot, latest first
             if (pos.slot == 0) {
@@ -627,7 +628,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtasPerSm) lp_rows_kernel(LpArg
                 pos.phase ^= 1u;
             }
             --pos.slot;
-            mbar_wait_bounded<false, kStreamSleepP>(smem_u32(&S.full[pos.slot]), pos.phase, abort);
+            mbar_wait_bounded<false, kStreamSleepP>(smem_u32(&S.full[pos.slot]), pos.phase, &S.drain_abort);
         }
     }
     // ---------------------------------------------------- batch loss (last cluster)

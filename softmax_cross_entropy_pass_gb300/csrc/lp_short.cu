@@ -208,6 +208,8 @@ __global__ void __launch_bounds__(kShortThreads, kShortCtasPerSm) lp_short_kerne
         if (warps > 1) {
             group_sync(1 + gid, G);
             g = grads[gid];
+        } else {
+            __syncwarp();  // every lane has the target's logit: it may be written over
         }
         // ---------------------------------------------------- gradient
         if (((reinterpret_cast<uintptr_t>(xrow) ^ reinterpret_cast<uintptr_t>(grow)) & 15u) != 0) {

@@ -22,6 +22,7 @@ from __future__ import annotations
 import ctypes
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import CE_DT, CE_RED, CEError, _check, _lib, ce_params, ce_scale_grad
 
@@ -310,6 +311,7 @@ class TokenLogprobFunction(torch.autograd.Function):
         return (logp, entropy) if with_entropy else logp
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad_logp, grad_entropy=None):
         if grad_logp is None and grad_entropy is None:
             return None, None, None, None, None, None
@@ -346,6 +348,7 @@ class _FormedGradientFunction(torch.autograd.Function):
         return loss if per_row else loss.reshape(())
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad_out):
         _once(ctx)
         (grad,) = ctx.saved_tensors
@@ -487,6 +490,7 @@ class LinearTokenLogprobFunction(torch.autograd.Function):
         return (logp, entropy) if with_entropy else logp
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad_logp, grad_entropy=None):
         hidden, weight, bias, target, stats = ctx.saved_tensors
         if grad_logp is None and grad_entropy is None:

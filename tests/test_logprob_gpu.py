@@ -603,6 +603,17 @@ def test_gradient_beside_the_logits(ce):
         ce.ce_policy_fwd_bwd(wide[:, :1001], t, adv, grad=wide[:, 1000:2001])
 
 
+def test_no_second_derivative(ce):
+    """A second differentiation is refused, not answered with nothing."""
+    x, t = torch.randn(4, 50, device="cuda", requires_grad=True), torch.zeros(4, dtype=torch.int64, device="cuda")
+    (g,) = torch.autograd.grad(ce.token_logprob(x, t).sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError):
+        g.square().sum().backward()
+    (g,) = torch.autograd.grad(ce.policy_loss(x, t, torch.ones(4, device="cuda")), x, create_graph=True)
+    with pytest.raises(RuntimeError):
+        g.square().sum().backward()
+
+
 def test_argument_errors(ce):
     x, t = torch.randn(4, 10, device="cuda"), torch.zeros(4, dtype=torch.int64, device="cuda")
     adv = torch.zeros(4, device="cuda")

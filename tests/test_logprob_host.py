@@ -130,17 +130,17 @@ def _backward(ce, p, t=1.0, x=FAKE, tgt=FAKE, stats=FAKE, g=FAKE, h=None, grad=F
     return ce._lib.ce_token_logprob_backward(ctypes.byref(p), t, x, tgt, stats, g, h, grad, ld, None)
 
 
-def _policy(ce, p, q=(1.0, 0.2, 0.2, 0.0, 0.0, 0), x=FAKE, adv=FAKE, old=None, ref=None, w=None, up=None, loss=FAKE,
+def _policy(ce, p, q=(1.0, 0.2, 0.2, 0.0, 0.0, 0), x=FAKE, tgt=FAKE, adv=FAKE, old=None, ref=None, w=None, up=None, loss=FAKE,
             stats=None, grad=FAKE, ld=100, ws=WS, nb=NB):
     q = ce.ce_policy_params(*q)
-    return ce._lib.ce_policy_fwd_bwd(ctypes.byref(p), ctypes.byref(q), x, FAKE, adv, old, ref, w, up, loss, stats, grad,
+    return ce._lib.ce_policy_fwd_bwd(ctypes.byref(p), ctypes.byref(q), x, tgt, adv, old, ref, w, up, loss, stats, grad,
                                      ld, ws, nb, None)
 
 
-def _preference(ce, p, q=(2, 0, 0, 0, 0.1, 0.0, 0), x=FAKE, off=FAKE, ref=None, loss=FAKE, grad=FAKE, ld=100, ws=WS,
+def _preference(ce, p, q=(2, 0, 0, 0, 0.1, 0.0, 0), x=FAKE, tgt=FAKE, off=FAKE, ref=None, loss=FAKE, grad=FAKE, ld=100, ws=WS,
                 nb=NB):
     q = ce.ce_preference_params(*q)
-    return ce._lib.ce_preference_fwd_bwd(ctypes.byref(p), ctypes.byref(q), x, FAKE, off, ref, None, loss, None, grad, ld,
+    return ce._lib.ce_preference_fwd_bwd(ctypes.byref(p), ctypes.byref(q), x, tgt, off, ref, None, loss, None, grad, ld,
                                          ws, nb, None)
 
 
@@ -157,6 +157,9 @@ def test_parameter_refusals(ce, call):
         assert call(ce, _p(ce, **kw)) == ce.CE_ERR_UNSUPPORTED, kw
     assert call(ce, _p(ce), x=ctypes.c_void_p(0x100001)) == ce.CE_ERR_INVALID_ARG   # not element aligned
     assert call(ce, _p(ce), x=None) == ce.CE_ERR_INVALID_ARG
+    assert call(ce, _p(ce), tgt=None) == ce.CE_ERR_INVALID_ARG
+    assert call(ce, _p(ce), tgt=ctypes.c_void_p(0x100004)) == ce.CE_ERR_INVALID_ARG   # int64 targets
+    assert call(ce, _p(ce, tgt=1), tgt=ctypes.c_void_p(0x100002)) == ce.CE_ERR_INVALID_ARG
 
 
 @pytest.mark.parametrize("t", [0.0, -1.0, math.nan, math.inf, 1e-5, 1e5])
@@ -295,7 +298,7 @@ def test_linear_refusals_on_host(ce, call):
     assert call(ce, p, H=0) == bad and call(ce, p, H=60) == uns
     assert call(ce, p, t=0.0) == bad and call(ce, p, t=math.nan) == bad
     odd = ctypes.c_void_p(0x100008)
-    for kw in (dict(h=None), dict(w=None), dict(tgt=None), dict(h=odd), dict(w=odd), dict(b=odd), dict(stats=odd)):
+    for kw in (dict(h=None), dict(w=None), dict(tgt=None), dict(tgt=ctypes.c_void_p(0x100004)), dict(h=odd), dict(w=odd), dict(b=odd), dict(stats=odd)):
         assert call(ce, p, **kw) == bad, kw
     assert call(ce, p, ws=None) == ce.CE_ERR_WORKSPACE
     assert call(ce, p, ws=ctypes.c_void_p(0x4000010)) == ce.CE_ERR_WORKSPACE
