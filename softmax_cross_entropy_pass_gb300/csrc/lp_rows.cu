@@ -25,6 +25,7 @@ constexpr int kLpThreads = kLpConsumers + 64;  // and the producer and the scala
 constexpr int kLpSlots = 6;
 constexpr int kLpCtasPerSm = 2;
 constexpr int kLpMaxCluster = 8;
+constexpr int kLpLagChunks = 3;  // two such rows fill the ring
 // Rows are shared out per window of at most kLpWindow rows and kLpList rows a cluster
 constexpr int kLpWindow = 8192;
 constexpr int kLpList = 256;
@@ -191,7 +192,19 @@ struct RingPos {
     }
 };
 
-template <int DT, int MODE, bool ENT>
+template <class T>
+__device__ inline void swap_values(T &a, T &b) {
+    const T c = a;
+    a = b;
+    b = c;
+}
+
+// LAG: rows of at most kLpLagChunks chunks. Their second pass comes after the
+// next row's first, both rows in the ring, so that a row's statistics are merged
+// meanwhile (8192 bf16 rows, without / with entropy: 10000 columns 115 / 128 us
+// to 97 / 113, 16384 121 / 135 to 105 / 120, 24000 154 / 173 to 146 / 171).
+// Compiled apart, since what it carries from row to row costs longer rows 3%.
+template <int DT, int MODE, bool ENT, bool LAG>
 __global__ void __launch_bounds__(kLpThreads, kLpCtasPerSm) lp_rows_kernel(LpArgs a) {
     using F = Fmt<DT>;
     constexpr int VEC = F::kVec, KB = F::kBytes, NCT = kLpConsumers;
@@ -256,7 +269,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtasPerSm) lp_rows_kernel(LpArg
     const int64_t window = single ? a.n_rows : (kLpList * nq < kLpWindow ? kLpList * nq : kLpWindow);
     RingPos pos{0u, 0u};     // producer and consumers
     uint32_t issued = 0;     // producer: copies so far
-    uint32_t j = 0;          // live rows done (their parities)
+    uint32_t j = 0, j2 = 0;  // live rows done (their parities), and with LAG second passes
     bool have_norm = false;  // scalar warp: the batch's weight sum, this cluster's row losses (lane 0 of its first CTA)
     float w_sum = 0.f;
     double cta_sum = 0.0;
@@ -281,7 +294,11 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtasPerSm) lp_rows_kernel(LpArg
         const int64_t t = load_target(a.target, a.tgt32, q0);  // at most one cluster a row is launched
         n_live = row_live(q0, t) ? 1 : 0;
         n_dead = POLICY ? 1 - n_live : 0;
-        if (n_live == 0 && tid == 0 && rank == 0) dead_outputs(q0, t);
+        if (tid == 0) {
+            S.live[0] = S.dead[0] = static_cast<int>(q0);
+            if (n_live == 0 && rank == 0) dead_outputs(q0, t);
+        }
+        __syncthreads();
     } else {
         const int cnt = static_cast<int>(a.n_rows - w0 < window ? a.n_rows - w0 : window);
         const int words = (cnt + 31) / 32;
@@ -345,8 +362,8 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtasPerSm) lp_rows_kernel(LpArg
         n_live = S.n_live;
         n_dead = POLICY ? S.n_dead : 0;
     }
-    const auto live_row = [&](int i) { return single ? q0 : static_cast<int64_t>(S.live[i]); };
-    const auto dead_row = [&](int i) { return single ? q0 : static_cast<int64_t>(S.dead[i]); };
+    const auto live_row = [&](int i) { return static_cast<int64_t>(S.live[i]); };
+    const auto dead_row = [&](int i) { return static_cast<int64_t>(S.dead[i]); };
 
     if (warp == kLpWarps) {
         // -------------------------------------------------------------- producer
@@ -462,14 +479,20 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtasPerSm) lp_rows_kernel(LpArg
     } else {
         // -------------------------------------------------------------- consumers
         const float k = a.k;
-        int64_t t_next = n_live > 0 ? load_target(a.target, a.tgt32, live_row(0)) : 0;
-        for (int li = 0; li < n_live; ++li) {
-            const int64_t row = live_row(li), t = t_next;
-            if (li + 1 < n_live) t_next = load_target(a.target, a.tgt32, live_row(li + 1));
-            const char *xrow = xbase + row * xstep;
+        // the row's target column in this slice (it may lie outside), read a row ahead
+        const auto target_column = [&](int i) { return static_cast<int>(load_target(a.target, a.tgt32, live_row(i))) - lo; };
+        int yc_next = n_live > 0 ? target_column(0) : 0;
+        constexpr int lag = LAG ? 1 : 0;
+        uint32_t held = 0, keep_slot = 0;           // the second pass's: chunks that need held exponents, its first kept slot
+        uint32_t held_before = 0, keep_before = 0;  // and those of the row before
+        int yc = 0, yc_before = 0;
+        for (int li = 0; li < n_live + lag; ++li) {
+            if (!LAG || li < n_live) {
+            yc = yc_next;
+            if (li + 1 < n_live) yc_next = target_column(li + 1);
+            const char *xrow = xbase + live_row(li) * xstep;
             const LpGeom gm = lp_geom<KB>(xrow, L);
             const int nvec = gm.nvec, nch = gm.nch, vlo = gm.head, tail0 = gm.tail0, nedge = vlo + L - tail0;
-            const int yc = static_cast<int>(t) - lo;  // target column of the slice (it may lie outside)
             const int y = yc >= vlo && yc < tail0 ? yc - vlo : -1;
             // the chunk with the target's column, for the warp that reads its vector
             const int y_thread = y >= 0 ? (y / VEC) % NCT : -32;
@@ -481,7 +504,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtasPerSm) lp_rows_kernel(LpArg
                 mbar_wait_bounded<false, kStreamSleepConsumer>(smem_u32(&S.taken[rp]), ((j >> 1) - 1u) & 1u, abort);
             // ------------------------------------------------ pass 1: statistics
             LpState st = lp_empty();
-            uint32_t held = 0, keep_slot = 0;  // the first kept chunk's slot
+            held = 0;
             for (int c = 0; c < nch; ++c) {
                 if (c == nch - nkeep) keep_slot = pos.slot;
                 mbar_wait_bounded<false, kStreamSleepConsumer>(smem_u32(&S.full[pos.slot]), pos.phase, abort);
@@ -514,8 +537,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtasPerSm) lp_rows_kernel(LpArg
                         plain = add_any<DT, ENT, VPT, false>(st, raw, n, k, y_warp, own);
                     }
                 }
-                // chunks whose exponents the second pass has to hold as well (31: any later one)
-                if (POLICY && ENT && !plain) held |= 1u << min(c, 31);
+                if (POLICY && ENT && !plain) held |= 1u << min(c, 31);  // 31: any later one
                 __syncwarp();
                 if (lane == 0 && c < nch - nkeep) mbar_arrive(smem_u32(&S.empty[pos.slot]));
                 pos.next();
@@ -531,10 +553,23 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtasPerSm) lp_rows_kernel(LpArg
             parts[rp * NCT + tid] = make_float4(st.m, st.s, st.u, 0.f);
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&S.done[rp]));
-            const uint32_t ph = (j >> 1) & 1u;
             ++j;
+            }
             if (!POLICY) continue;
-            mbar_wait_bounded<false, kStreamSleepConsumer>(smem_u32(&S.taken[rp]), ph, abort);
+            if (LAG) {  // on to the row before
+                swap_values(yc, yc_before);
+                swap_values(held, held_before);
+                swap_values(keep_slot, keep_before);
+                if (li == 0) continue;
+            }
+            const int64_t row = live_row(li - lag);
+            const char *xrow = xbase + row * xstep;
+            const LpGeom gm = lp_geom<KB>(xrow, L);
+            const int nvec = gm.nvec, nch = gm.nch, vlo = gm.head, tail0 = gm.tail0;
+            const int y = yc >= vlo && yc < tail0 ? yc - vlo : -1;
+            const int nkeep = min(nch, kLpSlots);
+            const uint32_t at = LAG ? j2++ : j - 1u, rp = at & 1u;
+            mbar_wait_bounded<false, kStreamSleepConsumer>(smem_u32(&S.taken[rp]), (at >> 1) & 1u, abort);
             const LpGrad g = S.grad[rp];
             // ------------------------------------------------ pass 2: gradient
             char *grow = gbase + row * gstep;
@@ -623,7 +658,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtasPerSm) lp_rows_kernel(LpArg
                 F::store1(grow, c, c == yc ? g.dy : lp_grad_elem<ENT>(g, F::load1(xrow, c), k));
             }
             // one of the rows that take no part, between two that do
-            if (li < n_dead) zero_row(dead_row(li));
+            if (li - lag < n_dead) zero_row(dead_row(li - lag));
         }
         if (POLICY)
             for (int di = n_live; di < n_dead; ++di) zero_row(dead_row(di));
@@ -678,12 +713,15 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtasPerSm) lp_rows_kernel(LpArg
 }
 
 template <int DT>
-static const void *rows_fn(int mode, bool ent) {
+static const void *rows_fn(int mode, bool ent, bool lag) {
     if (mode == LP_FWD)
-        return ent ? reinterpret_cast<const void *>(&lp_rows_kernel<DT, LP_FWD, true>)
-                   : reinterpret_cast<const void *>(&lp_rows_kernel<DT, LP_FWD, false>);
-    return ent ? reinterpret_cast<const void *>(&lp_rows_kernel<DT, LP_POLICY, true>)
-               : reinterpret_cast<const void *>(&lp_rows_kernel<DT, LP_POLICY, false>);
+        return ent ? reinterpret_cast<const void *>(&lp_rows_kernel<DT, LP_FWD, true, false>)
+                   : reinterpret_cast<const void *>(&lp_rows_kernel<DT, LP_FWD, false, false>);
+    if (lag)
+        return ent ? reinterpret_cast<const void *>(&lp_rows_kernel<DT, LP_POLICY, true, true>)
+                   : reinterpret_cast<const void *>(&lp_rows_kernel<DT, LP_POLICY, false, true>);
+    return ent ? reinterpret_cast<const void *>(&lp_rows_kernel<DT, LP_POLICY, true, false>)
+               : reinterpret_cast<const void *>(&lp_rows_kernel<DT, LP_POLICY, false, false>);
 }
 
 // The launch attributes of a kernel and cluster size on the current context,
@@ -731,16 +769,17 @@ static cudaError_t rows_ready(const void *fn, int cl, int *clusters, int *sms) {
 
 cudaError_t launch_lp_rows(const LpArgs &a0, int dtype, int mode, bool entropy, bool after_prep, cudaStream_t s) {
     LpArgs a = a0;
-    const void *fn = dtype == CE_DT_F32 ? rows_fn<CE_DT_F32>(mode, entropy)
-                   : dtype == CE_DT_BF16 ? rows_fn<CE_DT_BF16>(mode, entropy) : rows_fn<CE_DT_F16>(mode, entropy);
     const int64_t row_bytes = a.vocab * (dtype == CE_DT_F32 ? 4 : 2);
+    const bool lag = mode == LP_POLICY && row_bytes <= kLpLagChunks * kStreamChunk;
+    const void *fn = dtype == CE_DT_F32 ? rows_fn<CE_DT_F32>(mode, entropy, lag)
+                   : dtype == CE_DT_BF16 ? rows_fn<CE_DT_BF16>(mode, entropy, lag) : rows_fn<CE_DT_F16>(mode, entropy, lag);
     int clusters = 0, sms = 0;
     cudaError_t e = rows_ready(fn, 1, &clusters, &sms);
     if (e != cudaSuccess) return e;
     // Rows of up to 16 KB: a group of warps a row (GB300, 8192 rows with the
     // entropy, forward / policy: 2 KB rows 17 / 39 us against 39 / 91 here, 8 KB
     // 27 / 58 against 46 / 108, 16 KB 48 / 95 against 57 / 137; at 32 KB, with
-    // groups of eight warps, 80 / 192 against 74 / 166).
+    // groups of eight warps, 80 / 192 against 66 / 120).
     if (lp_short_takes(a.vocab, dtype)) return launch_lp_short(a, dtype, mode, entropy, after_prep, sms, s);
     const int64_t slots = static_cast<int64_t>(sms) * kLpCtasPerSm;
     int cl = 1;

@@ -354,6 +354,33 @@ def test_policy(ce, shape, dtype, form):
     outside_unchanged(buf, x_in, off, v)
 
 
+@pytest.mark.parametrize("row_kb", [17, 24, 32, 33, 47.9, 48, 48.1, 60])
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("ignored", [0.0, 0.6])
+def test_policy_rows_of_a_few_chunks(ce, row_kb, dtype, ignored):
+    """Several rows a CTA, of one to four chunks, that take part and that do not in any order; other alignments too."""
+    n, v = 1300, int(row_kb * 1024) // (4 if dtype == "f32" else 2)
+    lo, hi, ent = f32(0.2), f32(0.28), f32(0.01)
+    for ld, off, gld, goff in ((v, 0, v, 0), (v + 5, 3, v + 8, 2)):
+        g, buf, x, t = make(n, v, dtype, v + off, ld, off, ignored=ignored, int32=off == 3)
+        old, ref, adv, w = policy_inputs(g, x, t, 1.0, lo, hi)
+        kw = dict(old_logp=old, ref_logp=ref, row_weight=w, clip_low=lo, clip_high=hi, kl_coef=f32(0.05), entropy_coef=ent,
+                  reduction="sum")
+        want = L.policy_ref(x, t, adv, old, ref, w, lo, hi, f32(0.05), ent, 1.0, "sum", None)
+        out = torch.full((n, gld), 7.0, dtype=DT[dtype], device="cuda")
+        stats = torch.full((n, 4), 7.0, device="cuda")
+        loss, grad = ce.ce_policy_fwd_bwd(x, t, adv, grad=out[:, goff:goff + v], row_stats=stats, **kw)
+        L.check(loss, want["loss"], want["tol_loss"], "loss")
+        L.check(grad, want["grad"], want["tol_grad"], "gradient")
+        L.check(stats, want["stats"], want["tol_stats"], "row statistics")
+        outside_unchanged(out, torch.full_like(out, 7.0), goff, v)
+        before = buf.clone()
+        loss2, _ = ce.ce_policy_fwd_bwd(x, t, adv, **kw)
+        L.check(x, want["grad"], want["tol_grad"], "gradient in place")
+        assert torch.equal(loss2, loss)
+        outside_unchanged(buf, before, off, v)
+
+
 def test_policy_on_the_clip_border_and_beyond(ce):
     """Ratio exactly 1 with a clip range of no width: the unclipped slope. Advantage 0: no gradient. Far ratios."""
     x = torch.randn(6, 1000, device="cuda")
