@@ -10,7 +10,8 @@
 // its second pass reads the last chunks of the row where they still lie in
 // the ring and the earlier ones, last first, from L2 again, so HBM sees one
 // read and one write. The ring is not tied to a row, so copies go on while a
-// row's statistics are merged. Every wait is bounded.
+// row's statistics are merged; of rows that fill no more than half of it, the
+// next one's first pass comes in between. Every wait is bounded.
 #include <mutex>
 
 #include "ce_host.h"
