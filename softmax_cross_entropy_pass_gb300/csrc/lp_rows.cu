@@ -136,7 +136,7 @@ __device__ inline bool add_any(LpState &st, const uint4 (&raw)[NV], int n, float
     for (int i = 0; i < (ALL ? NV : n); ++i) {
         uint4 r = raw[0];
 #pragma unroll
-        for (int n = 1; n < NV; ++n) r = n == i ? raw[n] : r;
+        for (int v = 1; v < NV; ++v) r = v == i ? raw[v] : r;
         float x[Fmt<DT>::kVec];
         Fmt<DT>::unpack(r, x);
         lp_add<ENT, Fmt<DT>::kVec>(st, x, Fmt<DT>::vmax(r), k);
