@@ -65,16 +65,25 @@ __device__ inline float take_out(uint32_t addr) {
     return Fmt<DT>::load1(&b, 0);
 }
 
-// Add NV vectors of one thread to its statistics: one packed FMA an exponent
-// pair, a' = x k - mu with mu = m k rounded. The FMA rounds a' alone, and what
-// mu's rounding shifted (the same for every term) is taken out of the chunk's
-// sums, so the sums are as exact as those of (x - m) k. With the entropy, a
-// logit that is -inf (or so low that a' overflows) makes 0 * inf = NaN in u:
-// without CLAMP false is returned then, with st moved to the new maximum but
-// nothing added; with it exponents are held at kLpMinExp, and `low` counts
-// them. Either returns false where mu is not finite. ALL: every vector counts;
-// else the first n do, and the others hold -inf.
-template <int DT, bool ENT, int NV, bool CLAMP, bool ALL>
+// How add_vectors forms its exponents.
+// DIFF false: one packed FMA a pair, a' = x k - mu with mu = m k rounded. The FMA
+//   rounds a' alone. What mu's rounding shifted, the same for every term, is
+//   taken out of the vectors' sums by 2^-shift to second order: shift is at most
+//   half a unit in the last place of mu, 2^-7 while |mu| < kLpFmaMax, so the rest
+//   is below (2^-7 ln 2)^3 / 6 = 2.7e-8 of a term. It grows with mu^3 (from 2^25
+//   on a shift is no longer small against 1), so a larger |mu| takes the
+//   difference. With the entropy, a logit that is -inf makes 0 * inf = NaN in u,
+//   and the vectors are taken again with the difference.
+// DIFF true: (x - m) k, the difference first, at any finite m: a packed operation
+//   more a pair, and with the entropy exponents held at kLpMinExp, which `low`
+//   counts. (8192 x 128256 bf16, all chunks in this form instead of the first:
+//   forward 300 us against 302, with the entropy 361 against 310.)
+constexpr float kLpFmaMax = 131072.f;
+
+// Add NV vectors of one thread to its statistics. False where the form does not
+// take them, with st moved to the new maximum but nothing added. ALL: every
+// vector counts; else the first n do, and the others hold -inf.
+template <int DT, bool ENT, int NV, bool DIFF, bool ALL>
 __device__ inline bool add_vectors(LpState &st, const uint4 (&raw)[NV], int n, float k, int &low) {
     using F = Fmt<DT>;
     constexpr int VEC = F::kVec;
@@ -83,8 +92,8 @@ __device__ inline bool add_vectors(LpState &st, const uint4 (&raw)[NV], int n, f
     for (int i = 1; i < NV; ++i) cm = fmaxf(cm, F::vmax(raw[i]));
     if (cm > st.m) lp_rebase<ENT>(st, cm, k);
     const float mu = st.m * k;
-    if (!(fabsf(mu) < 1e38f)) return false;
-    const F2 kk = f2(k, k), nm = f2(-mu, -mu);
+    if (DIFF ? !(fabsf(st.m) < INFINITY) : !(fabsf(mu) < kLpFmaMax)) return false;
+    const F2 kk = f2(k, k), nm = DIFF ? f2(st.m, st.m) : f2(-mu, -mu);
     F2 s2[2] = {f2(0.f, 0.f), f2(0.f, 0.f)}, u2[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -93,8 +102,9 @@ __device__ inline bool add_vectors(LpState &st, const uint4 (&raw)[NV], int n, f
         F::unpack(raw[i], x);
 #pragma unroll
         for (int p = 0; p < VEC / 2; ++p) {
-            F2 e = f2_fma(f2(x[2 * p], x[2 * p + 1]), kk, nm);
-            if (CLAMP) {
+            const F2 xx = f2(x[2 * p], x[2 * p + 1]);
+            F2 e = DIFF ? f2_mul(f2_sub(xx, nm), kk) : f2_fma(xx, kk, nm);
+            if (DIFF && ENT) {
                 float a0, a1;
                 f2_split(e, a0, a1);
                 a0 = lp_clamp(a0);
@@ -107,15 +117,21 @@ __device__ inline bool add_vectors(LpState &st, const uint4 (&raw)[NV], int n, f
             if (ENT) u2[p & 1] = f2_fma(ex, e, u2[p & 1]);
         }
     }
-    float s0, s1, u0 = 0.f, u1 = 0.f;
+    float s0, s1, sc, uc = 0.f;
     f2_split(f2_add(s2[0], s2[1]), s0, s1);
-    const float sc = s0 + s1, shift = fmaf(st.m, k, -mu), f = fmaf(-shift, kLn2, 1.f);
+    sc = s0 + s1;
     if (ENT) {
-        f2_split(f2_add(u2[0], u2[1]), u0, u1);
-        const float uc = u0 + u1;
-        if (!CLAMP && uc != uc) return false;
-        st.u = fmaf(fmaf(-shift, sc, uc), f, st.u);
+        f2_split(f2_add(u2[0], u2[1]), s0, s1);
+        uc = s0 + s1;
     }
+    if (DIFF) {
+        st.s += sc;
+        if (ENT) st.u += uc;
+        return true;
+    }
+    if (ENT && uc != uc) return false;
+    const float shift = fmaf(st.m, k, -mu), d = shift * kLn2, f = fmaf(d, fmaf(d, 0.5f, -1.f), 1.f);
+    if (ENT) st.u = fmaf(fmaf(-shift, sc, uc), f, st.u);
     st.s = fmaf(sc, f, st.s);
     return true;
 }
@@ -124,14 +140,14 @@ __device__ inline bool add_vectors(LpState &st, const uint4 (&raw)[NV], int n, f
 // target column among them, set to -inf (own: this one), so that the warp takes
 // the held exponents at once instead of one lane after the others. Returns
 // whether the second pass needs no held exponents for these vectors (the
-// target's column it writes apart).
+// target's column it writes apart; far below another maximum than this thread's
+// so far, an exponent that was not held here can leave fp32's range there).
 template <int DT, bool ENT, int NV, bool ALL>
 __device__ inline bool add_any(LpState &st, const uint4 (&raw)[NV], int n, float k, bool y_warp, bool own) {
     int low = 0;
     if (!(ENT && y_warp) && add_vectors<DT, ENT, NV, false, ALL>(st, raw, n, k, low)) return true;
-    if constexpr (ENT) {
-        if (add_vectors<DT, ENT, NV, true, ALL>(st, raw, n, k, low)) return low <= (own ? 1 : 0);
-    }
+    if (add_vectors<DT, ENT, NV, true, ALL>(st, raw, n, k, low)) return low <= (own ? 1 : 0) && fabsf(st.m * k) < kLpFmaMax;
+    // no finite maximum: every value -inf or NaN so far, or +inf among them
 #pragma unroll 1
     for (int i = 0; i < (ALL ? NV : n); ++i) {
         uint4 r = raw[0];
@@ -581,8 +597,8 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtasPerSm) lp_rows_kernel(LpArg
             const float fold = fmaf(-g.M, k, g.neg_log2d);
             const float cexp = KB == 2 ? fold : g.neg_log2d;
             // the whole row takes the slow form where the folded constant is too large,
-            // and on fp32 rows where M might carry x - M out of range
-            if (!(fabsf(KB == 2 ? fold : g.M) < (KB == 2 ? kFoldC : 1e30f))) held = ~0u;
+            // and on fp32 rows where M might carry the exponent times B out of range
+            if (!(fabsf(KB == 2 ? fold : g.M * k) < (KB == 2 ? kFoldC : 1e20f))) held = ~0u;
             auto pass2 = [&](auto ent_tag) {
                 constexpr bool E = decltype(ent_tag)::value;
                 for (int i = 0; i < nch; ++i) {

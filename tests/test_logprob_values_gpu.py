@@ -1,0 +1,173 @@
+"""The log-probability operators on logits, margins and ratios far from the
+ordinary: finite masks and maxima of any magnitude, gradients under a loss
+scale, -inf on one side of a pair. Against the fp64 forms of lp_check.py, which
+derives the tolerances."""
+import math
+
+import pytest
+import torch
+
+import lp_check as L
+
+pytestmark = pytest.mark.gpu
+DT = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+
+
+@pytest.fixture(scope="module")
+def ce():
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    import softmax_cross_entropy_pass_gb300 as ce
+    return ce
+
+
+def f32(v):
+    """A constant as the kernels hold it."""
+    return float(torch.tensor(v, dtype=torch.float32))
+
+
+# ---------------------------------------------------------------------- finite logits of any magnitude
+def masks(dtype):
+    low = torch.finfo(DT[dtype]).min
+    return (-1e4, low) if dtype == "f16" else (-1e4, -1e6, -1e9, -1e10, -1e12, -1e30, -1e37, low)
+
+
+def far_rows(v, dtype, seed):
+    """Rows whose leading columns, all but 500 columns, or all columns hold a
+    finite mask; the same with the target masked, where its log-probability is
+    one of fp32; rows far above 0."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    rows, targets = [], []
+    for m in masks(dtype):
+        for form in ("leading", "few", "all", "target"):
+            if form == "target" and m < -1e30:
+                continue
+            x = torch.randn(v, generator=g, device="cuda") * 2
+            few = torch.randperm(v, generator=g, device="cuda")[:500]
+            t = int(few[0])
+            if form == "leading":
+                x[:min(8192, v - 1)] = m
+                t = v - 1
+            elif form == "all":
+                x[:] = m
+            else:
+                kept = x[few].clone()
+                x[:] = m
+                x[few] = kept
+                if form == "target":
+                    x[t] = m
+            rows.append(x)
+            targets.append(t)
+    for shift in (100.0, -300.0, 5e3):
+        rows.append(torch.randn(v, generator=g, device="cuda") + shift)
+        targets.append(v // 2)
+    return g, torch.stack(rows).to(DT[dtype]), torch.tensor(targets, device="cuda")
+
+
+@pytest.mark.parametrize("row_kb", [12, 17, 50, 200])
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("temperature", [1e-3, 0.01, 0.7, 1.0, 5.0, 10.0])
+def test_far_logits(ce, row_kb, dtype, temperature):
+    temperature = f32(temperature)
+    v = int(row_kb * 1024) // (4 if dtype == "f32" else 2) - 3
+    g, base, bt = far_rows(v, dtype, v)
+    n = len(bt)
+    valid, logq, want, want_h = L.rows_ref(base, bt, temperature)
+    d = L.delta(base, temperature)
+    gl, gh, z = (torch.randn(n, generator=g, device="cuda") for _ in range(3))
+    z.zero_()
+    ref = L.grad_ref(logq, valid, bt, gl, gh, temperature)
+    tol = L.tol_grad(base, ref, logq, valid, bt, gl, gh, z, z, DT[dtype], temperature)
+    ent_coef = f32(0.03)
+    pol = L.policy_ref(base, bt, gl, None, None, None, 0.2, 0.2, 0.0, ent_coef, temperature, "none", None)
+    bare = L.policy_ref(base, bt, gl, None, None, None, 0.2, 0.2, 0.0, 0.0, temperature, "none", None)
+    # few rows (clusters of CTAs a row) and more rows than CTAs; rows that start anywhere
+    for copies, off in ((1, 0), (320 // n + 1, 3)):
+        x = torch.empty(n * copies, v + 2 * off, dtype=DT[dtype], device="cuda")[:, off:off + v]
+        x.copy_(base.repeat(copies, 1))
+        t, rep = bt.repeat(copies), lambda a: a.repeat(copies, *[1] * (a.dim() - 1))  # noqa: E731
+        logp, ent, stats = ce.ce_token_logprob(x, t, temperature=temperature)
+        L.check(logp, rep(want), L.tol_logp(rep(d), rep(want)), "logp")
+        L.check(ent, rep(want_h), L.tol_entropy(rep(d), rep(want_h)), "entropy")
+        plain = ce.ce_token_logprob(x, t, temperature=temperature, with_entropy=False)[0]
+        L.check(plain, rep(want), L.tol_logp(rep(d), rep(want)), "logp without entropy")
+        grad = ce.ce_token_logprob_backward(x, t, stats, rep(gl), grad_entropy=rep(gh), temperature=temperature,
+                                            grad=torch.empty_like(x))
+        L.check(grad, rep(ref), rep(tol), "gradient from statistics")
+        kw = dict(temperature=temperature, reduction="none")
+        loss, grad = ce.ce_policy_fwd_bwd(x, t, rep(gl), grad=torch.empty_like(x), **kw)
+        L.check(loss, rep(bare["loss"]), rep(bare["tol_loss"]), "policy loss")
+        L.check(grad, rep(bare["grad"]), rep(bare["tol_grad"]), "policy gradient")
+        row = torch.empty(n * copies, 4, device="cuda")
+        loss, grad = ce.ce_policy_fwd_bwd(x, t, rep(gl), entropy_coef=ent_coef, row_stats=row, **kw)
+        L.check(loss, rep(pol["loss"]), rep(pol["tol_loss"]), "policy loss with the entropy")
+        L.check(grad, rep(pol["grad"]), rep(pol["tol_grad"]), "policy gradient with the entropy")
+        L.check(row, rep(pol["stats"]), rep(pol["tol_stats"]), "row statistics")
+
+
+@pytest.mark.parametrize("row_kb", [12, 50, 200])
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_far_logits_in_pairs(ce, row_kb, dtype):
+    v = int(row_kb * 1024) // (4 if dtype == "f32" else 2)
+    _, x, t = far_rows(v, dtype, v)
+    keep = L.rows_ref(x, t)[2] > -1e3      # sums of ordinary size
+    x, t = x[keep].contiguous(), t[keep].contiguous()
+    n = len(t)
+    off = torch.tensor([0, n // 4, n // 2, 3 * n // 4, n], device="cuda")
+    beta = f32(0.02)
+    want = L.preference_ref(x, t, off, None, "sigmoid", beta, 0.0, True, "mean", None)
+    loss, seq, grad = ce.ce_preference_fwd_bwd(x, t, off, beta=beta, length_normalize=True, grad=torch.empty_like(x))
+    L.check(loss, want["loss"], want["tol_loss"], "loss")
+    L.check(seq, want["seq"], want["tol_seq"], "sequence values")
+    L.check(grad, want["grad"], want["tol_grad"], "gradient")
+
+
+@pytest.mark.parametrize("v", [20000, 33000, 128256])
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_special_long_rows(ce, v, dtype):
+    """Rows without a distribution (NaN, +inf, all -inf) among ordinary ones, and
+    rows of one value, longer than the register kernel takes."""
+    dt = DT[dtype]
+    low = torch.finfo(dt).min
+    x = torch.randn(16, v, device="cuda").to(dt)
+    t = torch.arange(16, device="cuda") * 7
+    x[0, 100:] = -math.inf
+    x[1, 100:] = low
+    x[2] = low
+    x[3] = -math.inf
+    x[4, v // 2] = math.nan
+    x[5, v - 2] = math.inf
+    x[6] = math.nan
+    t[6] = -100
+    x[7] = 0.0
+    x[8] = 50000.0 if dtype == "f16" else 3e38
+    x[9, :] = -40000.0
+    x[9, v // 3] = 60000.0
+    x[10, t[10]] = -math.inf
+    t[11] = v
+    t[12] = -5
+    x[13] = -math.inf
+    x[13, t[13]] = 1.0
+    x[14] = math.nan
+    x[15, :9] = math.nan
+    x[15, 9:] = -math.inf
+    adv = torch.randn(16, device="cuda")
+    logp, ent, _ = ce.ce_token_logprob(x, t)
+    plain = ce.ce_token_logprob(x, t, with_entropy=False)[0]
+    coef = f32(0.1)
+    loss, grad = ce.ce_policy_fwd_bwd(x, t, adv, entropy_coef=coef, reduction="none", grad=torch.empty_like(x))
+    _, _, want, want_h = L.rows_ref(x, t)
+    nan = torch.tensor([3, 4, 5, 14, 15], device="cuda")
+    for name, val in (("logp", logp), ("entropy", ent), ("logp without entropy", plain)):
+        assert val[nan].isnan().all(), name
+        assert val[[11, 12]].isnan().all() and val[6] == 0, name
+    assert grad[nan].isnan().any(1).all() and loss[nan].isnan().all()
+    assert (grad[[6, 11, 12]] == 0).all() and (loss[[6, 11, 12]] == 0).all()
+    assert logp[10] == -math.inf and plain[10] == -math.inf and logp[13] == 0 and ent[13] == 0
+    ok = torch.tensor([0, 1, 2, 7, 8, 9, 13], device="cuda")
+    d = L.delta(x[ok])
+    L.check(logp[ok], want[ok], L.tol_logp(d, want[ok]), "logp")
+    L.check(plain[ok], want[ok], L.tol_logp(d, want[ok]), "logp without entropy")
+    L.check(ent[ok], want_h[ok], L.tol_entropy(d, want_h[ok]), "entropy")
+    ref = L.policy_ref(x[ok], t[ok], adv[ok], None, None, None, 0.2, 0.2, 0.0, coef, 1.0, "none", None)
+    L.check(loss[ok], ref["loss"], ref["tol_loss"], "policy loss")
+    L.check(grad[ok], ref["grad"], ref["tol_grad"], "policy gradient")
