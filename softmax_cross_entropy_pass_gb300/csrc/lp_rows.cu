@@ -596,9 +596,11 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtasPerSm) lp_rows_kernel(LpArg
             const uint32_t mis = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(gv)) & 15u;
             const float fold = fmaf(-g.M, k, g.neg_log2d);
             const float cexp = KB == 2 ? fold : g.neg_log2d;
-            // the whole row takes the slow form where the folded constant is too large,
-            // and on fp32 rows where M might carry the exponent times B out of range
+            // the whole row takes the slow form where the folded constant is too large, on
+            // fp32 rows where M might carry the exponent out of range, and where B times
+            // an exponent of down to -3.4e38 (a far finite mask) would be -inf, 0 * inf
             if (!(fabsf(KB == 2 ? fold : g.M * k) < (KB == 2 ? kFoldC : 1e20f))) held = ~0u;
+            if (ENT && !(fabsf(g.B) < 1.f)) held = ~0u;
             auto pass2 = [&](auto ent_tag) {
                 constexpr bool E = decltype(ent_tag)::value;
                 for (int i = 0; i < nch; ++i) {

@@ -171,3 +171,28 @@ def test_special_long_rows(ce, v, dtype):
     ref = L.policy_ref(x[ok], t[ok], adv[ok], None, None, None, 0.2, 0.2, 0.0, coef, 1.0, "none", None)
     L.check(loss[ok], ref["loss"], ref["tol_loss"], "policy loss")
     L.check(grad[ok], ref["grad"], ref["tol_grad"], "policy gradient")
+
+
+@pytest.mark.parametrize("row_kb", [12, 17, 50, 200])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("mask,temperature", [(-1e38, 1.0), (-3.3e38, 5.0), (-2e34, 1e-4)])
+def test_far_masks_under_a_large_entropy_gradient(ce, row_kb, dtype, mask, temperature):
+    """Masks whose exponent is just within fp32's range, times the entropy's coefficient: probability and gradient 0."""
+    n, v, temperature = 330, int(row_kb * 1024) // (4 if dtype == "f32" else 2), f32(temperature)
+    g = torch.Generator(device="cuda").manual_seed(v)
+    x = torch.randn(n, v, generator=g, device="cuda")
+    x[:, 100:v - 100][torch.rand(n, v - 200, generator=g, device="cuda") < 0.3] = mask
+    x = x.to(DT[dtype])
+    t = torch.randint(0, 100, (n,), generator=g, device="cuda")
+    adv, up = torch.randn(n, generator=g, device="cuda"), torch.full((1,), 65536.0, device="cuda")
+    coef = f32(0.25)
+    want = L.policy_ref(x, t, adv, None, None, None, 0.2, 0.2, 0.0, coef, temperature, "sum", up)
+    loss, grad = ce.ce_policy_fwd_bwd(x, t, adv, entropy_coef=coef, temperature=temperature, reduction="sum", grad_output=up,
+                                      grad=torch.empty_like(x))
+    L.check(loss, want["loss"], want["tol_loss"], "loss")
+    L.check(grad, want["grad"], want["tol_grad"], "gradient")
+    assert (grad[x < -1e30] == 0).all()
+    # over the logits, and into rows that lie otherwise
+    other = torch.empty(n, v + 3, dtype=DT[dtype], device="cuda")[:, 1:1 + v]
+    ce.ce_policy_fwd_bwd(x, t, adv, entropy_coef=coef, temperature=temperature, reduction="sum", grad_output=up, grad=other)
+    L.check(other, want["grad"], want["tol_grad"], "gradient at other offsets")
