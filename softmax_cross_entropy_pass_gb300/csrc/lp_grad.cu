@@ -228,7 +228,8 @@ __global__ void __launch_bounds__(kPairThreads) lp_pair_kernel(PairArgs a) {
                 const float q = expf(-fabsf(z)), l = log1pf(q), inv = 1.f / (1.f + q);
                 const float sp_pos = (z > 0.f ? z : 0.f) + l, sp_neg = (z > 0.f ? 0.f : -z) + l;
                 const float s_pos = z > 0.f ? inv : q * inv, s_neg = z > 0.f ? q * inv : inv;
-                loss = (1.f - eps) * sp_neg + eps * sp_pos;
+                loss = (1.f - eps) * sp_neg;
+                if (eps != 0.f) loss += eps * sp_pos;  // sp_pos is inf where the rejected side has probability 0
                 slope = be * (eps * s_pos - (1.f - eps) * s_neg);
             } else if (a.kind == CE_PREF_HINGE) {
                 loss = z < 1.f ? 1.f - z : (z >= 1.f ? 0.f : z);  // NaN stays

@@ -196,3 +196,30 @@ def test_far_masks_under_a_large_entropy_gradient(ce, row_kb, dtype, mask, tempe
     other = torch.empty(n, v + 3, dtype=DT[dtype], device="cuda")[:, 1:1 + v]
     ce.ce_policy_fwd_bwd(x, t, adv, entropy_coef=coef, temperature=temperature, reduction="sum", grad_output=up, grad=other)
     L.check(other, want["grad"], want["tol_grad"], "gradient at other offsets")
+
+
+# ---------------------------------------------------------------------- margins and ratios at their ends
+@pytest.mark.parametrize("eps", [0.0, 0.1])
+def test_rejected_sequence_of_probability_zero(ce, eps):
+    """A rejected sequence whose target is masked with -inf: the margin is +inf,
+    and without smoothing the loss and the gradient are 0."""
+    x = torch.randn(4, 300, device="cuda")
+    t = torch.zeros(4, dtype=torch.int64, device="cuda")
+    x[2, 0] = -math.inf
+    off = torch.tensor([0, 1, 2, 3, 4], device="cuda")
+    for reduction in ("none", "mean"):
+        loss, seq, grad = ce.ce_preference_fwd_bwd(x, t, off, beta=1.0, label_smoothing=eps, reduction=reduction,
+                                                   grad=torch.empty_like(x))
+        want = L.preference_ref(x[[1, 3]], t[:2], off[:3], None, "sigmoid", 1.0, f32(eps), False, "none", None)
+        assert seq[2] == -math.inf and seq[[0, 1, 3]].isfinite().all()
+        if eps:
+            assert loss[0] == math.inf     # -eps log sigmoid(-inf)
+        elif reduction == "none":
+            assert loss[0] == 0
+            L.check(loss[1:], want["loss"], want["tol_loss"], "the other pair's loss")
+        else:
+            L.check(loss, want["loss"] / 2, want["tol_loss"], "loss")
+        if not eps:
+            assert (grad[[0, 2]] == 0).all()
+        scale = 1.0 if reduction == "none" else 0.5
+        L.check(grad[[1, 3]], want["grad"] * scale, want["tol_grad"], "the other pair's gradient")
