@@ -7,8 +7,10 @@
 
 namespace ce {
 
-// e^g - g - 1 >= 0: near 0 by its series (the subtraction would cancel)
-__device__ inline float kl_of_gap(float g) {
+// e^g - g - 1 >= 0, and e^g - 1 as `slope`: near 0 the former by its series (the
+// subtraction would cancel) and the latter from it; elsewhere the latter from the
+// exponential (from the former it would lose its digits where -g is large)
+__device__ inline float kl_of_gap(float g, float &slope) {
     if (fabsf(g) < 0.25f) {
         float p = 1.f / 40320.f;  // g^8 / 8!, relative error below 2e-9 there
         p = fmaf(p, g, 1.f / 5040.f);
@@ -17,9 +19,13 @@ __device__ inline float kl_of_gap(float g) {
         p = fmaf(p, g, 1.f / 24.f);
         p = fmaf(p, g, 1.f / 6.f);
         p = fmaf(p, g, 0.5f);
-        return p * g * g;
+        const float kl = p * g * g;
+        slope = g + kl;
+        return kl;
     }
-    return expf(g) - g - 1.f;
+    const float e = expf(g);
+    slope = e - 1.f;
+    return e - g - 1.f;
 }
 
 // What a policy row reads besides its logits, fetched before its first pass.
@@ -56,11 +62,11 @@ __device__ inline PolicyOut policy_row(const LpArgs &a, const PolicyIn &in, cons
     float g = u1 < u2 ? 0.f : u1;
     o.kl = 0.f;
     if (a.ref_logp) {
-        const float gap = in.ref_logp - r.logp;
-        o.kl = kl_of_gap(gap);
+        float slope;
+        o.kl = kl_of_gap(in.ref_logp - r.logp, slope);
         if (a.kl_coef != 0.f) {
             loss = fmaf(a.kl_coef, o.kl, loss);
-            g = fmaf(-a.kl_coef, gap + o.kl, g);  // e^gap - 1
+            g = fmaf(-a.kl_coef, slope, g);
         }
     }
     o.h = 0.f;

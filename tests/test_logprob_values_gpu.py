@@ -223,3 +223,21 @@ def test_rejected_sequence_of_probability_zero(ce, eps):
             assert (grad[[0, 2]] == 0).all()
         scale = 1.0 if reduction == "none" else 0.5
         L.check(grad[[1, 3]], want["grad"] * scale, want["tol_grad"], "the other pair's gradient")
+
+
+@pytest.mark.parametrize("v", [300, 20000])
+def test_policy_far_below_its_reference(ce, v):
+    """d kl / d logp = 1 - e^(ref - logp) is 1 however far the reference lies below; its loss then is the gap."""
+    gaps = [-30.0, -1e4, -1e6, -3e7, -1e9, -1e20, -math.inf, 20.0, 0.1]
+    n = len(gaps)
+    x, t = torch.randn(n, v, device="cuda"), torch.arange(n, device="cuda")
+    adv = torch.randn(n, device="cuda")
+    ref = (L.rows_ref(x, t)[2] + torch.tensor(gaps, dtype=torch.float64, device="cuda")).float()
+    kl = f32(0.5)
+    want = L.policy_ref(x, t, adv, None, ref, None, 0.2, 0.2, kl, 0.0, 1.0, "none", None)
+    stats = torch.empty(n, 4, device="cuda")
+    loss, grad = ce.ce_policy_fwd_bwd(x, t, adv, ref_logp=ref, kl_coef=kl, reduction="none", row_stats=stats,
+                                      grad=torch.empty_like(x))
+    L.check(loss, want["loss"], want["tol_loss"], "loss")
+    L.check(grad, want["grad"], want["tol_grad"], "gradient")
+    L.check(stats[:, 3], want["stats"][:, 3], want["tol_stats"][:, 3], "kl")
