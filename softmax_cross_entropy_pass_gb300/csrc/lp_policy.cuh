@@ -55,9 +55,12 @@ struct PolicyOut {
 // the unclipped branch's slope is taken. NaN inputs come out NaN.
 __device__ inline PolicyOut policy_row(const LpArgs &a, const PolicyIn &in, const LpRow &r, float entropy) {
     PolicyOut o;
-    o.ratio = a.old_logp ? expf(r.logp - in.old_logp) : 1.f;
+    const float log_r = a.old_logp ? r.logp - in.old_logp : 0.f;
+    o.ratio = expf(log_r);
     const float clipped = fminf(fmaxf(o.ratio, a.clip_lo), a.clip_hi);
-    const float u1 = -in.adv * o.ratio, u2 = -in.adv * clipped;
+    // advantage 0 times a ratio that only fp32 takes for infinite is 0
+    const bool none = in.adv == 0.f && o.ratio == INFINITY && log_r < INFINITY;
+    const float u1 = none ? 0.f : -in.adv * o.ratio, u2 = -in.adv * clipped;
     float loss = u1 < u2 ? u2 : u1;
     float g = u1 < u2 ? 0.f : u1;
     o.kl = 0.f;

@@ -241,3 +241,30 @@ def test_policy_far_below_its_reference(ce, v):
     L.check(loss, want["loss"], want["tol_loss"], "loss")
     L.check(grad, want["grad"], want["tol_grad"], "gradient")
     L.check(stats[:, 3], want["stats"][:, 3], want["tol_stats"][:, 3], "kl")
+
+
+@pytest.mark.parametrize("v", [300, 20000])
+def test_policy_ratio_past_fp32(ce, v):
+    """A ratio over fp32's largest value: clipped where the advantage is positive, no part where it is 0."""
+    x, t = torch.randn(4, v, device="cuda"), torch.arange(4, device="cuda")
+    adv = torch.tensor([0.0, 2.0, -0.0, 1.0], device="cuda")
+    old = (L.rows_ref(x, t)[2] - torch.tensor([200.0, 200.0, 90.0, 0.3], device="cuda")).float()
+    lo = f32(0.2)
+    kw = dict(old_logp=old, clip_low=lo, clip_high=lo, reduction="none")
+    want = L.policy_ref(x, t, adv, old, None, None, lo, lo, 0.0, 0.0, 1.0, "none", None)
+    loss, grad = ce.ce_policy_fwd_bwd(x, t, adv, grad=torch.empty_like(x), **kw)
+    assert loss[0] == 0 and loss[2] == 0 and (grad[:3] == 0).all()
+    assert abs(loss[1].item() + 2 * (1 + lo)) < 1e-6
+    L.check(loss[3:], want["loss"][3:], want["tol_loss"][3:], "loss")
+    stats = torch.empty(4, 4, device="cuda")
+    coef = f32(0.1)
+    loss, grad = ce.ce_policy_fwd_bwd(x, t, adv, entropy_coef=coef, row_stats=stats, grad=torch.empty_like(x), **kw)
+    _, logq, _, ent = L.rows_ref(x, t)
+    z = torch.zeros(4, device="cuda")
+    ref = L.grad_ref(logq, t >= 0, t, z, z - coef)
+    tol = L.tol_grad(x, ref, logq, t >= 0, t, z, z - coef, z, z, torch.float32)
+    L.check(grad[:3], ref[:3], tol[:3], "the entropy's gradient")
+    assert stats[0, 2] == math.inf and (loss[[0, 2]].double() + coef * ent[[0, 2]]).abs().max() < 1e-5
+    # a token the old policy excluded: e^inf, of which 0 times is not a number
+    old[0] = -math.inf
+    assert ce.ce_policy_fwd_bwd(x, t, adv, grad=torch.empty_like(x), **kw)[0][0].isnan()
