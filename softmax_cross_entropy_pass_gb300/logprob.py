@@ -336,14 +336,19 @@ def token_logprob(logits, target, *, temperature=1.0, ignore_index=-100, with_en
 
 class _FormedGradientFunction(torch.autograd.Function):
     """A loss whose gradient the forward forms (one read and one write of the
-    logits); the backward multiplies it by grad_output, skipped on the device
-    where that is 1 (otherwise the product is rounded a second time)."""
+    logits), times ``upstream`` where that is given; the backward multiplies it
+    by grad_output over ``upstream``, skipped on the device where that is 1
+    (otherwise the product is rounded a second time)."""
 
     @staticmethod
-    def forward(ctx, logits, inplace, per_row, run):
+    def forward(ctx, logits, upstream, inplace, per_row, run):
         x = logits.detach()
-        loss, grad = run(x, x if inplace else torch.empty_like(x))
-        ctx.save_for_backward(grad)
+        if upstream is not None:
+            if not torch.is_tensor(upstream):
+                raise TypeError("grad_output must be a tensor on the logits' device")
+            upstream = upstream.detach().reshape(-1).contiguous()
+        loss, grad = run(x, x if inplace else torch.empty_like(x), upstream)
+        ctx.save_for_backward(grad, upstream)
         ctx.per_row = per_row
         return loss if per_row else loss.reshape(())
 
@@ -351,44 +356,54 @@ class _FormedGradientFunction(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, grad_out):
         _once(ctx)
-        (grad,) = ctx.saved_tensors
+        grad, upstream = ctx.saved_tensors
         if grad.shape[0]:
             g = grad_out.detach().to(torch.float32).reshape(-1).contiguous()
             with torch.cuda.device(grad.device):
+                if upstream is not None:
+                    g = torch.where(g == upstream, 1.0, g / upstream)
                 ce_scale_grad(grad, g, reduction="none" if ctx.per_row else "mean")
-        return grad, None, None, None
+        return grad, None, None, None, None
 
 
 def policy_loss(logits, target, advantage, *, old_logp=None, ref_logp=None, row_weight=None, clip_low=0.2,
                 clip_high=0.2, kl_coef=0.0, entropy_coef=0.0, temperature=1.0, ignore_index=-100, reduction="mean",
-                row_stats=None, inplace=False):
+                grad_output=None, row_stats=None, inplace=False):
     """Differentiable ce_policy_fwd_bwd: the loss (a scalar, or [n] for
     reduction "none"). The gradient reaches the logits only; advantage,
     old_logp, ref_logp and row_weight are constants. ``inplace``: the
-    gradient is formed over the logits, which nothing else may use then."""
-    def run(x, grad):
+    gradient is formed over the logits, which nothing else may use then.
+    ``grad_output``: what the backward will be given (an fp32 tensor of one
+    element, or [n] for reduction "none"; not 0 where the latter is not): a
+    loss scale, one over the accumulation steps. The forward has it in the
+    gradient's one rounding then. Without it the gradient is rounded to the
+    logits' type at 1 and scaled afterwards, so that in fp16 what lies below
+    2^-25 at 1 is 0 whatever the loss scale."""
+    def run(x, grad, upstream):
         return ce_policy_fwd_bwd(x, target, advantage, old_logp=old_logp, ref_logp=ref_logp, row_weight=row_weight,
                                  clip_low=clip_low, clip_high=clip_high, kl_coef=kl_coef, entropy_coef=entropy_coef,
-                                 temperature=temperature, ignore_index=ignore_index, reduction=reduction, grad=grad,
-                                 row_stats=row_stats)
-    return _FormedGradientFunction.apply(logits, inplace, reduction == "none", run)
+                                 temperature=temperature, ignore_index=ignore_index, reduction=reduction,
+                                 grad_output=upstream, grad=grad, row_stats=row_stats)
+    return _FormedGradientFunction.apply(logits, grad_output, inplace, reduction == "none", run)
 
 
 def preference_loss(logits, target, seq_offsets, *, ref_logp=None, loss_kind="sigmoid", beta=0.1, label_smoothing=0.0,
-                    length_normalize=False, ignore_index=-100, reduction="mean", seq_logp=None, inplace=False):
+                    length_normalize=False, ignore_index=-100, reduction="mean", grad_output=None, seq_logp=None,
+                    inplace=False):
     """Differentiable ce_preference_fwd_bwd: the scalar loss ("mean" or
     "sum"). ``seq_logp``, if given, receives the sequences' values. The
-    gradient reaches the logits only. ``inplace`` as in policy_loss."""
+    gradient reaches the logits only. ``grad_output`` (one element) and
+    ``inplace`` as in policy_loss."""
     if reduction not in ("mean", "sum"):
         raise ValueError("preference_loss takes reduction 'mean' or 'sum'")
 
-    def run(x, grad):
+    def run(x, grad, upstream):
         loss, _, grad = ce_preference_fwd_bwd(x, target, seq_offsets, ref_logp=ref_logp, loss_kind=loss_kind, beta=beta,
                                               label_smoothing=label_smoothing, length_normalize=length_normalize,
-                                              ignore_index=ignore_index, reduction=reduction, grad=grad,
-                                              seq_logp=seq_logp)
+                                              ignore_index=ignore_index, reduction=reduction, grad_output=upstream,
+                                              grad=grad, seq_logp=seq_logp)
         return loss, grad
-    return _FormedGradientFunction.apply(logits, inplace, False, run)
+    return _FormedGradientFunction.apply(logits, grad_output, inplace, False, run)
 
 
 # ---------------------------------------------------------------------- linear head

@@ -268,3 +268,77 @@ def test_policy_ratio_past_fp32(ce, v):
     # a token the old policy excluded: e^inf, of which 0 times is not a number
     old[0] = -math.inf
     assert ce.ce_policy_fwd_bwd(x, t, adv, grad=torch.empty_like(x), **kw)[0][0].isnan()
+
+
+# ---------------------------------------------------------------------- a loss scale in the one rounding
+def in_range(want, dtype):
+    """A gradient as its type holds it: fp16 rounds from 65520 on (65504 is its
+    largest, and the next value it could hold is 65536) to infinity."""
+    if dtype != "f16":
+        return want
+    return torch.where(want.abs() >= 65520.0, torch.sign(want) * math.inf, want)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("reduction", ["mean", "sum", "none"])
+def test_policy_loss_under_a_scale(ce, dtype, reduction):
+    """The upstream gradient given to the forward is in the gradient's one rounding: fp16 under a loss scale keeps what it holds."""
+    n, v, lo = 4096, 700, f32(0.2)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = (torch.randn(n, v, generator=g, device="cuda") * 2).to(DT[dtype])
+    t = torch.randint(0, v, (n,), generator=g, device="cuda")
+    t[::7] = -100
+    adv, ref = torch.randn(n, generator=g, device="cuda"), -torch.rand(n, generator=g, device="cuda") * 8
+    kw = dict(ref_logp=ref, clip_low=lo, clip_high=lo, kl_coef=f32(0.05), entropy_coef=f32(0.01), reduction=reduction)
+    scale = torch.full((n,) if reduction == "none" else (), 65536.0 if reduction == "mean" else 64.0, device="cuda")
+    want = L.policy_ref(x, t, adv, None, ref, None, lo, lo, f32(0.05), f32(0.01), 1.0, reduction, scale.reshape(-1))
+    want["grad"] = in_range(want["grad"], dtype)
+    for inplace in (False, True):
+        a = x.clone().requires_grad_()
+        loss = ce.policy_loss(a * 1, t, adv, grad_output=scale, inplace=inplace, **kw)
+        L.check(loss.detach().reshape(-1), want["loss"], want["tol_loss"], "loss")
+        loss.backward(scale)
+        L.check(a.grad, want["grad"], want["tol_grad"], "gradient")
+    direct = ce.ce_policy_fwd_bwd(x, t, adv, grad_output=scale.reshape(-1), grad=torch.empty_like(x), **kw)[1]
+    assert torch.equal(direct, a.grad)
+    # an upstream gradient other than the one announced: by the quotient, a second rounding
+    a = x.clone().requires_grad_()
+    ce.policy_loss(a, t, adv, grad_output=scale, **kw).backward(scale / 4)
+    off = torch.finfo(DT[dtype]).eps / 2 * want["grad"].abs().nan_to_num(posinf=0.0) / 4 + (2.0 ** -25 if dtype == "f16" else 0.0)
+    L.check(a.grad, want["grad"] / 4, want["tol_grad"] / 4 + 1.01 * off, "gradient by the quotient")
+    zero = torch.zeros_like(scale)
+    a = x.clone().requires_grad_()
+    ce.policy_loss(a, t, adv, grad_output=zero, **kw).backward(zero)
+    assert (a.grad == 0).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_preference_loss_under_a_scale(ce, dtype):
+    n, v, pairs = 2048, 700, 32
+    g = torch.Generator(device="cuda").manual_seed(4)
+    x = (torch.randn(n, v, generator=g, device="cuda") * 2).to(DT[dtype])
+    t = torch.randint(0, v, (n,), generator=g, device="cuda")
+    t[::5] = -100
+    off = torch.arange(2 * pairs + 1, device="cuda") * (n // (2 * pairs))
+    scale = torch.full((1,), 65536.0, device="cuda")
+    beta = f32(0.02)
+    want = L.preference_ref(x, t, off, None, "sigmoid", beta, 0.0, True, "mean", scale)
+    a = x.clone().requires_grad_()
+    loss = ce.preference_loss(a, t, off, beta=beta, length_normalize=True, grad_output=scale)
+    (loss * scale[0]).backward()
+    L.check(loss.detach().reshape(1), want["loss"], want["tol_loss"], "loss")
+    L.check(a.grad, want["grad"], want["tol_grad"], "gradient")
+
+
+def test_refused_scales(ce):
+    x, t, adv = torch.randn(4, 20, device="cuda"), torch.arange(4, device="cuda"), torch.ones(4, device="cuda")
+    with pytest.raises(ValueError, match="grad_output"):
+        ce.policy_loss(x, t, adv, grad_output=torch.ones(4, device="cuda"))
+    with pytest.raises(ValueError, match="grad_output"):
+        ce.policy_loss(x, t, adv, grad_output=torch.ones(1, device="cuda", dtype=torch.float64))
+    with pytest.raises(ValueError, match="grad_output"):
+        ce.policy_loss(x, t, adv, reduction="none", grad_output=torch.ones(1, device="cuda"))
+    with pytest.raises(ValueError, match="grad_output"):
+        ce.preference_loss(x, t, torch.tensor([0, 2, 4], device="cuda"), grad_output=torch.ones(1))
+    with pytest.raises(TypeError, match="grad_output"):
+        ce.policy_loss(x, t, adv, grad_output=2.0)
