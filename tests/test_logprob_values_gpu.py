@@ -342,3 +342,29 @@ def test_refused_scales(ce):
         ce.preference_loss(x, t, torch.tensor([0, 2, 4], device="cuda"), grad_output=torch.ones(1))
     with pytest.raises(TypeError, match="grad_output"):
         ce.policy_loss(x, t, adv, grad_output=2.0)
+
+
+# ---------------------------------------------------------------------- windows of long rows
+@pytest.mark.parametrize("ignored", [0.4, 0.6])
+def test_windows_of_long_rows(ce, ignored):
+    """More rows than one window of the row kernel deals out, each longer than the delayed second pass takes."""
+    n, v = 9001, 33000
+    g = torch.Generator(device="cuda").manual_seed(int(ignored * 10))
+    x = torch.empty(n, v, dtype=torch.bfloat16, device="cuda").normal_(0, 2, generator=g)
+    t = torch.randint(0, v, (n,), generator=g, device="cuda")
+    t[torch.rand(n, generator=g, device="cuda") < ignored] = -100
+    adv = torch.randn(n, generator=g, device="cuda")
+    stats = torch.full((n, 4), 9.0, device="cuda")
+    coef = f32(0.01)
+    loss, grad = ce.ce_policy_fwd_bwd(x, t, adv, entropy_coef=coef, reduction="sum", row_stats=stats, grad=torch.full_like(x, 3.0))
+    total = tol = 0.0
+    for r in range(0, n, 500):
+        s = slice(r, min(r + 500, n))
+        want = L.policy_ref(x[s], t[s], adv[s], None, None, None, 0.2, 0.2, 0.0, coef, 1.0, "sum", None)
+        L.check(grad[s], want["grad"], want["tol_grad"], f"gradient of rows from {r}")
+        L.check(stats[s], want["stats"], want["tol_stats"], f"row statistics from {r}")
+        total, tol = total + float(want["loss"]), tol + float(want["tol_loss"])
+    assert abs(loss.item() - total) <= tol + 2 * L.U * abs(total)
+    kept = grad.clone()
+    ce.ce_policy_fwd_bwd(x, t, adv, entropy_coef=coef, reduction="sum")
+    assert torch.equal(x, kept)
