@@ -22,6 +22,9 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
+#include <atomic>
+#include <mutex>
+
 #include "ce_device.cuh"
 #include "ce_kernels.h"
 #include "flce.h"
@@ -1188,8 +1191,10 @@ int gemm_fit_ksplit(int K, int ksplit) {
 
 // Resident CTA pairs of a pair kernel on a device (0 if unknown), asked once.
 static int pair_clusters(const void *fn, int dev, int threads) {
+    static std::mutex mu;  // calls may come from several threads at once
     static const void *fns[16];
     static int devs[16], vals[16], used = 0;
+    std::lock_guard<std::mutex> lk(mu);
     for (int i = 0; i < used; ++i)
         if (fns[i] == fn && devs[i] == dev) return vals[i];
     cudaLaunchConfig_t cfg = {};
@@ -1290,7 +1295,7 @@ cudaError_t gemm_bf16(int M, int N, int K, const void *A, int64_t lda, int a_mn,
     const void *fn = kernels[pair ? 1 : 0][epi];
     const size_t smem = pair ? GP_SMEM : GB_SMEM;
     // the shared-memory limit is a per-device attribute of each kernel: set it once per device
-    static uint64_t attr_set[2][6] = {};
+    static std::atomic<uint64_t> attr_set[2][6] = {};
     int dev = 0;
     if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
     const uint64_t bit = dev < 64 ? (1ull << dev) : 0ull;
