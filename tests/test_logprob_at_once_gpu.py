@@ -1,4 +1,5 @@
-"""The log-probability operators called from several threads at once."""
+"""The log-probability operators called from several threads at once, and whole
+autograd steps of theirs captured into a graph and replayed."""
 import threading
 
 import pytest
@@ -67,3 +68,68 @@ def test_threads_at_once(ce):
     for th in threads:
         th.join()
     assert not failed, failed
+
+
+def step(ce, d, scale, inplace):
+    """One training step's gradients; new leaves every time, so that no graph of theirs is left over."""
+    out = []
+    for k in ("x", "short"):
+        a = d[k].detach().clone().requires_grad_()
+        loss = ce.policy_loss(a * 1, d["t"], d["adv"], ref_logp=d["ref"], kl_coef=0.1, entropy_coef=0.01, grad_output=scale,
+                              inplace=inplace)
+        out += [loss.detach(), *torch.autograd.grad(loss * scale, a)]
+        loss = ce.preference_loss(a * 1, d["t"], d["off"], inplace=inplace)
+        out += [loss.detach(), *torch.autograd.grad(loss * scale, a)]
+        logp, ent = ce.token_logprob(a * 1, d["t"], with_entropy=True, inplace=inplace)
+        out += [logp.detach(), *torch.autograd.grad((logp * d["adv"] + 0.1 * ent).sum(), a)]
+    h, w = d["h"].detach().requires_grad_(), d["w"].detach().requires_grad_()
+    logp = ce.linear_token_logprob(h, w, d["t"])
+    return out + [logp.detach(), *torch.autograd.grad((logp * d["adv"]).sum(), [h, w])]
+
+
+@pytest.mark.parametrize("inplace", [False, True])
+def test_captured_training_step(ce, inplace):
+    d, scale = inputs(11), torch.full((), 8.0, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(ce, d, scale, inplace)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = step(ce, d, scale, inplace)
+    for seed in (12, 13):
+        for k, v in inputs(seed).items():
+            d[k].copy_(v)
+        scale.fill_(float(seed))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [o.clone() for o in outs]
+        assert same(got, [o.detach() for o in step(ce, d, scale, inplace)])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert same(got, outs)
+
+
+def test_captured_without_rows(ce):
+    """No rows at all, captured: the losses are written all the same."""
+    x, t, z = torch.empty(0, 50, device="cuda"), torch.empty(0, dtype=torch.int64, device="cuda"), torch.empty(0, device="cuda")
+    w, off = torch.randn(30, 64, device="cuda").bfloat16(), torch.zeros(3, dtype=torch.int64, device="cuda")
+    loss, ploss, gw = (torch.full(s, 9.0, device="cuda") for s in ((1,), (1,), (30, 64)))
+    ws, pws = ce.workspace(0), torch.empty(4096, dtype=torch.uint8, device="cuda")
+
+    def run():
+        ce.ce_policy_fwd_bwd(x, t, z, loss=loss, ws=ws)
+        ce.ce_preference_fwd_bwd(x, t, off, loss=ploss, ws=pws)
+        ce.flce_token_logprob_backward(w[:0], w, t, torch.empty(0, 4, device="cuda"), z, grad_weight=gw)
+    run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    for o in (loss, ploss, gw):
+        o.fill_(9.0)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert loss.item() == 0 and ploss.item() == 0 and (gw == 0).all()
