@@ -48,6 +48,8 @@ constexpr size_t GB_SMEM = 1024 + GB_STAGES * (GB_A_BYTES + GB_B_BYTES) + 256;
 // instead of four, so that a row's 256 running sums are two threads' 128. Parts
 // of 1024 (GB300, 4096 x 4096 x 128256): 2270 us and log p off by 1.7e-7
 // (2-norm); of 512 2425 us and 0.7e-7; the whole K at once 2214 us and 6.5e-7.
+// The gradient (EPI 5) takes the whole K at once: its logits differ by that much
+// from those its statistics were made of, and it is rounded to bf16 (2e-3).
 constexpr int kLpPartSteps = 16;  // of 64
 template <int EPI> struct GemmEpi {
     static constexpr int kWarps = EPI == 4 ? 8 : 4;
