@@ -559,6 +559,112 @@ ce_status flce_token_logprob_backward(const ce_params *p, int64_t hidden_dim, fl
                                       void *grad_weight, int32_t grad_weight_dtype, float *grad_bias,
                                       int64_t chunk_rows, void *workspace, size_t workspace_bytes, void *stream);
 
+/* ------------------------------------------------------------------------
+ * The serving head in 8 bits: norm, weights and activations in e4m3 with
+ * scales, the logits product, and the verification of drafted tokens.
+ *
+ * 8-bit layout: e4m3 bytes [rows, cols], row-major with a row stride ld that
+ * is a multiple of 16, first byte 16-byte aligned, and a scale (fp32) for every
+ * block: the value is byte * scale. Blocks span 128 columns and either one row
+ * (activations, scale [rows][ceil(cols / 128)]) or 128 rows (weights, scale
+ * [ceil(rows / 128)][ceil(cols / 128)]); the last block of a row or column may be
+ * smaller. A block's scale is max(max |y| / 448, 2^-126), its bytes the nearest
+ * e4m3 of y / scale (ties to even), so zeros stay zeros. A NaN makes its block's
+ * scale and bytes NaN; an infinity makes the scale infinite. Bytes between cols
+ * and ld are not written and never read.
+ * Inputs may have any row stride and element alignment; outputs share no memory
+ * with inputs or one another (CE_ERR_INVALID_ARG otherwise) except where said.
+ * ------------------------------------------------------------------------ */
+
+typedef struct ce_norm_params {
+    int64_t n_rows, cols;             /* cols in [1, 32768] (CE_ERR_UNSUPPORTED above) */
+    int64_t ld_x, ld_residual, ld_residual_out, ld_q; /* row strides, elements; >= cols */
+    int32_t dtype;                    /* ce_dtype of x, residual and residual_out */
+    int32_t weight_dtype;             /* dtype, or CE_DT_F32 */
+    float eps;                        /* >= 0 */
+    int32_t reserved;                 /* must be 0 */
+} ce_norm_params; /* 64 bytes */
+
+/*
+ * Root-mean-square norm with the residual's addition, in 8 bits:
+ *   h = x + residual,  y = h weight / sqrt(mean_c h_c^2 + eps),
+ * y quantised in blocks of 1 x 128. h and y are fp32: h is rounded once, where
+ * it is stored, and the norm is that of the unrounded sum.
+ *   x             device [n_rows, ld_x].
+ *   residual      device [n_rows, ld_residual], or NULL for 0.
+ *   weight        device [cols], 16-byte aligned.
+ *   residual_out  device [n_rows, ld_residual_out], or NULL; needs residual.
+ *                 May be x or residual itself (with the same row stride).
+ *   q, scale      the 8-bit rows.
+ * A row with a NaN comes out NaN.
+ */
+ce_status ce_rms_norm_fp8(const ce_norm_params *p, const void *x, const void *residual, const void *weight,
+                          void *residual_out, void *q, float *scale, void *stream);
+
+/*
+ * x (device [rows, ld_x] of dtype) in 8 bits, block_rows 1 or 128.
+ */
+ce_status ce_quantize_fp8(int64_t rows, int64_t cols, const void *x, int64_t ld_x, int32_t dtype, int32_t block_rows,
+                          void *q, int64_t ld_q, float *scale, void *stream);
+
+/*
+ * D[m, n] = sum_k A[m, k] B[n, k] (+ bias[n]) of 8-bit operands on the tcgen05
+ * tensor cores: A [M, K] in blocks of 1 x 128, B [N, K] (a weight) in blocks of
+ * 128 x 128, any scales. Sums of one block along K are formed by the tensor core,
+ * scaled and added up in fp32, and rounded once to D.
+ *   bias   device fp32 [N], or NULL.
+ *   dtype  of D, device [M, ldd], ldd >= N.
+ * K >= 1; M or N of 0 does nothing. Should a wait inside the kernel give up,
+ * the tiles concerned come out NaN.
+ */
+ce_status ce_gemm_fp8(int64_t M, int64_t N, int64_t K, const void *A, int64_t lda, const float *a_scale,
+                      const void *B, int64_t ldb, const float *b_scale, const float *bias, int32_t dtype, void *D,
+                      int64_t ldd, void *stream);
+
+typedef struct ce_verify_params {
+    int64_t n_seqs, n_drafts, vocab;  /* B, K in [0, 255], V */
+    int64_t seq_stride, ld;           /* logits [B][K + 1][V]: strides of a sequence and of a row, elements */
+    int64_t draft_seq_stride, ld_draft; /* draft_logits [B][K][V] */
+    int32_t dtype;                    /* ce_dtype of both */
+    int32_t token_is_int32;           /* draft_token and tokens: 0 int64, 1 int32 */
+    float temperature;                /* T, 0 or in [1e-4, 1e4]; not used where temperatures is given */
+    int32_t reserved;                 /* must be 0 */
+} ce_verify_params; /* 72 bytes */
+
+/* Workspace bytes of ce_verify_drafts: 16 for every row and part of at most 64 KB, plus 256. */
+ce_status ce_verify_workspace_size(const ce_verify_params *p, size_t *bytes);
+
+/*
+ * Verification of drafted tokens against the target's probabilities, from given
+ * random numbers. Sequence b has the drafts t_0 .. t_{K-1} and K + 1 rows of
+ * target logits z_0 .. z_K (row i: the distribution of the token in place of
+ * t_i). With p_i = softmax(z_i / T) and q_i = softmax(y_i / T) of the draft
+ * model's logits (or, without them, 1 at t_i and 0 elsewhere):
+ *   draft i stays while u_i q_i(t_i) < p_i(t_i); n drafts stay, up to the first that does not;
+ *   token n is the lowest v with sum_{c <= v} w_c > r sum_c w_c, where
+ *   w = max(p_n - q_n, 0) if position n has a draft, p_n otherwise (and if that sum is 0).
+ * So the tokens are distributed as the target alone would have drawn them, for
+ * u and r uniform in [0, 1). T = 0 (greedy): draft i stays while it is the lowest
+ * index of the maximum of z_i, and token n is that index of z_n.
+ *   draft_token    device [B][K]; one outside of [0, V) (say -1) ends its
+ *                  sequence's drafts: shorter drafts are padded with it.
+ *   accept_uniform device fp32 [B][K] (u), sample_uniform device fp32 [B] (r).
+ *   temperatures   device fp32 [B] (T of every sequence), or NULL.
+ *   accepted       device int32 [B] (n).
+ *   tokens         device [B][K + 1], of draft_token's type: t_0 .. t_{n-1}, token n, then -1.
+ *   logp           device fp32 [B][K + 1]: the target's log-probability of each
+ *                  token (T = 1 where T is 0), 0 behind the last.
+ * Logits of -inf have probability 0. Where a row that decides (the target's, or
+ * the draft model's at a draft) is all -inf or holds a NaN or +inf, or T is not
+ * as above, the sequence ends there with token -1 and log-probability NaN. Rows
+ * behind a sequence's last draft are not read. K = 0 (no draft pointers needed)
+ * draws one token a sequence.
+ */
+ce_status ce_verify_drafts(const ce_verify_params *p, const void *logits, const void *draft_logits,
+                           const void *draft_token, const float *accept_uniform, const float *sample_uniform,
+                           const float *temperatures, int32_t *accepted, void *tokens, float *logp, void *workspace,
+                           size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

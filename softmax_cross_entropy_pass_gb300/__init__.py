@@ -13,8 +13,8 @@ Entry points (same names as the C ABI):
   ce_fwd_bwd(logits, target, ...)            -> loss; gradient over logits
   ce_scale_grad(grad, grad_output, ...)      in-place grad_output scaling
   ce_workspace_size / ce_fused_plan / ce_get_status
-the token log-probability, policy and preference operators (logprob.py),
-and ``cross_entropy``: a torch.autograd entry with two modes.
+the token log-probability, policy and preference operators (logprob.py), the
+8-bit serving head (serving.py), and ``cross_entropy``: a torch.autograd entry with two modes.
 ``CrossEntropyFunction`` computes the gradient in the forward (in place) and
 scales it by grad_output in the backward, with a device-side skip when
 grad_output is 1 (one logits read and write; a second rounding when
@@ -513,3 +513,5 @@ from .logprob import (CE_FLAG_BAD_OFFSETS, PREFERENCE_KINDS, LinearTokenLogprobF
                       TokenLogprobFunction, ce_policy_fwd_bwd, ce_policy_params, ce_preference_fwd_bwd,
                       ce_preference_params, ce_token_logprob, ce_token_logprob_backward, flce_token_logprob,
                       flce_token_logprob_backward, linear_token_logprob, policy_loss, preference_loss, token_logprob)
+from .serving import (ce_gemm_fp8, ce_norm_params, ce_quantize_fp8, ce_rms_norm_fp8, ce_verify_drafts,  # noqa: E402
+                      ce_verify_params, fp8_head_logits)
