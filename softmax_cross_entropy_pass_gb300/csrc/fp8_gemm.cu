@@ -112,7 +112,7 @@ fp8_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
     const uint32_t tmem = tmem_slot;
 
     if (warp == 0) {
-        if (lane == 0) {
+        if (elect_one()) {
             // ------------------------------------------------ TMA producer
             uint32_t s = 0, round = 0;
             for (int tile = 0; tile < ntiles; ++tile) {
@@ -121,7 +121,7 @@ fp8_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
                 const uint32_t bytes = boxes * kFewBox * kFp8Block + NT * kFp8Block;
                 for (int kb = 0; kb < g.kblocks; ++kb) {
                     const uint32_t fb = smem_u32(&full[s]), dst = base + s * F::kStageBytes;
-                    if (round > 0) mbar_wait_bounded<false>(smem_u32(&empty[s]), (round - 1) & 1u, abort);
+                    if (round > 0) mbar_wait_polled(smem_u32(&empty[s]), (round - 1) & 1u, abort);
                     mbar_expect_tx(fb, bytes);
                     if (boxes == kFewM / kFewBox) {
                         tma_load_2d(dst, &tmW, kb * kFp8Block, v0, fb);
@@ -140,19 +140,19 @@ fp8_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
             const uint32_t used = round > 0 ? F::kStages : s;
             for (uint32_t i = 0; i < used; ++i) {
                 const uint32_t uses = round + (i < s ? 1u : 0u);
-                mbar_wait_bounded<false>(smem_u32(&full[i]), (uses - 1) & 1u, &drain_abort);
+                mbar_wait_polled(smem_u32(&full[i]), (uses - 1) & 1u, &drain_abort);
             }
         }
     } else if (warp == 1) {
-        if (lane == 0) {
+        if (elect_one()) {
             // ------------------------------------------------ MMA issuer: one accumulator a K block
             const uint32_t idesc = idesc_e4m3_f32(kFewM, NT);
             uint32_t s = 0, phase = 0, unit = 0;
             for (int tile = 0; tile < ntiles; ++tile)
                 for (int kb = 0; kb < g.kblocks; ++kb, ++unit) {
                     const uint32_t acc = unit % F::kAcc, u = unit / F::kAcc;
-                    if (u > 0) mbar_wait_bounded<false>(smem_u32(&tempty[acc]), (u - 1) & 1u, abort);
-                    mbar_wait_bounded<false>(smem_u32(&full[s]), phase, abort);
+                    if (u > 0) mbar_wait_polled(smem_u32(&tempty[acc]), (u - 1) & 1u, abort);
+                    mbar_wait_polled(smem_u32(&full[s]), phase, abort);
                     tc_fence_after();
                     const uint32_t a = base + s * F::kStageBytes, b = a + kFewWBytes;
 #pragma unroll
@@ -196,11 +196,11 @@ fp8_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
                 const float w = next;
                 if (kb + 1 < g.kblocks) next = __ldg(sb + kb + 1);
                 const uint32_t a = unit % F::kAcc, u = unit / F::kAcc;
-                mbar_wait_bounded<false>(smem_u32(&tfull[a]), u & 1u, abort);
+                mbar_wait_polled(smem_u32(&tfull[a]), u & 1u, abort);
                 tc_fence_after();
                 uint32_t v[C];
                 tmem_ld_cols<C>(taddr0 + a * NT, v);
-                tmem_ld_wait();
+                tmem_ld_wait(v);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&tempty[a]));
@@ -231,6 +231,254 @@ fp8_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
         tc_fence_after();
         tmem_dealloc(tmem, F::kTmemCols);
     }
+}
+
+// ------------------------------------------------------------------ CTA pairs
+// fp8_pair_kernel: many rows of A. A pair of CTAs (a cluster of 2, one CTA per
+// SM) per tile of 256 rows of A and 256 of the weight: the even CTA issues
+// tcgen05.mma.cta_group::2, each CTA loads its 128 rows of either operand a K
+// block (32 KB) and holds its 128 rows of the accumulator, 256 of the 512 columns
+// of tensor memory. Every K block's sums have to leave tensor memory before it is
+// used again, so the time from the end of a K block's MMAs to its accumulator's
+// return shows wherever it is longer than the next block's MMAs. Eight
+// epilogue warps a CTA scale and add a row and 128 columns a thread, with one scale
+// of A (through shared memory, copied half a chunk ahead) and one of the weight.
+// Barriers as in the bf16 product: `full` in the even CTA counts both CTAs'
+// bytes, `empty` and `tfull` are signalled by multicast commits, `tempty` in the
+// even CTA collects the 16 epilogue warps of the pair (each arrival from the other
+// CTA takes 6 ns: sixteen warps a CTA with half the columns were slower).
+constexpr int kPairM = 256, kPairN = 256, kPairStages = 6, kPairAcc = 2;
+constexpr int kPairHalf = 128 * kFp8Block;  // 16 KB: this CTA's half of an operand's stage
+constexpr int kPairEpi = 256;
+// four warps for the copies and the MMAs (two of them idle), so that warpgroups
+// can trade registers: launched with 168 a thread, the epilogue's two
+// warpgroups take 232 and the first keeps 40 (2 x 128 x 232 + 128 x 40 = 384 x 168)
+constexpr int kPairThreads = 128 + kPairEpi;
+constexpr int kPairLaunchRegs = 168, kPairEpiRegs = 232, kPairFirstRegs = 40;
+static_assert(kPairEpi * kPairEpiRegs + 128 * kPairFirstRegs <= kPairThreads * kPairLaunchRegs, "registers of the launch");
+constexpr int kPairChunk = 32;              // K blocks whose scales of A are in shared memory
+constexpr int kPairRow = 129;               // floats of one K block's scales: another bank for each block
+constexpr int kPairSmem = 1024 + kPairStages * 2 * kPairHalf + 2 * kPairChunk * kPairRow * 4;
+constexpr uint32_t kPairTmemCols = 512;
+
+// 32 bytes to a 32-byte aligned address: a whole sector a lane (rows lie apart)
+__device__ inline void st_sector(void *p, const uint4 &a, const uint4 &b) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w),
+                 "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w) : "memory");
+}
+
+// 16 consecutive columns of one row from column c on
+template <int DT>
+__device__ inline void store_cols(const Fp8Args &g, int row, int c, float (&x)[16], bool bad, bool sectors) {
+    if (g.bias) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+            if (c + j < g.n) x[j] += __ldg(g.bias + c + j);
+    }
+    if (bad) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) x[j] = NAN;
+    }
+    const int64_t at = static_cast<int64_t>(row) * g.ldo + c;
+    if (sectors && c + 16 <= g.n) {
+        char *o = reinterpret_cast<char *>(g.out) + at * Fmt<DT>::kBytes;
+        st_sector(o, Fmt<DT>::pack(x), Fmt<DT>::pack(x + Fmt<DT>::kVec));
+        if (DT == CE_DT_F32) st_sector(o + 32, Fmt<DT>::pack(x + 8), Fmt<DT>::pack(x + 12));
+    } else {
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+            if (c + j < g.n) store_out<DT>(g.out, at + j, x[j]);
+    }
+}
+
+template <int DT>
+__global__ void __launch_bounds__(kPairThreads, 1)
+fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, Fp8Args g) {
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint64_t full[kPairStages], empty[kPairStages], tfull[kPairAcc], tempty[kPairAcc];
+    __shared__ uint32_t tmem_slot;
+    __shared__ int abort_flag, drain_abort;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t rank = cluster_ctarank();
+    const int cid = static_cast<int>(cluster_id_x()), ncl = static_cast<int>(nclusters_x());
+    const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;  // the same offsets in both CTAs of the pair
+    float *scales = reinterpret_cast<float *>(smem_raw + (base - raw) + kPairStages * 2 * kPairHalf);
+    const uint32_t sA = base, sB = base + kPairStages * kPairHalf;
+    volatile int *abort = &abort_flag;
+    const int tiles_m = (g.m + kPairM - 1) / kPairM;
+    const int64_t tiles = static_cast<int64_t>(tiles_m) * ((g.n + kPairN - 1) / kPairN);
+
+    if (tid == 0) {
+        for (int st = 0; st < kPairStages; ++st) {
+            mbar_init(smem_u32(&full[st]), 1);
+            mbar_init(smem_u32(&empty[st]), 1);
+        }
+        for (int a = 0; a < kPairAcc; ++a) {
+            mbar_init(smem_u32(&tfull[a]), 1);
+            mbar_init(smem_u32(&tempty[a]), 2 * kPairEpi / 32);
+        }
+        abort_flag = drain_abort = 0;
+        fence_mbar_init_cluster();
+        tma_prefetch_desc(&tmA);
+        tma_prefetch_desc(&tmB);
+    }
+    __syncthreads();
+    cluster_sync_all();  // both CTAs' barriers exist before any remote arrive or copy
+    if (warp == 1) {
+        tmem_alloc_pair(smem_u32(&tmem_slot), kPairTmemCols);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPairFirstRegs));
+        if (warp == 0 && elect_one()) {
+            // ------------------------------------------------ TMA producer (both CTAs)
+            uint32_t s = 0, round = 0;
+            for (int64_t t = cid; t < tiles; t += ncl) {
+                const int row0 = static_cast<int>(t % tiles_m) * kPairM + static_cast<int>(rank) * 128;
+                const int col0 = static_cast<int>(t / tiles_m) * kPairN + static_cast<int>(rank) * 128;
+                for (int kb = 0; kb < g.kblocks; ++kb) {
+                    if (round > 0) mbar_wait_polled(smem_u32(&empty[s]), (round - 1) & 1u, abort);
+                    const uint32_t fb = mapa_shared(smem_u32(&full[s]), 0);  // the even CTA's barrier
+                    if (rank == 0) mbar_expect_tx(smem_u32(&full[s]), 4 * kPairHalf);
+                    tma_load_2d_pair(sA + s * kPairHalf, &tmA, kb * kFp8Block, row0, fb);
+                    tma_load_2d_pair(sB + s * kPairHalf, &tmB, kb * kFp8Block, col0, fb);
+                    if (++s == kPairStages) {
+                        s = 0;
+                        ++round;
+                    }
+                }
+            }
+            // the copies in flight, with a limit of their own where another wait gave up
+            if (rank == 0) {
+                const uint32_t used = round > 0 ? kPairStages : s;
+                for (uint32_t i = 0; i < used; ++i) {
+                    const uint32_t uses = round + (i < s ? 1u : 0u);
+                    mbar_wait_polled(smem_u32(&full[i]), (uses - 1) & 1u, &drain_abort);
+                }
+            }
+        }
+        if (warp == 1 && rank == 0 && elect_one()) {
+            // ------------------------------------------------ MMA issuer (even CTA): one accumulator a K block
+            const uint32_t idesc = idesc_e4m3_f32(kPairM, kPairN);
+            uint32_t s = 0, phase = 0, unit = 0;
+            for (int64_t t = cid; t < tiles; t += ncl)
+                for (int kb = 0; kb < g.kblocks; ++kb, ++unit) {
+                    const uint32_t acc = unit & 1u, u = unit >> 1;
+                    mbar_wait_polled(smem_u32(&full[s]), phase, abort);
+                    if (u > 0) mbar_wait_polled(smem_u32(&tempty[acc]), (u - 1) & 1u, abort);
+                    tc_fence_after();
+#pragma unroll
+                    for (int kk = 0; kk < kFp8Block / 32; ++kk)
+                        mma_e4m3_pair(tmem + acc * kPairN, smem_desc_sw128(sA + s * kPairHalf + kk * 32, 16, 1024),
+                                      smem_desc_sw128(sB + s * kPairHalf + kk * 32, 16, 1024), idesc, kk > 0 ? 1u : 0u);
+                    mma_commit_pair_mc(smem_u32(&tfull[acc]), 0x3);
+                    mma_commit_pair_mc(smem_u32(&empty[s]), 0x3);
+                    if (++s == kPairStages) {
+                        s = 0;
+                        phase ^= 1u;
+                    }
+                }
+        }
+    } else {
+        // ---------------------------------------------------- epilogue (warps 4..11, both CTAs)
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPairEpiRegs));
+        const int q = warp & 3, half = (warp - 4) >> 2;
+        const int et = tid - 128;
+        const uint32_t tempty0 = mapa_shared(smem_u32(&tempty[0]), 0);
+        const uint32_t lane_addr = tmem + (static_cast<uint32_t>(q * 32) << 16) + half * 128;
+        const bool sectors = ((reinterpret_cast<uintptr_t>(g.out) | static_cast<uintptr_t>(g.ldo * Fmt<DT>::kBytes)) & 31u) == 0;
+        // scales of A of this CTA's 128 rows of tile t, K blocks k0 .. k0 + 31, into buffer `buf` (rows past the last: its)
+        const auto fetch = [&](int64_t t, int k0, int buf) {
+            const int row0 = static_cast<int>(t % tiles_m) * kPairM + static_cast<int>(rank) * 128;
+            const int nb = min(kPairChunk, g.kblocks - k0), kb = et & 31;
+            const uint32_t dst = smem_u32(scales + buf * kPairChunk * kPairRow + kb * kPairRow);
+            if (kb < nb) {
+#pragma unroll
+                for (int r = et >> 5; r < 128; r += kPairEpi / 32) {
+                    const float *src = g.a_scale + static_cast<int64_t>(min(row0 + r, g.m - 1)) * g.kblocks + k0 + kb;
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst + r * 4), "l"(src) : "memory");
+                }
+            }
+        };
+        uint32_t unit = 0, chunk = 0;  // K blocks and chunks of scales so far
+        if (cid < tiles) fetch(cid, 0, 0);
+        for (int64_t t = cid; t < tiles; t += ncl) {
+            const int row = static_cast<int>(t % tiles_m) * kPairM + static_cast<int>(rank) * 128 + q * 32 + lane;
+            const int col0 = static_cast<int>(t / tiles_m) * kPairN + half * 128;
+            // columns past the last are multiplied like it, and not stored
+            const float *sb = g.b_scale + static_cast<int64_t>(min(col0, g.n - 1) / kFp8Block) * g.kblocks;
+            F2 acc[64];
+#pragma unroll
+            for (int j = 0; j < 64; ++j) acc[j] = f2(0.f, 0.f);
+            float next = __ldg(sb);
+            for (int kb = 0; kb < g.kblocks; ++kb, ++unit) {
+                const int k0 = kb % kPairChunk;
+                if (k0 == 0) {
+                    // this chunk's scales have arrived, and no warp reads the chunk before last any more
+                    asm volatile("cp.async.wait_all;" ::: "memory");
+                    asm volatile("bar.sync 1, %0;" ::"n"(kPairEpi) : "memory");
+                    ++chunk;
+                }
+                if (k0 == min(kPairChunk, g.kblocks - (kb - k0)) / 2) {
+                    // halfway: the next chunk's, of this tile or the next
+                    const int k1 = kb - k0 + kPairChunk;
+                    if (k1 < g.kblocks) fetch(t, k1, chunk & 1u);
+                    else if (t + ncl < tiles) fetch(t + ncl, 0, chunk & 1u);
+                }
+                const float w1 = scales[((chunk - 1) & 1u) * kPairChunk * kPairRow + k0 * kPairRow + q * 32 + lane] * next;
+                const F2 w = f2(w1, w1);
+                if (kb + 1 < g.kblocks) next = __ldg(sb + kb + 1);
+                const uint32_t a = unit & 1u;
+                mbar_wait_polled(smem_u32(&tfull[a]), (unit >> 1) & 1u, abort);
+                tc_fence_after();
+                const uint32_t taddr = lane_addr + a * kPairN;
+                // 96 columns at once, the last 32 while others are added: all 128 would not fit beside the sums
+                uint32_t v[3][32];
+                const auto add = [&](const uint32_t (&x)[32], int at) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        acc[at + j] = f2_fma(f2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])), w, acc[at + j]);
+                };
+                tmem_ld_32x32b_x32(taddr, v[0]);
+                tmem_ld_32x32b_x32(taddr + 32, v[1]);
+                tmem_ld_32x32b_x32(taddr + 64, v[2]);
+                tmem_ld_wait(v[0]);
+                tmem_ld_wait(v[1]);
+                tmem_ld_wait(v[2]);
+                add(v[0], 0);
+                tmem_ld_32x32b_x32(taddr + 96, v[0]);
+                add(v[1], 16);
+                tmem_ld_wait(v[0]);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_relaxed(tempty0 + a * 8u);
+                add(v[2], 32);
+                add(v[0], 48);
+            }
+            if (row < g.m) {
+                const bool bad = *abort != 0;  // a wait that gave up leaves no result
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    float x[16];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) f2_split(acc[c * 8 + j], x[2 * j], x[2 * j + 1]);
+                    if (col0 + c * 16 < g.n) store_cols<DT>(g, row, col0 + c * 16, x, bad, sectors);
+                }
+            }
+        }
+    }
+    __syncthreads();
+    cluster_sync_all();  // every MMA of the pair has completed and both CTAs have read their accumulators
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem, kPairTmemCols);
+    }
+    cluster_sync_all();  // no CTA leaves while its peer may still signal one of its barriers
 }
 
 template <typename Fn>
@@ -276,7 +524,75 @@ cudaError_t launch_few(const void *A, int64_t lda, const void *B, int64_t ldb, F
     return launch_few_t<NT, CE_DT_F32>(tw, tws, ta, g, grid, s);
 }
 
-cudaError_t fp8_gemm(const void *A, int64_t lda, const void *B, int64_t ldb, const Fp8Args &g, int dtype, cudaStream_t s) {
+// Resident CTA pairs of the pair kernel on a device (0 if unknown), asked once.
+int pair_clusters(const void *fn, int dev) {
+    constexpr int kDevs = 64;
+    static std::atomic<int> known[kDevs];
+    int n = 0;
+    if (dev < kDevs && (n = known[dev].load()) > 0) return n;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * 128);
+    cfg.blockDim = dim3(kPairThreads);
+    cfg.dynamicSmemBytes = kPairSmem;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = 2;
+    at.val.clusterDim.y = 1;
+    at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess) n = 0;
+    (void)cudaGetLastError();
+    if (dev < kDevs && n > 0) known[dev].store(n);
+    return n;
+}
+
+template <int DT>
+cudaError_t launch_pair(const void *A, int64_t lda, const void *B, int64_t ldb, Fp8Args g, cudaStream_t s) {
+    static std::atomic<uint64_t> done{0};
+    const void *fn = reinterpret_cast<const void *>(&fp8_pair_kernel<DT>);
+    CUtensorMap ta, tb;
+    cudaError_t e = make_tmap_bytes(&ta, A, g.m, g.K, lda, 128);
+    if (e == cudaSuccess) e = make_tmap_bytes(&tb, B, g.n, g.K, ldb, 128);
+    if (e == cudaSuccess && done.load() == 0) {
+        // a share above what the launch brings would wait for ever
+        cudaFuncAttributes at;
+        e = cudaFuncGetAttributes(&at, fn);
+        if (e == cudaSuccess && at.numRegs != kPairLaunchRegs) e = cudaErrorInvalidConfiguration;
+    }
+    if (e == cudaSuccess) e = allow_smem(fn, kPairSmem, done);
+    int dev = 0;
+    if (e == cudaSuccess) e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    int clusters = pair_clusters(fn, dev);
+    if (clusters < 1) clusters = kSms / 2;
+    const int64_t tiles = static_cast<int64_t>((g.m + kPairM - 1) / kPairM) * ((g.n + kPairN - 1) / kPairN);
+    if (clusters > tiles) clusters = static_cast<int>(tiles);
+    void *args[] = {&ta, &tb, &g};
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * clusters));
+    cfg.blockDim = dim3(kPairThreads);
+    cfg.dynamicSmemBytes = kPairSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = 2;
+    at.val.clusterDim.y = 1;
+    at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelExC(&cfg, fn, args);
+}
+
+enum { FP8_AUTO = 0, FP8_FEW = 1, FP8_PAIR = 2 };
+
+cudaError_t fp8_gemm(const void *A, int64_t lda, const void *B, int64_t ldb, const Fp8Args &g, int dtype, int mode,
+                     cudaStream_t s) {
+    if (mode == FP8_PAIR || (mode == FP8_AUTO && g.m > 256)) {
+        if (dtype == CE_DT_BF16) return launch_pair<CE_DT_BF16>(A, lda, B, ldb, g, s);
+        if (dtype == CE_DT_F16) return launch_pair<CE_DT_F16>(A, lda, B, ldb, g, s);
+        return launch_pair<CE_DT_F32>(A, lda, B, ldb, g, s);
+    }
     if (g.m <= 16) return launch_few<16>(A, lda, B, ldb, g, dtype, s);
     if (g.m <= 32) return launch_few<32>(A, lda, B, ldb, g, dtype, s);
     if (g.m <= 64) return launch_few<64>(A, lda, B, ldb, g, dtype, s);
@@ -317,6 +633,6 @@ extern "C" ce_status ce_gemm_fp8(int64_t M, int64_t N, int64_t K, const void *A,
     g.bias = bias;
     g.out = D;
     g.ldo = ldd;
-    const cudaError_t e = fp8_gemm(A, lda, B, ldb, g, dtype, reinterpret_cast<cudaStream_t>(stream));
+    const cudaError_t e = fp8_gemm(A, lda, B, ldb, g, dtype, FP8_AUTO, reinterpret_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? CE_OK : cuda_fail(e);
 }

@@ -40,27 +40,40 @@ __device__ inline uint32_t e4m3x4(float a, float b, float c, float d) {
     return lo | (hi << 16);
 }
 
-// Eight consecutive elements of a row from column c on, zeros past the last.
-// VEC: the row starts on a 16-byte boundary (c is a multiple of 8).
+// Eight consecutive elements of a row as they lie in memory.
+template <int DT> struct Raw8 {
+    uint4 v[DT == CE_DT_F32 ? 2 : 1];
+    __device__ inline void unpack(float (&x)[8]) const {
+        Fmt<DT>::unpack(v[0], x);
+        if constexpr (DT == CE_DT_F32) Fmt<DT>::unpack(v[1], x + 4);
+    }
+    __device__ inline void pack(const float (&x)[8]) {
+        v[0] = Fmt<DT>::pack(x);
+        if constexpr (DT == CE_DT_F32) v[1] = Fmt<DT>::pack(x + 4);
+    }
+};
+
+// ... from column c on, zeros past the last. VEC: the row starts on a 16-byte
+// boundary (c is a multiple of 8).
 template <int DT, bool VEC>
-__device__ inline void load8(const void *row, int64_t c, int64_t cols, float (&x)[8]) {
+__device__ inline Raw8<DT> load8(const void *row, int c, int cols) {
+    Raw8<DT> r;
     if (VEC && c + 8 <= cols) {
-        const char *p = reinterpret_cast<const char *>(row) + c * Fmt<DT>::kBytes;
-        const uint4 a = ld_stream(p);
-        Fmt<DT>::unpack(a, x);
-        if (DT == CE_DT_F32) {
-            const uint4 b = ld_stream(p + 16);
-            Fmt<DT>::unpack(b, x + 4);
-        }
+        const char *p = reinterpret_cast<const char *>(row) + static_cast<int64_t>(c) * Fmt<DT>::kBytes;
+        r.v[0] = ld_stream(p);
+        if constexpr (DT == CE_DT_F32) r.v[1] = ld_stream(p + 16);
     } else {
+        float x[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) x[j] = c + j < cols ? Fmt<DT>::load1(row, c + j) : 0.f;
+        r.pack(x);
     }
+    return r;
 }
 template <int DT, bool VEC>
-__device__ inline void store8(void *row, int64_t c, int64_t cols, const float (&x)[8]) {
+__device__ inline void store8(void *row, int c, int cols, const float (&x)[8]) {
     if (VEC && c + 8 <= cols) {
-        uint4 *p = reinterpret_cast<uint4 *>(reinterpret_cast<char *>(row) + c * Fmt<DT>::kBytes);
+        uint4 *p = reinterpret_cast<uint4 *>(reinterpret_cast<char *>(row) + static_cast<int64_t>(c) * Fmt<DT>::kBytes);
         p[0] = Fmt<DT>::pack(x);
         if (DT == CE_DT_F32) p[1] = Fmt<DT>::pack(x + 4);
     } else {
@@ -70,7 +83,7 @@ __device__ inline void store8(void *row, int64_t c, int64_t cols, const float (&
     }
 }
 // the rows of q start on 16-byte boundaries, whatever the input's do
-__device__ inline void store_q8(uint8_t *row, int64_t c, int64_t cols, const float (&y)[8], float inv) {
+__device__ inline void store_q8(uint8_t *row, int c, int cols, const float (&y)[8], float inv) {
     const uint32_t lo = e4m3x4(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
     const uint32_t hi = e4m3x4(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv);
     if (c + 8 <= cols) {
@@ -92,45 +105,56 @@ __device__ inline float block_amax(const float (&y)[8]) {
     return a;
 }
 
+// eight weights, read for every row: kept in L1
+template <int DT>
+__device__ inline void load_weight(const void *w, int c, int cols, float (&x)[8]) {
+    if (c + 8 <= cols) {
+        const uint4 *p = reinterpret_cast<const uint4 *>(reinterpret_cast<const char *>(w) + static_cast<int64_t>(c) * Fmt<DT>::kBytes);
+        Fmt<DT>::unpack(__ldg(p), x);
+        if constexpr (DT == CE_DT_F32) Fmt<DT>::unpack(__ldg(p + 1), x + 4);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = c + j < cols ? Fmt<DT>::load1(w, c + j) : 0.f;
+    }
+}
+
 struct NormArgs {
     const void *x, *residual, *weight;
     void *residual_out;
     uint8_t *q;
     float *scale;
-    int64_t n_rows, cols, ld_x, ld_res, ld_out, ld_q, blocks;
-    int weight_f32;
+    int64_t n_rows, ld_x, ld_res, ld_out, ld_q, blocks;
+    int cols, weight_f32;
     float eps;
 };
 
-// One CTA per row; thread t holds the vectors of 8 columns t, t + threads, ...
-// (16 neighbouring lanes hold a block).
-template <int DT, bool VEC, int VPT>
-__global__ void __launch_bounds__(1024) norm_fp8_kernel(NormArgs a) {
-    __shared__ float part[32];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nwarps = blockDim.x >> 5;
-    const int64_t row = blockIdx.x;
-    const char *x = reinterpret_cast<const char *>(a.x) + row * a.ld_x * Fmt<DT>::kBytes;
-    const char *r = reinterpret_cast<const char *>(a.residual) + row * a.ld_res * Fmt<DT>::kBytes;
-    float h[VPT][8];
+constexpr int kNormWarpThreads = 256;  // a warp a row; 512 and 1024: a CTA a row
+
+// A row by one warp (MAXT = kNormWarpThreads) or by a CTA's W; thread t of a row's holds the vectors of 8 columns t, t + 32 W, ... (16 neighbouring
+// lanes hold a block). Rows are dealt out round robin, and the next row's loads
+// are under way while the reductions of this one wait for one another (not above
+// 16384 columns, whose registers are all taken): a row at a time left HBM at 65%.
+template <int DT, bool VEC, int VPT, int MAXT>
+__global__ void __launch_bounds__(MAXT, 1) norm_fp8_kernel(NormArgs a) {
+    constexpr bool WARP = MAXT == kNormWarpThreads, AHEAD = MAXT <= 512;
+    __shared__ float part[2][32];
+    const int lane = threadIdx.x & 31, nwarps = WARP ? 1 : blockDim.x >> 5, warp = WARP ? 0 : threadIdx.x >> 5;
+    const int tid = WARP ? lane : threadIdx.x, step = 8 * 32 * nwarps;
+    const int64_t stride = WARP ? static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5) : gridDim.x;
+    int64_t row = WARP ? static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x;
+    Raw8<DT> x[VPT], r[VPT];
+    const auto fetch = [&](int64_t i) {
+        const char *px = reinterpret_cast<const char *>(a.x) + i * a.ld_x * Fmt<DT>::kBytes;
+        const char *pr = reinterpret_cast<const char *>(a.residual) + i * a.ld_res * Fmt<DT>::kBytes;
 #pragma unroll
-    for (int v = 0; v < VPT; ++v) {
-        const int64_t c = (static_cast<int64_t>(v) * blockDim.x + tid) * 8;
-        load8<DT, VEC>(x, c, a.cols, h[v]);
-        if (a.residual) {
-            float b[8];
-            load8<DT, VEC>(r, c, a.cols, b);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) h[v][j] += b[j];
+        for (int v = 0; v < VPT; ++v) {
+            x[v] = load8<DT, VEC>(px, tid * 8 + v * step, a.cols);
+            if (a.residual) r[v] = load8<DT, VEC>(pr, tid * 8 + v * step, a.cols);
         }
-    }
-    if (a.residual_out) {
-        char *o = reinterpret_cast<char *>(a.residual_out) + row * a.ld_out * Fmt<DT>::kBytes;
-#pragma unroll
-        for (int v = 0; v < VPT; ++v)
-            store8<DT, VEC>(o, (static_cast<int64_t>(v) * blockDim.x + tid) * 8, a.cols, h[v]);
-    }
+    };
+    int turn = 0;
     // sum over the row of (h f)^2, the same in every thread
-    const auto squares = [&](float f) {
+    const auto squares = [&](const float (&h)[VPT][8], float f) {
         float t = 0.f;
 #pragma unroll
         for (int v = 0; v < VPT; ++v)
@@ -138,38 +162,60 @@ __global__ void __launch_bounds__(1024) norm_fp8_kernel(NormArgs a) {
             for (int j = 0; j < 8; ++j) t = fmaf(h[v][j] * f, h[v][j] * f, t);
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
-        if (lane == 0) part[warp] = t;
-        __syncthreads();
-        t = lane < nwarps ? part[lane] : 0.f;
+        if (!WARP) {
+            // two buffers in turn: nobody writes one that a warp may still read
+            if (lane == 0) part[turn][warp] = t;
+            __syncthreads();
+            t = lane < nwarps ? part[turn][lane] : 0.f;
+            turn ^= 1;
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
+            for (int off = 16; off > 0; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
+        }
         return t;
     };
-    // squares past fp32's range, or under it beside an eps that small, are taken of h 2^-80 or h 2^80
-    float f = 1.f, ss = squares(1.f);
-    if (ss == INFINITY) f = 0x1p-80f;
-    else if (ss < 1e-28f && a.eps < 1e-28f) f = 0x1p80f;
-    if (f != 1.f) {
-        __syncthreads();
-        ss = squares(f);
-    }
-    const float rstd = f / sqrtf(ss / static_cast<float>(a.cols) + a.eps * f * f);
-    uint8_t *q = a.q + row * a.ld_q;
-    float *scales = a.scale + row * a.blocks;
+    if (row < a.n_rows) fetch(row);
+    for (; row < a.n_rows; row += stride) {
+        float h[VPT][8];
 #pragma unroll
-    for (int v = 0; v < VPT; ++v) {
-        const int64_t c = (static_cast<int64_t>(v) * blockDim.x + tid) * 8;
-        float w[8];
-        if (a.weight_f32) load8<CE_DT_F32, true>(a.weight, c, a.cols, w);
-        else load8<DT, true>(a.weight, c, a.cols, w);
+        for (int v = 0; v < VPT; ++v) {
+            x[v].unpack(h[v]);
+            if (a.residual) {
+                float b[8];
+                r[v].unpack(b);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) h[v][j] = h[v][j] * rstd * w[j];
-        float inv;
-        const float scale = block_scale(block_amax(h[v]), inv);
-        if (c < a.cols) {
-            store_q8(q, c, a.cols, h[v], inv);
-            if ((lane & 15) == 0) scales[c / kFp8Block] = scale;
+                for (int j = 0; j < 8; ++j) h[v][j] += b[j];
+            }
         }
+        if (AHEAD && row + stride < a.n_rows) fetch(row + stride);
+        if (a.residual_out) {
+            char *o = reinterpret_cast<char *>(a.residual_out) + row * a.ld_out * Fmt<DT>::kBytes;
+#pragma unroll
+            for (int v = 0; v < VPT; ++v) store8<DT, VEC>(o, tid * 8 + v * step, a.cols, h[v]);
+        }
+        // squares past fp32's range, or under it beside an eps that small, are taken of h 2^-80 or h 2^80
+        float f = 1.f, ss = squares(h, 1.f);
+        if (ss == INFINITY) f = 0x1p-80f;
+        else if (ss < 1e-28f && a.eps < 1e-28f) f = 0x1p80f;
+        if (f != 1.f) ss = squares(h, f);
+        const float rstd = f / sqrtf(ss / static_cast<float>(a.cols) + a.eps * f * f);
+        uint8_t *q = a.q + row * a.ld_q;
+        float *scales = a.scale + row * a.blocks;
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) {
+            const int c = tid * 8 + v * step;
+            float w[8];
+            if (a.weight_f32) load_weight<CE_DT_F32>(a.weight, c, a.cols, w);
+            else load_weight<DT>(a.weight, c, a.cols, w);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) h[v][j] = h[v][j] * rstd * w[j];
+            float inv;
+            const float scale = block_scale(block_amax(h[v]), inv);
+            if (c < a.cols) {
+                store_q8(q, c, a.cols, h[v], inv);
+                if ((lane & 15) == 0) scales[c / kFp8Block] = scale;
+            }
+        }
+        if (!AHEAD && row + stride < a.n_rows) fetch(row + stride);
     }
 }
 
@@ -177,51 +223,61 @@ struct QuantArgs {
     const void *x;
     uint8_t *q;
     float *scale;
-    int64_t rows, cols, ld, ld_q, blocks;
-    int64_t parts;  // CTAs of a row
+    int64_t rows, ld, ld_q;
+    int cols, blocks;
+    int parts;  // CTAs of a row (of a row of blocks)
 };
 
 // 1 x 128: a half warp per block, kRowVecs vectors a thread
 constexpr int kRowVecs = 4, kRowQuantThreads = 128;
 template <int DT, bool VEC>
 __global__ void __launch_bounds__(kRowQuantThreads) quant_rows_kernel(QuantArgs a) {
-    const int64_t row = blockIdx.x / a.parts, part = blockIdx.x % a.parts;
+    const int64_t row = blockIdx.x / a.parts;
+    const int part = blockIdx.x % a.parts;
     const char *x = reinterpret_cast<const char *>(a.x) + row * a.ld * Fmt<DT>::kBytes;
-    float y[kRowVecs][8];
-    const int64_t c0 = (part * kRowVecs * kRowQuantThreads + threadIdx.x) * 8;
+    Raw8<DT> raw[kRowVecs];
+    const int c0 = (part * kRowVecs * kRowQuantThreads + threadIdx.x) * 8;
 #pragma unroll
-    for (int v = 0; v < kRowVecs; ++v) load8<DT, VEC>(x, c0 + v * kRowQuantThreads * 8, a.cols, y[v]);
+    for (int v = 0; v < kRowVecs; ++v) raw[v] = load8<DT, VEC>(x, c0 + v * kRowQuantThreads * 8, a.cols);
 #pragma unroll
     for (int v = 0; v < kRowVecs; ++v) {
-        const int64_t c = c0 + v * kRowQuantThreads * 8;
-        float inv;
-        const float scale = block_scale(block_amax(y[v]), inv);
+        const int c = c0 + v * kRowQuantThreads * 8;
+        float y[8], inv;
+        raw[v].unpack(y);
+        const float scale = block_scale(block_amax(y), inv);
         if (c < a.cols) {
-            store_q8(a.q + row * a.ld_q, c, a.cols, y[v], inv);
+            store_q8(a.q + row * a.ld_q, c, a.cols, y, inv);
             if ((threadIdx.x & 15) == 0) a.scale[row * a.blocks + c / kFp8Block] = scale;
         }
     }
 }
 
-// 128 x 128: a CTA per block, half a warp per row, 8 rows a half warp
+// 128 x 128: a CTA per block, half a warp per row, 8 rows a half warp. The block
+// stays in registers as it was read (32 of them in 16 bits), so that three CTAs an
+// SM have their loads in flight.
 constexpr int kTileThreads = 256, kTileRows = kFp8Block / (kTileThreads / 16);
 template <int DT, bool VEC>
-__global__ void __launch_bounds__(kTileThreads) quant_tiles_kernel(QuantArgs a) {
+__global__ void __launch_bounds__(kTileThreads, DT == CE_DT_F32 ? 2 : 3) quant_tiles_kernel(QuantArgs a) {
     __shared__ float part[kTileThreads / 32];
-    const int64_t up = blockIdx.x / a.blocks, across = blockIdx.x % a.blocks;
-    const int64_t c = across * kFp8Block + (threadIdx.x & 15) * 8;
+    const int64_t up = blockIdx.x / a.blocks;
+    const int across = blockIdx.x % a.blocks;
+    const int c = across * kFp8Block + (threadIdx.x & 15) * 8;
     const int64_t r0 = up * kFp8Block + (threadIdx.x >> 4);
-    float y[kTileRows][8], amax = 0.f;
+    Raw8<DT> raw[kTileRows];
+    float amax = 0.f;
 #pragma unroll
     for (int v = 0; v < kTileRows; ++v) {
         const int64_t r = r0 + v * (kTileThreads / 16);
         const char *x = reinterpret_cast<const char *>(a.x) + r * a.ld * Fmt<DT>::kBytes;
-        load8<DT, VEC>(x, c, r < a.rows ? a.cols : 0, y[v]);
+        raw[v] = load8<DT, VEC>(x, c, r < a.rows ? a.cols : 0);
     }
 #pragma unroll
-    for (int v = 0; v < kTileRows; ++v)
+    for (int v = 0; v < kTileRows; ++v) {
+        float y[8];
+        raw[v].unpack(y);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) amax = max_nan(amax, fabsf(y[v][j]));
+        for (int j = 0; j < 8; ++j) amax = max_nan(amax, fabsf(y[j]));
+    }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, off));
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = amax;
@@ -235,24 +291,43 @@ __global__ void __launch_bounds__(kTileThreads) quant_tiles_kernel(QuantArgs a) 
 #pragma unroll
     for (int v = 0; v < kTileRows; ++v) {
         const int64_t r = r0 + v * (kTileThreads / 16);
-        if (r < a.rows && c < a.cols) store_q8(a.q + r * a.ld_q, c, a.cols, y[v], inv);
+        float y[8];
+        raw[v].unpack(y);
+        if (r < a.rows && c < a.cols) store_q8(a.q + r * a.ld_q, c, a.cols, y, inv);
     }
 }
 
-// Vectors a thread: one while the row's 8-column vectors fit 1024 threads.
+// A warp a row up to 1024 columns; above, a CTA a row, with one vector of 8 columns
+// a thread while the rows are few (latency) or short, two or four otherwise.
 cudaError_t launch_norm(const NormArgs &a, int dtype, bool vec, cudaStream_t s) {
-    const int64_t vecs = (a.cols + 7) / 8;
-    const int vpt = vecs <= 1024 ? 1 : (vecs <= 2048 ? 2 : 4);
-    const int threads = static_cast<int>(((vecs + vpt - 1) / vpt + 31) / 32 * 32);
+    const int vecs = (a.cols + 7) / 8;
     using Fn = void (*)(NormArgs);
-#define CE_NORM(DT) {{norm_fp8_kernel<DT, false, 1>, norm_fp8_kernel<DT, false, 2>, norm_fp8_kernel<DT, false, 4>}, \
-                     {norm_fp8_kernel<DT, true, 1>, norm_fp8_kernel<DT, true, 2>, norm_fp8_kernel<DT, true, 4>}}
-    static const Fn fns[3][2][3] = {CE_NORM(CE_DT_F32), CE_NORM(CE_DT_BF16), CE_NORM(CE_DT_F16)};
+#define CE_NORM(DT, V) {norm_fp8_kernel<DT, V, 1, 256>, norm_fp8_kernel<DT, V, 2, 256>, norm_fp8_kernel<DT, V, 4, 256>, \
+                        norm_fp8_kernel<DT, V, 1, 512>, norm_fp8_kernel<DT, V, 2, 512>, norm_fp8_kernel<DT, V, 4, 512>, \
+                        norm_fp8_kernel<DT, V, 4, 1024>}
+    static const Fn fns[3][2][7] = {{CE_NORM(CE_DT_F32, false), CE_NORM(CE_DT_F32, true)},
+                                    {CE_NORM(CE_DT_BF16, false), CE_NORM(CE_DT_BF16, true)},
+                                    {CE_NORM(CE_DT_F16, false), CE_NORM(CE_DT_F16, true)}};
 #undef CE_NORM
+    constexpr int kSms = 152;
     NormArgs b = a;
     void *args[] = {&b};
-    return cudaLaunchKernel(reinterpret_cast<const void *>(fns[dtype][vec ? 1 : 0][vpt >> 1]),
-                            dim3(static_cast<unsigned>(a.n_rows)), dim3(threads), args, 0, s);
+    int which, threads;
+    int64_t grid;
+    if (vecs <= 128) {
+        which = vecs <= 32 ? 0 : (vecs <= 64 ? 1 : 2);
+        threads = a.n_rows >= 8 * kSms ? 256 : 32;
+        grid = (a.n_rows + threads / 32 - 1) / (threads / 32);
+    } else {
+        const int vpt = vecs > 1024 ? 4 : (vecs > 512 || (vecs > 256 && a.n_rows > 2 * kSms) ? 2 : 1);
+        which = vecs > 2048 ? 6 : 3 + (vpt >> 1);
+        threads = ((vecs + vpt - 1) / vpt + 31) / 32 * 32;
+        grid = a.n_rows;
+    }
+    const int64_t most = static_cast<int64_t>(kSms) * (1024 / threads > 0 ? 1024 / threads : 1);
+    if (grid > most) grid = most;
+    return cudaLaunchKernel(reinterpret_cast<const void *>(fns[dtype][vec ? 1 : 0][which]),
+                            dim3(static_cast<unsigned>(grid)), dim3(threads), args, 0, s);
 }
 
 bool vec_rows(const void *p, int64_t ld, int esz, int64_t rows) {
@@ -309,7 +384,7 @@ ce_status ce_rms_norm_fp8(const ce_norm_params *p, const void *x, const void *re
     a.x = x; a.residual = residual; a.weight = weight; a.residual_out = residual_out;
     a.q = reinterpret_cast<uint8_t *>(q);
     a.scale = scale;
-    a.n_rows = n; a.cols = p->cols;
+    a.n_rows = n; a.cols = static_cast<int>(p->cols);
     a.ld_x = p->ld_x; a.ld_res = p->ld_residual; a.ld_out = p->ld_residual_out; a.ld_q = p->ld_q;
     a.blocks = blocks;
     a.weight_f32 = p->weight_dtype == CE_DT_F32;
@@ -332,12 +407,13 @@ ce_status ce_quantize_fp8(int64_t rows, int64_t cols, const void *x, int64_t ld_
     a.x = x;
     a.q = reinterpret_cast<uint8_t *>(q);
     a.scale = scale;
-    a.rows = rows; a.cols = cols; a.ld = ld_x; a.ld_q = ld_q;
-    a.blocks = (cols + kFp8Block - 1) / kFp8Block;
+    if (rows > kMaxRows || cols > kMaxRows - 8192) return CE_ERR_UNSUPPORTED;  // column indices are 32-bit
+    a.rows = rows; a.cols = static_cast<int>(cols); a.ld = ld_x; a.ld_q = ld_q;
+    a.blocks = static_cast<int>((cols + kFp8Block - 1) / kFp8Block);
     const int64_t up = block_rows == 1 ? rows : (rows + kFp8Block - 1) / kFp8Block;
-    const int64_t per = kRowVecs * kRowQuantThreads * 8;
-    a.parts = block_rows == 1 ? (cols + per - 1) / per : a.blocks;
-    if (rows > kMaxRows || cols > kMaxRows || up > kMaxRows / a.parts) return CE_ERR_UNSUPPORTED;
+    constexpr int64_t per = kRowVecs * kRowQuantThreads * 8;
+    a.parts = block_rows == 1 ? static_cast<int>((cols + per - 1) / per) : a.blocks;
+    if (up > kMaxRows / a.parts) return CE_ERR_UNSUPPORTED;
     const int64_t xb = span(rows, ld_x, cols, esz), qb = span(rows, ld_q, cols, 1), sb = up * a.blocks * 4;
     if (!fp8_apart(q, qb, x, xb) || !fp8_apart(scale, sb, x, xb) || !fp8_apart(q, qb, scale, sb)) return CE_ERR_INVALID_ARG;
     using Fn = void (*)(QuantArgs);

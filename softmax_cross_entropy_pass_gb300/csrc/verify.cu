@@ -7,8 +7,8 @@
 //            w = max(p_n - q_n, 0) where position n has a draft, p_n otherwise (and where that sum is 0)
 //   T = 0: draft i stays where it is the lowest index of the row's maximum, which is also token n
 //
-// Two kernels. The first forms, for parts of every row, M = max x, s = sum
-// 2^((x - M) k), k = log2(e) / T, and the lowest index of M. The second (a
+// Two kernels. The first forms, for parts of every row, M = max x, its lowest index,
+// and the sum of the other terms 2^((x - M) k), k = log2(e) / T. The second (a
 // cluster of CTAs per sequence) merges them in a fixed order, decides, and reads
 // row n once more to draw the token: every warp sums w over a contiguous range,
 // the ranges' sums (fp64) meet in the cluster, and the CTA whose range holds
@@ -59,17 +59,22 @@ __device__ inline bool vf_temp_ok(float t) { return t == 0.f || (t >= 1e-4f && t
 // log2(e) / T; greedy sequences report log-probabilities at T = 1
 __device__ inline float vf_k(float t) { return t == 0.f ? kLog2e : kLog2e / t; }
 
+// Statistics of a set of logits: the maximum m, its lowest index, and the sum s of
+// the other terms 2^((x - m) k). The maximum's own term is exactly 1 and kept
+// out of the sum, so that the log-probability -log1p(s) of a likely token forms
+// without cancellation. Empty (or -inf alone): m = -inf, s = 0; NaN stays in s.
 struct VfState {
     float m, s;
     int at;
 };
+// what a set with maximum m and sum s adds to the others of a set whose maximum M >= m is another element
+__device__ inline float vf_shift(float m, float s, float M, float k) {
+    return m == -INFINITY ? s : (1.f + s) * ex2_hw((m - M) * k);
+}
 __device__ inline VfState vf_merge(const VfState &a, const VfState &b, float k) {
     const bool first = a.m > b.m || (a.m == b.m && a.at <= b.at);
     const VfState &hi = first ? a : b, &lo = first ? b : a;
-    VfState r = hi;
-    // an empty side has s = 0, a side of -inf alone too; NaN sums stay
-    r.s += lo.m == -INFINITY ? lo.s : lo.s * ex2_hw((lo.m - hi.m) * k);
-    return r;
+    return VfState{hi.m, hi.s + vf_shift(lo.m, lo.s, hi.m, k), hi.at};
 }
 
 // Statistics of elements [lo, hi) of one row by the whole CTA; the result in thread 0.
@@ -84,12 +89,8 @@ __device__ inline VfState vf_row_part(const void *row, int lo, int hi, float k, 
     VfState st{-INFINITY, 0.f, kNone};
     const auto one = [&](int i) {
         const float x = Fmt<DT>::load1(row, i);
-        if (x > st.m) {
-            st.s = st.m == -INFINITY ? st.s : st.s * ex2_hw((st.m - x) * k);
-            st.m = x;
-            st.at = i;
-        }
-        if (st.m != -INFINITY || x != x) st.s += ex2_hw((x - (st.m == -INFINITY ? 0.f : st.m)) * k);
+        if (x > st.m) st = VfState{x, x == INFINITY ? NAN : vf_shift(st.m, st.s, x, k), i};
+        else st.s += st.m == -INFINITY ? (x != x ? x : 0.f) : ex2_hw((x - st.m) * k);
     };
     const int t = threadIdx.x;
     if (t < head) one(lo + t);
@@ -106,21 +107,26 @@ __device__ inline VfState vf_row_part(const void *row, int lo, int hi, float k, 
                 Fmt<DT>::unpack(raw[q], x);
                 const float vmax = Fmt<DT>::vmax(raw[q]);
                 if (vmax > st.m) {
-                    st.s = st.m == -INFINITY ? st.s : st.s * ex2_hw((st.m - vmax) * k);
-                    st.m = vmax;
-                    st.at = lo + head + (i + q * kThreads) * N;  // the vector's first element, made exact below
-                }
-                const float m = st.m == -INFINITY ? 0.f : st.m;
-                float s = 0.f;
+                    // the vector's first maximum leaves the sum, what was there joins it
+                    float sum = vmax == INFINITY ? NAN : vf_shift(st.m, st.s, vmax, k);
+                    int at = -1;
 #pragma unroll
-                for (int j = 0; j < N; ++j) s += ex2_hw((x[j] - m) * k);
-                st.s += s;
+                    for (int j = 0; j < N; ++j) {
+                        if (at < 0 && x[j] == vmax) at = j;
+                        else sum += ex2_hw((x[j] - vmax) * k);
+                    }
+                    st = VfState{vmax, sum, lo + head + (i + q * kThreads) * N + at};
+                } else {
+                    const float m = st.m == -INFINITY ? 0.f : st.m;
+                    float s = 0.f;
+#pragma unroll
+                    for (int j = 0; j < N; ++j) s += ex2_hw((x[j] - m) * k);
+                    st.s += s;
+                }
             }
         }
     }
     if (t < hi - tail) one(tail + t);
-    if (st.at != kNone)
-        while (st.at < hi - 1 && Fmt<DT>::load1(row, st.at) != st.m) ++st.at;  // ends inside the vector that holds the maximum
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) {
         VfState o;
@@ -180,7 +186,8 @@ __device__ inline VfState vf_row(const VfPart *p, int parts, float k) {
     }
     return st;
 }
-__device__ inline bool vf_defined(const VfState &s) { return s.s > 0.f && s.s < INFINITY && fabsf(s.m) < INFINITY; }
+__device__ inline bool vf_defined(const VfState &s) { return s.s < INFINITY && fabsf(s.m) < INFINITY; }
+__device__ inline float vf_total(const VfState &s) { return 1.f + s.s; }
 
 // Sums over a vocabulary as pairs of fp32 (value hi + lo, |lo| at most half a
 // unit of hi; each addition exact to about 2^-46): fp64 additions run at 1/64 of
@@ -272,7 +279,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) vf_
         const VfState p = vf_row(a.px + (static_cast<int64_t>(b) * (a.K + 1) + i) * a.parts, a.parts, k);
         const int64_t t = i < a.K ? vf_draft(a, b, i) : -1;
         const bool has = vf_valid(a, t);
-        VfState q{0.f, 1.f, 0};
+        VfState q{0.f, 0.f, 0};
         const bool model = a.y && has && !greedy;
         if (model) q = vf_row(a.py + (static_cast<int64_t>(b) * a.K + i) * a.parts, a.parts, k);
         if (lane == 0) {
@@ -283,7 +290,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) vf_
             if (stays && !greedy) {
                 const float pt = ex2_hw((Fmt<DT>::load1(a.x, b * a.xs + i * a.xr + t) - p.m) * k);
                 const float qt = model ? ex2_hw((Fmt<DT>::load1(a.y, b * a.ys + i * a.yr + t) - q.m) * k) : 1.f;
-                stays = __ldg(a.u + static_cast<int64_t>(b) * a.K + i) * qt * p.s < pt * q.s;
+                stays = __ldg(a.u + static_cast<int64_t>(b) * a.K + i) * qt * vf_total(p) < pt * vf_total(q);
             }
             if (!stays && i < a.K) atomicMin(&count, i);
         }
@@ -293,7 +300,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) vf_
     const int64_t tn = n < a.K ? vf_draft(a, b, n) : -1;
     const bool turned = usable && vf_valid(a, tn), model = turned && a.y && !greedy;
     const VfState p = usable ? sx[n] : VfState{0.f, 0.f, 0};
-    const VfState q = model ? sy[n] : VfState{0.f, 1.f, 0};
+    const VfState q = model ? sy[n] : VfState{0.f, 0.f, 0};
     const bool defined = usable && vf_defined(p) && vf_defined(q);
     const int64_t row = static_cast<int64_t>(b) * (a.K + 1);
     const float ln2_k = k * 0.6931471805599453f;  // 1 / T
@@ -306,7 +313,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) vf_
             float lp = 0.f;
             if (i < n) {
                 t = vf_draft(a, b, i);
-                lp = (Fmt<DT>::load1(a.x, b * a.xs + i * a.xr + t) - sx[i].m) * ln2_k - logf(sx[i].s);
+                lp = (Fmt<DT>::load1(a.x, b * a.xs + i * a.xr + t) - sx[i].m) * ln2_k - log1pf(sx[i].s);
             }
             if (a.tok32) reinterpret_cast<int32_t *>(a.tokens)[row + i] = static_cast<int32_t>(t);
             else reinterpret_cast<int64_t *>(a.tokens)[row + i] = t;
@@ -315,7 +322,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) vf_
     }
     const int64_t xrow = b * a.xs + n * a.xr;
     const auto emit = [&](int t) {
-        const float lp = t < 0 ? NAN : (Fmt<DT>::load1(a.x, xrow + t) - p.m) * ln2_k - logf(p.s);
+        const float lp = t < 0 ? NAN : (Fmt<DT>::load1(a.x, xrow + t) - p.m) * ln2_k - log1pf(p.s);
         if (a.tok32) reinterpret_cast<int32_t *>(a.tokens)[row + n] = t;
         else reinterpret_cast<int64_t *>(a.tokens)[row + n] = t;
         a.logp[row + n] = lp;
@@ -327,7 +334,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) vf_
     VfWeights<DT> w;
     w.x = reinterpret_cast<const char *>(a.x) + xrow * Fmt<DT>::kBytes;
     w.y = model ? reinterpret_cast<const char *>(a.y) + (b * a.ys + n * a.yr) * Fmt<DT>::kBytes : nullptr;
-    w.mx = p.m; w.ix = 1.f / p.s; w.my = q.m; w.iy = 1.f / q.s; w.k = k;
+    w.mx = p.m; w.ix = 1.f / vf_total(p); w.my = q.m; w.iy = 1.f / vf_total(q); w.k = k;
     w.drop = turned && !a.y ? static_cast<int>(tn) : -1;
     // contiguous ranges of the row, one a warp of the cluster, in steps of 256 elements
     const int steps = (a.V + 255) / 256, all = kCluster * kWarps;
