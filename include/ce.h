@@ -631,7 +631,8 @@ typedef struct ce_verify_params {
     int32_t reserved;                 /* must be 0 */
 } ce_verify_params; /* 72 bytes */
 
-/* Workspace bytes of ce_verify_drafts: 16 for every row and part of at most 64 KB, plus 256. */
+/* Workspace bytes of ce_verify_drafts: 16 for every row and part of it (2 KB, or down to
+ * 512 bytes while the rows are few), plus 256. */
 ce_status ce_verify_workspace_size(const ce_verify_params *p, size_t *bytes);
 
 /*

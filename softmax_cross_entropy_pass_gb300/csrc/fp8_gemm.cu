@@ -11,8 +11,13 @@
 //
 // fp8_few_kernel: the weight's rows are the tensor core's M side, so that few
 // rows of A cost no more than reading the weights: a CTA multiplies tiles of 128
-// weight rows by NT rows of A and owns a contiguous share of the weight's rows,
-// cut at multiples of 16.
+// weight rows by NT rows of A. Either it owns a contiguous share of the weight's
+// rows, cut at multiples of 16, so that one CTA per SM ends with the others; or,
+// where that share would be less than half a tile, a cluster of up to eight CTAs
+// takes one tile, each a part of K, and adds the parts up through distributed
+// shared memory, in the order of the ranks (a K block's copies, MMAs and epilogue
+// follow one another in 0.3 us whatever the rows: 64 x 4096 x 4096 took 14.9 us
+// in 32 such steps).
 #include <atomic>
 
 #include "ce_device.cuh"
@@ -33,8 +38,8 @@ struct Fp8Args {
     const float *bias;        // [n] or NULL
     void *out;
     int64_t ldo;
-    int shares;               // CTAs along the weight's rows
-    int stages;
+    int shares;               // CTAs (clusters) along the weight's rows
+    int ksplit;               // CTAs of a cluster, each a part of K
 };
 
 template <int DT>
@@ -47,24 +52,30 @@ constexpr int kFewMaxStages = 12;
 constexpr int kFewSmem = 218 * 1024;
 constexpr int kScaleBlocks = 32;              // K blocks whose scales of A are in shared memory at a time
 
-// NT rows of A a tile, COLS of them an epilogue thread
+// NT rows of A a tile, kCols of them an epilogue thread
 template <int NT> struct Few {
-    static constexpr int kCols = NT <= 64 ? 16 : 32;
+    static constexpr int kCols = NT < 32 ? NT : 32;
     static constexpr int kSets = NT / kCols;
     static constexpr int kThreads = 64 + 128 * kSets;
-    static constexpr int kAcc = NT <= 64 ? 8 : 4;  // accumulators in tensor memory
+    static constexpr int kAcc = 8;  // accumulators in tensor memory
     static constexpr uint32_t kTmemCols = kAcc * NT;
     static constexpr int kStageBytes = kFewWBytes + NT * kFp8Block;
     static constexpr int kScaleBytes = kScaleBlocks * NT * 4;
     static constexpr int kStages = (kFewSmem - 1024 - kScaleBytes) / kStageBytes < kFewMaxStages
                                        ? (kFewSmem - 1024 - kScaleBytes) / kStageBytes : kFewMaxStages;
     static constexpr int kSmem = 1024 + kStages * kStageBytes + kScaleBytes;
+    static_assert(kStages * kStageBytes >= NT * kFewM * 4, "a cluster's partial tiles take the stages' place");
 };
 
 template <int C>
 __device__ inline void tmem_ld_cols(uint32_t taddr, uint32_t (&v)[C]) {
     if constexpr (C == 16) tmem_ld_32x32b_x16(taddr, v);
     else tmem_ld_32x32b_x32(taddr, v);
+}
+__device__ inline float ld_cluster_f32(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
 }
 
 template <int NT, int DT>
@@ -78,14 +89,19 @@ fp8_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
     __shared__ int abort_flag, drain_abort;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;  // 128-byte swizzle atoms
+    float *parts = reinterpret_cast<float *>(smem_raw + (base - raw));  // [NT][kFewM], once the stages are done with
     float *scales = reinterpret_cast<float *>(smem_raw + (base - raw) + F::kStages * F::kStageBytes);  // [kScaleBlocks][NT]
     volatile int *abort = &abort_flag;
-    const int share = blockIdx.x % g.shares, m0 = (blockIdx.x / g.shares) * NT;
+    const int split = g.ksplit, rank = static_cast<int>(blockIdx.x) % split, work = static_cast<int>(blockIdx.x) / split;
+    const int share = work % g.shares, m0 = work / g.shares * NT;
     const int64_t units = (g.n + kFewBox - 1) / kFewBox;
-    const int v_lo = static_cast<int>(units * share / g.shares) * kFewBox;
-    const int v_end = static_cast<int>(units * (share + 1) / g.shares) * kFewBox;
+    // split: shares are tiles
+    const int v_lo = split > 1 ? share * kFewM : static_cast<int>(units * share / g.shares) * kFewBox;
+    const int v_end = split > 1 ? v_lo + kFewM : static_cast<int>(units * (share + 1) / g.shares) * kFewBox;
     const int v_hi = v_end < g.n ? v_end : g.n;
     const int ntiles = (v_hi - v_lo + kFewM - 1) / kFewM;
+    const int kb0 = static_cast<int>(static_cast<int64_t>(g.kblocks) * rank / split);
+    const int kb1 = static_cast<int>(static_cast<int64_t>(g.kblocks) * (rank + 1) / split);
 
     if (tid == 0) {
         for (int s = 0; s < F::kStages; ++s) {
@@ -119,7 +135,7 @@ fp8_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
                 const int v0 = v_lo + tile * kFewM;
                 const int boxes = (min(kFewM, v_hi - v0) + kFewBox - 1) / kFewBox;
                 const uint32_t bytes = boxes * kFewBox * kFp8Block + NT * kFp8Block;
-                for (int kb = 0; kb < g.kblocks; ++kb) {
+                for (int kb = kb0; kb < kb1; ++kb) {
                     const uint32_t fb = smem_u32(&full[s]), dst = base + s * F::kStageBytes;
                     if (round > 0) mbar_wait_polled(smem_u32(&empty[s]), (round - 1) & 1u, abort);
                     mbar_expect_tx(fb, bytes);
@@ -149,7 +165,7 @@ fp8_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
             const uint32_t idesc = idesc_e4m3_f32(kFewM, NT);
             uint32_t s = 0, phase = 0, unit = 0;
             for (int tile = 0; tile < ntiles; ++tile)
-                for (int kb = 0; kb < g.kblocks; ++kb, ++unit) {
+                for (int kb = kb0; kb < kb1; ++kb, ++unit) {
                     const uint32_t acc = unit % F::kAcc, u = unit / F::kAcc;
                     if (u > 0) mbar_wait_polled(smem_u32(&tempty[acc]), (u - 1) & 1u, abort);
                     mbar_wait_polled(smem_u32(&full[s]), phase, abort);
@@ -159,8 +175,8 @@ fp8_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
                     for (int kk = 0; kk < kFp8Block / 32; ++kk)
                         mma_e4m3(tmem + acc * NT, smem_desc_sw128(a + kk * 32, 16, 1024),
                                  smem_desc_sw128(b + kk * 32, 16, 1024), idesc, kk > 0 ? 1u : 0u);
-                    mma_commit(smem_u32(&empty[s]));
                     mma_commit(smem_u32(&tfull[acc]));
+                    mma_commit(smem_u32(&empty[s]));
                     if (++s == F::kStages) {
                         s = 0;
                         phase ^= 1u;
@@ -176,52 +192,62 @@ fp8_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
         uint32_t unit = 0;
         for (int tile = 0; tile < ntiles; ++tile) {
             const int row = v_lo + tile * kFewM + q * 32 + lane;
+            const bool live = v_lo + tile * kFewM + q * 32 < v_hi;  // any row of this warp's
             const float *sb = g.b_scale + static_cast<int64_t>(min(row, g.n - 1) / kFp8Block) * g.kblocks;
-            float acc[C];
+            F2 acc[C / 2];
 #pragma unroll
-            for (int j = 0; j < C; ++j) acc[j] = 0.f;
-            float next = __ldg(sb);
-            for (int kb = 0; kb < g.kblocks; ++kb, ++unit) {
-                const int k0 = kb % kScaleBlocks;
-                if (k0 == 0 && (tile == 0 || g.kblocks > kScaleBlocks)) {
-                    // the next blocks' scales of A, columns of the tile side by side
-                    const int nb = min(kScaleBlocks, g.kblocks - kb);
+            for (int j = 0; j < C / 2; ++j) acc[j] = f2(0.f, 0.f);
+            float next = __ldg(sb + kb0);
+            for (int kb = kb0; kb < kb1; ++kb, ++unit) {
+                const int k0 = (kb - kb0) % kScaleBlocks;
+                if (k0 == 0 && (tile == 0 || kb1 - kb0 > kScaleBlocks)) {
+                    // the next blocks' scales of A, rows of the tile side by side
+                    const int nb = min(kScaleBlocks, kb1 - kb);
                     asm volatile("bar.sync 1, %0;" ::"r"(128 * F::kSets) : "memory");
-                    for (int i = et; i < nb * NT; i += 128 * F::kSets) {
-                        const int r = i / nb, b = i % nb;
-                        scales[b * NT + r] = m0 + r < g.m ? __ldg(g.a_scale + static_cast<int64_t>(m0 + r) * g.kblocks + kb + b) : 0.f;
+                    for (int i = et; i < kScaleBlocks * NT; i += 128 * F::kSets) {
+                        const int r = i / kScaleBlocks, b = i % kScaleBlocks;
+                        if (b < nb)
+                            scales[b * NT + r] = m0 + r < g.m ? __ldg(g.a_scale + static_cast<int64_t>(m0 + r) * g.kblocks + kb + b) : 0.f;
                     }
                     asm volatile("bar.sync 1, %0;" ::"r"(128 * F::kSets) : "memory");
                 }
-                const float w = next;
-                if (kb + 1 < g.kblocks) next = __ldg(sb + kb + 1);
+                const F2 w = f2(next, next);
+                if (kb + 1 < kb1) next = __ldg(sb + kb + 1);
                 const uint32_t a = unit % F::kAcc, u = unit / F::kAcc;
                 mbar_wait_polled(smem_u32(&tfull[a]), u & 1u, abort);
-                tc_fence_after();
-                uint32_t v[C];
-                tmem_ld_cols<C>(taddr0 + a * NT, v);
-                tmem_ld_wait(v);
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&tempty[a]));
-                const float4 *sa = reinterpret_cast<const float4 *>(scales + k0 * NT + set * C);
+                if (live) {
+                    tc_fence_after();
+                    uint32_t v[C];
+                    tmem_ld_cols<C>(taddr0 + a * NT, v);
+                    tmem_ld_wait(v);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&tempty[a]));
+                    const float4 *sa = reinterpret_cast<const float4 *>(scales + k0 * NT + set * C);
 #pragma unroll
-                for (int j = 0; j < C / 4; ++j) {
-                    const float4 s4 = sa[j];
-                    acc[4 * j] = fmaf(s4.x * w, __uint_as_float(v[4 * j]), acc[4 * j]);
-                    acc[4 * j + 1] = fmaf(s4.y * w, __uint_as_float(v[4 * j + 1]), acc[4 * j + 1]);
-                    acc[4 * j + 2] = fmaf(s4.z * w, __uint_as_float(v[4 * j + 2]), acc[4 * j + 2]);
-                    acc[4 * j + 3] = fmaf(s4.w * w, __uint_as_float(v[4 * j + 3]), acc[4 * j + 3]);
+                    for (int j = 0; j < C / 4; ++j) {
+                        const float4 s4 = sa[j];
+                        acc[2 * j] = f2_fma(f2_mul(f2(s4.x, s4.y), w), f2(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1])), acc[2 * j]);
+                        acc[2 * j + 1] = f2_fma(f2_mul(f2(s4.z, s4.w), w), f2(__uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3])), acc[2 * j + 1]);
+                    }
+                } else if (lane == 0) {
+                    mbar_arrive(smem_u32(&tempty[a]));
                 }
             }
-            if (row < v_hi) {
-                // a wait that gave up leaves no result: NaN
-                const float bias = *abort ? NAN : (g.bias ? __ldg(g.bias + row) : 0.f);
-                const bool add = g.bias || *abort;
+            float x[C];
+#pragma unroll
+            for (int j = 0; j < C / 2; ++j) f2_split(acc[j], x[2 * j], x[2 * j + 1]);
+            const bool bad = *abort != 0;  // a wait that gave up leaves no result
+            if (split > 1) {
+                // every copy of this CTA has landed and every MMA has read it
+#pragma unroll
+                for (int j = 0; j < C; ++j) parts[(set * C + j) * kFewM + q * 32 + lane] = bad ? NAN : x[j];
+            } else if (row < v_hi) {
+                const float bias = g.bias ? __ldg(g.bias + row) : 0.f;
 #pragma unroll
                 for (int j = 0; j < C; ++j) {
                     const int r = m0 + set * C + j;
-                    if (r < g.m) store_out<DT>(g.out, static_cast<int64_t>(r) * g.ldo + row, add ? acc[j] + bias : acc[j]);
+                    if (r < g.m) store_out<DT>(g.out, static_cast<int64_t>(r) * g.ldo + row, bad ? NAN : (g.bias ? x[j] + bias : x[j]));
                 }
             }
         }
@@ -230,6 +256,21 @@ fp8_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem, F::kTmemCols);
+    }
+    if (split > 1) {
+        // this rank's share of the rows of A: the parts' sums
+        cluster_sync_all();
+        const int c0 = NT * rank / split, c1 = min(NT * (rank + 1) / split, g.m - m0);
+        const uint32_t mine = smem_u32(parts);
+        for (int i = tid; i < (c1 - c0) * kFewM; i += F::kThreads) {
+            const int c = c0 + i / kFewM, r = i % kFewM, row = v_lo + r;
+            if (row >= v_hi) continue;
+            float v = 0.f;
+            for (int k = 0; k < split; ++k) v += ld_cluster_f32(mapa_shared(mine + (c * kFewM + r) * 4, k));
+            if (g.bias) v += __ldg(g.bias + row);
+            store_out<DT>(g.out, static_cast<int64_t>(m0 + c) * g.ldo + row, v);
+        }
+        cluster_sync_all();  // no CTA leaves while another reads its part
     }
 }
 
@@ -247,7 +288,7 @@ fp8_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
 // bytes, `empty` and `tfull` are signalled by multicast commits, `tempty` in the
 // even CTA collects the 16 epilogue warps of the pair (each arrival from the other
 // CTA takes 6 ns: sixteen warps a CTA with half the columns were slower).
-constexpr int kPairM = 256, kPairN = 256, kPairStages = 6, kPairAcc = 2;
+constexpr int kPairM = 256, kPairN = 256, kPairAcc = 2;
 constexpr int kPairHalf = 128 * kFp8Block;  // 16 KB: this CTA's half of an operand's stage
 constexpr int kPairEpi = 256;
 // four warps for the copies and the MMAs (two of them idle), so that warpgroups
@@ -258,7 +299,12 @@ constexpr int kPairLaunchRegs = 168, kPairEpiRegs = 232, kPairFirstRegs = 40;
 static_assert(kPairEpi * kPairEpiRegs + 128 * kPairFirstRegs <= kPairThreads * kPairLaunchRegs, "registers of the launch");
 constexpr int kPairChunk = 32;              // K blocks whose scales of A are in shared memory
 constexpr int kPairRow = 129;               // floats of one K block's scales: another bank for each block
-constexpr int kPairSmem = 1024 + kPairStages * 2 * kPairHalf + 2 * kPairChunk * kPairRow * 4;
+constexpr int kPairStage = 32 * 33;         // floats: 32 x 32 sums of an epilogue warp on their way out
+constexpr int pair_stages(bool staged) { return staged ? 5 : 6; }
+constexpr int pair_smem(bool staged) {
+    return 1024 + pair_stages(staged) * 2 * kPairHalf + 2 * kPairChunk * kPairRow * 4 +
+           (staged ? kPairEpi / 32 * kPairStage * 4 : 0);
+}
 constexpr uint32_t kPairTmemCols = 512;
 
 // 32 bytes to a 32-byte aligned address: a whole sector a lane (rows lie apart)
@@ -267,9 +313,9 @@ __device__ inline void st_sector(void *p, const uint4 &a, const uint4 &b) {
                  "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w) : "memory");
 }
 
-// 16 consecutive columns of one row from column c on
+// 16 consecutive columns of one row from column c on; rows start on whole sectors
 template <int DT>
-__device__ inline void store_cols(const Fp8Args &g, int row, int c, float (&x)[16], bool bad, bool sectors) {
+__device__ inline void store_cols(const Fp8Args &g, int row, int c, float (&x)[16], bool bad) {
     if (g.bias) {
 #pragma unroll
         for (int j = 0; j < 16; ++j)
@@ -280,7 +326,7 @@ __device__ inline void store_cols(const Fp8Args &g, int row, int c, float (&x)[1
         for (int j = 0; j < 16; ++j) x[j] = NAN;
     }
     const int64_t at = static_cast<int64_t>(row) * g.ldo + c;
-    if (sectors && c + 16 <= g.n) {
+    if (c + 16 <= g.n) {
         char *o = reinterpret_cast<char *>(g.out) + at * Fmt<DT>::kBytes;
         st_sector(o, Fmt<DT>::pack(x), Fmt<DT>::pack(x + Fmt<DT>::kVec));
         if (DT == CE_DT_F32) st_sector(o + 32, Fmt<DT>::pack(x + 8), Fmt<DT>::pack(x + 12));
@@ -291,9 +337,35 @@ __device__ inline void store_cols(const Fp8Args &g, int row, int c, float (&x)[1
     }
 }
 
+// 32 rows (a lane's each) of 32 columns from column c on through a warp's shared
+// memory, so that lanes store neighbouring columns: for rows that start anywhere
+// (a lane storing its own row would touch 32 sectors a store).
 template <int DT>
+__device__ inline void store_staged(const Fp8Args &g, int row0, int c, const F2 *acc, float *stage, bool bad) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) f2_split(acc[j], stage[lane * 33 + 2 * j], stage[lane * 33 + 2 * j + 1]);
+    __syncwarp();
+    const int col = c + lane;
+    if (col < g.n) {
+        const float bias = g.bias ? __ldg(g.bias + col) : 0.f;
+        const int64_t at = static_cast<int64_t>(row0) * g.ldo + col;
+        if (row0 + 32 <= g.m && !bad) {
+#pragma unroll
+            for (int r = 0; r < 32; ++r) store_out<DT>(g.out, at + r * g.ldo, g.bias ? stage[r * 33 + lane] + bias : stage[r * 33 + lane]);
+        } else {
+            for (int r = 0; r < min(32, g.m - row0); ++r)
+                store_out<DT>(g.out, at + r * g.ldo, bad ? NAN : (g.bias ? stage[r * 33 + lane] + bias : stage[r * 33 + lane]));
+        }
+    }
+    __syncwarp();
+}
+
+// STAGED: the output's rows do not all start on sectors
+template <int DT, bool STAGED>
 __global__ void __launch_bounds__(kPairThreads, 1)
 fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, Fp8Args g) {
+    constexpr int kPairStages = pair_stages(STAGED);
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t full[kPairStages], empty[kPairStages], tfull[kPairAcc], tempty[kPairAcc];
     __shared__ uint32_t tmem_slot;
@@ -389,9 +461,9 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPairEpiRegs));
         const int q = warp & 3, half = (warp - 4) >> 2;
         const int et = tid - 128;
+        float *stage = scales + 2 * kPairChunk * kPairRow + (warp - 4) * kPairStage;
         const uint32_t tempty0 = mapa_shared(smem_u32(&tempty[0]), 0);
         const uint32_t lane_addr = tmem + (static_cast<uint32_t>(q * 32) << 16) + half * 128;
-        const bool sectors = ((reinterpret_cast<uintptr_t>(g.out) | static_cast<uintptr_t>(g.ldo * Fmt<DT>::kBytes)) & 31u) == 0;
         // scales of A of this CTA's 128 rows of tile t, K blocks k0 .. k0 + 31, into buffer `buf` (rows past the last: its)
         const auto fetch = [&](int64_t t, int k0, int buf) {
             const int row0 = static_cast<int>(t % tiles_m) * kPairM + static_cast<int>(rank) * 128;
@@ -460,15 +532,21 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 add(v[2], 32);
                 add(v[0], 48);
             }
-            if (row < g.m) {
-                const bool bad = *abort != 0;  // a wait that gave up leaves no result
+            const bool bad = *abort != 0;  // a wait that gave up leaves no result
+            if (!STAGED) {
+                if (row < g.m) {
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    float x[16];
+                    for (int c = 0; c < 8; ++c) {
+                        float x[16];
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) f2_split(acc[c * 8 + j], x[2 * j], x[2 * j + 1]);
-                    if (col0 + c * 16 < g.n) store_cols<DT>(g, row, col0 + c * 16, x, bad, sectors);
+                        for (int j = 0; j < 8; ++j) f2_split(acc[c * 8 + j], x[2 * j], x[2 * j + 1]);
+                        if (col0 + c * 16 < g.n) store_cols<DT>(g, row, col0 + c * 16, x, bad);
+                    }
                 }
+            } else {
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    if (col0 + c * 32 < g.n && row - lane < g.m) store_staged<DT>(g, row - lane, col0 + c * 32, acc + c * 16, stage, bad);
             }
         }
     }
@@ -505,35 +583,51 @@ cudaError_t launch_few_t(const CUtensorMap &tw, const CUtensorMap &tws, const CU
     if (e != cudaSuccess) return e;
     void *args[] = {const_cast<CUtensorMap *>(&tw), const_cast<CUtensorMap *>(&tws), const_cast<CUtensorMap *>(&ta),
                     const_cast<Fp8Args *>(&g)};
-    return cudaLaunchKernel(fn, dim3(grid), dim3(Few<NT>::kThreads), args, Few<NT>::kSmem, s);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(Few<NT>::kThreads);
+    cfg.dynamicSmemBytes = Few<NT>::kSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = static_cast<unsigned>(g.ksplit);
+    at.val.clusterDim.y = 1;
+    at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelExC(&cfg, fn, args);
 }
 template <int NT>
 cudaError_t launch_few(const void *A, int64_t lda, const void *B, int64_t ldb, Fp8Args g, int dtype, cudaStream_t s) {
-    const int mt = (g.m + NT - 1) / NT, units = (g.n + kFewBox - 1) / kFewBox;
+    const int mt = (g.m + NT - 1) / NT, units = (g.n + kFewBox - 1) / kFewBox, tiles = (g.n + kFewM - 1) / kFewM;
+    const int64_t all = static_cast<int64_t>(tiles) * mt;
+    g.ksplit = 1;
+    while (g.ksplit < 8 && all * g.ksplit * 2 <= kSms && g.ksplit * 4 <= g.kblocks) g.ksplit *= 2;
     int shares = kSms / mt > 0 ? kSms / mt : 1;
     if (shares > units) shares = units;
-    g.shares = shares;
+    g.shares = g.ksplit > 1 ? tiles : shares;
+    if (static_cast<int64_t>(g.shares) * mt * g.ksplit > INT32_MAX) return cudaErrorInvalidValue;
     CUtensorMap tw, tws, ta;  // weight boxes of a whole tile, and of 16 rows for a share's last one
     cudaError_t e = make_tmap_bytes(&tw, B, g.n, g.K, ldb, kFewM);
     if (e == cudaSuccess) e = make_tmap_bytes(&tws, B, g.n, g.K, ldb, kFewBox);
     if (e == cudaSuccess) e = make_tmap_bytes(&ta, A, g.m, g.K, lda, NT);
     if (e != cudaSuccess) return e;
-    const int grid = shares * mt;
+    const int grid = g.shares * mt * g.ksplit;
     if (dtype == CE_DT_BF16) return launch_few_t<NT, CE_DT_BF16>(tw, tws, ta, g, grid, s);
     if (dtype == CE_DT_F16) return launch_few_t<NT, CE_DT_F16>(tw, tws, ta, g, grid, s);
     return launch_few_t<NT, CE_DT_F32>(tw, tws, ta, g, grid, s);
 }
 
 // Resident CTA pairs of the pair kernel on a device (0 if unknown), asked once.
-int pair_clusters(const void *fn, int dev) {
+int pair_clusters(const void *fn, bool staged, int dev) {
     constexpr int kDevs = 64;
-    static std::atomic<int> known[kDevs];
+    static std::atomic<int> known[kDevs];  // both variants fill an SM's shared memory
     int n = 0;
     if (dev < kDevs && (n = known[dev].load()) > 0) return n;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * 128);
     cfg.blockDim = dim3(kPairThreads);
-    cfg.dynamicSmemBytes = kPairSmem;
+    cfg.dynamicSmemBytes = pair_smem(staged);
     cudaLaunchAttribute at;
     at.id = cudaLaunchAttributeClusterDimension;
     at.val.clusterDim.x = 2;
@@ -547,10 +641,10 @@ int pair_clusters(const void *fn, int dev) {
     return n;
 }
 
-template <int DT>
+template <int DT, bool STAGED>
 cudaError_t launch_pair(const void *A, int64_t lda, const void *B, int64_t ldb, Fp8Args g, cudaStream_t s) {
     static std::atomic<uint64_t> done{0};
-    const void *fn = reinterpret_cast<const void *>(&fp8_pair_kernel<DT>);
+    const void *fn = reinterpret_cast<const void *>(&fp8_pair_kernel<DT, STAGED>);
     CUtensorMap ta, tb;
     cudaError_t e = make_tmap_bytes(&ta, A, g.m, g.K, lda, 128);
     if (e == cudaSuccess) e = make_tmap_bytes(&tb, B, g.n, g.K, ldb, 128);
@@ -560,11 +654,11 @@ cudaError_t launch_pair(const void *A, int64_t lda, const void *B, int64_t ldb, 
         e = cudaFuncGetAttributes(&at, fn);
         if (e == cudaSuccess && at.numRegs != kPairLaunchRegs) e = cudaErrorInvalidConfiguration;
     }
-    if (e == cudaSuccess) e = allow_smem(fn, kPairSmem, done);
+    if (e == cudaSuccess) e = allow_smem(fn, pair_smem(STAGED), done);
     int dev = 0;
     if (e == cudaSuccess) e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    int clusters = pair_clusters(fn, dev);
+    int clusters = pair_clusters(fn, STAGED, dev);
     if (clusters < 1) clusters = kSms / 2;
     const int64_t tiles = static_cast<int64_t>((g.m + kPairM - 1) / kPairM) * ((g.n + kPairN - 1) / kPairN);
     if (clusters > tiles) clusters = static_cast<int>(tiles);
@@ -572,7 +666,7 @@ cudaError_t launch_pair(const void *A, int64_t lda, const void *B, int64_t ldb, 
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(2 * clusters));
     cfg.blockDim = dim3(kPairThreads);
-    cfg.dynamicSmemBytes = kPairSmem;
+    cfg.dynamicSmemBytes = pair_smem(STAGED);
     cfg.stream = s;
     cudaLaunchAttribute at;
     at.id = cudaLaunchAttributeClusterDimension;
@@ -588,15 +682,18 @@ enum { FP8_AUTO = 0, FP8_FEW = 1, FP8_PAIR = 2 };
 
 cudaError_t fp8_gemm(const void *A, int64_t lda, const void *B, int64_t ldb, const Fp8Args &g, int dtype, int mode,
                      cudaStream_t s) {
-    if (mode == FP8_PAIR || (mode == FP8_AUTO && g.m > 256)) {
-        if (dtype == CE_DT_BF16) return launch_pair<CE_DT_BF16>(A, lda, B, ldb, g, s);
-        if (dtype == CE_DT_F16) return launch_pair<CE_DT_F16>(A, lda, B, ldb, g, s);
-        return launch_pair<CE_DT_F32>(A, lda, B, ldb, g, s);
+    if (mode == FP8_PAIR || (mode == FP8_AUTO && g.m > 64)) {
+        const int esz = fp8_elem(dtype);
+        const bool staged = ((reinterpret_cast<uintptr_t>(g.out) | static_cast<uintptr_t>(g.m > 1 ? g.ldo * esz : 0)) & 31u) != 0;
+        using Fn = cudaError_t (*)(const void *, int64_t, const void *, int64_t, Fp8Args, cudaStream_t);
+        static const Fn fns[3][2] = {{launch_pair<CE_DT_F32, false>, launch_pair<CE_DT_F32, true>},
+                                     {launch_pair<CE_DT_BF16, false>, launch_pair<CE_DT_BF16, true>},
+                                     {launch_pair<CE_DT_F16, false>, launch_pair<CE_DT_F16, true>}};
+        return fns[dtype][staged ? 1 : 0](A, lda, B, ldb, g, s);
     }
     if (g.m <= 16) return launch_few<16>(A, lda, B, ldb, g, dtype, s);
     if (g.m <= 32) return launch_few<32>(A, lda, B, ldb, g, dtype, s);
-    if (g.m <= 64) return launch_few<64>(A, lda, B, ldb, g, dtype, s);
-    return launch_few<128>(A, lda, B, ldb, g, dtype, s);
+    return launch_few<64>(A, lda, B, ldb, g, dtype, s);
 }
 
 }  // namespace

@@ -128,15 +128,23 @@ struct NormArgs {
     float eps;
 };
 
-constexpr int kNormWarpThreads = 256;  // a warp a row; 512 and 1024: a CTA a row
+// How a row is split: a warp of 8 in a CTA, or a CTA of up to 256, 512 or 1024
+// threads; the registers are held to what lets 1024 threads of an SM run (512
+// with four vectors a thread, or two of fp32).
+enum { NORM_WARP = 0, NORM_256 = 1, NORM_512 = 2, NORM_1024 = 3 };
+__host__ __device__ constexpr int norm_threads(int mode) { return mode < NORM_512 ? 256 : (mode == NORM_512 ? 512 : 1024); }
+__host__ __device__ constexpr int norm_resident(int dtype, int vpt) { return vpt * (dtype == CE_DT_F32 ? 2 : 1) >= 4 ? 512 : 1024; }
+__host__ __device__ constexpr int norm_ctas(int dtype, int mode, int vpt) {
+    return mode == NORM_1024 ? 1 : norm_resident(dtype, vpt) / norm_threads(mode);
+}
 
-// A row by one warp (MAXT = kNormWarpThreads) or by a CTA's W; thread t of a row's holds the vectors of 8 columns t, t + 32 W, ... (16 neighbouring
+// A row by one warp or by a CTA's W; thread t of a row's holds the vectors of 8 columns t, t + 32 W, ... (16 neighbouring
 // lanes hold a block). Rows are dealt out round robin, and the next row's loads
 // are under way while the reductions of this one wait for one another (not above
 // 16384 columns, whose registers are all taken): a row at a time left HBM at 65%.
-template <int DT, bool VEC, int VPT, int MAXT>
-__global__ void __launch_bounds__(MAXT, 1) norm_fp8_kernel(NormArgs a) {
-    constexpr bool WARP = MAXT == kNormWarpThreads, AHEAD = MAXT <= 512;
+template <int DT, bool VEC, int VPT, int MODE>
+__global__ void __launch_bounds__(norm_threads(MODE), norm_ctas(DT, MODE, VPT)) norm_fp8_kernel(NormArgs a) {
+    constexpr bool WARP = MODE == NORM_WARP, AHEAD = MODE != NORM_1024;
     __shared__ float part[2][32];
     const int lane = threadIdx.x & 31, nwarps = WARP ? 1 : blockDim.x >> 5, warp = WARP ? 0 : threadIdx.x >> 5;
     const int tid = WARP ? lane : threadIdx.x, step = 8 * 32 * nwarps;
@@ -252,48 +260,61 @@ __global__ void __launch_bounds__(kRowQuantThreads) quant_rows_kernel(QuantArgs 
     }
 }
 
-// 128 x 128: a CTA per block, half a warp per row, 8 rows a half warp. The block
-// stays in registers as it was read (32 of them in 16 bits), so that three CTAs an
-// SM have their loads in flight.
-constexpr int kTileThreads = 256, kTileRows = kFp8Block / (kTileThreads / 16);
+// 128 x 128: a CTA per block at a time, half a warp per row, 4 rows a half warp.
+// The block stays in registers as it was read, and the next one's loads are under
+// way while this one's maximum is found and its bytes written: a CTA per block
+// without that left HBM at 72%.
+constexpr int kTileThreads = 512, kTileRows = kFp8Block / (kTileThreads / 16);
 template <int DT, bool VEC>
-__global__ void __launch_bounds__(kTileThreads, DT == CE_DT_F32 ? 2 : 3) quant_tiles_kernel(QuantArgs a) {
-    __shared__ float part[kTileThreads / 32];
-    const int64_t up = blockIdx.x / a.blocks;
-    const int across = blockIdx.x % a.blocks;
-    const int c = across * kFp8Block + (threadIdx.x & 15) * 8;
-    const int64_t r0 = up * kFp8Block + (threadIdx.x >> 4);
-    Raw8<DT> raw[kTileRows];
-    float amax = 0.f;
+__global__ void __launch_bounds__(kTileThreads, DT == CE_DT_F32 ? 1 : 2) quant_tiles_kernel(QuantArgs a) {
+    __shared__ float part[2][kTileThreads / 32];
+    const int64_t tiles = (a.rows + kFp8Block - 1) / kFp8Block * a.blocks;
+    Raw8<DT> next[kTileRows];
+    const auto fetch = [&](int64_t tile) {
+        const int64_t r0 = tile / a.blocks * kFp8Block + (threadIdx.x >> 4);
+        const int c = static_cast<int>(tile % a.blocks) * kFp8Block + (threadIdx.x & 15) * 8;
 #pragma unroll
-    for (int v = 0; v < kTileRows; ++v) {
-        const int64_t r = r0 + v * (kTileThreads / 16);
-        const char *x = reinterpret_cast<const char *>(a.x) + r * a.ld * Fmt<DT>::kBytes;
-        raw[v] = load8<DT, VEC>(x, c, r < a.rows ? a.cols : 0);
-    }
+        for (int v = 0; v < kTileRows; ++v) {
+            const int64_t r = r0 + v * (kTileThreads / 16);
+            const char *x = reinterpret_cast<const char *>(a.x) + r * a.ld * Fmt<DT>::kBytes;
+            next[v] = load8<DT, VEC>(x, c, r < a.rows ? a.cols : 0);
+        }
+    };
+    int64_t tile = blockIdx.x;
+    int turn = 0;
+    if (tile < tiles) fetch(tile);
+    for (; tile < tiles; tile += gridDim.x, turn ^= 1) {
+        Raw8<DT> raw[kTileRows];
+        float amax = 0.f;
 #pragma unroll
-    for (int v = 0; v < kTileRows; ++v) {
-        float y[8];
-        raw[v].unpack(y);
+        for (int v = 0; v < kTileRows; ++v) {
+            raw[v] = next[v];
+            float y[8];
+            raw[v].unpack(y);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) amax = max_nan(amax, fabsf(y[j]));
-    }
+            for (int j = 0; j < 8; ++j) amax = max_nan(amax, fabsf(y[j]));
+        }
+        if (tile + gridDim.x < tiles) fetch(tile + gridDim.x);
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, off));
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = amax;
-    __syncthreads();
-    amax = part[0];
+        for (int off = 16; off > 0; off >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+        // two buffers in turn: nobody writes one that a warp may still read
+        if ((threadIdx.x & 31) == 0) part[turn][threadIdx.x >> 5] = amax;
+        __syncthreads();
+        amax = part[turn][threadIdx.x & (kTileThreads / 32 - 1)];
 #pragma unroll
-    for (int i = 1; i < kTileThreads / 32; ++i) amax = max_nan(amax, part[i]);
-    float inv;
-    const float scale = block_scale(amax, inv);
-    if (threadIdx.x == 0) a.scale[blockIdx.x] = scale;
+        for (int off = kTileThreads / 64; off > 0; off >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+        float inv;
+        const float scale = block_scale(amax, inv);
+        if (threadIdx.x == 0) a.scale[tile] = scale;
+        const int64_t r0 = tile / a.blocks * kFp8Block + (threadIdx.x >> 4);
+        const int c = static_cast<int>(tile % a.blocks) * kFp8Block + (threadIdx.x & 15) * 8;
 #pragma unroll
-    for (int v = 0; v < kTileRows; ++v) {
-        const int64_t r = r0 + v * (kTileThreads / 16);
-        float y[8];
-        raw[v].unpack(y);
-        if (r < a.rows && c < a.cols) store_q8(a.q + r * a.ld_q, c, a.cols, y, inv);
+        for (int v = 0; v < kTileRows; ++v) {
+            const int64_t r = r0 + v * (kTileThreads / 16);
+            float y[8];
+            raw[v].unpack(y);
+            if (r < a.rows && c < a.cols) store_q8(a.q + r * a.ld_q, c, a.cols, y, inv);
+        }
     }
 }
 
@@ -302,30 +323,34 @@ __global__ void __launch_bounds__(kTileThreads, DT == CE_DT_F32 ? 2 : 3) quant_t
 cudaError_t launch_norm(const NormArgs &a, int dtype, bool vec, cudaStream_t s) {
     const int vecs = (a.cols + 7) / 8;
     using Fn = void (*)(NormArgs);
-#define CE_NORM(DT, V) {norm_fp8_kernel<DT, V, 1, 256>, norm_fp8_kernel<DT, V, 2, 256>, norm_fp8_kernel<DT, V, 4, 256>, \
-                        norm_fp8_kernel<DT, V, 1, 512>, norm_fp8_kernel<DT, V, 2, 512>, norm_fp8_kernel<DT, V, 4, 512>, \
-                        norm_fp8_kernel<DT, V, 4, 1024>}
-    static const Fn fns[3][2][7] = {{CE_NORM(CE_DT_F32, false), CE_NORM(CE_DT_F32, true)},
+#define CE_NORM(DT, V) {norm_fp8_kernel<DT, V, 1, NORM_WARP>, norm_fp8_kernel<DT, V, 2, NORM_WARP>, \
+                        norm_fp8_kernel<DT, V, 4, NORM_WARP>, norm_fp8_kernel<DT, V, 1, NORM_256>, \
+                        norm_fp8_kernel<DT, V, 2, NORM_256>, norm_fp8_kernel<DT, V, 1, NORM_512>, \
+                        norm_fp8_kernel<DT, V, 2, NORM_512>, norm_fp8_kernel<DT, V, 4, NORM_512>, \
+                        norm_fp8_kernel<DT, V, 4, NORM_1024>}
+    static const Fn fns[3][2][9] = {{CE_NORM(CE_DT_F32, false), CE_NORM(CE_DT_F32, true)},
                                     {CE_NORM(CE_DT_BF16, false), CE_NORM(CE_DT_BF16, true)},
                                     {CE_NORM(CE_DT_F16, false), CE_NORM(CE_DT_F16, true)}};
 #undef CE_NORM
     constexpr int kSms = 152;
     NormArgs b = a;
     void *args[] = {&b};
-    int which, threads;
+    int which, threads, per_sm;
     int64_t grid;
     if (vecs <= 128) {
-        which = vecs <= 32 ? 0 : (vecs <= 64 ? 1 : 2);
+        const int vpt = vecs <= 32 ? 1 : (vecs <= 64 ? 2 : 4);
+        which = vpt >> 1;
         threads = a.n_rows >= 8 * kSms ? 256 : 32;
         grid = (a.n_rows + threads / 32 - 1) / (threads / 32);
+        per_sm = norm_resident(dtype, vpt) / threads;
     } else {
         const int vpt = vecs > 1024 ? 4 : (vecs > 512 || (vecs > 256 && a.n_rows > 2 * kSms) ? 2 : 1);
-        which = vecs > 2048 ? 6 : 3 + (vpt >> 1);
         threads = ((vecs + vpt - 1) / vpt + 31) / 32 * 32;
+        which = threads > 512 ? 8 : (threads > 256 || vpt == 4 ? 5 : 3) + (vpt >> 1);
         grid = a.n_rows;
+        per_sm = threads > 512 ? 1 : norm_resident(dtype, vpt) / threads;
     }
-    const int64_t most = static_cast<int64_t>(kSms) * (1024 / threads > 0 ? 1024 / threads : 1);
-    if (grid > most) grid = most;
+    if (grid > static_cast<int64_t>(kSms) * per_sm) grid = static_cast<int64_t>(kSms) * per_sm;
     return cudaLaunchKernel(reinterpret_cast<const void *>(fns[dtype][vec ? 1 : 0][which]),
                             dim3(static_cast<unsigned>(grid)), dim3(threads), args, 0, s);
 }
@@ -426,9 +451,11 @@ ce_status ce_quantize_fp8(int64_t rows, int64_t cols, const void *x, int64_t ld_
          {quant_tiles_kernel<CE_DT_F16, false>, quant_tiles_kernel<CE_DT_F16, true>}}};
     void *args[] = {&a};
     const int tall = block_rows == 1 ? 0 : 1;
+    int64_t grid = up * a.parts;
+    if (tall && grid > 152 * 2) grid = 152 * 2;
     const cudaError_t e = cudaLaunchKernel(
         reinterpret_cast<const void *>(fns[tall][dtype][vec_rows(x, ld_x, esz, rows) ? 1 : 0]),
-        dim3(static_cast<unsigned>(up * a.parts)), dim3(tall ? kTileThreads : kRowQuantThreads), args, 0,
+        dim3(static_cast<unsigned>(grid)), dim3(tall ? kTileThreads : kRowQuantThreads), args, 0,
         reinterpret_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? CE_OK : cuda_fail(e);
 }

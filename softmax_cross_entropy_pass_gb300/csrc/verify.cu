@@ -7,14 +7,27 @@
 //            w = max(p_n - q_n, 0) where position n has a draft, p_n otherwise (and where that sum is 0)
 //   T = 0: draft i stays where it is the lowest index of the row's maximum, which is also token n
 //
-// Two kernels. The first forms, for parts of every row, M = max x, its lowest index,
-// and the sum of the other terms 2^((x - M) k), k = log2(e) / T. The second (a
-// cluster of CTAs per sequence) merges them in a fixed order, decides, and reads
-// row n once more to draw the token: every warp sums w over a contiguous range,
-// the ranges' sums (fp64) meet in the cluster, and the CTA whose range holds
-// r sum w walks it. Exponents are formed by the difference x - M first, so that
-// equal logits have equal probabilities whatever part they lie in.
-// Bound by HBM: rows of both models once, and one row of each again from L2.
+// A row's statistics are M = max x, its lowest index, and the sum of the other terms
+// 2^((x - M) k), k = log2(e) / T. Exponents are formed by the difference x - M first,
+// so that equal logits have equal probabilities wherever in the row they lie.
+//
+// Many sequences: one kernel, a cluster of CTAs per sequence. Position by position
+// the cluster reads the row of both models (a contiguous slice a CTA), its warps
+// exchange statistics through distributed shared memory, every warp merges them
+// in the same order and decides; of the rows behind the first draft that is turned
+// down only the first copies of the next one are made, ahead of the decision. Few sequences would leave SMs idle that way: there a first kernel
+// forms the statistics of parts of all rows at once, and a second (a cluster a
+// sequence) merges them and decides. Either draws the token by reading row n once
+// more, mostly from L2: every warp sums w over a contiguous range, the ranges' sums
+// meet in the cluster, and the CTA whose range holds r sum w walks it.
+//
+// Bound by HBM (many sequences), by the chain of dependent steps (few).
+// Tried for many sequences and slower (128 sequences of 4 drafts, 128256 columns
+// of bf16): parts of all rows dealt out position by position, the CTA or warp that
+// completes a row by a counter deciding whether the next ones are read: 108 and
+// 224 us; its fences and atomics took longer than the reading.
+#include <atomic>
+
 #include "ce_device.cuh"
 #include "ce_kernels.h"
 #include "fp8.h"
@@ -24,11 +37,11 @@ namespace ce {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kCluster = 8;
+constexpr int kCluster = 8;  // CTAs of a cluster at most
 constexpr int kMaxDrafts = 255;
 constexpr int kNone = 0x7fffffff;
 
-struct VfPart {
+struct alignas(16) VfPart {
     float m, s;
     int at;      // lowest index of the maximum
     float pad;
@@ -43,7 +56,7 @@ struct VfArgs {
     const float *u, *r;              // [B][K], [B]
     const float *temps;              // [B] or NULL
     float temp;
-    int parts, part_len;
+    int parts, per;                  // parts of a row, elements of a part
     VfPart *px, *py;                 // [B][K + 1][parts], [B][K][parts]
     int *accepted;
     void *tokens;                    // [B][K + 1]
@@ -77,95 +90,103 @@ __device__ inline VfState vf_merge(const VfState &a, const VfState &b, float k) 
     return VfState{hi.m, hi.s + vf_shift(lo.m, lo.s, hi.m, k), hi.at};
 }
 
-// Statistics of elements [lo, hi) of one row by the whole CTA; the result in thread 0.
-template <int DT>
-__device__ inline VfState vf_row_part(const void *row, int lo, int hi, float k, VfState *red) {
-    constexpr int N = Fmt<DT>::kVec;
-    const char *p = reinterpret_cast<const char *>(row) + static_cast<int64_t>(lo) * Fmt<DT>::kBytes;
-    int head = static_cast<int>((16u - (reinterpret_cast<uintptr_t>(p) & 15u)) & 15u) / Fmt<DT>::kBytes;
-    if (head > hi - lo) head = hi - lo;
-    const int vecs = (hi - lo - head) / N, tail = lo + head + vecs * N;
-    const uint4 *v4 = reinterpret_cast<const uint4 *>(p + head * Fmt<DT>::kBytes);
-    VfState st{-INFINITY, 0.f, kNone};
-    const auto one = [&](int i) {
-        const float x = Fmt<DT>::load1(row, i);
-        if (x > st.m) st = VfState{x, x == INFINITY ? NAN : vf_shift(st.m, st.s, x, k), i};
-        else st.s += st.m == -INFINITY ? (x != x ? x : 0.f) : ex2_hw((x - st.m) * k);
-    };
-    const int t = threadIdx.x;
-    if (t < head) one(lo + t);
-    constexpr int U = 4;
-    for (int i = t; i < vecs; i += U * kThreads) {
-        uint4 raw[U];
+// U vectors of 16 bytes a thread of a row: vector v0 and every `stride`-th after it,
+// counted from the 16-byte boundary at or before the row's first element.
+template <int DT, int U> struct VfTile {
+    static constexpr int N = Fmt<DT>::kVec;
+    uint4 raw[U];
+    int first, step;  // index of the first vector's first element (negative before the row), elements between vectors
+
+    // (the first `limit` of the U vectors)
+    __device__ inline void load(const void *row, int V, int v0, int stride, int limit = U) {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(row);
+        const int before = static_cast<int>(at & 15u) / Fmt<DT>::kBytes;
+        const uint4 *base = reinterpret_cast<const uint4 *>(at & ~static_cast<uintptr_t>(15));
+        first = v0 * N - before;
+        step = stride * N;
 #pragma unroll
-        for (int q = 0; q < U; ++q)
-            if (i + q * kThreads < vecs) raw[q] = ld_stream_ro(v4 + i + q * kThreads);
-#pragma unroll
-        for (int q = 0; q < U; ++q) {
-            if (i + q * kThreads < vecs) {
+        for (int u = 0; u < U; ++u) {
+            const int c = first + u * step;
+            if (u < limit && c >= 0 && c + N <= V) {
+                raw[u] = ld_stream_ro(base + v0 + u * stride);
+            } else {
                 float x[N];
-                Fmt<DT>::unpack(raw[q], x);
-                const float vmax = Fmt<DT>::vmax(raw[q]);
-                if (vmax > st.m) {
-                    // the vector's first maximum leaves the sum, what was there joins it
-                    float sum = vmax == INFINITY ? NAN : vf_shift(st.m, st.s, vmax, k);
-                    int at = -1;
 #pragma unroll
-                    for (int j = 0; j < N; ++j) {
-                        if (at < 0 && x[j] == vmax) at = j;
-                        else sum += ex2_hw((x[j] - vmax) * k);
-                    }
-                    st = VfState{vmax, sum, lo + head + (i + q * kThreads) * N + at};
-                } else {
-                    const float m = st.m == -INFINITY ? 0.f : st.m;
-                    float s = 0.f;
-#pragma unroll
-                    for (int j = 0; j < N; ++j) s += ex2_hw((x[j] - m) * k);
-                    st.s += s;
-                }
+                for (int j = 0; j < N; ++j) x[j] = u < limit && c + j >= 0 && c + j < V ? Fmt<DT>::load1(row, c + j) : -INFINITY;
+                raw[u] = Fmt<DT>::pack(x);
             }
         }
     }
-    if (t < hi - tail) one(tail + t);
+    // this lane's statistics
+    __device__ inline VfState stats(float k) {
+        float top[U], m = -INFINITY;
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-        VfState o;
-        o.m = __shfl_xor_sync(0xffffffffu, st.m, off);
-        o.s = __shfl_xor_sync(0xffffffffu, st.s, off);
-        o.at = __shfl_xor_sync(0xffffffffu, st.at, off);
-        st = vf_merge(st, o, k);
+        for (int u = 0; u < U; ++u) {
+            top[u] = Fmt<DT>::vmax(raw[u]);
+            m = fmaxf(m, top[u]);
+        }
+        VfState st{m, 0.f, kNone};
+        if (m == -INFINITY || m == INFINITY) {  // nothing but -inf and NaN, or +inf
+            float nan = 0.f;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                float x[N];
+                Fmt<DT>::unpack(raw[u], x);
+#pragma unroll
+                for (int j = 0; j < N; ++j)
+                    if (x[j] != x[j]) nan = x[j];
+            }
+            st.s = m == INFINITY ? NAN : nan;
+            return st;
+        }
+        // the lowest element that holds the maximum leaves the sum
+        uint4 hit = raw[U - 1];
+        int at = U - 1;
+#pragma unroll
+        for (int u = U - 2; u >= 0; --u)
+            if (top[u] == m) {
+                hit = raw[u];
+                at = u;
+            }
+        float h[N];
+        Fmt<DT>::unpack(hit, h);
+        int j0 = 0;
+#pragma unroll
+        for (int j = N - 1; j >= 0; --j) j0 = h[j] == m ? j : j0;
+        st.at = first + at * step + j0;
+        const F2 mm = f2(m, m), kk = f2(k, k);
+        F2 sum = f2(0.f, 0.f);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            float x[N];
+            Fmt<DT>::unpack(raw[u], x);
+            const int skip = at == u ? j0 : -1;
+#pragma unroll
+            for (int j = 0; j < N; j += 2) {
+                const F2 v = f2(skip == j ? -INFINITY : x[j], skip == j + 1 ? -INFINITY : x[j + 1]);
+                sum = f2_add(sum, f2_ex2(f2_mul(f2_sub(v, mm), kk)));
+            }
+        }
+        float lo, hi;
+        f2_split(sum, lo, hi);
+        st.s = lo + hi;
+        return st;
     }
-    if ((t & 31) == 0) red[t >> 5] = st;
-    __syncthreads();
-    if (t == 0)
-        for (int w = 1; w < kWarps; ++w) st = vf_merge(st, red[w], k);
-    __syncthreads();
-    return st;
-}
+};
 
-template <int DT>
-__global__ void __launch_bounds__(kThreads) vf_stats_kernel(VfArgs a) {
-    __shared__ VfState red[kWarps];
-    pdl_launch_dependents();
-    // position by position, so that a batch's first rows come first
-    const int part = blockIdx.x % a.parts, rest = blockIdx.x / a.parts, b = rest % a.B, i = rest / a.B;
-    const float temp = vf_temp(a, b), k = vf_k(temp);
-    if (!vf_temp_ok(temp)) return;
-    // a missing draft ends the sequence: rows behind it are not read
-    bool ended = false;
-    for (int j = threadIdx.x; j < i; j += kThreads) ended |= !vf_valid(a, vf_draft(a, b, j));
-    if (__syncthreads_or(ended)) return;
-    const int lo = part * a.part_len, hi = min(a.V, lo + a.part_len);
-    const char *x = reinterpret_cast<const char *>(a.x) + (b * a.xs + i * a.xr) * Fmt<DT>::kBytes;
-    const VfState sx = vf_row_part<DT>(x, lo, hi, k, red);
-    if (threadIdx.x == 0)
-        a.px[(static_cast<int64_t>(b) * (a.K + 1) + i) * a.parts + part] = VfPart{sx.m, sx.s, sx.at, 0.f};
-    if (a.y && i < a.K && temp != 0.f && vf_valid(a, vf_draft(a, b, i))) {
-        const char *y = reinterpret_cast<const char *>(a.y) + (b * a.ys + i * a.yr) * Fmt<DT>::kBytes;
-        const VfState sy = vf_row_part<DT>(y, lo, hi, k, red);
-        if (threadIdx.x == 0)
-            a.py[(static_cast<int64_t>(b) * a.K + i) * a.parts + part] = VfPart{sy.m, sy.s, sy.at, 0.f};
-    }
+// over the warp, the same in every lane: the maximum first, then one move of each lane's sum to it
+__device__ inline VfState vf_reduce(const VfState &st, float k) {
+    float M = st.m;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+    // the lowest index of the maximum: its lane's own term stays out of the sum
+    int at = st.m == M ? st.at : kNone;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) at = min(at, __shfl_xor_sync(0xffffffffu, at, off));
+    float s = st.m == M && st.at == at ? st.s : vf_shift(st.m, st.s, M, k);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+    return VfState{M, s, at};
 }
 
 // a row's statistics from its parts, by one warp, the same in every lane
@@ -176,18 +197,70 @@ __device__ inline VfState vf_row(const VfPart *p, int parts, float k) {
         const float4 v = __ldcg(reinterpret_cast<const float4 *>(p + j));
         st = vf_merge(st, VfState{v.x, v.y, __float_as_int(v.z)}, k);
     }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-        VfState o;
-        o.m = __shfl_xor_sync(0xffffffffu, st.m, off);
-        o.s = __shfl_xor_sync(0xffffffffu, st.s, off);
-        o.at = __shfl_xor_sync(0xffffffffu, st.at, off);
-        st = vf_merge(st, o, k);
-    }
-    return st;
+    return vf_reduce(st, k);
 }
-__device__ inline bool vf_defined(const VfState &s) { return s.s < INFINITY && fabsf(s.m) < INFINITY; }
-__device__ inline float vf_total(const VfState &s) { return 1.f + s.s; }
+// Exponents are x k - r with r = R k rounded once: what that rounding shifts is the
+// same for every term of the row, so it leaves the probabilities alone.
+__device__ inline void cp_async16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ inline float vf_exp(float x, float k, float r) { return ex2_hw(fmaf(x, k, -r)); }
+// 2^(x k - r) of N values
+template <int N>
+__device__ inline void vf_exps(const float *x, float k, float r, float *e) {
+    const F2 kk = f2(k, k), rr = f2(-r, -r);
+#pragma unroll
+    for (int j = 0; j < N; j += 2) f2_split(f2_ex2(f2_fma(f2(x[j], x[j + 1]), kk, rr)), e[j], e[j + 1]);
+}
+
+// A row's distribution: p_c = 2^(x_c k - R k) / S, R k rounded once. M the maximum; at its lowest index
+// and s1 = sum of the terms 2^((x - M) k) without that one, where they are known.
+struct VfRow {
+    float R, S, M, s1;
+    int at;
+};
+// (the terms of a VfState are relative to exactly M: S takes the shift that R k's rounding makes)
+__device__ inline VfRow vf_of(const VfState &s, float k) {
+    return VfRow{s.m, (1.f + s.s) * vf_exp(s.m, k, s.m * k), s.m, s.s, s.at};
+}
+__device__ inline VfRow vf_none() { return VfRow{0.f, 1.f, 0.f, 0.f, 0}; }
+__device__ inline bool vf_defined(const VfRow &r) {
+    return r.S > 0.f && r.S < INFINITY && fabsf(r.M) < INFINITY && fabsf(r.R) < INFINITY;
+}
+
+// Whether a draft stays: its logits xt, yt in the rows p, q (model: there is a draft model's).
+__device__ inline bool vf_stays(int64_t t, float u, float xt, float yt, const VfRow &p, const VfRow &q, bool model,
+                                bool greedy, float k) {
+    if (!vf_defined(p) || !vf_defined(q)) return false;
+    if (greedy) return p.at == static_cast<int>(t);
+    const float pt = vf_exp(xt, k, p.R * k), qt = model ? vf_exp(yt, k, q.R * k) : 1.f;
+    return u * qt * p.S < pt * q.S;
+}
+
+// Few sequences: one warp a part of a row, parts dealt out round robin.
+template <int DT, int U>
+__global__ void __launch_bounds__(kThreads, 3) vf_stats_kernel(VfArgs a) {
+    pdl_launch_dependents();
+    const int lane = threadIdx.x & 31, warps = gridDim.x * kWarps, items = a.B * (a.K + 1) * a.parts;
+    for (int item = blockIdx.x * kWarps + (threadIdx.x >> 5); item < items;) {
+        const int part = item % a.parts, rest = item / a.parts, b = rest % a.B, i = rest / a.B;
+        item = item < items - warps ? item + warps : items;
+        const float temp = vf_temp(a, b), k = vf_k(temp);
+        // a missing draft ends the sequence: rows behind it are not read
+        bool ended = !vf_temp_ok(temp);
+        for (int j = lane; j < i; j += 32) ended |= !vf_valid(a, vf_draft(a, b, j));
+        if (__any_sync(0xffffffffu, ended)) continue;
+        const bool model = a.y && temp != 0.f && i < a.K && vf_valid(a, vf_draft(a, b, i));
+        VfTile<DT, U> tx, ty;
+        tx.load(reinterpret_cast<const char *>(a.x) + (b * a.xs + i * a.xr) * Fmt<DT>::kBytes, a.V, part * U * 32 + lane, 32);
+        if (model) ty.load(reinterpret_cast<const char *>(a.y) + (b * a.ys + i * a.yr) * Fmt<DT>::kBytes, a.V, part * U * 32 + lane, 32);
+        const VfState sx = vf_reduce(tx.stats(k), k);
+        if (lane == 0) a.px[(static_cast<int64_t>(b) * (a.K + 1) + i) * a.parts + part] = VfPart{sx.m, sx.s, sx.at, 0.f};
+        if (!model) continue;
+        const VfState sy = vf_reduce(ty.stats(k), k);
+        if (lane == 0) a.py[(static_cast<int64_t>(b) * a.K + i) * a.parts + part] = VfPart{sy.m, sy.s, sy.at, 0.f};
+    }
+}
 
 // Sums over a vocabulary as pairs of fp32 (value hi + lo, |lo| at most half a
 // unit of hi; each addition exact to about 2^-46): fp64 additions run at 1/64 of
@@ -224,144 +297,332 @@ __device__ inline FF ff_scan(FF a) {
     }
     return a;
 }
-__device__ inline void st_cluster_ff(uint32_t addr, FF v) {
-    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(v.hi), "f"(v.lo) : "memory");
-}
-
-// What row n's token is drawn from.
-template <int DT>
-struct VfWeights {
-    const void *x, *y;    // y: NULL without a draft model at this position
-    float mx, ix, my, iy; // maxima and 1 / sums
-    float k;
-    int drop;             // the draft without a draft model, or -1
-    // eight weights from element c on (zeros from `end` on)
-    __device__ inline void get(int c, int end, float (&w)[8]) const {
+// A row as vectors of 16 bytes, counted from the boundary at or before its first
+// element; elements outside of the row read as -inf.
+template <int DT> struct VfRowIn {
+    static constexpr int N = Fmt<DT>::kVec;
+    const char *row;
+    int before, V;  // elements of vector 0 before the row, elements of the row
+    __device__ inline VfRowIn(const void *p, int vocab)
+        : row(reinterpret_cast<const char *>(p)), before(static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15u) / Fmt<DT>::kBytes), V(vocab) {}
+    __device__ inline int first(int v) const { return v * N - before; }
+    __device__ inline bool whole(int v) const { return first(v) >= 0 && first(v) + N <= V; }
+    __device__ inline const void *at(int v) const { return row + static_cast<int64_t>(first(v)) * Fmt<DT>::kBytes; }
+    __device__ inline uint4 edge(int v) const {  // element by element
+        float t[N];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            float v = 0.f;
-            if (c + j < end) {
-                v = ex2_hw((Fmt<DT>::load1(x, c + j) - mx) * k) * ix;
-                if (y) v = fmaxf(v - ex2_hw((Fmt<DT>::load1(y, c + j) - my) * k) * iy, 0.f);
-                if (c + j == drop) v = 0.f;
+        for (int j = 0; j < N; ++j) t[j] = first(v) + j >= 0 && first(v) + j < V ? Fmt<DT>::load1(row, first(v) + j) : -INFINITY;
+        return Fmt<DT>::pack(t);
+    }
+    __device__ inline uint4 get(int v) const { return whole(v) ? __ldg(reinterpret_cast<const uint4 *>(at(v))) : edge(v); }
+};
+
+// A thread's vectors v0, v0 + stride, ... < v1 of two rows (two: is there a second) on
+// their way through its own slots of shared memory, kDepth of them in flight: 64 KB
+// a CTA, so that one CTA alone on an SM reads at the rate that it could read at.
+// Vectors that reach over an end of either row are taken element by element,
+// before and after; `apart`: the second row's elements lie elsewhere in their
+// vectors than the first's, and are wanted at the first's places.
+constexpr int kDepth = 8;
+constexpr int kRing = kDepth * 2 * kThreads * 16;  // bytes of dynamic shared memory
+template <int DT> struct VfStream {
+    static constexpr int N = Fmt<DT>::kVec;
+    VfRowIn<DT> x, y;
+    bool two, apart;
+    int v, v1, stride, left, ahead;  // the next vector; whole vectors to use, and to ask for
+    const char *px, *py;
+    uint32_t mine;
+
+    __device__ inline void ask(int slot) {
+        if (ahead > 0) {
+            cp_async16(mine + slot * 2 * kThreads * 16, px);
+            if (two) cp_async16(mine + (slot * 2 + 1) * kThreads * 16, py);
+            px += static_cast<int64_t>(stride) * 16;
+            py += static_cast<int64_t>(stride) * 16;
+            --ahead;
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    // the first copies; `use` of run() follows, or drop()
+    __device__ inline VfStream(const VfRowIn<DT> &x_, const VfRowIn<DT> &y_, bool two_, bool apart_, int v0, int v1_, int stride_,
+                               uint4 *ring)
+        : x(x_), y(y_), two(two_), apart(apart_), v(v0), v1(v1_), stride(stride_), mine(smem_u32(ring + threadIdx.x)) {
+        // where whole vectors of both rows begin (at vector 0 or 1) and end
+        const int v_in = v == 0 && (!x.whole(0) || (two && !y.whole(0))) ? v + stride : v;
+        int end = (x.V + x.before) / N;
+        if (two) end = min(end, (y.V + y.before) / N);
+        end = min(end, v1);
+        left = !(two && apart) && v_in < end ? (end - v_in + stride - 1) / stride : 0;
+        ahead = left;
+        px = reinterpret_cast<const char *>(x.at(v_in));
+        py = reinterpret_cast<const char *>(y.at(v_in));
+#pragma unroll
+        for (int j = 0; j < kDepth - 2; ++j) ask(j);
+    }
+    __device__ inline void drop() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+    template <typename F> __device__ inline void slow(F use) {
+        uint4 ry = make_uint4(0u, 0u, 0u, 0u);
+        if (two && apart) {
+            float t[N];
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                const int c = x.first(v) + j;
+                t[j] = c >= 0 && c < y.V ? Fmt<DT>::load1(y.row, c) : -INFINITY;
             }
-            w[j] = v;
+            ry = Fmt<DT>::pack(t);
+        } else if (two) {
+            ry = y.get(v);
+        }
+        use(v, x.get(v), ry);
+        v += stride;
+    }
+    template <typename F> __device__ inline void run(F use) {
+        if (!(two && apart) && v == 0 && v < v1 && (!x.whole(0) || (two && !y.whole(0)))) slow(use);
+        // two vectors at a time, so that their arithmetic overlaps
+        while (left > 0) {
+#pragma unroll
+            for (int j = 0; j < kDepth; j += 2) {
+                if (left <= 0) break;
+                ask((j + kDepth - 2) % kDepth);
+                ask((j + kDepth - 1) % kDepth);
+                asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 2) : "memory");
+                const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+                const uint4 rx0 = ld_shared_v4(mine + j * 2 * kThreads * 16), rx1 = ld_shared_v4(mine + (j + 1) * 2 * kThreads * 16);
+                uint4 ry0 = none, ry1 = none;
+                if (two) {
+                    ry0 = ld_shared_v4(mine + (j * 2 + 1) * kThreads * 16);
+                    ry1 = ld_shared_v4(mine + (j * 2 + 3) * kThreads * 16);
+                }
+                if (left == 1) {
+                    use(v, rx0, ry0);
+                    v += stride;
+                    left = 0;
+                    break;
+                }
+                use(v, rx0, ry0, v + stride, rx1, ry1);
+                v += 2 * stride;
+                left -= 2;
+            }
+        }
+        drop();
+        while (v < v1) slow(use);
+    }
+};
+
+// What row n's token is drawn from: w_c = max(p_c - q_c, 0), or p_c.
+template <int DT> struct VfWeights {
+    static constexpr int N = Fmt<DT>::kVec;
+    VfRowIn<DT> x, y;
+    bool two, apart;  // a draft model at this position; its row starts elsewhere in its 16 bytes than x's
+    float rx, ix, ry, iy, k;
+    int drop;         // the draft without a draft model, or kNone
+
+    // the weights of vector v from its logits; e: p's terms (not scaled)
+    __device__ inline void get(int v, const uint4 &ux, const uint4 &uy, float (&e)[N], float (&w)[N]) const {
+        float t[N];
+        Fmt<DT>::unpack(ux, t);
+        vf_exps<N>(t, k, rx, e);
+        const F2 sx = f2(ix, ix);
+        if (two) {
+            float d[N];
+            Fmt<DT>::unpack(uy, t);
+            vf_exps<N>(t, k, ry, d);
+            const F2 sy = f2(-iy, -iy);
+#pragma unroll
+            for (int j = 0; j < N; j += 2) {
+                f2_split(f2_fma(sy, f2(d[j], d[j + 1]), f2_mul(f2(e[j], e[j + 1]), sx)), w[j], w[j + 1]);
+                w[j] = fmaxf(w[j], 0.f);
+                w[j + 1] = fmaxf(w[j + 1], 0.f);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < N; j += 2) f2_split(f2_mul(f2(e[j], e[j + 1]), sx), w[j], w[j + 1]);
+        }
+        const unsigned rel = static_cast<unsigned>(drop) - static_cast<unsigned>(x.first(v));
+        if (rel < static_cast<unsigned>(N)) {
+#pragma unroll
+            for (int j = 0; j < N; ++j) w[j] = static_cast<unsigned>(j) == rel ? 0.f : w[j];
         }
     }
 };
 
-template <int DT>
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) vf_pick_kernel(VfArgs a) {
-    __shared__ VfState sx[kMaxDrafts + 1], sy[kMaxDrafts];
-    __shared__ FF ranges[2][kCluster * kWarps];
-    __shared__ FF scan[kWarps], from, goal;
-    __shared__ float mass;
-    __shared__ int count, bad, pick, last, own;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int rank = static_cast<int>(cluster_ctarank()), b = blockIdx.x / kCluster;
-    const float temp = vf_temp(a, b), k = vf_k(temp);
-    const bool greedy = temp == 0.f;
-    if (tid == 0) {
-        count = a.K;
-        bad = vf_temp_ok(temp) ? 0 : 1;
-        last = -1;
-        pick = kNone;
-    }
-    __syncthreads();
-    cluster_sync_all();  // every CTA of the cluster runs before one writes into another
-    pdl_wait();
-    const bool usable = !bad;
-    // every row's statistics and whether its draft stays
-    for (int i = warp; i <= a.K && usable; i += kWarps) {
-        bool ended = false;
-        for (int j = lane; j < i; j += 32) ended |= !vf_valid(a, vf_draft(a, b, j));
-        if (__any_sync(0xffffffffu, ended)) break;
-        const VfState p = vf_row(a.px + (static_cast<int64_t>(b) * (a.K + 1) + i) * a.parts, a.parts, k);
-        const int64_t t = i < a.K ? vf_draft(a, b, i) : -1;
-        const bool has = vf_valid(a, t);
-        VfState q{0.f, 0.f, 0};
-        const bool model = a.y && has && !greedy;
-        if (model) q = vf_row(a.py + (static_cast<int64_t>(b) * a.K + i) * a.parts, a.parts, k);
-        if (lane == 0) {
-            sx[i] = p;
-            if (i < a.K) sy[i] = q;
-            bool stays = has && vf_defined(p) && vf_defined(q);
-            if (stays && greedy) stays = p.at == static_cast<int>(t);
-            if (stays && !greedy) {
-                const float pt = ex2_hw((Fmt<DT>::load1(a.x, b * a.xs + i * a.xr + t) - p.m) * k);
-                const float qt = model ? ex2_hw((Fmt<DT>::load1(a.y, b * a.ys + i * a.yr + t) - q.m) * k) : 1.f;
-                stays = __ldg(a.u + static_cast<int64_t>(b) * a.K + i) * qt * vf_total(p) < pt * vf_total(q);
+__device__ inline void vf_put(const VfArgs &a, int64_t at, int64_t token, float lp) {
+    if (a.tok32) reinterpret_cast<int32_t *>(a.tokens)[at] = static_cast<int32_t>(token);
+    else reinterpret_cast<int64_t *>(a.tokens)[at] = token;
+    a.logp[at] = lp;
+}
+// log p of a token with logit x from the sum beside the maximum's term; ln2_k = 1 / T
+__device__ inline float vf_logp(float x, float M, float s1, float ln2_k) { return (x - M) * ln2_k - log1pf(s1); }
+
+// Every warp of the cluster gives 16 bytes to all, and all go on once they have
+// them: asynchronous stores that count on each CTA's mbarrier, two sets of slots by
+// turns. (A cluster barrier's release waits for the copies in flight too.) A warp
+// gives for the next turn only after it has read this one's, so no slot is written
+// while it is read.
+struct VfMeetMem {
+    float4 slot[2][kCluster * kWarps];
+    uint64_t bar[2];
+    int abort;
+};
+struct VfMeet {
+    VfMeetMem &m;
+    int rank, size, turn;
+    __device__ inline VfMeet(VfMeetMem &mem) : m(mem), rank(cluster_ctarank()), size(cluster_nctarank()), turn(0) {
+        if (threadIdx.x == 0) {
+            m.abort = 0;
+            for (int i = 0; i < 2; ++i) {
+                mbar_init(smem_u32(&m.bar[i]), 1);
             }
-            if (!stays && i < a.K) atomicMin(&count, i);
+            fence_mbar_init_cluster();
+            for (int i = 0; i < 2; ++i) mbar_expect_tx(smem_u32(&m.bar[i]), size * kWarps * 16);
         }
+        __syncthreads();
+        cluster_sync_all();  // every CTA of the cluster runs, and its barriers exist, before one writes into another
     }
-    __syncthreads();
-    const int n = usable ? count : 0;
-    const int64_t tn = n < a.K ? vf_draft(a, b, n) : -1;
-    const bool turned = usable && vf_valid(a, tn), model = turned && a.y && !greedy;
-    const VfState p = usable ? sx[n] : VfState{0.f, 0.f, 0};
-    const VfState q = model ? sy[n] : VfState{0.f, 0.f, 0};
-    const bool defined = usable && vf_defined(p) && vf_defined(q);
-    const int64_t row = static_cast<int64_t>(b) * (a.K + 1);
-    const float ln2_k = k * 0.6931471805599453f;  // 1 / T
-    // accepted tokens, and what lies behind the last one
+    __device__ inline const float4 *all(float a, float b, float c, float d) {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, set = turn & 1;
+        const uint32_t bar = smem_u32(&m.bar[set]);
+        __syncwarp();  // every lane has read the last turn's
+        if (lane < size) {
+            asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(
+                             mapa_shared(smem_u32(&m.slot[set][rank * kWarps + warp]), lane)),
+                         "f"(a), "f"(b), "f"(c), "f"(d), "r"(mapa_shared(bar, lane))
+                         : "memory");
+        }
+        mbar_wait_bounded<true>(bar, (turn >> 1) & 1, &m.abort);
+        if (threadIdx.x == 0) mbar_expect_tx(bar, size * kWarps * 16);  // the turn after the next
+        ++turn;
+        return m.slot[set];
+    }
+    // no CTA leaves while another may still write into it (one whose wait gave up may be early)
+    __device__ inline void leave() {
+        __syncthreads();
+        cluster_sync_all();
+    }
+    __device__ inline bool failed() const { return *const_cast<volatile int *>(&m.abort) != 0; }
+};
+
+struct VfDrawMem {
+    FF scan[kWarps], from, goal;
+    float mass, s1;
+    int own, pick, last;
+};
+
+// Token n of sequence b, by its whole cluster, and what lies behind it. p, q: the
+// rows (q: vf_none() without a draft model at n), the same in every thread of the
+// cluster; turned: position n has a draft; S1: p.s1 is known (else it is formed
+// here, for the log-probability of a token that holds the maximum). The CTAs have
+// met in a cluster barrier since they started.
+template <int DT, bool S1>
+__device__ inline void vf_draw(const VfArgs &a, int b, int n, const VfRow &p, const VfRow &q, bool turned, bool model,
+                               bool usable, bool greedy, float k, VfDrawMem &m, VfMeet &meet, uint4 *ring) {
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rank = static_cast<int>(cluster_ctarank()), size = static_cast<int>(cluster_nctarank());
+    const int64_t row = static_cast<int64_t>(b) * (a.K + 1), xrow = b * a.xs + n * a.xr;
+    const float ln2_k = k * 0.6931471805599453f;
     if (rank == 0) {
         if (tid == 0) a.accepted[b] = n;
-        for (int i = tid; i <= a.K; i += kThreads) {
-            if (i == n) continue;
-            int64_t t = -1;
-            float lp = 0.f;
-            if (i < n) {
-                t = vf_draft(a, b, i);
-                lp = (Fmt<DT>::load1(a.x, b * a.xs + i * a.xr + t) - sx[i].m) * ln2_k - log1pf(sx[i].s);
-            }
-            if (a.tok32) reinterpret_cast<int32_t *>(a.tokens)[row + i] = static_cast<int32_t>(t);
-            else reinterpret_cast<int64_t *>(a.tokens)[row + i] = t;
-            a.logp[row + i] = lp;
-        }
+        for (int i = n + 1 + tid; i <= a.K; i += kThreads) vf_put(a, row + i, -1, 0.f);
     }
-    const int64_t xrow = b * a.xs + n * a.xr;
     const auto emit = [&](int t) {
-        const float lp = t < 0 ? NAN : (Fmt<DT>::load1(a.x, xrow + t) - p.m) * ln2_k - log1pf(p.s);
-        if (a.tok32) reinterpret_cast<int32_t *>(a.tokens)[row + n] = t;
-        else reinterpret_cast<int64_t *>(a.tokens)[row + n] = t;
-        a.logp[row + n] = lp;
+        float lp = NAN;
+        if (t >= 0) {
+            const float x = Fmt<DT>::load1(a.x, xrow + t);
+            if (S1 || greedy) lp = vf_logp(x, p.M, p.s1, ln2_k);
+            else lp = x == p.M ? -log1pf(m.s1) : (x - p.R) * ln2_k - logf(p.S);
+        }
+        vf_put(a, row + n, t, lp);
     };
+    const bool defined = usable && vf_defined(p) && vf_defined(q);
     if (!defined || greedy) {  // the same in every CTA of the cluster
         if (rank == 0 && tid == 0) emit(defined ? p.at : -1);
         return;
     }
-    VfWeights<DT> w;
-    w.x = reinterpret_cast<const char *>(a.x) + xrow * Fmt<DT>::kBytes;
-    w.y = model ? reinterpret_cast<const char *>(a.y) + (b * a.ys + n * a.yr) * Fmt<DT>::kBytes : nullptr;
-    w.mx = p.m; w.ix = 1.f / vf_total(p); w.my = q.m; w.iy = 1.f / vf_total(q); w.k = k;
-    w.drop = turned && !a.y ? static_cast<int>(tn) : -1;
-    // contiguous ranges of the row, one a warp of the cluster, in steps of 256 elements
-    const int steps = (a.V + 255) / 256, all = kCluster * kWarps;
+    constexpr int N = Fmt<DT>::kVec;
+    const char *px = reinterpret_cast<const char *>(a.x) + xrow * Fmt<DT>::kBytes;
+    const char *py = model ? reinterpret_cast<const char *>(a.y) + (b * a.ys + n * a.yr) * Fmt<DT>::kBytes : px;
+    VfWeights<DT> w{VfRowIn<DT>(px, a.V), VfRowIn<DT>(py, a.V), model, false, p.R * k, 1.f / p.S, q.R * k, 1.f / q.S, k,
+                    turned && !model ? static_cast<int>(vf_draft(a, b, n)) : kNone};
+    w.apart = w.x.before != w.y.before;
+    // contiguous ranges of the row, one a warp of the cluster, in steps of 32 vectors
+    const int steps = (a.V + N - 1 + 32 * N - 1) / (32 * N), all = size * kWarps;
+    const auto step_of = [&](int range) { return static_cast<int>(static_cast<int64_t>(steps) * range / all); };
     for (int pass = 0;; ++pass) {
-        const int g = rank * kWarps + warp;
-        const int s0 = static_cast<int>(static_cast<int64_t>(steps) * g / all);
-        const int s1 = static_cast<int>(static_cast<int64_t>(steps) * (g + 1) / all);
+        const int g = rank * kWarps + warp, s0 = step_of(g), s1 = step_of(g + 1);
         FF sum{0.f, 0.f};
-        for (int st = s0; st < s1; ++st) {
-            float v[8], t = 0.f;
-            w.get(st * 256 + lane * 8, a.V, v);
+        float rest = 0.f, tops = 0.f;
+        VfStream<DT> in(w.x, w.y, w.two, w.apart, s0 * 32 + lane, s1 * 32, 32, ring);
+        const auto one = [&](int v, const uint4 &ux, const uint4 &uy, float &r) {
+            float e[N], g[N];
+            w.get(v, ux, uy, e, g);
+            F2 t = f2(g[0], g[1]);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) t += v[j];
-            sum = ff_add(sum, FF{t, 0.f});
+            for (int j = 2; j < N; j += 2) t = f2_add(t, f2(g[j], g[j + 1]));
+            if (!S1) {
+                // p's terms off the maximum, and how many elements hold it
+                if (Fmt<DT>::vmax(ux) == p.M) {
+                    float x[N];
+                    Fmt<DT>::unpack(ux, x);
+#pragma unroll
+                    for (int j = 0; j < N; ++j) {
+                        tops += x[j] == p.M ? 1.f : 0.f;
+                        e[j] = x[j] == p.M ? 0.f : e[j];
+                    }
+                }
+                F2 o = f2(e[0], e[1]);
+#pragma unroll
+                for (int j = 2; j < N; j += 2) o = f2_add(o, f2(e[j], e[j + 1]));
+                float lo, hi;
+                f2_split(o, lo, hi);
+                r += lo + hi;
+            }
+            float lo, hi;
+            f2_split(t, lo, hi);
+            return lo + hi;
+        };
+        float rest2 = 0.f;
+        struct Use {
+            const decltype(one) &f;
+            FF &sum;
+            float &rest, &rest2;
+            __device__ inline void operator()(int v, const uint4 &ux, const uint4 &uy) const { sum = ff_add(sum, FF{f(v, ux, uy, rest), 0.f}); }
+            __device__ inline void operator()(int v, const uint4 &ux, const uint4 &uy, int v2, const uint4 &ux2, const uint4 &uy2) const {
+                const float t = f(v, ux, uy, rest), t2 = f(v2, ux2, uy2, rest2);
+                sum = ff_add(ff_add(sum, FF{t, 0.f}), FF{t2, 0.f});
+            }
+        };
+        in.run(Use{one, sum, rest, rest2});
+        rest += rest2;
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) {
+            sum = ff_add(sum, ff_shfl_xor(sum, off));
+            if (!S1) {
+                rest += __shfl_xor_sync(0xffffffffu, rest, off);
+                tops += __shfl_xor_sync(0xffffffffu, tops, off);
+            }
         }
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) sum = ff_add(sum, ff_shfl_xor(sum, off));
-        if (lane < kCluster) st_cluster_ff(mapa_shared(smem_u32(&ranges[pass][g]), lane), sum);
-        cluster_sync_all();
+        const float4 *ranges = meet.all(sum.hi, sum.lo, rest, tops);
         // Every CTA finds the same range: the first whose end lies above the aim;
         // rounding may leave none, then the last that holds anything.
         if (warp == 0) {
             static_assert(kCluster * kWarps == 64, "two ranges a lane");
-            const FF v0 = ranges[pass][2 * lane], v1 = ranges[pass][2 * lane + 1];
+            const FF zero{0.f, 0.f};
+            const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
+            const float4 r0 = 2 * lane < all ? ranges[2 * lane] : none, r1 = 2 * lane < all ? ranges[2 * lane + 1] : none;
+            const FF v0{r0.x, r0.y}, v1{r1.x, r1.y};
+            if (!S1) {
+                float rest_all = r0.z + r1.z, tops_all = r0.w + r1.w;
+#pragma unroll
+                for (int off = 16; off > 0; off >>= 1) {
+                    rest_all += __shfl_xor_sync(0xffffffffu, rest_all, off);
+                    tops_all += __shfl_xor_sync(0xffffffffu, tops_all, off);
+                }
+                // from terms relative to R to those relative to M
+                if (lane == 0) m.s1 = (tops_all - 1.f) + rest_all / vf_exp(p.M, k, w.rx);
+            }
             const FF incl = ff_scan(ff_add(v0, v1));
             FF before = ff_shfl_up(incl, 1);
-            if (lane == 0) before = FF{0.f, 0.f};
+            if (lane == 0) before = zero;
             const FF sum_all = ff_shfl(incl, 31), aim = ff_scale(sum_all, __ldg(a.r + b));
             const FF mid = ff_add(before, v0);
             const int hit = ff_above(mid, aim) ? 2 * lane : (ff_above(incl, aim) ? 2 * lane + 1 : -1);
@@ -370,78 +631,340 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) vf_
             const int src = hits ? __ffs(hits) - 1 : (fulls ? 31 - __clz(fulls) : 0);
             const int found = hits ? hit : full;
             if (lane == src) {
-                own = found;
-                from = (found & 1) ? mid : before;
-                goal = aim;
-                mass = sum_all.hi;
+                m.own = meet.failed() ? -1 : found;  // a wait that gave up leaves no token
+                m.from = (found & 1) ? mid : before;
+                m.goal = aim;
+                m.mass = meet.failed() ? 1.f : sum_all.hi;
+                m.pick = kNone;
+                m.last = -1;
             }
         }
         __syncthreads();
         // p <= q everywhere (p = q): drawn from p
-        if (mass > 0.f || pass == 1) break;
-        w.y = nullptr;
-        w.drop = -1;
+        if (m.mass > 0.f || pass == 1) break;
+        w.two = false;
+        w.drop = kNone;
     }
-    const int range = own;
+    const int range = m.own;
     if (range < 0) {  // nothing to draw from
         if (rank == 0 && tid == 0) emit(-1);
         return;
     }
     if (range / kWarps != rank) return;
-    // the CTA walks its warp's range, 2048 elements at a time
-    const FF aim = goal;
-    FF below = from;
-    const int e0 = static_cast<int>(static_cast<int64_t>(steps) * range / all) * 256;
-    const int64_t end = static_cast<int64_t>(steps) * (range + 1) / all * 256;
-    const int e1 = end < a.V ? static_cast<int>(end) : a.V;
-    for (int c0 = e0; c0 < e1; c0 += kThreads * 8) {
-        float v[8], t = 0.f;
-        const int c = c0 + tid * 8;
-        w.get(c, e1, v);
+    // the CTA walks its warp's range, a vector a thread at a time
+    const FF aim = m.goal;
+    FF below = m.from;
+    const int v1 = step_of(range + 1) * 32;
+    for (int v0 = step_of(range) * 32; v0 < v1; v0 += kThreads) {
+        float v[N], t = 0.f;
+        const int c = w.x.first(v0 + tid);
+        if (v0 + tid < v1) {
+            uint4 uy = make_uint4(0u, 0u, 0u, 0u);
+            if (w.two && !w.apart) uy = w.y.get(v0 + tid);
+            if (w.two && w.apart) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) t += v[j];
+                for (int j = 0; j < N; ++j) v[j] = c + j >= 0 && c + j < a.V ? Fmt<DT>::load1(py, c + j) : -INFINITY;
+                uy = Fmt<DT>::pack(v);
+            }
+            float e[N];
+            w.get(v0 + tid, w.x.get(v0 + tid), uy, e, v);
+        } else {
+#pragma unroll
+            for (int j = 0; j < N; ++j) v[j] = 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < N; ++j) t += v[j];
         const FF incl = ff_scan(FF{t, 0.f});
-        if (lane == 31) scan[warp] = incl;
+        if (lane == 31) m.scan[warp] = incl;
         __syncthreads();
         FF start = below;
-        for (int j = 0; j < warp; ++j) start = ff_add(start, scan[j]);
+        for (int j = 0; j < warp; ++j) start = ff_add(start, m.scan[j]);
         FF before = ff_shfl_up(incl, 1);
         before = lane == 0 ? start : ff_add(start, before);
         int found = -1, lastpos = -1;
         float run = 0.f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < N; ++j) {
             run += v[j];
             if (v[j] > 0.f) {
                 lastpos = c + j;
                 if (found < 0 && ff_above(ff_add(before, FF{run, 0.f}), aim)) found = c + j;
             }
         }
-        if (found >= 0) atomicMin(&pick, found);
-        if (lastpos >= 0) atomicMax(&last, lastpos);
-        for (int j = 0; j < kWarps; ++j) below = ff_add(below, scan[j]);
+        if (found >= 0) atomicMin(&m.pick, found);
+        if (lastpos >= 0) atomicMax(&m.last, lastpos);
+        for (int j = 0; j < kWarps; ++j) below = ff_add(below, m.scan[j]);
         __syncthreads();
-        if (pick != kNone) break;  // written before the barrier above, read after it
+        if (m.pick != kNone) break;  // written before the barrier above, read after it
     }
-    if (tid == 0) emit(pick != kNone ? pick : last);
+    // rounding may leave no such element: then the last that holds anything
+    if (tid == 0) emit(m.pick != kNone ? m.pick : m.last);
+}
+
+// Few sequences, after vf_stats_kernel.
+template <int DT>
+__global__ void __launch_bounds__(kThreads, 2) vf_pick_kernel(VfArgs a) {
+    extern __shared__ uint4 ring[];
+    __shared__ VfState sx[kMaxDrafts + 1], sy[kMaxDrafts];
+    __shared__ VfDrawMem mem;
+    __shared__ VfMeetMem meeting;
+    __shared__ int count;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rank = static_cast<int>(cluster_ctarank()), b = blockIdx.x / cluster_nctarank();
+    const float temp = vf_temp(a, b), k = vf_k(temp);
+    const bool greedy = temp == 0.f, usable = vf_temp_ok(temp);
+    if (tid == 0) count = a.K;
+    VfMeet meet(meeting);
+    pdl_wait();
+    // every row's statistics and whether its draft stays
+    for (int i = warp; i <= a.K && usable; i += kWarps) {
+        bool ended = false;
+        for (int j = lane; j < i; j += 32) ended |= !vf_valid(a, vf_draft(a, b, j));
+        if (__any_sync(0xffffffffu, ended)) break;
+        const int64_t t = i < a.K ? vf_draft(a, b, i) : -1;
+        const bool has = vf_valid(a, t), model = a.y && has && !greedy;
+        const float u = has ? __ldg(a.u + static_cast<int64_t>(b) * a.K + i) : 0.f;
+        const float xt = has ? Fmt<DT>::load1(a.x, b * a.xs + i * a.xr + t) : 0.f;
+        const float yt = model ? Fmt<DT>::load1(a.y, b * a.ys + i * a.yr + t) : 0.f;
+        const VfState p = vf_row(a.px + (static_cast<int64_t>(b) * (a.K + 1) + i) * a.parts, a.parts, k);
+        VfState q{0.f, 0.f, 0};
+        if (model) q = vf_row(a.py + (static_cast<int64_t>(b) * a.K + i) * a.parts, a.parts, k);
+        if (lane == 0) {
+            sx[i] = p;
+            if (i < a.K) {
+                sy[i] = q;
+                if (!has || !vf_stays(t, u, xt, yt, vf_of(p, k), model ? vf_of(q, k) : vf_none(), model, greedy, k)) atomicMin(&count, i);
+            }
+        }
+    }
+    __syncthreads();
+    const int n = usable ? count : 0;
+    if (rank == 0) {
+        for (int i = tid; i < n; i += kThreads) {
+            const int64_t t = vf_draft(a, b, i);
+            vf_put(a, static_cast<int64_t>(b) * (a.K + 1) + i, t,
+                   vf_logp(Fmt<DT>::load1(a.x, b * a.xs + i * a.xr + t), sx[i].m, sx[i].s, k * 0.6931471805599453f));
+        }
+    }
+    const bool turned = usable && n < a.K && vf_valid(a, vf_draft(a, b, n)), model = turned && a.y && !greedy;
+    vf_draw<DT, true>(a, b, n, usable ? vf_of(sx[n], k) : vf_none(), model ? vf_of(sy[n], k) : vf_none(), turned, model, usable,
+                      greedy, k, mem, meet, ring);
+    meet.leave();
+}
+
+// Adds 2^(x k - r) of a vector whose first element is c, without element `skip`, and
+// follows the maximum (with it): a conversion, half a multiplication, an
+// exponential, half an addition and half a maximum an element.
+template <int DT> struct VfAdd {
+    static constexpr int N = Fmt<DT>::kVec;
+    F2 sum = f2(0.f, 0.f);
+    uint32_t top16 = Fmt<DT>::kNegInfWord;  // packed maxima of 16-bit types
+    float top = -INFINITY;
+    __device__ inline void add(const uint4 &r, int c, float k, float rk, int skip) {
+        float x[N];
+        Fmt<DT>::unpack(r, x);
+        if constexpr (DT == CE_DT_F32) top = fmaxf(top, Fmt<DT>::vmax(r));
+        else top16 = Fmt<DT>::hmax2(top16, Fmt<DT>::hmax2(Fmt<DT>::hmax2(r.x, r.y), Fmt<DT>::hmax2(r.z, r.w)));
+        const unsigned rel = static_cast<unsigned>(skip) - static_cast<unsigned>(c);
+        if (rel < static_cast<unsigned>(N)) {
+#pragma unroll
+            for (int j = 0; j < N; ++j) x[j] = static_cast<unsigned>(j) == rel ? -INFINITY : x[j];
+        }
+        const F2 kk = f2(k, k), rr = f2(-rk, -rk);
+#pragma unroll
+        for (int j = 0; j < N; j += 2) sum = f2_add(sum, f2_ex2(f2_fma(f2(x[j], x[j + 1]), kk, rr)));
+    }
+    __device__ inline void join(const VfAdd &o) {
+        sum = f2_add(sum, o.sum);
+        top = fmaxf(top, o.top);
+        if constexpr (DT != CE_DT_F32) top16 = Fmt<DT>::hmax2(top16, o.top16);
+    }
+    __device__ inline void finish(float &m, float &s) const {
+        float lo, hi;
+        f2_split(sum, lo, hi);
+        s = lo + hi;
+        m = top;
+        if constexpr (DT != CE_DT_F32) {
+            Fmt<DT>::unpack2(top16, lo, hi);
+            m = fmaxf(lo, hi);
+        }
+    }
+};
+
+// Many sequences: everything of one by its cluster, position by position. Sums are
+// taken from a reference R that every thread knows at the start, the draft's own
+// logit x_t (then log p_t = -log1p(s), s without the draft's term), or the largest
+// of 32 spread elements: no running maximum, no rebasing, and the warps' sums
+// just add up. Where the maximum turns out 2^60 or more away, the row is taken
+// again from its maximum. (With each thread's running maximum and its element kept
+// out of the sum the instructions took twice as long as the reading: 108 us for
+// 128 sequences of 4 drafts and 128256 columns of bf16.)
+template <int DT>
+__global__ void __launch_bounds__(kThreads, 3) vf_seq_kernel(VfArgs a) {
+    extern __shared__ uint4 ring[];
+    constexpr int N = Fmt<DT>::kVec;
+    constexpr float kFar = 60.f;
+    __shared__ VfMeetMem meeting;
+    __shared__ int drafts[kMaxDrafts + 1];         // -1: none
+    __shared__ float us[kMaxDrafts + 1], xts[kMaxDrafts + 1], yts[kMaxDrafts + 1];
+    __shared__ VfDrawMem mem;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int rank = static_cast<int>(cluster_ctarank()), size = static_cast<int>(cluster_nctarank()), b = blockIdx.x / size;
+    const float temp = vf_temp(a, b), k = vf_k(temp), ln2_k = k * 0.6931471805599453f;
+    const bool greedy = temp == 0.f, usable = vf_temp_ok(temp);
+    // every position's scalars
+    for (int i = tid; i <= a.K; i += kThreads) {
+        const int64_t t = i < a.K ? vf_draft(a, b, i) : -1;
+        const bool has = vf_valid(a, t);
+        drafts[i] = has ? static_cast<int>(t) : -1;
+        us[i] = has ? __ldg(a.u + static_cast<int64_t>(b) * a.K + i) : 0.f;
+        xts[i] = has ? Fmt<DT>::load1(a.x, b * a.xs + i * a.xr + t) : 0.f;
+        yts[i] = has && a.y && !greedy ? Fmt<DT>::load1(a.y, b * a.ys + i * a.yr + t) : 0.f;
+    }
+    VfMeet meet(meeting);
+    // this CTA's slice of a row, in steps of a vector a thread
+    const int steps = (a.V + N - 1 + kThreads * N - 1) / (kThreads * N);
+    const int t0 = static_cast<int>(static_cast<int64_t>(steps) * rank / size), t1 = static_cast<int>(static_cast<int64_t>(steps) * (rank + 1) / size);
+    // position i's rows on their way (the rows' vectors need not lie alike: each row's slice is its own)
+    const auto stream = [&](int i) {
+        const bool two = a.y && drafts[i] >= 0;
+        const VfRowIn<DT> in(reinterpret_cast<const char *>(a.x) + (b * a.xs + i * a.xr) * Fmt<DT>::kBytes, a.V);
+        const VfRowIn<DT> yin(two ? reinterpret_cast<const char *>(a.y) + (b * a.ys + i * a.yr) * Fmt<DT>::kBytes : in.row, a.V);
+        return VfStream<DT>(in, yin, two, false, t0 * kThreads + tid, greedy || !usable ? 0 : t1 * kThreads, kThreads, ring);
+    };
+    // the largest of 32 elements spread over a row (0 if none is finite)
+    const auto sample = [&](const void *row) {
+        float v = Fmt<DT>::load1(row, static_cast<int>(static_cast<int64_t>(a.V) * lane / 32));
+        v = fabsf(v) < INFINITY ? v : -INFINITY;
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
+        return v == -INFINITY ? 0.f : v;
+    };
+    VfRow p = vf_none(), q = vf_none();
+    bool has = false, model = false;
+    int n = 0;
+    VfStream<DT> in = stream(0);  // (greedy sequences read without it)
+    for (; usable; ++n) {
+        const int t = drafts[n];
+        has = t >= 0;
+        model = a.y && has && !greedy;
+        const char *x = reinterpret_cast<const char *>(a.x) + (b * a.xs + n * a.xr) * Fmt<DT>::kBytes;
+        const char *y = reinterpret_cast<const char *>(a.y) + (b * a.ys + n * a.yr) * Fmt<DT>::kBytes;
+        const float u = us[n], xt = xts[n], yt = yts[n];
+        const int skip = has ? t : kNone;
+        q = vf_none();
+        if (greedy) {
+            VfState st{-INFINITY, 0.f, kNone};
+            for (int step = t0; step < t1; step += 4) {
+                VfTile<DT, 4> tx;
+                tx.load(x, a.V, step * kThreads + tid, kThreads, t1 - step);
+                st = vf_merge(st, tx.stats(k), k);
+            }
+            st = vf_reduce(st, k);
+            const float4 *all = meet.all(st.m, st.s, __int_as_float(st.at), 0.f);
+            st = VfState{-INFINITY, 0.f, kNone};
+            for (int j = lane; j < size * kWarps; j += 32) st = vf_merge(st, VfState{all[j].x, all[j].y, __float_as_int(all[j].z)}, k);
+            p = vf_of(vf_reduce(st, k), k);
+        } else {
+            float R = has && fabsf(xt) < INFINITY ? xt : sample(x), Q = 0.f;
+            if (model) Q = fabsf(yt) < INFINITY ? yt : sample(y);
+            for (int again = 0;; ++again) {
+                VfAdd<DT> ax, ay;
+                const float rk = R * k, qk = Q * k;
+                VfAdd<DT> bx, by;  // of every second vector
+                struct Use {
+                    VfAdd<DT> &ax, &ay, &bx, &by;
+                    const VfStream<DT> &in;
+                    float k, rk, qk;
+                    int skip;
+                    bool model;
+                    __device__ inline void operator()(int v, const uint4 &ux, const uint4 &uy) const {
+                        ax.add(ux, in.x.first(v), k, rk, skip);
+                        if (model) ay.add(uy, in.y.first(v), k, qk, kNone);
+                    }
+                    __device__ inline void operator()(int v, const uint4 &ux, const uint4 &uy, int v2, const uint4 &ux2, const uint4 &uy2) const {
+                        ax.add(ux, in.x.first(v), k, rk, skip);
+                        bx.add(ux2, in.x.first(v2), k, rk, skip);
+                        if (model) {
+                            ay.add(uy, in.y.first(v), k, qk, kNone);
+                            by.add(uy2, in.y.first(v2), k, qk, kNone);
+                        }
+                    }
+                };
+                in.run(Use{ax, ay, bx, by, in, k, rk, qk, skip, model});
+                ax.join(bx);
+                ay.join(by);
+                // the next position's rows, in case this draft stays
+                if (has) in = stream(n + 1);
+                float mx, vx, my, vy;
+                ax.finish(mx, vx);
+                ay.finish(my, vy);
+                const auto over = [&](float &m0, float &v0, float &m1, float &v1) {
+#pragma unroll
+                    for (int off = 16; off > 0; off >>= 1) {
+                        m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, off));
+                        v0 += __shfl_xor_sync(0xffffffffu, v0, off);
+                        m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, off));
+                        v1 += __shfl_xor_sync(0xffffffffu, v1, off);
+                    }
+                };
+                over(mx, vx, my, vy);
+                const float4 *all = meet.all(mx, vx, my, vy);
+                const int slots = size * kWarps;
+                const float4 none = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
+                const float4 f0 = lane < slots ? all[lane] : none, f1 = lane + 32 < slots ? all[lane + 32] : none;
+                mx = fmaxf(f0.x, f1.x);
+                vx = f0.y + f1.y;
+                my = fmaxf(f0.z, f1.z);
+                vy = f0.w + f1.w;
+                over(mx, vx, my, vy);
+                // the draft's own term beside the others' sum; a NaN in the draft's place shows in xt
+                const float et = has ? vf_exp(xt, k, rk) : 0.f;
+                p = VfRow{R, et + vx, mx, R == xt ? vx / et : vx, kNone};
+                if (model) q = VfRow{Q, vy, my, 0.f, kNone};
+                // (the maximum of a row with NaN is that of the others: its sum is NaN)
+                const bool far = fabsf(mx) < INFINITY && !(fabsf((mx - R) * k) <= kFar) && R != mx;
+                const bool qfar = model && fabsf(my) < INFINITY && !(fabsf((my - Q) * k) <= kFar) && Q != my;
+                if (again || !(far || qfar)) break;
+                if (far) R = mx;
+                if (qfar) Q = my;
+                in.drop();
+                in = stream(n);
+            }
+        }
+        if (!has || !vf_stays(t, u, xt, yt, p, q, model, greedy, k)) break;
+        if (rank == 0 && tid == 0) {
+            float lp;
+            if (greedy) lp = vf_logp(xt, p.M, p.s1, ln2_k);
+            else lp = p.R == xt ? -log1pf(p.s1) : (xt - p.R) * ln2_k - logf(p.S);
+            vf_put(a, static_cast<int64_t>(b) * (a.K + 1) + n, t, lp);
+        }
+    }
+    in.drop();
+    if (meet.failed()) p.S = NAN;  // (no result: token -1)
+    vf_draw<DT, false>(a, b, n, p, q, has, model, usable, greedy, k, mem, meet, ring);
+    meet.leave();
 }
 
 }  // namespace
 
-static int vf_part_len(int64_t rows, int64_t vocab, int dtype) {
-    // parts of at most 64 KB, more of them while the rows do not fill the GPU, none under 2048 elements
-    const int64_t most = 65536 / fp8_elem(dtype);
-    int64_t parts = (vocab + most - 1) / most;
-    const int64_t want = rows > 0 ? (1216 + rows - 1) / rows : 1, fit = (vocab + 2047) / 2048;
-    if (parts < want) parts = want;
-    if (parts > fit) parts = fit;
-    const int64_t len = (vocab + parts - 1) / parts;
-    return static_cast<int>((len + 7) / 8 * 8);
-}
-
-static int64_t vf_parts(int64_t rows, int64_t vocab, int dtype) {
-    const int64_t len = vf_part_len(rows, vocab, dtype);
-    return (vocab + len - 1) / len;
+// How the rows are cut: U vectors a lane (4, or fewer while that leaves warps
+// without a part), and how many parts a row has wherever it starts.
+constexpr int kStatsWarps = 152 * 3 * kWarps;  // three CTAs an SM
+struct VfCut {
+    int U, per;
+    int64_t parts;
+};
+static VfCut vf_cut(int64_t rows, int64_t vocab, int dtype) {
+    const int N = 16 / fp8_elem(dtype);
+    VfCut c{};
+    for (int U = 4; U >= 1; U >>= 1) {
+        c.U = U;
+        c.per = U * 32 * N;
+        c.parts = (vocab + N - 1 + c.per - 1) / c.per;
+        if (rows * c.parts >= kStatsWarps) break;
+    }
+    return c;
 }
 
 }  // namespace ce
@@ -456,16 +979,40 @@ ce_status vf_check(const ce_verify_params *p) {
     if (p->token_is_int32 != 0 && p->token_is_int32 != 1) return CE_ERR_INVALID_ARG;
     if (!(p->temperature == 0.f || (p->temperature >= 1e-4f && p->temperature <= 1e4f))) return CE_ERR_INVALID_ARG;
     if (p->ld < p->vocab || p->ld_draft < p->vocab || p->seq_stride < 0 || p->draft_seq_stride < 0) return CE_ERR_INVALID_ARG;
-    constexpr int64_t kMost = (int64_t(1) << 31) - 4096;
+    constexpr int64_t kMost = (int64_t(1) << 31) - 65536;  // element indices are 32-bit
     if (p->n_drafts > kMaxDrafts || p->vocab > kMost || p->n_seqs > kMost / kCluster ||
-        p->n_seqs * (p->n_drafts + 1) > kMost / vf_parts(p->n_seqs * (p->n_drafts + 1), p->vocab, p->dtype))
+        p->n_seqs * (p->n_drafts + 1) > kMost / vf_cut(p->n_seqs * (p->n_drafts + 1), p->vocab, p->dtype).parts)
         return CE_ERR_UNSUPPORTED;
     return CE_OK;
 }
 
 size_t vf_bytes(const ce_verify_params *p) {
     const int64_t rows = p->n_seqs * (p->n_drafts + 1);
-    return static_cast<size_t>(vf_parts(rows, p->vocab, p->dtype) * (rows + p->n_seqs * p->n_drafts)) * sizeof(VfPart) + 256;
+    return static_cast<size_t>(vf_cut(rows, p->vocab, p->dtype).parts * (rows + p->n_seqs * p->n_drafts)) * sizeof(VfPart) + 256;
+}
+
+// the shared-memory limit is a per-device attribute of each kernel: set once per device
+cudaError_t vf_allow_ring(const void *fn, int which) {
+    static std::atomic<uint64_t> done[6];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? (1ull << dev) : 0ull;
+    if (bit && (done[which].load() & bit)) return cudaSuccess;
+    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kRing);
+    if (e == cudaSuccess) done[which].fetch_or(bit);
+    return e;
+}
+
+// CTAs a sequence where a cluster a sequence fills the GPU (three CTAs an SM), 0 where
+// the rows of all positions at once do it better. With 4 drafts and a draft model, a
+// cluster a sequence / all rows at once took (us) 30 / 31 at 24 sequences and 32 / 44
+// at 32 (128256 columns of bf16), 19 / 16 and 20 / 24 (32000).
+constexpr int64_t kSeqMin = 28;
+int vf_seq_cluster(const ce_verify_params *p) {
+    if (p->n_seqs < kSeqMin) return 0;
+    const int64_t c = 152 * 3 / p->n_seqs;
+    return c > kCluster ? kCluster : (c < 2 ? 2 : static_cast<int>(c));
 }
 
 }  // namespace
@@ -519,8 +1066,9 @@ ce_status ce_verify_drafts(const ce_verify_params *p, const void *logits, const 
     a.temps = temperatures;
     a.temp = p->temperature;
     const int64_t rows = p->n_seqs * (p->n_drafts + 1);
-    a.part_len = vf_part_len(rows, p->vocab, p->dtype);
-    a.parts = static_cast<int>(vf_parts(rows, p->vocab, p->dtype));
+    const VfCut cut = vf_cut(rows, p->vocab, p->dtype);
+    a.parts = static_cast<int>(cut.parts);
+    a.per = cut.per;
     a.px = reinterpret_cast<VfPart *>(ws);
     a.py = a.px + rows * a.parts;
     a.accepted = accepted;
@@ -528,21 +1076,41 @@ ce_status ce_verify_drafts(const ce_verify_params *p, const void *logits, const 
     a.logp = logp;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     using Fn = void (*)(VfArgs);
-    static const Fn stats[3] = {vf_stats_kernel<CE_DT_F32>, vf_stats_kernel<CE_DT_BF16>, vf_stats_kernel<CE_DT_F16>};
+#define CE_STATS(DT) {vf_stats_kernel<DT, 1>, vf_stats_kernel<DT, 2>, vf_stats_kernel<DT, 4>}
+    static const Fn stats[3][3] = {CE_STATS(CE_DT_F32), CE_STATS(CE_DT_BF16), CE_STATS(CE_DT_F16)};
+#undef CE_STATS
     static const Fn picks[3] = {vf_pick_kernel<CE_DT_F32>, vf_pick_kernel<CE_DT_BF16>, vf_pick_kernel<CE_DT_F16>};
+    static const Fn seqs[3] = {vf_seq_kernel<CE_DT_F32>, vf_seq_kernel<CE_DT_BF16>, vf_seq_kernel<CE_DT_F16>};
     void *args[] = {&a};
-    cudaError_t e = cudaLaunchKernel(reinterpret_cast<const void *>(stats[p->dtype]),
-                                     dim3(static_cast<unsigned>(rows * a.parts)), dim3(kThreads), args, 0, s);
-    if (e != cudaSuccess) return cuda_fail(e);
     cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = kCluster;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.gridDim = dim3(static_cast<unsigned>(a.B) * kCluster);
     cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kRing;
     cfg.stream = s;
-    cudaLaunchAttribute at;
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
+    cfg.attrs = at;
+    if (const int c = vf_seq_cluster(p)) {
+        cfg.numAttrs = 1;
+        cfg.gridDim = dim3(static_cast<unsigned>(a.B) * c);
+        at[0].val.clusterDim.x = static_cast<unsigned>(c);
+        cudaError_t e = vf_allow_ring(reinterpret_cast<const void *>(seqs[p->dtype]), p->dtype);
+        if (e == cudaSuccess) e = cudaLaunchKernelExC(&cfg, reinterpret_cast<const void *>(seqs[p->dtype]), args);
+        return e == cudaSuccess ? CE_OK : cuda_fail(e);
+    }
+    const int64_t warps = rows * a.parts;
+    cudaError_t e = vf_allow_ring(reinterpret_cast<const void *>(picks[p->dtype]), 3 + p->dtype);
+    if (e != cudaSuccess) return cuda_fail(e);
+    e = cudaLaunchKernel(reinterpret_cast<const void *>(stats[p->dtype][cut.U >> 1]),
+                                     dim3(static_cast<unsigned>(warps < kStatsWarps ? (warps + kWarps - 1) / kWarps : kStatsWarps / kWarps)),
+                                     dim3(kThreads), args, 0, s);
+    if (e != cudaSuccess) return cuda_fail(e);
+    cfg.numAttrs = 2;
     e = cudaLaunchKernelExC(&cfg, reinterpret_cast<const void *>(picks[p->dtype]), args);
     return e == cudaSuccess ? CE_OK : cuda_fail(e);
 }

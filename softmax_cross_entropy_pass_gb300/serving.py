@@ -60,37 +60,54 @@ _sign()
 
 
 # ---------------------------------------------------------------------- arguments
-def _rows(name, t, shape=None, dtype=None):
-    """The row stride of a 2-D tensor with unit column stride (of a given shape and type)."""
-    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] != 1):
+# (A call's host time is what the smallest calls take: sizes and strides are asked
+# for once, and tensors made here are not checked.)
+def _matrix(name, t):
+    """(rows, columns, row stride) of a 2-D tensor with unit column stride."""
+    shape, strides = t.shape, t.stride()
+    if len(shape) != 2 or (strides[1] != 1 and shape[1] != 1):
         raise ValueError(f"{name} must be a 2-D tensor with unit column stride")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} must have the shape {tuple(shape)}")
-    if dtype is not None and t.dtype is not dtype:
+    return shape[0], shape[1], strides[0] if shape[0] > 1 else shape[1]
+
+
+def _like(name, t, n, cols, dtype):
+    """The row stride of a matrix of the given size and type."""
+    rows, columns, ld = _matrix(name, t)
+    if rows != n or columns != cols:
+        raise ValueError(f"{name} must have the shape ({n}, {cols})")
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    return ld
 
 
-def _rows8(name, t, shape=None):
-    """The row stride of an 8-bit matrix."""
-    ld = _rows(name, t, shape, _E4M3)
-    if t.shape[0] < 2:
-        ld = -(-t.shape[1] // 16) * 16
+def _matrix8(name, t):
+    """The same of an 8-bit matrix, whose rows start at multiples of 16 bytes."""
+    if t.dtype is not _E4M3:
+        raise TypeError(f"{name} must be {_E4M3}")
+    rows, cols, ld = _matrix(name, t)
+    if rows < 2:
+        ld = (cols + 15) // 16 * 16
     if ld % 16 or t.data_ptr() % 16:
         raise ValueError(f"{name}'s rows must start at multiples of 16 bytes")
-    return ld
+    return rows, cols, ld
+
+
+def _out8(call, q, n, cols):
+    """(an 8-bit matrix to write, its row stride): the given one, or a new one."""
+    if q is None:
+        ld = (cols + 15) // 16 * 16
+        q = call.empty(n, ld, dtype=_E4M3)
+        return (q if ld == cols else q[:, :cols]), ld
+    rows, columns, ld = _matrix8("q", q)
+    if rows != n or columns != cols:
+        raise ValueError(f"q must have the shape ({n}, {cols})")
+    return q, ld
 
 
 def _scales(name, t, rows, cols):
     if t.dtype is not _F32 or t.shape != (rows, cols) or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous fp32 tensor [{rows}, {cols}]")
     return t
-
-
-def _new8(call, rows, cols):
-    ld = -(-cols // 16) * 16
-    t = call.empty(rows, ld, dtype=_E4M3)
-    return t if ld == cols else t[:, :cols]
 
 
 def _dtype(name, t):
@@ -109,30 +126,30 @@ def ce_rms_norm_fp8(x, weight, *, residual=None, eps=1e-6, with_residual_out=Tru
     be ``residual`` or ``x`` itself; not formed with ``with_residual_out=False``).
     x, residual: [n, H] bf16, fp16 or fp32; weight: [H] of x's type or fp32.
     One kernel, no workspace."""
-    ld = _rows("x", x)
-    n, cols = x.shape
+    n, cols, ld = _matrix("x", x)
+    dtype = x.dtype
     dt = _dtype("x", x)
     call = _Call(x, (weight, residual, residual_out, q, scale), stream)
-    if weight.dim() != 1 or weight.shape[0] != cols or not weight.is_contiguous() or weight.dtype not in (x.dtype, _F32):
+    wt = weight.dtype
+    if weight.shape != (cols,) or not weight.is_contiguous() or (wt is not dtype and wt is not _F32):
         raise ValueError("weight must be a contiguous tensor of H entries, of x's dtype or fp32")
     ldr = ldo = 0
     if residual is None:
         if residual_out is not None:
             raise ValueError("residual_out given without residual")
     else:
-        ldr = _rows("residual", residual, x.shape, x.dtype)
+        ldr = _like("residual", residual, n, cols, dtype)
         if residual_out is not None:
             if not with_residual_out:
                 raise ValueError("residual_out given with with_residual_out=False")
-            ldo = _rows("residual_out", residual_out, x.shape, x.dtype)
+            ldo = _like("residual_out", residual_out, n, cols, dtype)
         elif with_residual_out:
-            residual_out = call.empty(n, cols, dtype=x.dtype)
+            residual_out = call.empty(n, cols, dtype=dtype)
             ldo = cols
-    q = _new8(call, n, cols) if q is None else q
-    ldq = _rows8("q", q, x.shape)
-    blocks = -(-cols // 128)
+    q, ldq = _out8(call, q, n, cols)
+    blocks = (cols + 127) // 128
     scale = call.empty(n, blocks) if scale is None else _scales("scale", scale, n, blocks)
-    p = ce_norm_params(n, cols, ld, ldr, ldo, ldq, dt, CE_DT[weight.dtype], float(eps), 0)
+    p = ce_norm_params(n, cols, ld, ldr, ldo, ldq, dt, CE_DT[wt], eps, 0)
     call.run("ce_rms_norm_fp8", _byref(p), x.data_ptr(), _ptr(residual), weight.data_ptr(), _ptr(residual_out),
              q.data_ptr(), scale.data_ptr())
     return q, scale, residual_out
@@ -141,15 +158,13 @@ def ce_rms_norm_fp8(x, weight, *, residual=None, eps=1e-6, with_residual_out=Tru
 def ce_quantize_fp8(x, *, block_rows=1, q=None, scale=None, stream=None):
     """(q, scale) of a matrix in 8 bits: ``block_rows`` 1 for activations (a
     scale for every row and 128 columns), 128 for weights (for every 128 x 128)."""
-    ld = _rows("x", x)
-    n, cols = x.shape
+    n, cols, ld = _matrix("x", x)
     dt = _dtype("x", x)
     if block_rows not in (1, 128):
         raise ValueError("block_rows must be 1 or 128")
     call = _Call(x, (q, scale), stream)
-    q = _new8(call, n, cols) if q is None else q
-    ldq = _rows8("q", q, x.shape)
-    up, blocks = -(-n // block_rows), -(-cols // 128)
+    q, ldq = _out8(call, q, n, cols)
+    up, blocks = -(-n // block_rows), (cols + 127) // 128
     scale = call.empty(up, blocks) if scale is None else _scales("scale", scale, up, blocks)
     call.run("ce_quantize_fp8", n, cols, x.data_ptr(), ld, dt, block_rows, q.data_ptr(), ldq, scale.data_ptr())
     return q, scale
@@ -159,23 +174,25 @@ def ce_quantize_fp8(x, *, block_rows=1, q=None, scale=None, stream=None):
 def ce_gemm_fp8(A, a_scale, B, b_scale, *, bias=None, out=None, out_dtype=torch.bfloat16, stream=None):
     """A [M, K] times B^T, B [N, K], both in 8 bits (A in blocks of 1 x 128, B of
     128 x 128), plus bias [N] fp32: [M, N] of ``out_dtype`` or into ``out``."""
-    lda, ldb = _rows8("A", A), _rows8("B", B)
-    (m, k), n = A.shape, B.shape[0]
-    if B.shape[1] != k:
+    (m, k, lda), (n, kb, ldb) = _matrix8("A", A), _matrix8("B", B)
+    if kb != k:
         raise ValueError("inner dimensions differ")
     call = _Call(A, (a_scale, B, b_scale, bias, out), stream)
-    blocks = -(-k // 128)
+    blocks = (k + 127) // 128
     _scales("a_scale", a_scale, m, blocks)
-    _scales("b_scale", b_scale, -(-n // 128), blocks)
+    _scales("b_scale", b_scale, (n + 127) // 128, blocks)
     if bias is not None and (bias.dtype is not _F32 or bias.shape != (n,) or not bias.is_contiguous()):
         raise ValueError("bias must be a contiguous fp32 tensor of N entries")
     if out is None:
-        if out_dtype not in CE_DT:
+        dt = CE_DT.get(out_dtype)
+        if dt is None:
             raise TypeError(f"unsupported out_dtype {out_dtype}")
-        out = call.empty(m, n, dtype=out_dtype)
-    ldd = _rows("out", out, (m, n))
+        out, ldd = call.empty(m, n, dtype=out_dtype), n
+    else:
+        dt = _dtype("out", out)
+        ldd = _like("out", out, m, n, out.dtype)
     call.run("ce_gemm_fp8", m, n, k, A.data_ptr(), lda, a_scale.data_ptr(), B.data_ptr(), ldb, b_scale.data_ptr(),
-             _ptr(bias), _dtype("out", out), out.data_ptr(), ldd)
+             _ptr(bias), dt, out.data_ptr(), ldd)
     return out
 
 
@@ -193,22 +210,13 @@ def fp8_head_logits(x, norm_weight, weight, weight_scale, *, residual=None, eps=
 
 
 # ---------------------------------------------------------------------- verification
-def _logits3(name, t, seqs, rows, vocab, dtype):
-    """(sequence stride, row stride) of logits [seqs, rows, vocab]."""
-    if t.shape != (seqs, rows, vocab) or t.dtype is not dtype or (t.stride(2) != 1 and vocab != 1):
-        raise ValueError(f"{name} must be [{seqs}, {rows}, {vocab}] of the logits' dtype with unit column stride")
-    return t.stride(0) if seqs > 1 else 0, t.stride(1) if rows > 1 else vocab
-
-
 def _verify_ws_bytes(p) -> int:
     out = ctypes.c_size_t()
     _check(_lib.ce_verify_workspace_size(_byref(p), _byref(out)), "ce_verify_workspace_size")
     return out.value
 
 
-def _out(name, t, call, shape, dtype):
-    if t is None:
-        return call.empty(*shape, dtype=dtype)
+def _given(name, t, call, shape, dtype):
     if t.shape != shape or t.dtype is not dtype or not t.is_contiguous() or t.get_device() != call.index:
         raise ValueError(f"{name} must be a contiguous {dtype} tensor {shape} on the logits' device")
     return t
@@ -224,33 +232,43 @@ def ce_verify_drafts(logits, draft_token, accept_uniform, sample_uniform, *, dra
     [0, 1), draft_logits [B, K, V] of the logits' type, or None where the drafts
     were not sampled. ``temperature``: a number, or an fp32 tensor [B]; 0 is
     greedy. K = 0 draws one token a sequence."""
-    if logits.dim() != 3:
+    shape = logits.shape
+    if len(shape) != 3 or shape[1] < 1:
         raise ValueError("logits must be [B, K + 1, V]")
-    B, K, V = logits.shape[0], logits.shape[1] - 1, logits.shape[2]
+    B, rows, V = shape
+    K = rows - 1
+    dtype = logits.dtype
     dt = _dtype("logits", logits)
-    if K < 0:
-        raise ValueError("logits must have at least one row a sequence")
-    if draft_token.dtype is not _I64 and draft_token.dtype is not _I32:
+    tok = draft_token.dtype
+    if tok is not _I64 and tok is not _I32:
         raise TypeError("draft_token must be int64 or int32")
     if draft_token.shape != (B, K) or not draft_token.is_contiguous():
         raise ValueError("draft_token must be a contiguous tensor [B, K]")
-    for name, t, shape in (("accept_uniform", accept_uniform, (B, K)), ("sample_uniform", sample_uniform, (B,))):
-        if t.dtype is not _F32 or t.shape != shape or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous fp32 tensor {shape}")
+    if accept_uniform.dtype is not _F32 or accept_uniform.shape != (B, K) or not accept_uniform.is_contiguous():
+        raise ValueError("accept_uniform must be a contiguous fp32 tensor [B, K]")
+    if sample_uniform.dtype is not _F32 or sample_uniform.shape != (B,) or not sample_uniform.is_contiguous():
+        raise ValueError("sample_uniform must be a contiguous fp32 tensor [B]")
     temps = None
-    if torch.is_tensor(temperature):
+    if isinstance(temperature, torch.Tensor):
         temps, temperature = temperature, 1.0
         if temps.dtype is not _F32 or temps.shape != (B,) or not temps.is_contiguous():
             raise ValueError("temperature must be a number or a contiguous fp32 tensor [B]")
     call = _Call(logits, (draft_token, accept_uniform, sample_uniform, draft_logits, temps), stream)
-    xs, xr = _logits3("logits", logits, B, K + 1, V, logits.dtype)
+    xs, xr, unit = logits.stride()
     ys, yr = 0, V
     if draft_logits is not None:
-        ys, yr = _logits3("draft_logits", draft_logits, B, K, V, logits.dtype)
-    p = ce_verify_params(B, K, V, xs, xr, ys, yr, dt, 1 if draft_token.dtype is _I32 else 0, float(temperature), 0)
-    accepted = _out("accepted", accepted, call, (B,), _I32)
-    tokens = _out("tokens", tokens, call, (B, K + 1), draft_token.dtype)
-    logp = _out("logp", logp, call, (B, K + 1), _F32)
+        if draft_logits.shape != (B, K, V) or draft_logits.dtype is not dtype:
+            raise ValueError("draft_logits must be [B, K, V] of the logits' dtype")
+        ys, yr, unit_y = draft_logits.stride()
+        if unit_y != 1 and V != 1:
+            raise ValueError("draft_logits must have unit column stride")
+        ys, yr = ys if B > 1 else 0, yr if K > 1 else V
+    if unit != 1 and V != 1:
+        raise ValueError("logits must have unit column stride")
+    p = ce_verify_params(B, K, V, xs if B > 1 else 0, xr if K else V, ys, yr, dt, 1 if tok is _I32 else 0, temperature, 0)
+    accepted = call.empty(B, dtype=_I32) if accepted is None else _given("accepted", accepted, call, (B,), _I32)
+    tokens = call.empty(B, rows, dtype=tok) if tokens is None else _given("tokens", tokens, call, (B, rows), tok)
+    logp = call.empty(B, rows) if logp is None else _given("logp", logp, call, (B, rows), _F32)
     ws, nbytes = _workspace(call, ws, _verify_ws_bytes(p))
     call.run("ce_verify_drafts", _byref(p), logits.data_ptr(), _ptr(draft_logits), draft_token.data_ptr(),
              accept_uniform.data_ptr(), sample_uniform.data_ptr(), _ptr(temps), accepted.data_ptr(),
