@@ -228,13 +228,19 @@ __device__ inline bool vf_defined(const VfRow &r) {
     return r.S > 0.f && r.S < INFINITY && fabsf(r.M) < INFINITY && fabsf(r.R) < INFINITY;
 }
 
-// Whether a draft stays: its logits xt, yt in the rows p, q (model: there is a draft model's).
+// log p of a logit x from the row's sum (the same exponent as the sum's terms: R k's rounding cancels)
+__device__ inline float vf_logp_of(float x, const VfRow &p, float k) {
+    return fmaf(x, k, -(p.R * k)) * 0.6931471805599453f - logf(p.S);
+}
+
+// Whether a draft stays, u q_t < p_t: its logits xt, yt in the rows p, q (model: there
+// is a draft model's). In logarithms, so that no probability is too small.
 __device__ inline bool vf_stays(int64_t t, float u, float xt, float yt, const VfRow &p, const VfRow &q, bool model,
                                 bool greedy, float k) {
     if (!vf_defined(p) || !vf_defined(q)) return false;
     if (greedy) return p.at == static_cast<int>(t);
-    const float pt = vf_exp(xt, k, p.R * k), qt = model ? vf_exp(yt, k, q.R * k) : 1.f;
-    return u * qt * p.S < pt * q.S;
+    const float lp = fmaf(xt, k, -(p.R * k)) - log2f(p.S), lq = model ? fmaf(yt, k, -(q.R * k)) - log2f(q.S) : 0.f;
+    return log2f(u) + lq < lp;
 }
 
 // Few sequences: one warp a part of a row, parts dealt out round robin.
@@ -529,7 +535,7 @@ __device__ inline void vf_draw(const VfArgs &a, int b, int n, const VfRow &p, co
         if (t >= 0) {
             const float x = Fmt<DT>::load1(a.x, xrow + t);
             if (S1 || greedy) lp = vf_logp(x, p.M, p.s1, ln2_k);
-            else lp = x == p.M ? -log1pf(m.s1) : (x - p.R) * ln2_k - logf(p.S);
+            else lp = x == p.M ? -log1pf(m.s1) : vf_logp_of(x, p, k);
         }
         vf_put(a, row + n, t, lp);
     };
@@ -936,7 +942,7 @@ __global__ void __launch_bounds__(kThreads, 3) vf_seq_kernel(VfArgs a) {
         if (rank == 0 && tid == 0) {
             float lp;
             if (greedy) lp = vf_logp(xt, p.M, p.s1, ln2_k);
-            else lp = p.R == xt ? -log1pf(p.s1) : (xt - p.R) * ln2_k - logf(p.S);
+            else lp = p.R == xt ? -log1pf(p.s1) : vf_logp_of(xt, p, k);
             vf_put(a, static_cast<int64_t>(b) * (a.K + 1) + n, t, lp);
         }
     }

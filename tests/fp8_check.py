@@ -16,11 +16,13 @@ their kernels are held to (u = 2^-24, half a step of fp32).
   bias round to nearest: (ceil(K / 128) + 3) u. Then half a step of the output's type.
 * Verification. A probability: an exponential (2^-21) of an exponent that is a
   difference, times a rounded constant (3 u |a| ln 2, a = log2 of it), over a sum of
-  such terms, V / 256 + 64 additions in a row at most: rel(V). The decision and
-  the place of the drawn token are checked against the fp64 probabilities with
-  that room on both sides; a log-probability is off by rel(V), and 6 u of its
+  such terms, V / 256 + 64 additions in a row at most: rel(V). The decision
+  (in logarithms) and the place of the drawn token are checked against the fp64
+  probabilities with that room on both sides; a log-probability is off by rel(V), and 6 u of its
   parts |x - M| / T and log s."""
 from __future__ import annotations
+
+import math
 
 import torch
 
@@ -103,6 +105,25 @@ def softmax(z, t):
     return torch.softmax(z.double() / (float(t) if t else 1.0), -1)
 
 
+def logs(z, y, d, u, t):
+    """fp64 (log p, log q, log u) of draft d."""
+    lp = float(torch.log_softmax(z.double() / (t or 1.0), 0)[d])
+    lq = 0.0 if y is None else float(torch.log_softmax(y.double() / (t or 1.0), 0)[d])
+    return lp, lq, math.log(u) if u > 0 else -math.inf
+
+
+def stays_by(z, y, d, u, t):
+    """By how much log u + log q lies below log p (above 0: the draft stays)."""
+    lp, lq, lu = logs(z, y, d, u, t)
+    return -math.inf if lp == -math.inf else lp - lq - lu
+
+
+def room_by(z, y, d, u, t):
+    """What rounding may make of it: rel(V) in either sum, and 8 u of the logarithms' own parts."""
+    size = sum(abs(v) for v in logs(z, y, d, u, t) if math.isfinite(v))
+    return 4 * rel(z.shape[0]) + 8 * U * (size + 64)
+
+
 def check_sequence(z, y, draft, u, r, t, accepted, tokens, logp):
     """One sequence's answer (lists) against fp64: z [K + 1, V], y [K, V] or None, draft [K]."""
     K, V = z.shape[0] - 1, z.shape[1]
@@ -127,13 +148,13 @@ def check_sequence(z, y, draft, u, r, t, accepted, tokens, logp):
             if t == 0:
                 assert draft[i] == best
             else:
-                assert u[i] * float(q[draft[i]]) < float(p[draft[i]]) * (1 + 4 * e)
+                assert stays_by(z[i], None if y is None else y[i], draft[i], u[i], t) > -room_by(z[i], None if y is None else y[i], draft[i], u[i], t)
         else:
             if has:
                 if t == 0:
                     assert draft[i] != best
                 else:
-                    assert u[i] * float(q[draft[i]]) >= float(p[draft[i]]) * (1 - 4 * e)
+                    assert stays_by(z[i], None if y is None else y[i], draft[i], u[i], t) < room_by(z[i], None if y is None else y[i], draft[i], u[i], t)
             tok = tokens[i]
             assert 0 <= tok < V
             if t == 0:
@@ -141,12 +162,19 @@ def check_sequence(z, y, draft, u, r, t, accepted, tokens, logp):
             else:
                 w = (p - q).clamp_min(0) if has else p
                 room = 4 * e * (2.0 if has else 1.0)
-                if float(w.sum()) <= room:
-                    w = p   # nothing, or rounding, is left: either answer
-                total, upto = float(w.sum()), w.cumsum(0)
-                below = float(upto[tok - 1]) if tok else 0.0
-                assert below <= r * total + room and float(upto[tok]) >= r * total - room
-                assert float(w[tok]) > 0 or room >= float(p[tok]) * 1e-3
+
+                def drawn(w):
+                    total, upto = float(w.sum()), w.cumsum(0)
+                    below = float(upto[tok - 1]) if tok else 0.0
+                    return (below <= r * total + room and float(upto[tok]) >= r * total - room
+                            and (float(w[tok]) > 0 or room >= float(p[tok]) * 1e-3))
+                if has and float(w.sum()) <= room:
+                    # max(p - q, 0) adds up to less than what the roundings of p and q may be, e (p + q) in a term:
+                    # where fp32 finds nothing left the draw is p's, else one of the terms that are above 0 within
+                    # those roundings (a sum of true terms may well be as small as this)
+                    assert drawn(p) or float(p[tok] - q[tok]) > -e * float(p[tok] + q[tok])
+                else:
+                    assert drawn(w)
         x = z[i].double()
         s = float((x[x > -float("inf")].max() - x[tokens[i]]) / (t or 1.0)) if tokens[i] >= 0 else 0.0
         want = float(torch.log_softmax(x / (float(t) if t else 1.0), 0)[tokens[i]])

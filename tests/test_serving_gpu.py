@@ -149,6 +149,7 @@ def operands(ce, m, n, k, seed, pad=0):
 
 GEMMS = [
     # M, N, K
+    (70, 1024, 1100), (129, 700, 2064), (40, 500, 5000), (16, 4096, 4096),
     (1, 1, 1), (1, 16, 128), (2, 17, 100), (16, 128, 256), (5, 300, 130), (17, 1000, 520), (32, 129, 4096), (33, 2433, 384),
     (64, 4096, 1024), (65, 515, 777), (100, 20000, 256), (128, 128, 128), (130, 300, 4224), (200, 2500, 640), (300, 1111, 300),
     (1, 50257, 512), (513, 260, 256), (1000, 1000, 1000), (256, 256, 8320), (700, 3000, 200), (4, 152 * 16 + 5, 9000),
@@ -226,11 +227,17 @@ def verify_inputs(B, K, V, dtype, model, seed, pad=0, off=0, temps=None, padded=
     return z, y if model else None, draft.int() if int32 else draft, u, r, 1.0 if temps is None else temps
 
 
+def many(times, *tensors):
+    """The batch several times over: from 28 sequences on another kernel verifies them."""
+    return tuple(t.repeat(times, *[1] * (t.dim() - 1)) if torch.is_tensor(t) else t for t in tensors)
+
+
 VERIFIES = [
     # B, K, V, padding, first column
     (1, 0, 1, 0, 0), (3, 2, 2, 0, 0), (2, 1, 7, 0, 0), (5, 3, 257, 0, 0), (4, 4, 1000, 0, 0), (2, 3, 4099, 3, 1),
     (9, 0, 5000, 0, 0), (1, 3, 128256, 0, 0), (3, 2, 50257, 0, 0), (40, 5, 3001, 7, 8), (2, 20, 300, 0, 0),
-    (150, 3, 2050, 0, 0), (2, 1, 300001, 0, 0),
+    (150, 3, 2050, 0, 0), (2, 1, 300001, 0, 0), (28, 0, 3, 0, 0), (29, 2, 8200, 0, 0), (33, 1, 9, 7, 3), (60, 3, 20011, 5, 1),
+    (27, 4, 6000, 8, 8), (100, 1, 40000, 0, 0), (230, 6, 1000, 0, 0),
 ]
 
 
@@ -250,8 +257,10 @@ def test_verify(ce, shape, dtype, model):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-def test_verify_all_stay_or_none(ce, dtype):
+@pytest.mark.parametrize("times", [1, 6])
+def test_verify_all_stay_or_none(ce, dtype, times):
     z, _, draft, u, r, _ = verify_inputs(6, 4, 5000, dtype, False, 8, padded=False)
+    z, draft, u, r = many(times, z, draft, u, r)
     y = z[:, :4].clone()
     # the draft model is the target: every draft stays, whatever u
     got = ce.ce_verify_drafts(z, draft, u, r, draft_logits=y)
@@ -268,19 +277,22 @@ def test_verify_all_stay_or_none(ce, dtype):
     assert got[0].tolist() == [1, 0] and got[1].tolist() == [[5, 0], [0, -1]]
 
 
-def test_verify_greedy_ties_take_the_lowest_index(ce):
+@pytest.mark.parametrize("times", [1, 10])
+def test_verify_greedy_ties_take_the_lowest_index(ce, times):
     for V in (64, 5003, 131072):
         z = torch.zeros(3, 3, V, device="cuda", dtype=torch.bfloat16)
         z[0, :, 9] = z[0, :, V - 1] = z[0, :, V // 2] = 4.0
         z[1, :, V - 2] = z[1, :, V - 1] = 4.0
         z[2, 0, 3] = 1.0
         draft = torch.tensor([[9, V - 1], [V - 2, V - 2], [3, 1]], device="cuda")
-        got = ce.ce_verify_drafts(z, draft, torch.rand(3, 2, device="cuda"), torch.rand(3, device="cuda"), temperature=0.0)
-        assert got[0].tolist() == [1, 2, 1]
-        assert got[1].tolist() == [[9, 9, -1], [V - 2, V - 2, V - 2], [3, 0, -1]]
+        z, draft = many(times, z, draft)
+        got = ce.ce_verify_drafts(z, draft, torch.rand(3 * times, 2, device="cuda"), torch.rand(3 * times, device="cuda"), temperature=0.0)
+        assert got[0].tolist() == [1, 2, 1] * times
+        assert got[1].tolist() == [[9, 9, -1], [V - 2, V - 2, V - 2], [3, 0, -1]] * times
 
 
-def test_verify_masks(ce):
+@pytest.mark.parametrize("times", [1, 4])
+def test_verify_masks(ce, times):
     """Most of the vocabulary masked (-inf, the type's lowest value), rows with one value left, equal rows."""
     for dtype, low in (("bf16", -math.inf), ("f32", -math.inf), ("bf16", float(torch.finfo(torch.bfloat16).min)),
                        ("f32", float(torch.finfo(torch.float32).min)), ("f16", -65504.0)):
@@ -293,6 +305,7 @@ def test_verify_masks(ce):
         draft = (draft % 100)
         draft[1] += 4000
         draft[3] = 77
+        z, y, draft, u, r = many(times, z, y, draft, u, r)
         got = ce.ce_verify_drafts(z, draft, u, r, draft_logits=y)
         F.check_verify(z, y, draft.cpu(), u.cpu(), r.cpu(), 1.0, got)
         assert got[0][3] == 3 and (got[1][3] == 77).all() and (got[2][3] == 0).all()
@@ -300,7 +313,8 @@ def test_verify_masks(ce):
         F.check_verify(z, None, draft.cpu(), u.cpu(), r.cpu(), 1.0, got)
 
 
-def test_verify_undefined_rows(ce):
+@pytest.mark.parametrize("times", [1, 4])
+def test_verify_undefined_rows(ce, times):
     """A row with nothing left, a NaN or +inf ends its sequence with -1; rows behind the decision may hold anything."""
     z, y, draft, u, r, _ = verify_inputs(9, 2, 3000, "bf16", True, 31, padded=False)
     y.copy_(z[:, :2])                      # all drafts stay where the rows allow it
@@ -315,12 +329,14 @@ def test_verify_undefined_rows(ce):
     y[6, 1] = math.nan
     temps = torch.ones(9, device="cuda")
     temps[7], temps[8] = -1.0, math.nan
+    z, y, draft, u, r, temps = many(times, z, y, draft, u, r, temps)
     n, tok, lp = (v.tolist() for v in ce.ce_verify_drafts(z, draft, u, r, draft_logits=y, temperature=temps))
-    assert n == [0, 1, 2, 0, 1, 0, 1, 0, 0]
-    for b in (0, 1, 2, 3, 4, 7, 8):
+    assert n == [0, 1, 2, 0, 1, 0, 1, 0, 0] * times
+    at = [9 * i for i in range(times)]
+    for b in [i + j for i in (0, 1, 2, 3, 4, 7, 8) for j in at]:
         assert tok[b][n[b]] == -1 and math.isnan(lp[b][n[b]]) and all(t == -1 for t in tok[b][n[b]:])
         assert all(v == 0 for v in lp[b][n[b] + 1:])
-    for b in (5, 6):
+    for b in [i + j for i in (5, 6) for j in at]:
         assert 0 <= tok[b][n[b]] < 3000 and math.isfinite(lp[b][n[b]])
     greedy = ce.ce_verify_drafts(z, draft, u, r, draft_logits=y, temperature=0.0)
     assert greedy[1][0, 0] == -1 and greedy[0][0] == 0
@@ -332,6 +348,42 @@ def test_verify_ends_of_the_random_numbers(ce):
         r = torch.full((64,), v, device="cuda")
         got = ce.ce_verify_drafts(z, draft, u, r, draft_logits=y)
         F.check_verify(z, y, draft.cpu(), u.cpu(), r.cpu(), 1.0, got)
+
+
+@pytest.mark.parametrize("B", [5, 40])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_verify_far_logits(ce, B, dtype):
+    """Drafts far below the row's maximum, maxima far from 0, low and high temperatures: references that do not hold
+    the row's terms."""
+    z, y, draft, u, r, _ = verify_inputs(B, 3, 7000, dtype, True, 91, padded=False)
+    z[:, 0] += 300.0
+    y[:, 1] -= 500.0
+    rows = torch.arange(B, device="cuda")
+    z[rows[::3], 1, draft[::3, 1]] = -200.0            # turned down: its probability is 0 in fp32
+    y[rows[::4], 0, draft[::4, 0]] = -150.0            # a draft that its own model would hardly draw stays
+    z[1, 2], y[1, 2] = -3e4, -3e4
+    z[1, 2, 17] = 3e4
+    for t in (1.0, 0.05, 30.0):
+        got = ce.ce_verify_drafts(z, draft, u, r, draft_logits=y, temperature=t)
+        # 3 u |a| of an exponent relative to the reference or the maximum, |a| up to 60
+        F.check_verify(z, y, draft.cpu(), u.cpu(), r.cpu(), t, got)
+        F.check_verify(z, None, draft.cpu(), u.cpu(), r.cpu(), t, ce.ce_verify_drafts(z, draft, u, r, temperature=t))
+
+
+@pytest.mark.parametrize("B", [3, 32])
+def test_verify_likely_tokens(ce, B):
+    """log p of tokens with probabilities near 1 keeps its relative precision, staying, greedy or drawn."""
+    z = torch.randn(B, 2, 9000, generator=gen(95), device="cuda")
+    tops = 9.0 + 8.0 * torch.rand(B, 2, generator=gen(96), device="cuda") + 9.0
+    z[:, :, 4321] = tops
+    draft = torch.full((B, 1), 4321, device="cuda")
+    u, r = torch.zeros(B, 1, device="cuda"), torch.full((B,), 0.5, device="cuda")
+    for t in (1.0, 0.0):
+        n, tok, lp = ce.ce_verify_drafts(z, draft, u, r, temperature=t)
+        assert (n == 1).all() and (tok == 4321).all()
+        want = torch.log_softmax(z.double(), 2)[:, :, 4321]
+        # -log1p(s): s is off by rel(V), log1p by its own rounding; s itself is below 0.02 here
+        assert ((lp.double() - want).abs() <= want.abs() * (F.rel(9000) + 4 * F.U)).all()
 
 
 def test_verify_strides_and_buffers(ce):
