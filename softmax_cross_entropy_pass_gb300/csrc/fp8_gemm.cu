@@ -16,8 +16,8 @@
 // where that share would be less than half a tile, a cluster of up to eight CTAs
 // takes one tile, each a part of K, and adds the parts up through distributed
 // shared memory, in the order of the ranks (a K block's copies, MMAs and epilogue
-// follow one another in 0.3 us whatever the rows: 64 x 4096 x 4096 took 14.9 us
-// in 32 such steps).
+// follow one another in 0.3 us whatever the rows: 64 x 4096 x 4096 took 14.9 us in
+// 32 such steps, 11.1 in a cluster's 8).
 #include <atomic>
 
 #include "ce_device.cuh"
@@ -317,9 +317,17 @@ __device__ inline void st_sector(void *p, const uint4 &a, const uint4 &b) {
 template <int DT>
 __device__ inline void store_cols(const Fp8Args &g, int row, int c, float (&x)[16], bool bad) {
     if (g.bias) {
+        if (c + 16 <= g.n && (reinterpret_cast<uintptr_t>(g.bias) & 15u) == 0) {
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
-            if (c + j < g.n) x[j] += __ldg(g.bias + c + j);
+            for (int j = 0; j < 4; ++j) {
+                const float4 b = __ldg(reinterpret_cast<const float4 *>(g.bias + c) + j);
+                x[4 * j] += b.x; x[4 * j + 1] += b.y; x[4 * j + 2] += b.z; x[4 * j + 3] += b.w;
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                if (c + j < g.n) x[j] += __ldg(g.bias + c + j);
+        }
     }
     if (bad) {
 #pragma unroll
@@ -351,7 +359,7 @@ __device__ inline void store_staged(const Fp8Args &g, int row0, int c, const F2 
         const float bias = g.bias ? __ldg(g.bias + col) : 0.f;
         const int64_t at = static_cast<int64_t>(row0) * g.ldo + col;
         if (row0 + 32 <= g.m && !bad) {
-#pragma unroll
+#pragma unroll 4
             for (int r = 0; r < 32; ++r) store_out<DT>(g.out, at + r * g.ldo, g.bias ? stage[r * 33 + lane] + bias : stage[r * 33 + lane]);
         } else {
             for (int r = 0; r < min(32, g.m - row0); ++r)
@@ -378,7 +386,7 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     const uint32_t sA = base, sB = base + kPairStages * kPairHalf;
     volatile int *abort = &abort_flag;
     const int tiles_m = (g.m + kPairM - 1) / kPairM;
-    const int64_t tiles = static_cast<int64_t>(tiles_m) * ((g.n + kPairN - 1) / kPairN);
+    const int tiles = tiles_m * ((g.n + kPairN - 1) / kPairN);
 
     if (tid == 0) {
         for (int st = 0; st < kPairStages; ++st) {
@@ -410,9 +418,9 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         if (warp == 0 && elect_one()) {
             // ------------------------------------------------ TMA producer (both CTAs)
             uint32_t s = 0, round = 0;
-            for (int64_t t = cid; t < tiles; t += ncl) {
-                const int row0 = static_cast<int>(t % tiles_m) * kPairM + static_cast<int>(rank) * 128;
-                const int col0 = static_cast<int>(t / tiles_m) * kPairN + static_cast<int>(rank) * 128;
+            for (int t = cid; t < tiles; t += ncl) {
+                const int row0 = t % tiles_m * kPairM + static_cast<int>(rank) * 128;
+                const int col0 = t / tiles_m * kPairN + static_cast<int>(rank) * 128;
                 for (int kb = 0; kb < g.kblocks; ++kb) {
                     if (round > 0) mbar_wait_polled(smem_u32(&empty[s]), (round - 1) & 1u, abort);
                     const uint32_t fb = mapa_shared(smem_u32(&full[s]), 0);  // the even CTA's barrier
@@ -438,7 +446,7 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             // ------------------------------------------------ MMA issuer (even CTA): one accumulator a K block
             const uint32_t idesc = idesc_e4m3_f32(kPairM, kPairN);
             uint32_t s = 0, phase = 0, unit = 0;
-            for (int64_t t = cid; t < tiles; t += ncl)
+            for (int t = cid; t < tiles; t += ncl)
                 for (int kb = 0; kb < g.kblocks; ++kb, ++unit) {
                     const uint32_t acc = unit & 1u, u = unit >> 1;
                     mbar_wait_polled(smem_u32(&full[s]), phase, abort);
@@ -461,12 +469,11 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPairEpiRegs));
         const int q = warp & 3, half = (warp - 4) >> 2;
         const int et = tid - 128;
-        float *stage = scales + 2 * kPairChunk * kPairRow + (warp - 4) * kPairStage;
         const uint32_t tempty0 = mapa_shared(smem_u32(&tempty[0]), 0);
         const uint32_t lane_addr = tmem + (static_cast<uint32_t>(q * 32) << 16) + half * 128;
         // scales of A of this CTA's 128 rows of tile t, K blocks k0 .. k0 + 31, into buffer `buf` (rows past the last: its)
-        const auto fetch = [&](int64_t t, int k0, int buf) {
-            const int row0 = static_cast<int>(t % tiles_m) * kPairM + static_cast<int>(rank) * 128;
+        const auto fetch = [&](int t, int k0, int buf) {
+            const int row0 = t % tiles_m * kPairM + static_cast<int>(rank) * 128;
             const int nb = min(kPairChunk, g.kblocks - k0), kb = et & 31;
             const uint32_t dst = smem_u32(scales + buf * kPairChunk * kPairRow + kb * kPairRow);
             if (kb < nb) {
@@ -479,9 +486,9 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         };
         uint32_t unit = 0, chunk = 0;  // K blocks and chunks of scales so far
         if (cid < tiles) fetch(cid, 0, 0);
-        for (int64_t t = cid; t < tiles; t += ncl) {
-            const int row = static_cast<int>(t % tiles_m) * kPairM + static_cast<int>(rank) * 128 + q * 32 + lane;
-            const int col0 = static_cast<int>(t / tiles_m) * kPairN + half * 128;
+        for (int t = cid; t < tiles; t += ncl) {
+            const int row = t % tiles_m * kPairM + static_cast<int>(rank) * 128 + q * 32 + lane;
+            const int col0 = t / tiles_m * kPairN + half * 128;
             // columns past the last are multiplied like it, and not stored
             const float *sb = g.b_scale + static_cast<int64_t>(min(col0, g.n - 1) / kFp8Block) * g.kblocks;
             F2 acc[64];
@@ -500,7 +507,7 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                     // halfway: the next chunk's, of this tile or the next
                     const int k1 = kb - k0 + kPairChunk;
                     if (k1 < g.kblocks) fetch(t, k1, chunk & 1u);
-                    else if (t + ncl < tiles) fetch(t + ncl, 0, chunk & 1u);
+                    else if (t < tiles - ncl) fetch(t + ncl, 0, chunk & 1u);
                 }
                 const float w1 = scales[((chunk - 1) & 1u) * kPairChunk * kPairRow + k0 * kPairRow + q * 32 + lane] * next;
                 const F2 w = f2(w1, w1);
@@ -509,28 +516,53 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 mbar_wait_polled(smem_u32(&tfull[a]), (unit >> 1) & 1u, abort);
                 tc_fence_after();
                 const uint32_t taddr = lane_addr + a * kPairN;
-                // 96 columns at once, the last 32 while others are added: all 128 would not fit beside the sums
-                uint32_t v[3][32];
-                const auto add = [&](const uint32_t (&x)[32], int at) {
+                const auto add = [&](const uint32_t *x, int n, int at) {
 #pragma unroll
                     for (int j = 0; j < 16; ++j)
-                        acc[at + j] = f2_fma(f2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])), w, acc[at + j]);
+                        if (j < n / 2)
+                            acc[at / 2 + j] = f2_fma(f2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])), w, acc[at / 2 + j]);
                 };
-                tmem_ld_32x32b_x32(taddr, v[0]);
-                tmem_ld_32x32b_x32(taddr + 32, v[1]);
-                tmem_ld_32x32b_x32(taddr + 64, v[2]);
-                tmem_ld_wait(v[0]);
-                tmem_ld_wait(v[1]);
-                tmem_ld_wait(v[2]);
-                add(v[0], 0);
-                tmem_ld_32x32b_x32(taddr + 96, v[0]);
-                add(v[1], 16);
-                tmem_ld_wait(v[0]);
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_relaxed(tempty0 + a * 8u);
-                add(v[2], 32);
-                add(v[0], 48);
+                const auto give_back = [&] {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_relaxed(tempty0 + a * 8u);
+                };
+                // As many columns at once as fit beside the sums (all 128 do not), the others while those are added.
+                // With 80 at once a K block takes 5% longer; with 96 the staged store's registers spill, 7%.
+                if constexpr (!STAGED) {
+                    uint32_t v0[32], v1[32], v2[32];
+                    tmem_ld_32x32b_x32(taddr, v0);
+                    tmem_ld_32x32b_x32(taddr + 32, v1);
+                    tmem_ld_32x32b_x32(taddr + 64, v2);
+                    tmem_ld_wait(v0);
+                    tmem_ld_wait(v1);
+                    tmem_ld_wait(v2);
+                    add(v0, 32, 0);
+                    tmem_ld_32x32b_x32(taddr + 96, v0);
+                    add(v1, 32, 32);
+                    tmem_ld_wait(v0);
+                    give_back();
+                    add(v2, 32, 64);
+                    add(v0, 32, 96);
+                } else {
+                    uint32_t v0[32], v1[32], v2[16];
+                    tmem_ld_32x32b_x32(taddr, v0);
+                    tmem_ld_32x32b_x16(taddr + 32, v2);
+                    tmem_ld_32x32b_x32(taddr + 48, v1);
+                    tmem_ld_wait(v0);
+                    tmem_ld_wait(v1);
+                    tmem_ld_wait(v2);
+                    add(v0, 32, 0);
+                    tmem_ld_32x32b_x32(taddr + 80, v0);
+                    add(v2, 16, 32);
+                    tmem_ld_32x32b_x16(taddr + 112, v2);
+                    tmem_ld_wait(v0);
+                    tmem_ld_wait(v2);
+                    give_back();
+                    add(v1, 32, 48);
+                    add(v0, 32, 80);
+                    add(v2, 16, 112);
+                }
             }
             const bool bad = *abort != 0;  // a wait that gave up leaves no result
             if (!STAGED) {
@@ -546,7 +578,7 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             } else {
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
-                    if (col0 + c * 32 < g.n && row - lane < g.m) store_staged<DT>(g, row - lane, col0 + c * 32, acc + c * 16, stage, bad);
+                    if (col0 + c * 32 < g.n && row - lane < g.m) store_staged<DT>(g, row - lane, col0 + c * 32, acc + c * 16, scales + 2 * kPairChunk * kPairRow + ((threadIdx.x >> 5) - 4) * kPairStage, bad);
             }
         }
     }
@@ -661,6 +693,7 @@ cudaError_t launch_pair(const void *A, int64_t lda, const void *B, int64_t ldb, 
     int clusters = pair_clusters(fn, STAGED, dev);
     if (clusters < 1) clusters = kSms / 2;
     const int64_t tiles = static_cast<int64_t>((g.m + kPairM - 1) / kPairM) * ((g.n + kPairN - 1) / kPairN);
+    if (tiles > INT32_MAX - 1024) return cudaErrorInvalidValue;
     if (clusters > tiles) clusters = static_cast<int>(tiles);
     void *args[] = {&ta, &tb, &g};
     cudaLaunchConfig_t cfg = {};
@@ -678,11 +711,20 @@ cudaError_t launch_pair(const void *A, int64_t lda, const void *B, int64_t ldb, 
     return cudaLaunchKernelExC(&cfg, fn, args);
 }
 
+// Which kernel: up to 64 rows of A the weights are read at HBM's rate by the first.
+// Above, pairs of CTAs, except where the first kernel's tiles of 128 x 64 fill at
+// most half the SMs, so that clusters can split K. First / pairs (us, with a cold
+// L2): 65 x 128256 x 4096 182 / 119, 129 x 14336 x 4096 47 / 27, 300 x 4096 x 4096
+// 35 / 24, 65 x 4096 x 4096 23 / 23, 300 x 1024 x 8192 27 / 35, 1024 x 1024 x 8192 37 / 35.
+bool fp8_takes_pairs(int m, int n) {
+    return m > 64 && static_cast<int64_t>((n + kFewM - 1) / kFewM) * ((m + 63) / 64) * 2 > kSms;
+}
+
 enum { FP8_AUTO = 0, FP8_FEW = 1, FP8_PAIR = 2 };
 
 cudaError_t fp8_gemm(const void *A, int64_t lda, const void *B, int64_t ldb, const Fp8Args &g, int dtype, int mode,
                      cudaStream_t s) {
-    if (mode == FP8_PAIR || (mode == FP8_AUTO && g.m > 64)) {
+    if (mode == FP8_PAIR || (mode == FP8_AUTO && fp8_takes_pairs(g.m, g.n))) {
         const int esz = fp8_elem(dtype);
         const bool staged = ((reinterpret_cast<uintptr_t>(g.out) | static_cast<uintptr_t>(g.m > 1 ? g.ldo * esz : 0)) & 31u) != 0;
         using Fn = cudaError_t (*)(const void *, int64_t, const void *, int64_t, Fp8Args, cudaStream_t);
