@@ -296,14 +296,15 @@ constexpr int kPairEpi = 256;
 // warpgroups take 232 and the first keeps 40 (2 x 128 x 232 + 128 x 40 = 384 x 168)
 constexpr int kPairThreads = 128 + kPairEpi;
 constexpr int kPairLaunchRegs = 168, kPairEpiRegs = 232, kPairFirstRegs = 40;
+static_assert(kPairEpi == kPairN, "a column's bias a thread");
 static_assert(kPairEpi * kPairEpiRegs + 128 * kPairFirstRegs <= kPairThreads * kPairLaunchRegs, "registers of the launch");
 constexpr int kPairChunk = 32;              // K blocks whose scales of A are in shared memory
 constexpr int kPairRow = 129;               // floats of one K block's scales: another bank for each block
 constexpr int kPairStage = 32 * 33;         // floats: 32 x 32 sums of an epilogue warp on their way out
-constexpr int pair_stages(bool staged) { return staged ? 5 : 6; }
+constexpr int kPairStages = 5;
 constexpr int pair_smem(bool staged) {
-    return 1024 + pair_stages(staged) * 2 * kPairHalf + 2 * kPairChunk * kPairRow * 4 +
-           (staged ? kPairEpi / 32 * kPairStage * 4 : 0);
+    return 1024 + kPairStages * 2 * kPairHalf + 2 * kPairChunk * kPairRow * 4 +
+           (staged ? kPairEpi / 32 * kPairStage : kPairN) * 4;
 }
 constexpr uint32_t kPairTmemCols = 512;
 
@@ -315,18 +316,12 @@ __device__ inline void st_sector(void *p, const uint4 &a, const uint4 &b) {
 
 // 16 consecutive columns of one row from column c on; rows start on whole sectors
 template <int DT>
-__device__ inline void store_cols(const Fp8Args &g, int row, int c, float (&x)[16], bool bad) {
+__device__ inline void store_cols(const Fp8Args &g, int row, int c, float (&x)[16], const float *bias, bool bad) {
     if (g.bias) {
-        if (c + 16 <= g.n && (reinterpret_cast<uintptr_t>(g.bias) & 15u) == 0) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float4 b = __ldg(reinterpret_cast<const float4 *>(g.bias + c) + j);
-                x[4 * j] += b.x; x[4 * j + 1] += b.y; x[4 * j + 2] += b.z; x[4 * j + 3] += b.w;
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-                if (c + j < g.n) x[j] += __ldg(g.bias + c + j);
+        for (int j = 0; j < 4; ++j) {
+            const float4 b = *reinterpret_cast<const float4 *>(bias + 4 * j);
+            x[4 * j] += b.x; x[4 * j + 1] += b.y; x[4 * j + 2] += b.z; x[4 * j + 3] += b.w;
         }
     }
     if (bad) {
@@ -373,7 +368,6 @@ __device__ inline void store_staged(const Fp8Args &g, int row0, int c, const F2 
 template <int DT, bool STAGED>
 __global__ void __launch_bounds__(kPairThreads, 1)
 fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, Fp8Args g) {
-    constexpr int kPairStages = pair_stages(STAGED);
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t full[kPairStages], empty[kPairStages], tfull[kPairAcc], tempty[kPairAcc];
     __shared__ uint32_t tmem_slot;
@@ -383,6 +377,7 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     const int cid = static_cast<int>(cluster_id_x()), ncl = static_cast<int>(nclusters_x());
     const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;  // the same offsets in both CTAs of the pair
     float *scales = reinterpret_cast<float *>(smem_raw + (base - raw) + kPairStages * 2 * kPairHalf);
+    float *extra = scales + 2 * kPairChunk * kPairRow;  // the bias of this tile's columns; STAGED: the warps' sums on their way out
     const uint32_t sA = base, sB = base + kPairStages * kPairHalf;
     volatile int *abort = &abort_flag;
     const int tiles_m = (g.m + kPairM - 1) / kPairM;
@@ -502,6 +497,10 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                     asm volatile("cp.async.wait_all;" ::: "memory");
                     asm volatile("bar.sync 1, %0;" ::"n"(kPairEpi) : "memory");
                     ++chunk;
+                    // the tile's bias, for its end (all warps have added the last one's)
+                    const int c = t / tiles_m * kPairN + et;
+                    if (!STAGED && kb == 0 && g.bias && c < g.n)
+                        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(extra + et)), "l"(g.bias + c) : "memory");
                 }
                 if (k0 == min(kPairChunk, g.kblocks - (kb - k0)) / 2) {
                     // halfway: the next chunk's, of this tile or the next
@@ -564,6 +563,10 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                     add(v2, 16, 112);
                 }
             }
+            if (!STAGED && g.bias) {
+                asm volatile("cp.async.wait_all;" ::: "memory");
+                asm volatile("bar.sync 1, %0;" ::"n"(kPairEpi) : "memory");
+            }
             const bool bad = *abort != 0;  // a wait that gave up leaves no result
             if (!STAGED) {
                 if (row < g.m) {
@@ -572,13 +575,14 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                         float x[16];
 #pragma unroll
                         for (int j = 0; j < 8; ++j) f2_split(acc[c * 8 + j], x[2 * j], x[2 * j + 1]);
-                        if (col0 + c * 16 < g.n) store_cols<DT>(g, row, col0 + c * 16, x, bad);
+                        if (col0 + c * 16 < g.n) store_cols<DT>(g, row, col0 + c * 16, x, extra + half * 128 + c * 16, bad);
                     }
                 }
             } else {
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
-                    if (col0 + c * 32 < g.n && row - lane < g.m) store_staged<DT>(g, row - lane, col0 + c * 32, acc + c * 16, scales + 2 * kPairChunk * kPairRow + ((threadIdx.x >> 5) - 4) * kPairStage, bad);
+                    if (col0 + c * 32 < g.n && row - lane < g.m)
+                        store_staged<DT>(g, row - lane, col0 + c * 32, acc + c * 16, extra + (warp - 4) * kPairStage, bad);
             }
         }
     }
