@@ -998,27 +998,58 @@ size_t vf_bytes(const ce_verify_params *p) {
 }
 
 // the shared-memory limit is a per-device attribute of each kernel: set once per device
-cudaError_t vf_allow_ring(const void *fn, int which) {
+cudaError_t vf_allow_ring(const void *fn, int which, int dev) {
     static std::atomic<uint64_t> done[6];
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
     const uint64_t bit = dev < 64 ? (1ull << dev) : 0ull;
     if (bit && (done[which].load() & bit)) return cudaSuccess;
-    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kRing);
+    const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kRing);
     if (e == cudaSuccess) done[which].fetch_or(bit);
     return e;
 }
 
-// CTAs a sequence where a cluster a sequence fills the GPU (three CTAs an SM), 0 where
-// the rows of all positions at once do it better. With 4 drafts and a draft model, a
-// cluster a sequence / all rows at once took (us) 30 / 31 at 24 sequences and 32 / 44
-// at 32 (128256 columns of bf16), 19 / 16 and 20 / 24 (32000).
-constexpr int64_t kSeqMin = 28;
-int vf_seq_cluster(const ce_verify_params *p) {
-    if (p->n_seqs < kSeqMin) return 0;
-    const int64_t c = 152 * 3 / p->n_seqs;
-    return c > kCluster ? kCluster : (c < 2 ? 2 : static_cast<int>(c));
+// Clusters of c CTAs that are resident at once (asked once a device): a cluster lies within one of the GPU's
+// partitions, so that fewer fit than the SMs' room says.
+int vf_resident(const void *fn, int which, int dev, int c) {
+    constexpr int kDevs = 64;
+    static std::atomic<int> known[6][kDevs][kCluster + 1];
+    int n = 0;
+    if (dev < kDevs && (n = known[which][dev][c].load()) > 0) return n;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = static_cast<unsigned>(c);
+    at.val.clusterDim.y = 1;
+    at.val.clusterDim.z = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(c) * 64);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kRing;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess || n < 1) n = 1;
+    (void)cudaGetLastError();
+    if (dev < kDevs) known[which][dev][c].store(n);
+    return n;
+}
+
+// CTAs a sequence: as many as let all sequences run at once, two at least (64 sequences of 2 drafts, 128256 columns of
+// bf16: 26 us with clusters of 6, 36 with clusters of 7, some of which wait for a second wave). The clusters that start
+// while the statistics are still being formed want more room: half of it again (32 sequences of 6 drafts, 32000 bf16
+// logits: 19 us with clusters of 5, 26 with clusters of 8, of which the device would hold 36).
+int vf_cluster(const void *fn, int which, int dev, int64_t seqs) {
+    int c = kCluster;
+    while (c > 2 && vf_resident(fn, which, dev, c) < (which < 3 ? seqs : seqs * 3 / 2)) --c;
+    return c;
+}
+
+// Whether the rows of all positions are read at once: where one position's rows, of all sequences and both models, are
+// few enough that reading them takes less than the steps that a cluster a sequence takes from a position to the next. All
+// at once / a cluster a sequence (us, 6 drafts): 48 sequences of 32000 bf16 logits (3 MB a position) 18 / 25, of 50257
+// fp32 (10 MB) 32 / 32, of 128256 bf16 with a draft model (23 MB) 63 / 49; over 168 sizes of 1 to 200 sequences, 0 to 6
+// drafts the rule's choice is 1% slower than the better one.
+constexpr int64_t kAtOnce = int64_t(8) << 20;
+bool vf_at_once(const VfArgs &a, int esz) {
+    const int64_t rows = static_cast<int64_t>(a.B) * (a.K + 1 + (a.y ? a.K : 0));
+    return rows * a.V * esz <= kAtOnce * (a.K + 1);
 }
 
 }  // namespace
@@ -1091,33 +1122,34 @@ ce_status ce_verify_drafts(const ce_verify_params *p, const void *logits, const 
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = kCluster;
     at[0].val.clusterDim.y = 1;
     at[0].val.clusterDim.z = 1;
     at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(static_cast<unsigned>(a.B) * kCluster);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = kRing;
     cfg.stream = s;
     cfg.attrs = at;
-    if (const int c = vf_seq_cluster(p)) {
-        cfg.numAttrs = 1;
-        cfg.gridDim = dim3(static_cast<unsigned>(a.B) * c);
-        at[0].val.clusterDim.x = static_cast<unsigned>(c);
-        cudaError_t e = vf_allow_ring(reinterpret_cast<const void *>(seqs[p->dtype]), p->dtype);
-        if (e == cudaSuccess) e = cudaLaunchKernelExC(&cfg, reinterpret_cast<const void *>(seqs[p->dtype]), args);
-        return e == cudaSuccess ? CE_OK : cuda_fail(e);
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_fail(e);
+    const bool seq = !vf_at_once(a, esz);
+    const void *fn = reinterpret_cast<const void *>(seq ? seqs[p->dtype] : picks[p->dtype]);
+    const int which = seq ? p->dtype : 3 + p->dtype;
+    e = vf_allow_ring(fn, which, dev);
+    if (e != cudaSuccess) return cuda_fail(e);
+    const int c = vf_cluster(fn, which, dev, p->n_seqs);
+    at[0].val.clusterDim.x = static_cast<unsigned>(c);
+    cfg.gridDim = dim3(static_cast<unsigned>(a.B) * c);
+    cfg.numAttrs = seq ? 1 : 2;
+    if (!seq) {
+        const int64_t warps = rows * a.parts;
+        e = cudaLaunchKernel(reinterpret_cast<const void *>(stats[p->dtype][cut.U >> 1]),
+                             dim3(static_cast<unsigned>(warps < kStatsWarps ? (warps + kWarps - 1) / kWarps : kStatsWarps / kWarps)),
+                             dim3(kThreads), args, 0, s);
+        if (e != cudaSuccess) return cuda_fail(e);
     }
-    const int64_t warps = rows * a.parts;
-    cudaError_t e = vf_allow_ring(reinterpret_cast<const void *>(picks[p->dtype]), 3 + p->dtype);
-    if (e != cudaSuccess) return cuda_fail(e);
-    e = cudaLaunchKernel(reinterpret_cast<const void *>(stats[p->dtype][cut.U >> 1]),
-                                     dim3(static_cast<unsigned>(warps < kStatsWarps ? (warps + kWarps - 1) / kWarps : kStatsWarps / kWarps)),
-                                     dim3(kThreads), args, 0, s);
-    if (e != cudaSuccess) return cuda_fail(e);
-    cfg.numAttrs = 2;
-    e = cudaLaunchKernelExC(&cfg, reinterpret_cast<const void *>(picks[p->dtype]), args);
+    e = cudaLaunchKernelExC(&cfg, fn, args);
     return e == cudaSuccess ? CE_OK : cuda_fail(e);
 }
 
