@@ -11,21 +11,26 @@
 // 2^((x - M) k), k = log2(e) / T. Exponents are formed by the difference x - M first,
 // so that equal logits have equal probabilities wherever in the row they lie.
 //
-// Many sequences: one kernel, a cluster of CTAs per sequence. Position by position
-// the cluster reads the row of both models (a contiguous slice a CTA), its warps
-// exchange statistics through distributed shared memory, every warp merges them
+// Long rows of many sequences: one kernel, a cluster of CTAs per sequence. Position by
+// position the cluster reads the row of both models (a contiguous slice a CTA), its
+// warps exchange statistics through distributed shared memory, every warp merges them
 // in the same order and decides; of the rows behind the first draft that is turned
-// down only the first copies of the next one are made, ahead of the decision. Few sequences would leave SMs idle that way: there a first kernel
-// forms the statistics of parts of all rows at once, and a second (a cluster a
-// sequence) merges them and decides. Either draws the token by reading row n once
-// more, mostly from L2: every warp sums w over a contiguous range, the ranges' sums
-// meet in the cluster, and the CTA whose range holds r sum w walks it.
+// down only the first copies of the next one are made, ahead of the decision. Few or
+// short rows would leave the memory idle that way: there a first kernel forms the
+// statistics of parts of all rows at once, and a second (a cluster a sequence) merges
+// them and decides (vf_at_once). Either draws the token by reading row n once more,
+// mostly from L2: every warp sums w over a contiguous range, the ranges' sums meet in
+// the cluster, and the CTA whose range holds r sum w walks it.
 //
-// Bound by HBM (many sequences), by the chain of dependent steps (few).
-// Tried for many sequences and slower (128 sequences of 4 drafts, 128256 columns
-// of bf16): parts of all rows dealt out position by position, the CTA or warp that
-// completes a row by a counter deciding whether the next ones are read: 108 and
-// 224 us; its fences and atomics took longer than the reading.
+// Bound by the chain of dependent steps: a launch, a row's reading, an exchange and
+// the draw where sequences are few (1 of 3 drafts and 128256 bf16 logits with a draft
+// model: 17 us), the longest sequence's positions where they are many (128 of 4
+// drafts: 73 us, of which the rows that decide would take 24 at the copy rate).
+// Tried for many sequences and slower (the latter): parts of all rows dealt out
+// position by position, the CTA or warp that completes a row by a counter deciding
+// whether the next ones are read: 108 and 224 us; its fences and atomics took longer
+// than the reading. The ring's loop rolled up (a fifth of the stalls are waits for
+// instructions): no change.
 #include <atomic>
 
 #include "ce_device.cuh"
