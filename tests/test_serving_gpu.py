@@ -62,6 +62,30 @@ def test_norm(ce, shape, dtype, residual):
         assert out is None
 
 
+@pytest.mark.parametrize("shape", [(700, 4096, 0, 0), (4100, 2048, 0, 0), (9001, 200, 3, 1), (3001, 1030, 2, 0), (500, 12000, 0, 0),
+                                   (310, 20000, 4, 4), (1300, 2056, 0, 0), (20000, 64, 0, 0)],
+                         ids=lambda s: f"{s[0]}x{s[1]}+{s[2]}@{s[3]}")
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_norm_of_many_rows(ce, shape, dtype):
+    """More rows than the GPU holds at once: every row as in a call of its own few."""
+    n, cols, pad, off = shape
+    g = gen(n + cols)
+    x, r = wide(n, cols, pad, off, dtype, g), wide(n, cols, pad, off, dtype, g)
+    w = 1 + 0.2 * torch.randn(cols, generator=g, device="cuda")
+    q, s, out = ce.ce_rms_norm_fp8(x, w, residual=r)
+    assert torch.equal(out, (x.float() + r.float()).to(x.dtype))
+    h = x.double() + r.double()
+    y = h / (h.square().mean(1, keepdim=True) + 1e-6).sqrt() * w.double()
+    up = torch.nn.functional.pad(y, (0, -cols % 128)).view(n, -1, 128)
+    want = up.abs().amax(2) / 448
+    # fp32: the sum of cols squares (pairwise over lanes: cols / 32 + 32 additions at most), a root, three products
+    tol = (cols / 32 + 48) * F.U
+    assert ((s.double() - want).abs() <= want * tol + 2.0 ** -126).all()
+    value = torch.nn.functional.pad(q.float().double(), (0, -cols % 128)).view(n, -1, 128) * s.double()[:, :, None]
+    # half a step of e4m3 (2^-4 relative, 2^-10 of the scale below its smallest normal), beside the roundings above
+    assert ((value - up).abs() <= up.abs() * (2.0 ** -4 + 2 * tol) + 2.0 ** -10 * s.double()[:, :, None] * (1 + 2 * tol)).all()
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_norm_in_place_and_given_buffers(ce, dtype):
     g = gen(5)
@@ -228,8 +252,17 @@ def verify_inputs(B, K, V, dtype, model, seed, pad=0, off=0, temps=None, padded=
 
 
 def many(times, *tensors):
-    """The batch several times over: from 28 sequences on another kernel verifies them."""
+    """The batch several times over: where a position's rows hold more than 8 MB another kernel verifies them."""
     return tuple(t.repeat(times, *[1] * (t.dim() - 1)) if torch.is_tensor(t) else t for t in tensors)
+
+
+def check(z, y, draft, u, r, t, got):
+    """Against fp64; of large batches every sequence of the first 24 and every 7th behind them."""
+    B = z.shape[0]
+    at = torch.tensor([b for b in range(B) if b < 24 or b % 7 == 0 or B <= 160], device=z.device)
+    pick = lambda v: v[at] if torch.is_tensor(v) and v.dim() else v  # noqa: E731
+    F.check_verify(pick(z), None if y is None else pick(y), pick(draft).cpu(), pick(u).cpu(), pick(r).cpu(),
+                   pick(t).cpu() if torch.is_tensor(t) else t, tuple(pick(v) for v in got))
 
 
 VERIFIES = [
@@ -238,6 +271,9 @@ VERIFIES = [
     (9, 0, 5000, 0, 0), (1, 3, 128256, 0, 0), (3, 2, 50257, 0, 0), (40, 5, 3001, 7, 8), (2, 20, 300, 0, 0),
     (150, 3, 2050, 0, 0), (2, 1, 300001, 0, 0), (28, 0, 3, 0, 0), (29, 2, 8200, 0, 0), (33, 1, 9, 7, 3), (60, 3, 20011, 5, 1),
     (27, 4, 6000, 8, 8), (100, 1, 40000, 0, 0), (230, 6, 1000, 0, 0),
+    # a position's rows above 8 MB
+    (130, 3, 34001, 7, 3), (300, 2, 17003, 5, 1), (29, 1, 300001, 0, 0), (40, 0, 120001, 0, 0), (210, 9, 24000, 8, 8),
+    (460, 1, 10007, 0, 1), (600, 2, 8192, 0, 0), (56, 4, 80000, 0, 0),
 ]
 
 
@@ -251,25 +287,25 @@ def test_verify(ce, shape, dtype, model):
     z, y, draft, u, r, t = args
     got = ce.ce_verify_drafts(z, draft, u, r, draft_logits=y, temperature=t)
     torch.cuda.synchronize()
-    F.check_verify(z, y, draft.cpu(), u.cpu(), r.cpu(), t.cpu() if torch.is_tensor(t) else t, got)
+    check(z, y, draft, u, r, t, got)
     again = ce.ce_verify_drafts(z, draft, u, r, draft_logits=y, temperature=t)
     assert all(torch.equal(a, b) for a, b in zip(got, again))
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("times", [1, 6])
+@pytest.mark.parametrize("times", [1, 6, 80])
 def test_verify_all_stay_or_none(ce, dtype, times):
     z, _, draft, u, r, _ = verify_inputs(6, 4, 5000, dtype, False, 8, padded=False)
     z, draft, u, r = many(times, z, draft, u, r)
     y = z[:, :4].clone()
     # the draft model is the target: every draft stays, whatever u
     got = ce.ce_verify_drafts(z, draft, u, r, draft_logits=y)
-    F.check_verify(z, y, draft.cpu(), u.cpu(), r.cpu(), 1.0, got)
+    check(z, y, draft, u, r, 1.0, got)
     assert (got[0] == 4).all() and torch.equal(got[1][:, :4], draft)
     # drafts that the target masks: none stays
     z.scatter_(2, torch.nn.functional.pad(draft, (0, 1))[:, :, None], -math.inf)
     got = ce.ce_verify_drafts(z, draft, u, r, draft_logits=y)
-    F.check_verify(z, y, draft.cpu(), u.cpu(), r.cpu(), 1.0, got)
+    check(z, y, draft, u, r, 1.0, got)
     assert (got[0] == 0).all() and (got[1][:, 1:] == -1).all()
     # u = 0 keeps any draft with a probability above 0
     got = ce.ce_verify_drafts(y.new_zeros(2, 2, 64), torch.tensor([[5], [-1]], device="cuda"), torch.zeros(2, 1, device="cuda"),
@@ -277,7 +313,7 @@ def test_verify_all_stay_or_none(ce, dtype, times):
     assert got[0].tolist() == [1, 0] and got[1].tolist() == [[5, 0], [0, -1]]
 
 
-@pytest.mark.parametrize("times", [1, 10])
+@pytest.mark.parametrize("times", [1, 10, 60])
 def test_verify_greedy_ties_take_the_lowest_index(ce, times):
     for V in (64, 5003, 131072):
         z = torch.zeros(3, 3, V, device="cuda", dtype=torch.bfloat16)
@@ -291,7 +327,7 @@ def test_verify_greedy_ties_take_the_lowest_index(ce, times):
         assert got[1].tolist() == [[9, 9, -1], [V - 2, V - 2, V - 2], [3, 0, -1]] * times
 
 
-@pytest.mark.parametrize("times", [1, 4])
+@pytest.mark.parametrize("times", [1, 4, 130])
 def test_verify_masks(ce, times):
     """Most of the vocabulary masked (-inf, the type's lowest value), rows with one value left, equal rows."""
     for dtype, low in (("bf16", -math.inf), ("f32", -math.inf), ("bf16", float(torch.finfo(torch.bfloat16).min)),
@@ -307,13 +343,13 @@ def test_verify_masks(ce, times):
         draft[3] = 77
         z, y, draft, u, r = many(times, z, y, draft, u, r)
         got = ce.ce_verify_drafts(z, draft, u, r, draft_logits=y)
-        F.check_verify(z, y, draft.cpu(), u.cpu(), r.cpu(), 1.0, got)
+        check(z, y, draft, u, r, 1.0, got)
         assert got[0][3] == 3 and (got[1][3] == 77).all() and (got[2][3] == 0).all()
         got = ce.ce_verify_drafts(z, draft, u, r)
-        F.check_verify(z, None, draft.cpu(), u.cpu(), r.cpu(), 1.0, got)
+        check(z, None, draft, u, r, 1.0, got)
 
 
-@pytest.mark.parametrize("times", [1, 4])
+@pytest.mark.parametrize("times", [1, 4, 100])
 def test_verify_undefined_rows(ce, times):
     """A row with nothing left, a NaN or +inf ends its sequence with -1; rows behind the decision may hold anything."""
     z, y, draft, u, r, _ = verify_inputs(9, 2, 3000, "bf16", True, 31, padded=False)
@@ -342,15 +378,16 @@ def test_verify_undefined_rows(ce, times):
     assert greedy[1][0, 0] == -1 and greedy[0][0] == 0
 
 
-def test_verify_ends_of_the_random_numbers(ce):
-    z, y, draft, u, _, _ = verify_inputs(64, 2, 6000, "bf16", True, 41, padded=False)
+@pytest.mark.parametrize("B", [64, 500])
+def test_verify_ends_of_the_random_numbers(ce, B):
+    z, y, draft, u, _, _ = verify_inputs(B, 2, 6000, "bf16", True, 41, padded=False)
     for v in (0.0, 1.0 - 2.0 ** -24):
-        r = torch.full((64,), v, device="cuda")
+        r = torch.full((B,), v, device="cuda")
         got = ce.ce_verify_drafts(z, draft, u, r, draft_logits=y)
-        F.check_verify(z, y, draft.cpu(), u.cpu(), r.cpu(), 1.0, got)
+        check(z, y, draft, u, r, 1.0, got)
 
 
-@pytest.mark.parametrize("B", [5, 40])
+@pytest.mark.parametrize("B", [5, 40, 640])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_verify_far_logits(ce, B, dtype):
     """Drafts far below the row's maximum, maxima far from 0, low and high temperatures: references that do not hold
@@ -366,11 +403,11 @@ def test_verify_far_logits(ce, B, dtype):
     for t in (1.0, 0.05, 30.0):
         got = ce.ce_verify_drafts(z, draft, u, r, draft_logits=y, temperature=t)
         # 3 u |a| of an exponent relative to the reference or the maximum, |a| up to 60
-        F.check_verify(z, y, draft.cpu(), u.cpu(), r.cpu(), t, got)
-        F.check_verify(z, None, draft.cpu(), u.cpu(), r.cpu(), t, ce.ce_verify_drafts(z, draft, u, r, temperature=t))
+        check(z, y, draft, u, r, t, got)
+        check(z, None, draft, u, r, t, ce.ce_verify_drafts(z, draft, u, r, temperature=t))
 
 
-@pytest.mark.parametrize("B", [3, 32])
+@pytest.mark.parametrize("B", [3, 32, 260])
 def test_verify_likely_tokens(ce, B):
     """log p of tokens with probabilities near 1 keeps its relative precision, staying, greedy or drawn."""
     z = torch.randn(B, 2, 9000, generator=gen(95), device="cuda")
@@ -384,6 +421,25 @@ def test_verify_likely_tokens(ce, B):
         want = torch.log_softmax(z.double(), 2)[:, :, 4321]
         # -log1p(s): s is off by rel(V), log1p by its own rounding; s itself is below 0.02 here
         assert ((lp.double() - want).abs() <= want.abs() * (F.rel(9000) + 4 * F.U)).all()
+
+
+@pytest.mark.parametrize("B,V", [(2, 700), (60, 80000)])
+def test_verify_as_many_drafts_as_there_may_be(ce, B, V):
+    """255 drafts that all stay, one that is turned down in the middle, a batch whose sequences are one in memory."""
+    K = 255
+    z = torch.empty(1, K + 1, V, device="cuda", dtype=torch.bfloat16).normal_(0, 3, generator=gen(7)).expand(B, -1, -1)
+    draft = z[:, :K].argmax(2).contiguous()
+    u, r = torch.zeros(B, K, device="cuda"), torch.rand(B, generator=gen(8), device="cuda")
+    draft[1, 100] = (draft[1, 100] + 1) % V
+    u[1, 100] = 0.999
+    n, tok, lp = ce.ce_verify_drafts(z, draft, u, r)
+    assert n[0] == K and n[1] == 100 and (n[2:] == K).all() and torch.equal(tok[0, :K], draft[0]) and (tok[1, 101:] == -1).all()
+    want = torch.log_softmax(z[0].double(), 1)
+    for b in (0, 1, B - 1):
+        i = torch.arange(int(n[b]) + 1, device="cuda")
+        got = want[i, tok[b, i]]
+        # a sum's relative error, and the roundings of exponents and log p of at most 64 in magnitude
+        assert ((lp[b, i].double() - got).abs() <= F.rel(V) + 8 * F.U * 64).all()
 
 
 def test_verify_strides_and_buffers(ce):
@@ -518,3 +574,53 @@ def test_offsets_past_32_bits(ce):
         got, want = call(x=x, q=q), call(x=x.contiguous())
         assert torch.equal(got[0].contiguous().view(torch.uint8), want[0].contiguous().view(torch.uint8))
         assert torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [131200, 131203])
+def test_gemm_output_past_32_bits(ce, n, dtype):
+    m, k = (17000, 100) if dtype == "bf16" else (16500, 100)
+    a, sa, b, sb, _ = operands(ce, m, n, k, 5)
+    out = ce.ce_gemm_fp8(a, sa, b, sb, out_dtype=DT[dtype])
+    at = torch.tensor([0, 255, 256, 8191, 16383, 16384, 16400, m - 1], device="cuda")
+    F.check_gemm(out[at], a.view(torch.uint8)[at].view(torch.float8_e4m3fn), sa[at], b, sb)
+
+
+@pytest.mark.parametrize("shape", [(20000, 100, 256), (3000, 16, 130), (40000, 1, 128), (1, 300000, 16), (66, 9728, 384), (640, 640, 20000)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_gemm_long_sides(ce, shape):
+    test_gemm(ce, shape, "bf16")
+
+
+FIRST = """
+import torch, softmax_cross_entropy_pass_gb300 as ce
+x = torch.randn({B}, 4, 256, device="cuda").bfloat16()
+w = torch.ones(256, device="cuda")
+W = (torch.randn({V}, 256, device="cuda") * 0.1).bfloat16()
+draft = torch.randint(0, {V}, ({B}, 3), device="cuda")
+u, r = torch.rand({B}, 3, device="cuda"), torch.rand({B}, device="cuda")
+ws = torch.empty(64 << 20, dtype=torch.uint8, device="cuda")
+def step():
+    W8, s = ce.ce_quantize_fp8(W, block_rows=128)
+    z = ce.fp8_head_logits(x, w, W8, s)
+    return (z,) + ce.ce_verify_drafts(z, draft, u, r, ws=ws)
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    outs = step()
+graph.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(outs, step()))
+print("first calls captured")
+"""
+
+
+@pytest.mark.parametrize("size", [(2, 3001), (260, 20000)])
+def test_first_calls_captured(size):
+    """A process whose very first calls are captured into a graph."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    got = subprocess.run([sys.executable, "-c", FIRST.format(B=size[0], V=size[1])], cwd=root, capture_output=True, text=True, timeout=200)
+    assert got.returncode == 0 and "first calls captured" in got.stdout, got.stderr[-2000:]
