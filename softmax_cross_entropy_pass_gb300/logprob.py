@@ -145,8 +145,9 @@ class _Call:
             if stream.cuda_stream != self.handle:
                 self.stream, self.other, self.handle = stream, torch.cuda.current_stream(self.device), stream.cuda_stream
 
-    def empty(self, *shape, dtype=_F32):
-        t = torch.empty(shape, dtype=dtype, device=self.device)
+    def empty(self, *shape, dtype=_F32, strides=None):
+        t = torch.empty(shape, dtype=dtype, device=self.device) if strides is None else \
+            torch.empty_strided(shape, strides, dtype=dtype, device=self.device)
         if self.other is not None:
             self.stream.wait_stream(self.other)  # the memory's last user may still be running there
             t.record_stream(self.stream)

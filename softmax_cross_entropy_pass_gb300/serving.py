@@ -9,7 +9,7 @@ layouts are in include/ce.h. These calls are not differentiable: what they
 return carries no graph.
 
 8-bit matrices are ``torch.float8_e4m3fn`` tensors [rows, cols] whose rows start
-at multiples of 16 bytes (new ones are views of such a buffer where cols is not
+at multiples of 16 bytes (new ones have such a row stride where cols is not
 a multiple of 16), with contiguous fp32 scales: [rows, ceil(cols / 128)] for
 activations, [ceil(rows / 128), ceil(cols / 128)] for weights. ``stream``
 defaults to the current stream of the first tensor's device.
@@ -96,8 +96,7 @@ def _out8(call, q, n, cols):
     """(an 8-bit matrix to write, its row stride): the given one, or a new one."""
     if q is None:
         ld = (cols + 15) // 16 * 16
-        q = call.empty(n, ld, dtype=_E4M3)
-        return (q if ld == cols else q[:, :cols]), ld
+        return call.empty(n, cols, dtype=_E4M3, strides=None if ld == cols else (ld, 1)), ld
     rows, columns, ld = _matrix8("q", q)
     if rows != n or columns != cols:
         raise ValueError(f"q must have the shape ({n}, {cols})")
