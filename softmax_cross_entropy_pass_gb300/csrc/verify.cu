@@ -838,10 +838,10 @@ __global__ void __launch_bounds__(kThreads, 3) vf_seq_kernel(VfArgs a) {
     const int t0 = static_cast<int>(static_cast<int64_t>(steps) * rank / size), t1 = static_cast<int>(static_cast<int64_t>(steps) * (rank + 1) / size);
     // position i's rows on their way (the rows' vectors need not lie alike: each row's slice is its own)
     const auto stream = [&](int i) {
-        const bool two = a.y && drafts[i] >= 0;
+        const bool two = a.y && drafts[i] >= 0 && !greedy;
         const VfRowIn<DT> in(reinterpret_cast<const char *>(a.x) + (b * a.xs + i * a.xr) * Fmt<DT>::kBytes, a.V);
         const VfRowIn<DT> yin(two ? reinterpret_cast<const char *>(a.y) + (b * a.ys + i * a.yr) * Fmt<DT>::kBytes : in.row, a.V);
-        return VfStream<DT>(in, yin, two, false, t0 * kThreads + tid, greedy || !usable ? 0 : t1 * kThreads, kThreads, ring);
+        return VfStream<DT>(in, yin, two, false, t0 * kThreads + tid, usable ? t1 * kThreads : 0, kThreads, ring);
     };
     // the largest of 32 elements spread over a row (0 if none is finite)
     const auto sample = [&](const void *row) {
@@ -854,7 +854,7 @@ __global__ void __launch_bounds__(kThreads, 3) vf_seq_kernel(VfArgs a) {
     VfRow p = vf_none(), q = vf_none();
     bool has = false, model = false;
     int n = 0;
-    VfStream<DT> in = stream(0);  // (greedy sequences read without it)
+    VfStream<DT> in = stream(0);
     for (; usable; ++n) {
         const int t = drafts[n];
         has = t >= 0;
@@ -865,12 +865,31 @@ __global__ void __launch_bounds__(kThreads, 3) vf_seq_kernel(VfArgs a) {
         const int skip = has ? t : kNone;
         q = vf_none();
         if (greedy) {
+            // the maximum's lowest index, through the same ring (200 sequences of 6 drafts, 50257 fp32 logits: 64 us; 74 with
+            // a tile's loads in registers, none of the next row's under way)
             VfState st{-INFINITY, 0.f, kNone};
-            for (int step = t0; step < t1; step += 4) {
-                VfTile<DT, 4> tx;
-                tx.load(x, a.V, step * kThreads + tid, kThreads, t1 - step);
-                st = vf_merge(st, tx.stats(k), k);
-            }
+            struct Use {
+                VfState &st;
+                const VfStream<DT> &in;
+                float k;
+                __device__ inline void operator()(int v, const uint4 &ux, const uint4 &) const {
+                    VfTile<DT, 1> tx;
+                    tx.raw[0] = ux;
+                    tx.first = in.x.first(v);
+                    tx.step = 0;
+                    st = vf_merge(st, tx.stats(k), k);
+                }
+                __device__ inline void operator()(int v, const uint4 &ux, const uint4 &, int v2, const uint4 &ux2, const uint4 &) const {
+                    VfTile<DT, 2> tx;
+                    tx.raw[0] = ux;
+                    tx.raw[1] = ux2;
+                    tx.first = in.x.first(v);
+                    tx.step = in.x.first(v2) - tx.first;
+                    st = vf_merge(st, tx.stats(k), k);
+                }
+            };
+            in.run(Use{st, in, k});
+            if (has) in = stream(n + 1);
             st = vf_reduce(st, k);
             const float4 *all = meet.all(st.m, st.s, __int_as_float(st.at), 0.f);
             st = VfState{-INFINITY, 0.f, kNone};
