@@ -569,7 +569,7 @@ ce_status flce_token_logprob_backward(const ce_params *p, int64_t hidden_dim, fl
  * (activations, scale [rows][ceil(cols / 128)]) or 128 rows (weights, scale
  * [ceil(rows / 128)][ceil(cols / 128)]); the last block of a row or column may be
  * smaller. A block's scale is max(max |y| / 448, 2^-126), its bytes the nearest
- * e4m3 of y / scale (ties to even), so zeros stay zeros. A NaN makes its block's
+ * e4m3 of the fp32 quotient y / scale (ties to even), so zeros stay zeros. A NaN makes its block's
  * scale and bytes NaN; an infinity makes the scale infinite. Bytes between cols
  * and ld are not written and never read.
  * Inputs may have any row stride and element alignment; outputs share no memory

@@ -1,0 +1,84 @@
+"""The 8-bit serving head where roundings, scales, references and lifetimes
+meet their ends: against the bytes' own rule, and against fp64 with the
+tolerances of fp8_check.py."""
+import math
+
+import pytest
+import torch
+
+import fp8_check as F
+
+pytestmark = pytest.mark.gpu
+DT = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+E4M3 = torch.float8_e4m3fn
+
+
+@pytest.fixture(scope="module")
+def ce():
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    import softmax_cross_entropy_pass_gb300 as ce
+    return ce
+
+
+def gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+# ---------------------------------------------------------------------- bytes
+def nearest(y, tall=1):
+    """(bytes, scales) of fp32 y on the CPU: one division a block for its scale, one an element, one rounding to e4m3."""
+    rows, cols = y.shape
+    n, m = -(-rows // tall), -(-cols // 128)
+    wide = torch.zeros(n * tall, m * 128)
+    wide[:rows, :cols] = y
+    t = wide.view(n, tall, m, 128)
+    scale = (t.abs().amax((1, 3)) / 448.0).clamp_min(2.0 ** -126)
+    q = (t / scale[:, None, :, None]).view(n * tall, m * 128)[:rows, :cols].to(E4M3)
+    return q.contiguous().view(torch.uint8), scale
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("tall", [1, 128])
+@pytest.mark.parametrize("shape", [(600, 1000), (130, 4096), (257, 129)], ids=lambda s: "x".join(map(str, s)))
+def test_quantized_bytes_are_the_nearest(ce, dtype, tall, shape):
+    """Every byte is the nearest e4m3 of the fp32 quotient y / scale, ties to even: 16-bit inputs meet many ties."""
+    x = torch.empty(shape, device="cuda").normal_(0, 1, generator=gen(shape[0])).to(DT[dtype])
+    q, s = ce.ce_quantize_fp8(x, block_rows=tall)
+    want, scale = nearest(x.float().cpu(), tall)
+    assert torch.equal(s.cpu(), scale)
+    assert torch.equal(q.contiguous().view(torch.uint8).cpu(), want)
+
+
+def test_quantized_bytes_of_any_magnitude(ce):
+    """Blocks from the least fp32 numbers to the largest, scales whose reciprocal or remainders leave the normal range."""
+    g = gen(2)
+    for dtype, lo, hi in (("f32", -148, 126), ("bf16", -132, 126), ("f16", -23, 14)):
+        x = torch.randn(hi - lo, 300, generator=g, device="cuda", dtype=torch.float64).clamp(-1.9, 1.9)
+        x = (x * torch.exp2(torch.arange(lo, hi, device="cuda", dtype=torch.float64))[:, None]).to(DT[dtype])
+        x[:, 7], x[:, 8] = 0.0, -0.0
+        q, s = ce.ce_quantize_fp8(x)
+        want, scale = nearest(x.float().cpu())
+        assert torch.equal(s.cpu(), scale)
+        assert torch.equal(q.contiguous().view(torch.uint8).cpu(), want)
+
+
+def test_quantized_tie(ce):
+    """-1.3671875 over a scale of 3.0625 / 448 is -200, between -192 and -208: the even one is -192."""
+    x = torch.zeros(128, 128, device="cuda", dtype=torch.bfloat16)
+    x[0, 0], x[0, 1] = 3.0625, -1.3671875
+    for tall in (1, 128):
+        q, _ = ce.ce_quantize_fp8(x, block_rows=tall)
+        assert q[0, :2].float().tolist() == [448.0, -192.0]
+
+
+@pytest.mark.parametrize("cols", [200, 1000, 4096, 9000, 20000])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_norm_bytes_are_the_nearest(ce, cols, dtype):
+    """Rows of 1 and -1 have a root mean square of exactly 1, so that y is the weight, with signs."""
+    g = gen(cols)
+    x = (torch.randint(0, 2, (40, cols), generator=g, device="cuda") * 2 - 1).to(DT[dtype])
+    w = torch.randn(cols, generator=g, device="cuda").to(torch.bfloat16).to(DT[dtype])
+    q, s, _ = ce.ce_rms_norm_fp8(x, w, eps=0.0)
+    want, scale = nearest((x.float() * w.float()).cpu())
+    assert torch.equal(s.cpu(), scale)
+    assert torch.equal(q.contiguous().view(torch.uint8).cpu(), want)
