@@ -153,6 +153,14 @@ class _Call:
             t.record_stream(self.stream)
         return t
 
+    def lend(self, t):
+        """A tensor that the current stream has made for this call alone: the kernels' stream waits for it, and the
+        memory is not handed out again before that stream has read it."""
+        if self.other is not None:
+            self.stream.wait_stream(self.other)
+            t.record_stream(self.stream)
+        return t
+
     def run(self, name, *args):
         fn = getattr(_lib, name)
         if _current_device() == self.index:

@@ -203,6 +203,11 @@ def fp8_head_logits(x, norm_weight, weight, weight_scale, *, residual=None, eps=
     head that sampled them."""
     h = x.reshape(-1, x.shape[-1])
     r = None if residual is None else residual.reshape(-1, residual.shape[-1])
+    if stream is not None:  # where reshape had to copy, nothing else holds the copies
+        call = _Call(x, (residual,), stream)
+        for given, rows in ((x, h), (residual, r)):
+            if rows is not None and rows.data_ptr() != given.data_ptr():
+                call.lend(rows)
     q, scale, _ = ce_rms_norm_fp8(h, norm_weight, residual=r, eps=eps, with_residual_out=False, stream=stream)
     out = ce_gemm_fp8(q, scale, weight, weight_scale, bias=bias, out_dtype=out_dtype, stream=stream)
     return out.view(*x.shape[:-1], weight.shape[0])

@@ -82,3 +82,29 @@ def test_norm_bytes_are_the_nearest(ce, cols, dtype):
     want, scale = nearest((x.float() * w.float()).cpu())
     assert torch.equal(s.cpu(), scale)
     assert torch.equal(q.contiguous().view(torch.uint8).cpu(), want)
+
+
+# ---------------------------------------------------------------------- lifetimes
+@pytest.mark.parametrize("residual", [True, False])
+def test_head_of_strided_states_on_another_stream(ce, residual):
+    """Hidden states that cannot be viewed as rows are copied. The copies live until the other stream has read them,
+    whatever the current stream allocates meanwhile."""
+    B, K1, H, V = 64, 4, 4096, 3001
+    g = gen(11)
+    x = torch.randn(K1, B, H, generator=g, device="cuda").bfloat16().transpose(0, 1)
+    r = torch.randn(K1, B, H, generator=g, device="cuda").bfloat16().transpose(0, 1) if residual else None
+    w = torch.ones(H, device="cuda")
+    W8, ws = ce.ce_quantize_fp8(torch.randn(V, H, generator=g, device="cuda"), block_rows=128)
+    want = ce.fp8_head_logits(x, w, W8, ws, residual=r)
+    side, busy = torch.cuda.Stream(), torch.randn(8192, 8192, device="cuda", dtype=torch.bfloat16)
+    for handle in (side, side.cuda_stream):
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            for _ in range(20):
+                torch.mm(busy, busy)
+        got = ce.fp8_head_logits(x, w, W8, ws, residual=r, stream=handle)
+        # memory of the copies' size, written by the current stream at once
+        over = [torch.full((B * K1, H), math.nan, device="cuda", dtype=torch.bfloat16) for _ in range(4)]
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+        del over, got
