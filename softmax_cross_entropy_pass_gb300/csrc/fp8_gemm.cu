@@ -386,7 +386,6 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     float *scales = reinterpret_cast<float *>(smem_raw + (base - raw) + kPairStages * 2 * kPairHalf);
     float *extra = scales + 2 * kPairChunk * kPairRow;  // the bias of this tile's columns; STAGED: the warps' sums on their way out
     const uint32_t sA = base, sB = base + kPairStages * kPairHalf;
-    volatile int *abort = &abort_flag;
     const int tiles_m = (g.m + kPairM - 1) / kPairM;
     const int tiles = tiles_m * ((g.n + kPairN - 1) / kPairN);
 
@@ -424,7 +423,7 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 const int row0 = t % tiles_m * kPairM + static_cast<int>(rank) * 128;
                 const int col0 = t / tiles_m * kPairN + static_cast<int>(rank) * 128;
                 for (int kb = 0; kb < g.kblocks; ++kb) {
-                    if (round > 0) mbar_wait_polled(smem_u32(&empty[s]), (round - 1) & 1u, abort);
+                    if (round > 0) mbar_wait_pair(smem_u32(&empty[s]), (round - 1) & 1u, &abort_flag);
                     const uint32_t fb = mapa_shared(smem_u32(&full[s]), 0);  // the even CTA's barrier
                     if (rank == 0) mbar_expect_tx(smem_u32(&full[s]), 4 * kPairHalf);
                     tma_load_2d_pair(sA + s * kPairHalf, &tmA, kb * kFp8Block, row0, fb);
@@ -451,8 +450,8 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             for (int t = cid; t < tiles; t += ncl)
                 for (int kb = 0; kb < g.kblocks; ++kb, ++unit) {
                     const uint32_t acc = unit & 1u, u = unit >> 1;
-                    mbar_wait_polled(smem_u32(&full[s]), phase, abort);
-                    if (u > 0) mbar_wait_polled(smem_u32(&tempty[acc]), (u - 1) & 1u, abort);
+                    mbar_wait_pair(smem_u32(&full[s]), phase, &abort_flag);
+                    if (u > 0) mbar_wait_pair(smem_u32(&tempty[acc]), (u - 1) & 1u, &abort_flag);
                     tc_fence_after();
 #pragma unroll
                     for (int kk = 0; kk < kFp8Block / 32; ++kk)
@@ -519,7 +518,7 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 const F2 w = f2(w1, w1);
                 if (kb + 1 < g.kblocks) next = __ldg(sb + kb + 1);
                 const uint32_t a = unit & 1u;
-                mbar_wait_polled(smem_u32(&tfull[a]), (unit >> 1) & 1u, abort);
+                mbar_wait_pair(smem_u32(&tfull[a]), (unit >> 1) & 1u, &abort_flag);
                 tc_fence_after();
                 const uint32_t taddr = lane_addr + a * kPairN;
                 const auto add = [&](const uint32_t *x, int n, int at) {
@@ -574,7 +573,7 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 asm volatile("cp.async.wait_all;" ::: "memory");
                 asm volatile("bar.sync 1, %0;" ::"n"(kPairEpi) : "memory");
             }
-            const bool bad = *abort != 0;  // a wait that gave up leaves no result
+            const bool bad = *const_cast<volatile int *>(&abort_flag) != 0;  // a wait of the pair that gave up leaves no result
             if (!STAGED) {
                 if (row < g.m) {
 #pragma unroll

@@ -57,6 +57,16 @@ __device__ inline bool mbar_wait_polled(uint32_t bar, uint32_t parity, volatile 
     }
 }
 
+// mbar_wait_polled in a CTA of a pair whose results depend on the waits of both: where it
+// gives up, the flag (at the same place in both CTAs) is set in both of them, before
+// anything that the caller then signals or copies without having waited.
+__device__ inline bool mbar_wait_pair(uint32_t bar, uint32_t parity, int *abort, uint64_t limit_ns = 2000000000ull) {
+    if (mbar_wait_polled(bar, parity, abort, limit_ns)) return true;
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(mapa_shared(smem_u32(abort), cluster_ctarank() ^ 1u)), "r"(1) : "memory");
+    asm volatile("fence.acq_rel.cluster;" ::: "memory");
+    return false;
+}
+
 // ---------------------------------------------------------------- descriptors
 // Shared-memory matrix descriptor, 128-byte swizzle: start address, leading
 // and stride byte offsets (16-byte units), descriptor version 1.
