@@ -84,9 +84,9 @@ fp8_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
                const __grid_constant__ CUtensorMap tmA, Fp8Args g) {
     using F = Few<NT>;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t full[F::kStages], empty[F::kStages], tfull[F::kAcc], tempty[F::kAcc];
+    __shared__ uint64_t full[F::kStages], empty[F::kStages], tfull[F::kAcc], tempty[F::kAcc], done;
     __shared__ uint32_t tmem_slot;
-    __shared__ int abort_flag, drain_abort;
+    __shared__ int abort_flag, drain_abort[2];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;  // 128-byte swizzle atoms
     float *parts = reinterpret_cast<float *>(smem_raw + (base - raw));  // [NT][kFewM], once the stages are done with
@@ -112,7 +112,8 @@ fp8_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
             mbar_init(smem_u32(&tfull[a]), 1);
             mbar_init(smem_u32(&tempty[a]), 4 * F::kSets);
         }
-        abort_flag = drain_abort = 0;
+        mbar_init(smem_u32(&done), 1);
+        abort_flag = drain_abort[0] = drain_abort[1] = 0;
         fence_mbar_init_cluster();
         tma_prefetch_desc(&tmW);
         tma_prefetch_desc(&tmWs);
@@ -156,7 +157,7 @@ fp8_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
             const uint32_t used = round > 0 ? F::kStages : s;
             for (uint32_t i = 0; i < used; ++i) {
                 const uint32_t uses = round + (i < s ? 1u : 0u);
-                mbar_wait_polled(smem_u32(&full[i]), (uses - 1) & 1u, &drain_abort);
+                mbar_wait_polled(smem_u32(&full[i]), (uses - 1) & 1u, &drain_abort[0]);
             }
         }
     } else if (warp == 1) {
@@ -182,6 +183,9 @@ fp8_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
                         phase ^= 1u;
                     }
                 }
+            // the MMAs in flight end before tensor memory is given back, whatever the epilogue waited for
+            mma_commit(smem_u32(&done));
+            mbar_wait_polled(smem_u32(&done), 0, &drain_abort[1]);
         }
     } else {
         // ---------------------------------------------------- epilogue: 4 warps for every kCols rows of A
@@ -376,9 +380,9 @@ template <int DT, bool STAGED>
 __global__ void __launch_bounds__(kPairThreads, 1)
 fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, Fp8Args g) {
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t full[kPairStages], empty[kPairStages], tfull[kPairAcc], tempty[kPairAcc];
+    __shared__ uint64_t full[kPairStages], empty[kPairStages], tfull[kPairAcc], tempty[kPairAcc], done;
     __shared__ uint32_t tmem_slot;
-    __shared__ int abort_flag, drain_abort;
+    __shared__ int abort_flag, drain_abort[2];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = cluster_ctarank();
     const int cid = static_cast<int>(cluster_id_x()), ncl = static_cast<int>(nclusters_x());
@@ -398,7 +402,8 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             mbar_init(smem_u32(&tfull[a]), 1);
             mbar_init(smem_u32(&tempty[a]), 2 * kPairEpi / 32);
         }
-        abort_flag = drain_abort = 0;
+        mbar_init(smem_u32(&done), 1);
+        abort_flag = drain_abort[0] = drain_abort[1] = 0;
         fence_mbar_init_cluster();
         tma_prefetch_desc(&tmA);
         tma_prefetch_desc(&tmB);
@@ -439,7 +444,7 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 const uint32_t used = round > 0 ? kPairStages : s;
                 for (uint32_t i = 0; i < used; ++i) {
                     const uint32_t uses = round + (i < s ? 1u : 0u);
-                    mbar_wait_polled(smem_u32(&full[i]), (uses - 1) & 1u, &drain_abort);
+                    mbar_wait_polled(smem_u32(&full[i]), (uses - 1) & 1u, &drain_abort[0]);
                 }
             }
         }
@@ -464,6 +469,9 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                         phase ^= 1u;
                     }
                 }
+            // the MMAs in flight end before tensor memory is given back, whatever the epilogue waited for
+            mma_commit_pair_mc(smem_u32(&done), 0x1);
+            mbar_wait_polled(smem_u32(&done), 0, &drain_abort[1]);
         }
     } else {
         // ---------------------------------------------------- epilogue (warps 4..11, both CTAs)

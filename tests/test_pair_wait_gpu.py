@@ -32,3 +32,17 @@ def test_pair_kernel_waits_for_both():
     alone = [line for line in kernel.split("\n") if "mbar_wait_polled" in line or "mbar_wait_bounded" in line]
     assert kernel.count("mbar_wait_pair(") == 4
     assert all("drain_abort" in line for line in alone), alone
+
+
+@pytest.mark.parametrize("name,commit", [("fp8_few_kernel(const", "mma_commit(smem_u32(&done))"),
+                                         ("fp8_pair_kernel(const", "mma_commit_pair_mc(smem_u32(&done), 0x1)")])
+def test_products_wait_for_their_mmas_before_they_leave(name, commit):
+    """Tensor memory is given back behind a wait of the issuer for all of its MMAs: an epilogue whose own waits gave
+    up may be there first."""
+    with open(os.path.join(_build.CSRC, "fp8_gemm.cu")) as f:
+        text = f.read()
+    kernel = text[text.index(name):]
+    end = kernel.index("tmem_dealloc")
+    at = kernel.index(commit)
+    wait = kernel.index("mbar_wait_polled(smem_u32(&done), 0, &drain_abort[1])")
+    assert kernel.rindex("mma_e4m3", 0, end) < at < wait < kernel.rindex("__syncthreads", 0, end) < end
