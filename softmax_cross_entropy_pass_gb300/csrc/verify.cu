@@ -823,10 +823,18 @@ __global__ void __launch_bounds__(kThreads, 3) vf_seq_kernel(VfArgs a) {
     const int rank = static_cast<int>(cluster_ctarank()), size = static_cast<int>(cluster_nctarank()), b = blockIdx.x / size;
     const float temp = vf_temp(a, b), k = vf_k(temp), ln2_k = k * 0.6931471805599453f;
     const bool greedy = temp == 0.f, usable = vf_temp_ok(temp);
-    // every position's scalars
-    for (int i = tid; i <= a.K; i += kThreads) {
-        const int64_t t = i < a.K ? vf_draft(a, b, i) : -1;
-        const bool has = vf_valid(a, t);
+    // Every position's scalars; a position behind a missing draft has none, for its rows are not read. (A warp looks at the
+    // drafts before its own itself: a barrier instead took 1 us.)
+    static_assert(kMaxDrafts < kThreads, "a position a thread");
+    int64_t t = -1;
+    unsigned missing = 0;
+    for (int c = 0; c <= tid >> 5; ++c) {
+        t = c * 32 + lane < a.K && !missing ? vf_draft(a, b, c * 32 + lane) : -1;
+        missing = __ballot_sync(0xffffffffu, !vf_valid(a, t));
+    }
+    if (tid <= a.K) {
+        const int i = tid;
+        const bool has = !(missing & ((2u << lane) - 1u));
         drafts[i] = has ? static_cast<int>(t) : -1;
         us[i] = has ? __ldg(a.u + static_cast<int64_t>(b) * a.K + i) : 0.f;
         xts[i] = has ? Fmt<DT>::load1(a.x, b * a.xs + i * a.xr + t) : 0.f;

@@ -108,3 +108,29 @@ def test_head_of_strided_states_on_another_stream(ce, residual):
         torch.cuda.synchronize()
         assert torch.equal(got, want)
         del over, got
+
+
+# ---------------------------------------------------------------------- ends of sequences
+@pytest.mark.parametrize("size", [(5, 3, 5003), (200, 3, 30011), (200, 40, 17003)], ids=["at_once", "clusters", "many"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_verify_valid_drafts_behind_a_missing_one(ce, size, dtype):
+    """Drafts like [7, -1, 5]: nothing behind the missing one counts, whatever its rows and random numbers hold."""
+    B, K, V = size
+    g = gen(13)
+    z = torch.empty(B, K + 1, V, device="cuda").normal_(0, 2, generator=g).to(DT[dtype])
+    y = (z[:, :K].float() + torch.empty(B, K, V, device="cuda").normal_(0, 0.5, generator=g)).to(DT[dtype])
+    draft = y.argmax(2)
+    u, r = torch.rand(B, K, generator=g, device="cuda") * 0.2, torch.rand(B, generator=g, device="cuda")
+    at = torch.randint(0, K + 1, (B,), generator=g, device="cuda")
+    place = torch.arange(K, device="cuda")
+    draft = torch.where(place == at[:, None], -1, draft)
+    cut = torch.where(place > at[:, None], -1, draft)
+    for model in (y, None):
+        for t in (1.0, 0.0):
+            want = ce.ce_verify_drafts(z, cut, u, r, draft_logits=model, temperature=t)
+            zz, yy, uu = z.clone(), y.clone(), u.clone()
+            zz[torch.arange(K + 1, device="cuda") > at[:, None]] = math.nan
+            yy[place >= at[:, None]] = math.nan
+            uu[place >= at[:, None]] = math.nan
+            got = ce.ce_verify_drafts(zz, draft, uu, r, draft_logits=None if model is None else yy, temperature=t)
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
