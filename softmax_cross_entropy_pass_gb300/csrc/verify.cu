@@ -32,6 +32,7 @@
 // than the reading. The ring's loop rolled up (a fifth of the stalls are waits for
 // instructions): no change.
 #include <atomic>
+#include <type_traits>
 
 #include "ce_device.cuh"
 #include "ce_kernels.h"
@@ -204,21 +205,29 @@ __device__ inline VfState vf_row(const VfPart *p, int parts, float k) {
     }
     return vf_reduce(st, k);
 }
-// Exponents are x k - r with r = R k rounded once: what that rounding shifts is the
-// same for every term of the row, so it leaves the probabilities alone.
 __device__ inline void cp_async16(uint32_t dst, const void *src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ inline float vf_exp(float x, float k, float r) { return ex2_hw(fmaf(x, k, -r)); }
-// 2^(x k - r) of N values
+// A term's exponent relative to the reference R is x k - r with r = R k rounded once:
+// what that rounding shifts is the same for every term of the row, so it leaves the
+// probabilities alone. From 2^24 on it may shift by whole powers of two, further up by
+// more than fp32 holds, and R k itself may be infinite: there it is (x - R) k. That is an
+// instruction more for every two elements, and no row of a model needs it: the loops over
+// a row have a plain second form for it.
+__device__ inline bool vf_far(float R, float k) { return !(fabsf(R * k) < 0x1p24f); }
+__device__ inline float vf_arg(float x, float R, float k) { return vf_far(R, k) ? (x - R) * k : fmaf(x, k, -(R * k)); }
+// 2^ those of N values, r = R k, or R itself where that is far
 template <int N>
-__device__ inline void vf_exps(const float *x, float k, float r, float *e) {
+__device__ inline void vf_exps(const float *x, float k, float r, bool far, float *e) {
     const F2 kk = f2(k, k), rr = f2(-r, -r);
 #pragma unroll
-    for (int j = 0; j < N; j += 2) f2_split(f2_ex2(f2_fma(f2(x[j], x[j + 1]), kk, rr)), e[j], e[j + 1]);
+    for (int j = 0; j < N; j += 2) {
+        const F2 v = f2(x[j], x[j + 1]);
+        f2_split(f2_ex2(far ? f2_mul(f2_add(v, rr), kk) : f2_fma(v, kk, rr)), e[j], e[j + 1]);
+    }
 }
 
-// A row's distribution: p_c = 2^(x_c k - R k) / S, R k rounded once. M the maximum; at its lowest index
+// A row's distribution: p_c = 2^vf_arg(x_c, R, k) / S. M the maximum; at its lowest index
 // and s1 = sum of the terms 2^((x - M) k) without that one, where they are known.
 struct VfRow {
     float R, S, M, s1;
@@ -226,7 +235,7 @@ struct VfRow {
 };
 // (the terms of a VfState are relative to exactly M: S takes the shift that R k's rounding makes)
 __device__ inline VfRow vf_of(const VfState &s, float k) {
-    return VfRow{s.m, (1.f + s.s) * vf_exp(s.m, k, s.m * k), s.m, s.s, s.at};
+    return VfRow{s.m, (1.f + s.s) * ex2_hw(vf_arg(s.m, s.m, k)), s.m, s.s, s.at};
 }
 __device__ inline VfRow vf_none() { return VfRow{0.f, 1.f, 0.f, 0.f, 0}; }
 __device__ inline bool vf_defined(const VfRow &r) {
@@ -235,7 +244,7 @@ __device__ inline bool vf_defined(const VfRow &r) {
 
 // log p of a logit x from the row's sum (the same exponent as the sum's terms: R k's rounding cancels)
 __device__ inline float vf_logp_of(float x, const VfRow &p, float k) {
-    return fmaf(x, k, -(p.R * k)) * 0.6931471805599453f - logf(p.S);
+    return vf_arg(x, p.R, k) * 0.6931471805599453f - logf(p.S);
 }
 
 // Whether a draft stays, u q_t < p_t: its logits xt, yt in the rows p, q (model: there
@@ -244,7 +253,7 @@ __device__ inline bool vf_stays(int64_t t, float u, float xt, float yt, const Vf
                                 bool greedy, float k) {
     if (!vf_defined(p) || !vf_defined(q)) return false;
     if (greedy) return p.at == static_cast<int>(t);
-    const float lp = fmaf(xt, k, -(p.R * k)) - log2f(p.S), lq = model ? fmaf(yt, k, -(q.R * k)) - log2f(q.S) : 0.f;
+    const float lp = vf_arg(xt, p.R, k) - log2f(p.S), lq = model ? vf_arg(yt, q.R, k) - log2f(q.S) : 0.f;
     return log2f(u) + lq < lp;
 }
 
@@ -371,6 +380,10 @@ template <int DT> struct VfStream {
         for (int j = 0; j < kDepth - 2; ++j) ask(j);
     }
     __device__ inline void drop() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+    // every vector without the ring, whose copies have been dropped
+    template <typename F> __device__ inline void all(F use) {
+        while (v < v1) slow(use);
+    }
     template <typename F> __device__ inline void slow(F use) {
         uint4 ry = make_uint4(0u, 0u, 0u, 0u);
         if (two && apart) {
@@ -425,19 +438,33 @@ template <int DT> struct VfWeights {
     static constexpr int N = Fmt<DT>::kVec;
     VfRowIn<DT> x, y;
     bool two, apart;  // a draft model at this position; its row starts elsewhere in its 16 bytes than x's
-    float rx, ix, ry, iy, k;
-    int drop;         // the draft without a draft model, or kNone
+    float rx, ix, ry, iy, k;  // R k, or R where that is far; 1 / S
+    int drop;                 // the draft without a draft model, or kNone
+    bool far_x, far_y;
 
-    // the weights of vector v from its logits; e: p's terms (not scaled)
+    // y's elements in the places of x's vector v
+    __device__ inline uint4 second(int v) const {
+        if (!two) return make_uint4(0u, 0u, 0u, 0u);
+        if (!apart) return y.get(v);
+        float t[N];
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const int c = x.first(v) + j;
+            t[j] = c >= 0 && c < y.V ? Fmt<DT>::load1(y.row, c) : -INFINITY;
+        }
+        return Fmt<DT>::pack(t);
+    }
+    // the weights of vector v from its logits; e: p's terms (not scaled). NEAR: neither reference is far
+    template <bool NEAR>
     __device__ inline void get(int v, const uint4 &ux, const uint4 &uy, float (&e)[N], float (&w)[N]) const {
         float t[N];
         Fmt<DT>::unpack(ux, t);
-        vf_exps<N>(t, k, rx, e);
+        vf_exps<N>(t, k, rx, !NEAR && far_x, e);
         const F2 sx = f2(ix, ix);
         if (two) {
             float d[N];
             Fmt<DT>::unpack(uy, t);
-            vf_exps<N>(t, k, ry, d);
+            vf_exps<N>(t, k, ry, !NEAR && far_y, d);
             const F2 sy = f2(-iy, -iy);
 #pragma unroll
             for (int j = 0; j < N; j += 2) {
@@ -552,8 +579,9 @@ __device__ inline void vf_draw(const VfArgs &a, int b, int n, const VfRow &p, co
     constexpr int N = Fmt<DT>::kVec;
     const char *px = reinterpret_cast<const char *>(a.x) + xrow * Fmt<DT>::kBytes;
     const char *py = model ? reinterpret_cast<const char *>(a.y) + (b * a.ys + n * a.yr) * Fmt<DT>::kBytes : px;
-    VfWeights<DT> w{VfRowIn<DT>(px, a.V), VfRowIn<DT>(py, a.V), model, false, p.R * k, 1.f / p.S, q.R * k, 1.f / q.S, k,
-                    turned && !model ? static_cast<int>(vf_draft(a, b, n)) : kNone};
+    const bool far_x = vf_far(p.R, k), far_y = vf_far(q.R, k);
+    VfWeights<DT> w{VfRowIn<DT>(px, a.V), VfRowIn<DT>(py, a.V), model, false, far_x ? p.R : p.R * k, 1.f / p.S,
+                    far_y ? q.R : q.R * k, 1.f / q.S, k, turned && !model ? static_cast<int>(vf_draft(a, b, n)) : kNone, far_x, far_y};
     w.apart = w.x.before != w.y.before;
     // contiguous ranges of the row, one a warp of the cluster, in steps of 32 vectors
     const int steps = (a.V + N - 1 + 32 * N - 1) / (32 * N), all = size * kWarps;
@@ -562,10 +590,9 @@ __device__ inline void vf_draw(const VfArgs &a, int b, int n, const VfRow &p, co
         const int g = rank * kWarps + warp, s0 = step_of(g), s1 = step_of(g + 1);
         FF sum{0.f, 0.f};
         float rest = 0.f, tops = 0.f;
-        VfStream<DT> in(w.x, w.y, w.two, w.apart, s0 * 32 + lane, s1 * 32, 32, ring);
-        const auto one = [&](int v, const uint4 &ux, const uint4 &uy, float &r) {
+        const auto one = [&](auto near, int v, const uint4 &ux, const uint4 &uy, float &r) {
             float e[N], g[N];
-            w.get(v, ux, uy, e, g);
+            w.template get<decltype(near)::value>(v, ux, uy, e, g);
             F2 t = f2(g[0], g[1]);
 #pragma unroll
             for (int j = 2; j < N; j += 2) t = f2_add(t, f2(g[j], g[j + 1]));
@@ -591,19 +618,26 @@ __device__ inline void vf_draw(const VfArgs &a, int b, int n, const VfRow &p, co
             f2_split(t, lo, hi);
             return lo + hi;
         };
-        float rest2 = 0.f;
-        struct Use {
-            const decltype(one) &f;
-            FF &sum;
-            float &rest, &rest2;
-            __device__ inline void operator()(int v, const uint4 &ux, const uint4 &uy) const { sum = ff_add(sum, FF{f(v, ux, uy, rest), 0.f}); }
-            __device__ inline void operator()(int v, const uint4 &ux, const uint4 &uy, int v2, const uint4 &ux2, const uint4 &uy2) const {
-                const float t = f(v, ux, uy, rest), t2 = f(v2, ux2, uy2, rest2);
-                sum = ff_add(ff_add(sum, FF{t, 0.f}), FF{t2, 0.f});
-            }
-        };
-        in.run(Use{one, sum, rest, rest2});
-        rest += rest2;
+        if (!far_x && !(w.two && far_y)) {
+            VfStream<DT> in(w.x, w.y, w.two, w.apart, s0 * 32 + lane, s1 * 32, 32, ring);
+            float rest2 = 0.f;
+            struct Use {
+                const decltype(one) &f;
+                FF &sum;
+                float &rest, &rest2;
+                __device__ inline void operator()(int v, const uint4 &ux, const uint4 &uy) const {
+                    sum = ff_add(sum, FF{f(std::true_type(), v, ux, uy, rest), 0.f});
+                }
+                __device__ inline void operator()(int v, const uint4 &ux, const uint4 &uy, int v2, const uint4 &ux2, const uint4 &uy2) const {
+                    const float t = f(std::true_type(), v, ux, uy, rest), t2 = f(std::true_type(), v2, ux2, uy2, rest2);
+                    sum = ff_add(ff_add(sum, FF{t, 0.f}), FF{t2, 0.f});
+                }
+            };
+            in.run(Use{one, sum, rest, rest2});
+            rest += rest2;
+        } else {
+            for (int v = s0 * 32 + lane; v < s1 * 32; v += 32) sum = ff_add(sum, FF{one(std::false_type(), v, w.x.get(v), w.second(v), rest), 0.f});
+        }
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) {
             sum = ff_add(sum, ff_shfl_xor(sum, off));
@@ -629,7 +663,7 @@ __device__ inline void vf_draw(const VfArgs &a, int b, int n, const VfRow &p, co
                     tops_all += __shfl_xor_sync(0xffffffffu, tops_all, off);
                 }
                 // from terms relative to R to those relative to M
-                if (lane == 0) m.s1 = (tops_all - 1.f) + rest_all / vf_exp(p.M, k, w.rx);
+                if (lane == 0) m.s1 = (tops_all - 1.f) + rest_all / ex2_hw(vf_arg(p.M, p.R, k));
             }
             const FF incl = ff_scan(ff_add(v0, v1));
             FF before = ff_shfl_up(incl, 1);
@@ -670,15 +704,8 @@ __device__ inline void vf_draw(const VfArgs &a, int b, int n, const VfRow &p, co
         float v[N], t = 0.f;
         const int c = w.x.first(v0 + tid);
         if (v0 + tid < v1) {
-            uint4 uy = make_uint4(0u, 0u, 0u, 0u);
-            if (w.two && !w.apart) uy = w.y.get(v0 + tid);
-            if (w.two && w.apart) {
-#pragma unroll
-                for (int j = 0; j < N; ++j) v[j] = c + j >= 0 && c + j < a.V ? Fmt<DT>::load1(py, c + j) : -INFINITY;
-                uy = Fmt<DT>::pack(v);
-            }
             float e[N];
-            w.get(v0 + tid, w.x.get(v0 + tid), uy, e, v);
+            w.template get<false>(v0 + tid, w.x.get(v0 + tid), w.second(v0 + tid), e, v);
         } else {
 #pragma unroll
             for (int j = 0; j < N; ++j) v[j] = 0.f;
@@ -771,7 +798,8 @@ template <int DT> struct VfAdd {
     F2 sum = f2(0.f, 0.f);
     uint32_t top16 = Fmt<DT>::kNegInfWord;  // packed maxima of 16-bit types
     float top = -INFINITY;
-    __device__ inline void add(const uint4 &r, int c, float k, float rk, int skip) {
+    // (rk: R k, or R itself where that is far)
+    __device__ inline void add(const uint4 &r, int c, float k, float rk, int skip, bool far = false) {
         float x[N];
         Fmt<DT>::unpack(r, x);
         if constexpr (DT == CE_DT_F32) top = fmaxf(top, Fmt<DT>::vmax(r));
@@ -783,7 +811,10 @@ template <int DT> struct VfAdd {
         }
         const F2 kk = f2(k, k), rr = f2(-rk, -rk);
 #pragma unroll
-        for (int j = 0; j < N; j += 2) sum = f2_add(sum, f2_ex2(f2_fma(f2(x[j], x[j + 1]), kk, rr)));
+        for (int j = 0; j < N; j += 2) {
+            const F2 v = f2(x[j], x[j + 1]);
+            sum = f2_add(sum, f2_ex2(far ? f2_mul(f2_add(v, rr), kk) : f2_fma(v, kk, rr)));
+        }
     }
     __device__ inline void join(const VfAdd &o) {
         sum = f2_add(sum, o.sum);
@@ -904,8 +935,8 @@ __global__ void __launch_bounds__(kThreads, 3) vf_seq_kernel(VfArgs a) {
             for (int j = lane; j < size * kWarps; j += 32) st = vf_merge(st, VfState{all[j].x, all[j].y, __float_as_int(all[j].z)}, k);
             p = vf_of(vf_reduce(st, k), k);
         } else {
-            float R = has && fabsf(xt) < INFINITY ? xt : sample(x), Q = 0.f;
-            if (model) Q = fabsf(yt) < INFINITY ? yt : sample(y);
+            float R = has && !vf_far(xt, k) ? xt : sample(x), Q = 0.f;  // (no NaN or infinity, and rather no far one)
+            if (model) Q = !vf_far(yt, k) ? yt : sample(y);
             for (int again = 0;; ++again) {
                 VfAdd<DT> ax, ay;
                 const float rk = R * k, qk = Q * k;
@@ -929,7 +960,16 @@ __global__ void __launch_bounds__(kThreads, 3) vf_seq_kernel(VfArgs a) {
                         }
                     }
                 };
-                in.run(Use{ax, ay, bx, by, in, k, rk, qk, skip, model});
+                const bool far_x = vf_far(R, k), far_y = model && vf_far(Q, k);
+                if (!far_x && !far_y) {
+                    in.run(Use{ax, ay, bx, by, in, k, rk, qk, skip, model});
+                } else {
+                    in.drop();
+                    in.all([&](int v, const uint4 &ux, const uint4 &uy) {
+                        ax.add(ux, in.x.first(v), k, far_x ? R : rk, skip, far_x);
+                        if (model) ay.add(uy, in.y.first(v), k, far_y ? Q : qk, kNone, far_y);
+                    });
+                }
                 ax.join(bx);
                 ay.join(by);
                 // the next position's rows, in case this draft stays
@@ -957,7 +997,7 @@ __global__ void __launch_bounds__(kThreads, 3) vf_seq_kernel(VfArgs a) {
                 vy = f0.w + f1.w;
                 over(mx, vx, my, vy);
                 // the draft's own term beside the others' sum; a NaN in the draft's place shows in xt
-                const float et = has ? vf_exp(xt, k, rk) : 0.f;
+                const float et = has ? ex2_hw(vf_arg(xt, R, k)) : 0.f;
                 p = VfRow{R, et + vx, mx, R == xt ? vx / et : vx, kNone};
                 if (model) q = VfRow{Q, vy, my, 0.f, kNone};
                 // (the maximum of a row with NaN is that of the others: its sum is NaN)

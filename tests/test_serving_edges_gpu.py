@@ -134,3 +134,62 @@ def test_verify_valid_drafts_behind_a_missing_one(ce, size, dtype):
             uu[place >= at[:, None]] = math.nan
             got = ce.ce_verify_drafts(zz, draft, uu, r, draft_logits=None if model is None else yy, temperature=t)
             assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+# ---------------------------------------------------------------------- references
+FAR = [
+    # dtype, offset, step between logits, temperature
+    ("f32", 2e7, 2.0, 1.0), ("f32", -2e7, 2.0, 2.0), ("f32", 1e12, 65536.0, 1e4), ("f32", 1e15, 2.0 ** 27, 1e4),
+    ("f32", 1e6, 0.0625, 1e-4), ("f32", -3e37, 2.0 ** 102, 1.0), ("f32", 1.2e38, 2.0 ** 103, 0.5), ("bf16", 1e10, 2.0 ** 26, 1e4),
+    ("bf16", 2.0 ** 33, 2.0 ** 26, 1.0), ("bf16", -1e38, 2.0 ** 119, 0.7), ("f16", 4e4, 32.0, 1e-4), ("f16", -4e4, 32.0, 30.0),
+]
+
+
+def far_inputs(B, K, V, dtype, offset, step, seed):
+    """Rows of four neighbouring values around the offset, both models' alike but for some of their entries."""
+    g = gen(seed)
+    z = torch.randint(0, 4, (B, K + 1, V), generator=g, device="cuda")
+    move = torch.rand(B, K, V, generator=g, device="cuda") < 0.2
+    y = torch.where(move, torch.randint(0, 4, (B, K, V), generator=g, device="cuda"), z[:, :K])
+    z, y = ((offset + step * v.double()).to(DT[dtype]) for v in (z, y))
+    draft = torch.where(torch.rand(B, K, generator=g, device="cuda") < 0.8, y.argmax(2), torch.randint(0, V, (B, K), generator=g, device="cuda"))
+    return z, y, draft, torch.rand(B, K, generator=g, device="cuda"), torch.rand(B, generator=g, device="cuda")
+
+
+@pytest.mark.parametrize("case", FAR, ids=lambda c: f"{c[0]}{c[1]:g}T{c[3]:g}")
+@pytest.mark.parametrize("size", [(6, 2, 3001), (160, 1, 30011)], ids=["at_once", "clusters"])
+def test_verify_rows_far_from_zero(ce, case, size):
+    """Finite logits are defined wherever they lie: their exponents' reference times log2(e) / T may round by whole
+    powers of two, or leave fp32's range."""
+    dtype, offset, step, t = case
+    z, y, draft, u, r = far_inputs(*size, dtype, offset, step, 5)
+    pick = torch.arange(0, size[0], max(1, size[0] // 24), device="cuda")
+    for model in (y, None):
+        for temp in (t, 0.0):
+            got = ce.ce_verify_drafts(z, draft, u, r, draft_logits=model, temperature=temp)
+            assert (got[1][torch.arange(size[0], device="cuda"), got[0].long()] >= 0).all()
+            F.check_verify(z[pick], None if model is None else y[pick], draft[pick].cpu(), u[pick].cpu(), r[pick].cpu(), temp,
+                           tuple(v[pick] for v in got))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("size", [(6, 2, 5000), (300, 2, 20000)], ids=["at_once", "clusters"])
+def test_verify_wholly_masked_rows(ce, dtype, size):
+    """A row wholly at its type's lowest value is uniform: index 0 for greedy, any token otherwise."""
+    B, K, V = size
+    low = torch.finfo(DT[dtype]).min
+    g = gen(7)
+    z = torch.full((B, K + 1, V), low, device="cuda", dtype=DT[dtype])
+    z[::2, 0, 17] = 1.0                         # (the first draft of every second sequence is certain)
+    draft = torch.randint(1, V, (B, K), generator=g, device="cuda")
+    draft[::2, 0] = 17
+    draft[1::3, 1] = 0
+    u, r = torch.rand(B, K, generator=g, device="cuda"), torch.rand(B, generator=g, device="cuda")
+    y = z[:, :K].clone()
+    y[::4, 1] = torch.randn(V, generator=g, device="cuda").to(DT[dtype])
+    pick = torch.arange(0, B, max(1, B // 24), device="cuda")
+    for model in (None, y):
+        for t in (1.0, 0.5, 1e-4, 0.0):
+            got = ce.ce_verify_drafts(z, draft, u, r, draft_logits=model, temperature=t)
+            F.check_verify(z[pick], None if model is None else y[pick], draft[pick].cpu(), u[pick].cpu(), r[pick].cpu(), t,
+                           tuple(v[pick] for v in got))
