@@ -429,7 +429,10 @@ template <int DT> struct VfStream {
             }
         }
         drop();
-        while (v < v1) slow(use);
+        // The warp's lanes leave together. They come here by loops of different lengths, and the compiler may give lanes that
+        // leave in different places a copy each of what follows, shuffles included, which then miss one another.
+        while (__any_sync(0xffffffffu, v < v1))
+            if (v < v1) slow(use);
     }
 };
 
