@@ -32,7 +32,6 @@
 // than the reading. The ring's loop rolled up (a fifth of the stalls are waits for
 // instructions): no change.
 #include <atomic>
-#include <type_traits>
 
 #include "ce_device.cuh"
 #include "ce_kernels.h"
@@ -437,13 +436,19 @@ template <int DT> struct VfStream {
 };
 
 // What row n's token is drawn from: w_c = max(p_c - q_c, 0), or p_c.
+// Where little is left over, the roundings of p, q and S would be drawn from: below
+// kLittle of all probability the terms of both rows are summed once more, by the
+// difference and in the same order, as pairs, and p - q is formed of those with a
+// remainder (VF_FINE): equal rows leave exactly nothing then, and are drawn from p.
+constexpr float kLittle = 0x1p-8f;
+enum { VF_FAR_X = 1, VF_FAR_Y = 2, VF_FINE = 4 };
 template <int DT> struct VfWeights {
     static constexpr int N = Fmt<DT>::kVec;
     VfRowIn<DT> x, y;
     bool two, apart;  // a draft model at this position; its row starts elsewhere in its 16 bytes than x's
     float rx, ix, ry, iy, k;  // R k, or R where that is far; 1 / S
     int drop;                 // the draft without a draft model, or kNone
-    bool far_x, far_y;
+    int form;                 // VF_FAR_X | VF_FAR_Y | VF_FINE
 
     // y's elements in the places of x's vector v
     __device__ inline uint4 second(int v) const {
@@ -457,18 +462,26 @@ template <int DT> struct VfWeights {
         }
         return Fmt<DT>::pack(t);
     }
-    // the weights of vector v from its logits; e: p's terms (not scaled). NEAR: neither reference is far
+    // the weights of vector v from its logits; e, d: p's and q's terms (not scaled). NEAR: form is 0; low: VF_FINE's 1 / S less ix, iy
     template <bool NEAR>
-    __device__ inline void get(int v, const uint4 &ux, const uint4 &uy, float (&e)[N], float (&w)[N]) const {
+    __device__ inline void get(int v, const uint4 &ux, const uint4 &uy, const float2 &low, float (&e)[N], float (&d)[N], float (&w)[N]) const {
         float t[N];
         Fmt<DT>::unpack(ux, t);
-        vf_exps<N>(t, k, rx, !NEAR && far_x, e);
+        vf_exps<N>(t, k, rx, !NEAR && (form & VF_FAR_X), e);
         const F2 sx = f2(ix, ix);
         if (two) {
-            float d[N];
             Fmt<DT>::unpack(uy, t);
-            vf_exps<N>(t, k, ry, !NEAR && far_y, d);
+            vf_exps<N>(t, k, ry, !NEAR && (form & VF_FAR_Y), d);
             const F2 sy = f2(-iy, -iy);
+            if (!NEAR && (form & VF_FINE)) {
+#pragma unroll
+                for (int j = 0; j < N; ++j) {
+                    // (no product here may be fused into a difference: both sides are rounded alike)
+                    const float u = __fmul_rn(d[j], iy), r = fmaf(d[j], iy, -u);
+                    w[j] = fmaxf((fmaf(e[j], ix, -u) - r) + (__fmul_rn(e[j], low.x) - __fmul_rn(d[j], low.y)), 0.f);
+                }
+                return;
+            }
 #pragma unroll
             for (int j = 0; j < N; j += 2) {
                 f2_split(f2_fma(sy, f2(d[j], d[j + 1]), f2_mul(f2(e[j], e[j + 1]), sx)), w[j], w[j + 1]);
@@ -545,6 +558,7 @@ struct VfMeet {
 
 struct VfDrawMem {
     FF scan[kWarps], from, goal;
+    float2 refs, low;  // R of both rows, VF_FINE's 1 / S less their fp32
     float mass, s1;
     int own, pick, last;
 };
@@ -584,18 +598,21 @@ __device__ inline void vf_draw(const VfArgs &a, int b, int n, const VfRow &p, co
     const char *py = model ? reinterpret_cast<const char *>(a.y) + (b * a.ys + n * a.yr) * Fmt<DT>::kBytes : px;
     const bool far_x = vf_far(p.R, k), far_y = vf_far(q.R, k);
     VfWeights<DT> w{VfRowIn<DT>(px, a.V), VfRowIn<DT>(py, a.V), model, false, far_x ? p.R : p.R * k, 1.f / p.S,
-                    far_y ? q.R : q.R * k, 1.f / q.S, k, turned && !model ? static_cast<int>(vf_draft(a, b, n)) : kNone, far_x, far_y};
+                    far_y ? q.R : q.R * k, 1.f / q.S, k, turned && !model ? static_cast<int>(vf_draft(a, b, n)) : kNone,
+                    (far_x ? VF_FAR_X : 0) | (far_y ? VF_FAR_Y : 0)};
+    if (tid == 0) m.refs = make_float2(p.R, q.R);  // (read behind a barrier)
     w.apart = w.x.before != w.y.before;
     // contiguous ranges of the row, one a warp of the cluster, in steps of 32 vectors
     const int steps = (a.V + N - 1 + 32 * N - 1) / (32 * N), all = size * kWarps;
     const auto step_of = [&](int range) { return static_cast<int>(static_cast<int64_t>(steps) * range / all); };
+    bool terms = false;  // this pass sums the terms for VF_FINE
     for (int pass = 0;; ++pass) {
         const int g = rank * kWarps + warp, s0 = step_of(g), s1 = step_of(g + 1);
         FF sum{0.f, 0.f};
         float rest = 0.f, tops = 0.f;
-        const auto one = [&](auto near, int v, const uint4 &ux, const uint4 &uy, float &r) {
-            float e[N], g[N];
-            w.template get<decltype(near)::value>(v, ux, uy, e, g);
+        const auto one = [&](int v, const uint4 &ux, const uint4 &uy, float &r) {
+            float e[N], d[N], g[N];
+            w.template get<true>(v, ux, uy, make_float2(0.f, 0.f), e, d, g);
             F2 t = f2(g[0], g[1]);
 #pragma unroll
             for (int j = 2; j < N; j += 2) t = f2_add(t, f2(g[j], g[j + 1]));
@@ -621,25 +638,64 @@ __device__ inline void vf_draw(const VfArgs &a, int b, int n, const VfRow &p, co
             f2_split(t, lo, hi);
             return lo + hi;
         };
-        if (!far_x && !(w.two && far_y)) {
+        if (w.form == 0) {
             VfStream<DT> in(w.x, w.y, w.two, w.apart, s0 * 32 + lane, s1 * 32, 32, ring);
             float rest2 = 0.f;
             struct Use {
                 const decltype(one) &f;
                 FF &sum;
                 float &rest, &rest2;
-                __device__ inline void operator()(int v, const uint4 &ux, const uint4 &uy) const {
-                    sum = ff_add(sum, FF{f(std::true_type(), v, ux, uy, rest), 0.f});
-                }
+                __device__ inline void operator()(int v, const uint4 &ux, const uint4 &uy) const { sum = ff_add(sum, FF{f(v, ux, uy, rest), 0.f}); }
                 __device__ inline void operator()(int v, const uint4 &ux, const uint4 &uy, int v2, const uint4 &ux2, const uint4 &uy2) const {
-                    const float t = f(std::true_type(), v, ux, uy, rest), t2 = f(std::true_type(), v2, ux2, uy2, rest2);
+                    const float t = f(v, ux, uy, rest), t2 = f(v2, ux2, uy2, rest2);
                     sum = ff_add(ff_add(sum, FF{t, 0.f}), FF{t2, 0.f});
                 }
             };
             in.run(Use{one, sum, rest, rest2});
             rest += rest2;
         } else {
-            for (int v = s0 * 32 + lane; v < s1 * 32; v += 32) sum = ff_add(sum, FF{one(std::false_type(), v, w.x.get(v), w.second(v), rest), 0.f});
+            FF more{0.f, 0.f};  // terms: sum and more are those of p's terms and of q's
+            const float2 low = m.low;
+#pragma unroll 1
+            for (int step = s0; step < s1; ++step) {
+                const int v = step * 32 + lane;
+                const uint4 ux = w.x.get(v);
+                float x[N], e[N], d[N] = {}, g[N], se = 0.f, sd = 0.f;
+                w.template get<false>(v, ux, w.second(v), low, e, d, g);
+                Fmt<DT>::unpack(ux, x);
+#pragma unroll
+                for (int j = 0; j < N; ++j) {
+                    se += terms ? e[j] : g[j];
+                    sd += d[j];
+                    tops += x[j] == p.M ? 1.f : 0.f;
+                    rest += x[j] == p.M ? 0.f : e[j];
+                }
+                sum = ff_add(sum, FF{se, 0.f});
+                more = ff_add(more, FF{sd, 0.f});
+                __syncwarp();
+            }
+            if (terms) {
+#pragma unroll
+                for (int off = 16; off > 0; off >>= 1) {
+                    sum = ff_add(sum, ff_shfl_xor(sum, off));
+                    more = ff_add(more, ff_shfl_xor(more, off));
+                }
+                const float4 *given = meet.all(sum.hi, sum.lo, more.hi, more.lo);
+                sum = more = FF{0.f, 0.f};
+                for (int j = 0; j < all; ++j) {
+                    sum = ff_add(sum, FF{given[j].x, given[j].y});
+                    more = ff_add(more, FF{given[j].z, given[j].w});
+                }
+                w.ix = 1.f / sum.hi;
+                w.iy = 1.f / more.hi;
+                w.form |= VF_FINE;
+                terms = false;
+                // the same value from every thread
+                m.low = make_float2(fmaf(-w.ix, sum.lo, fmaf(-w.ix, sum.hi, 1.f)) * w.ix,
+                                    fmaf(-w.iy, more.lo, fmaf(-w.iy, more.hi, 1.f)) * w.iy);
+                __syncthreads();
+                continue;
+            }
         }
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) {
@@ -658,7 +714,7 @@ __device__ inline void vf_draw(const VfArgs &a, int b, int n, const VfRow &p, co
             const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
             const float4 r0 = 2 * lane < all ? ranges[2 * lane] : none, r1 = 2 * lane < all ? ranges[2 * lane + 1] : none;
             const FF v0{r0.x, r0.y}, v1{r1.x, r1.y};
-            if (!S1) {
+            if (!S1 && pass == 0) {
                 float rest_all = r0.z + r1.z, tops_all = r0.w + r1.w;
 #pragma unroll
                 for (int off = 16; off > 0; off >>= 1) {
@@ -688,8 +744,15 @@ __device__ inline void vf_draw(const VfArgs &a, int b, int n, const VfRow &p, co
             }
         }
         __syncthreads();
+        if (w.two && !(w.form & VF_FINE) && m.mass <= kLittle) {
+            terms = true;
+            w.form = VF_FAR_X | VF_FAR_Y;
+            w.rx = m.refs.x;
+            w.ry = m.refs.y;
+            continue;
+        }
+        if (m.mass > 0.f || (!w.two && w.drop == kNone)) break;
         // p <= q everywhere (p = q): drawn from p
-        if (m.mass > 0.f || pass == 1) break;
         w.two = false;
         w.drop = kNone;
     }
@@ -707,8 +770,8 @@ __device__ inline void vf_draw(const VfArgs &a, int b, int n, const VfRow &p, co
         float v[N], t = 0.f;
         const int c = w.x.first(v0 + tid);
         if (v0 + tid < v1) {
-            float e[N];
-            w.template get<false>(v0 + tid, w.x.get(v0 + tid), w.second(v0 + tid), e, v);
+            float e[N], d[N];
+            w.template get<false>(v0 + tid, w.x.get(v0 + tid), w.second(v0 + tid), m.low, e, d, v);
         } else {
 #pragma unroll
             for (int j = 0; j < N; ++j) v[j] = 0.f;

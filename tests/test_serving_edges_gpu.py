@@ -193,3 +193,49 @@ def test_verify_wholly_masked_rows(ce, dtype, size):
             got = ce.ce_verify_drafts(z, draft, u, r, draft_logits=model, temperature=t)
             F.check_verify(z[pick], None if model is None else y[pick], draft[pick].cpu(), u[pick].cpu(), r[pick].cpu(), t,
                            tuple(v[pick] for v in got))
+
+
+# ---------------------------------------------------------------------- nothing left over
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("size", [(4, 2, 5000), (3, 1, 128256), (200, 2, 17003), (128, 1, 80000), (160, 1, 30011)],
+                         ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("shift", [0.0, 2.0])
+def test_verify_equal_rows_draw_from_the_target(ce, dtype, size, shift):
+    """Both models' rows are equal (or equal but for a constant), and a number above 1 turns the first draft down: there
+    is nothing in max(p - q, 0), and the token is p's, at its place on p's cumulative sum."""
+    B, K, V = size
+    g = gen(V)
+    # multiples of 1/16: adding the constant is exact in every type
+    y = (torch.empty(B, K, V, device="cuda").normal_(0, 2, generator=g) * 16).round().div(16).clamp(-6, 6)
+    z = torch.cat([y + shift, y[:, :1]], 1).to(DT[dtype])
+    y = y.to(DT[dtype])
+    draft = y.argmax(2)
+    u, r = torch.full((B, K), 1.0 + 2.0 ** -10, device="cuda"), torch.rand(B, generator=g, device="cuda")
+    n, tokens, logp = ce.ce_verify_drafts(z, draft, u, r, draft_logits=y)
+    assert (n == 0).all()
+    p = torch.softmax(z[:, 0].double(), 1)
+    upto = p.cumsum(1)
+    at = tokens[:, :1]
+    end = upto.gather(1, at)[:, 0]
+    start = end - p.gather(1, at)[:, 0]
+    assert ((start <= r + 4 * F.rel(V)) & (end >= r - 4 * F.rel(V))).all()
+
+
+@pytest.mark.parametrize("size", [(4, 5003), (160, 30011)], ids=["at_once", "clusters"])
+@pytest.mark.parametrize("part", [1e-4, 1e-6, 1e-8])
+def test_verify_little_left_over(ce, size, part):
+    """One token of the target above the draft model's by a small part of all probability: what is left over is that
+    token's alone, however little it is beside the roundings of the others."""
+    B, V = size
+    g = gen(3)
+    y = torch.empty(B, 1, V, device="cuda").normal_(0, 1, generator=g)
+    at = torch.randint(0, V, (B,), generator=g, device="cuda")
+    rows = torch.arange(B, device="cuda")
+    total = torch.logsumexp(y[:, 0].double(), 1)
+    y[rows, 0, at] = (total + math.log(part)).float()
+    z = torch.cat([y, y], 1)
+    z[rows, 0, at] += 1.0                                   # e times as likely, before the sum grows by as little
+    draft = torch.where(y[:, 0].argmax(1) == at, 0, y[:, 0].argmax(1))[:, None]
+    u, r = torch.full((B, 1), 1.25, device="cuda"), torch.rand(B, generator=g, device="cuda")
+    n, tokens, _ = ce.ce_verify_drafts(z, draft, u, r, draft_logits=y)
+    assert (n == 0).all() and torch.equal(tokens[:, 0], at)
