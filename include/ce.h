@@ -610,8 +610,13 @@ ce_status ce_quantize_fp8(int64_t rows, int64_t cols, const void *x, int64_t ld_
 /*
  * D[m, n] = sum_k A[m, k] B[n, k] (+ bias[n]) of 8-bit operands on the tcgen05
  * tensor cores: A [M, K] in blocks of 1 x 128, B [N, K] (a weight) in blocks of
- * 128 x 128, any scales. Sums of one block along K are formed by the tensor core,
+ * 128 x 128. Sums of one block along K are formed by the tensor core,
  * scaled and added up in fp32, and rounded once to D.
+ * Scales may be any numbers, their products below fp32's normal range or above
+ * it among them, while the products for one row of A and one block of B's rows lie
+ * within 2^160 of one another; terms further below may lose bits. Blocks with
+ * a scale of 2^-126 count as blocks of zeros in this: what else they hold is below 5.3e-36,
+ * and may lose bits.
  *   bias   device fp32 [N], or NULL.
  *   dtype  of D, device [M, ldd], ldd >= N.
  * K >= 1; M or N of 0 does nothing. Should a wait inside the kernel give up,

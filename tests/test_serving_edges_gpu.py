@@ -239,3 +239,111 @@ def test_verify_little_left_over(ce, size, part):
     u, r = torch.full((B, 1), 1.25, device="cuda"), torch.rand(B, generator=g, device="cuda")
     n, tokens, _ = ce.ce_verify_drafts(z, draft, u, r, draft_logits=y)
     assert (n == 0).all() and torch.equal(tokens[:, 0], at)
+
+
+# ---------------------------------------------------------------------- scales
+SCALED = [(5, 300, 260), (40, 1000, 4500), (70, 300, 260), (130, 20000, 384), (300, 20003, 384)]
+
+
+def scaled_operands(m, n, k, seed):
+    g = gen(seed)
+    a = torch.randn(m, -(-k // 16) * 16, generator=g, device="cuda").mul_(40).to(E4M3)[:, :k]
+    b = torch.randn(n, -(-k // 16) * 16, generator=g, device="cuda").mul_(40).to(E4M3)[:, :k]
+    blocks = -(-k // 128)
+    return a, 1 + torch.rand(m, blocks, generator=g, device="cuda"), b, 1 + torch.rand(-(-n // 128), blocks, generator=g, device="cuda")
+
+
+def check_scaled(out, a, sa, b, sb):
+    """check_gemm's tolerance, and half a step of the least fp32 number for each block's addition."""
+    d, s = F.gemm_ref(a, sa, b, sb)
+    tol = s * (16 + sa.shape[1] + 3) * F.U + d.abs() * F.HALF[out.dtype] * (1 + 2.0 ** -10) + (d.abs() + s) * F.U
+    tol = tol + (sa.shape[1] + 1) * 2.0 ** -149
+    if out.dtype == torch.bfloat16:
+        tol = tol + 2.0 ** -134
+    assert ((out.double() - d).abs() <= tol).all(), float(((out.double() - d).abs() / tol).max())
+
+
+@pytest.mark.parametrize("shape", SCALED, ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("ends", [(1e-22, 1e-22), (2.0 ** -120, 1e-9), (1e-14, 2.0 ** -126), (2.0 ** -149, 2.0 ** 20), (1e19, 1e-40)],
+                         ids=lambda e: f"{e[0]:.0e}x{e[1]:.0e}")
+def test_gemm_scales_with_tiny_products(ce, shape, ends):
+    """The product of two scales below fp32's normal range, their results in or near it."""
+    a, sa, b, sb = scaled_operands(*shape, 3)
+    sa, sb = (sa.double() * ends[0]).float(), (sb.double() * ends[1]).float()
+    sa[::2, 1] = 1.5 / ends[1] * 1e-30                      # rows with ordinary blocks among them
+    for dtype in (torch.float32, torch.bfloat16):
+        check_scaled(ce.ce_gemm_fp8(a, sa, b, sb, out_dtype=dtype), a, sa, b, sb)
+
+
+@pytest.mark.parametrize("shape", SCALED, ids=lambda s: "x".join(map(str, s)))
+def test_gemm_scales_with_huge_products(ce, shape):
+    """The product of two scales above fp32's range: blocks of zeros add 0, and small sums stay finite."""
+    m, n, k = shape
+    a, sa, b, sb = scaled_operands(m, n, k, 4)
+    a, b = a.float(), b.float()
+    a[1, :128] = 0                                          # row 1, block 0: zeros under a huge scale
+    a[2, :128] = 0
+    a[2, 3], b[:, 3] = 2.0 ** -9, 2.0 ** -9                 # row 2, block 0: a sum of 2^-18
+    a, b = (padded8(v) for v in (a, b))
+    sa[1, 0] = sa[2, 0] = 2.0 ** 67
+    sb[:, 0] = 2.0 ** 63
+    sa[0, 0] = 2.0 ** -63
+    sa[3:, 0] = 2.0 ** -64
+    out = ce.ce_gemm_fp8(a, sa, b, sb, out_dtype=torch.float32)
+    assert out.isfinite().all()
+    check_scaled(out, a, sa, b, sb)
+    sa[1, 0] = math.inf                                     # an infinite scale is no number of its block's zeros
+    out = ce.ce_gemm_fp8(a, sa, b, sb, out_dtype=torch.float32)
+    assert out[1].isnan().all() and out[0].isfinite().all() and out[2:].isfinite().all()
+
+
+def padded8(v):
+    """e4m3 with rows at multiples of 16 bytes."""
+    buf = torch.zeros(v.shape[0], -(-v.shape[1] // 16) * 16, device=v.device)
+    buf[:, :v.shape[1]] = v
+    return buf.to(E4M3)[:, :v.shape[1]]
+
+
+@pytest.mark.parametrize("shape", [(40, 3000, 1024), (300, 20000, 384)], ids=lambda s: "x".join(map(str, s)))
+def test_gemm_rows_of_zeros_leave_the_others_alone(ce, shape):
+    """Rows of zeros carry the least scale, whose product with a weight's is below the normal range: they come out 0,
+    and the others bit for bit as without them."""
+    m, n, k = shape
+    g = gen(6)
+    x = torch.randn(m, k, generator=g, device="cuda")
+    W8, sb = ce.ce_quantize_fp8(torch.randn(n, k, generator=g, device="cuda") * 0.02, block_rows=128)
+    q, s = ce.ce_quantize_fp8(x)
+    want = ce.ce_gemm_fp8(q, s, W8, sb, out_dtype=torch.float32)
+    zero = torch.arange(m, device="cuda") % 3 == 1
+    x[zero] = 0
+    q, s = ce.ce_quantize_fp8(x)
+    got = ce.ce_gemm_fp8(q, s, W8, sb, out_dtype=torch.float32)
+    assert (got[zero] == 0).all() and torch.equal(got[~zero], want[~zero])
+
+
+@pytest.mark.parametrize("shape", [(40, 700, 8320), (70, 9900, 8320), (300, 5003, 8320)], ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("kind", ["low behind zeros", "high behind low", "mixed", "zeros under high"])
+def test_gemm_scales_that_change_along_k(ce, shape, kind):
+    """65 blocks along K whose scales change their order of magnitude on the way."""
+    m, n, k = shape
+    a, sa, b, sb = scaled_operands(m, n, k, 8)
+    a = a.float()
+    if kind == "low behind zeros":
+        a[:, :40 * 128] = 0
+        sa[:, 40:] *= 2.0 ** -70
+        sb[:, 40:] *= 2.0 ** -70
+    elif kind == "high behind low":
+        sa[:, :40] *= 2.0 ** -70
+        sb[:, :40] *= 2.0 ** -65
+        sa[1::2, 40:] = 0                                   # (half of the rows have the low ones alone)
+    elif kind == "mixed":
+        sa *= torch.exp2(torch.randint(-60, 60, sa.shape, generator=gen(9), device="cuda").float())
+        sb *= torch.exp2(torch.randint(-60, 0, sb.shape, generator=gen(10), device="cuda").float())
+    else:
+        a[::2, 33 * 128:34 * 128] = 0
+        sa[::2, 33] = 2.0 ** 70
+        sb[:, 33] = 2.0 ** 62
+        sa[1::2, 33] = 2.0 ** -62
+    a = padded8(a)
+    out = ce.ce_gemm_fp8(a, sa, b, sb, out_dtype=torch.float32)
+    check_scaled(out, a, sa, b, sb)
