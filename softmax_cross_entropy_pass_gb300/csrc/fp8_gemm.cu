@@ -877,11 +877,8 @@ bool fp8_takes_pairs(int m, int n) {
     return m > 64 && static_cast<int64_t>((n + kFewM - 1) / kFewM) * ((m + 63) / 64) * 2 > kSms;
 }
 
-enum { FP8_AUTO = 0, FP8_FEW = 1, FP8_PAIR = 2 };
-
-cudaError_t fp8_gemm(const void *A, int64_t lda, const void *B, int64_t ldb, const Fp8Args &g, int dtype, int mode,
-                     cudaStream_t s) {
-    if (mode == FP8_PAIR || (mode == FP8_AUTO && fp8_takes_pairs(g.m, g.n))) {
+cudaError_t fp8_gemm(const void *A, int64_t lda, const void *B, int64_t ldb, const Fp8Args &g, int dtype, cudaStream_t s) {
+    if (fp8_takes_pairs(g.m, g.n)) {
         const int esz = fp8_elem(dtype);
         const bool staged = ((reinterpret_cast<uintptr_t>(g.out) | static_cast<uintptr_t>(g.m > 1 ? g.ldo * esz : 0)) & 31u) != 0;
         using Fn = cudaError_t (*)(const void *, int64_t, const void *, int64_t, Fp8Args, cudaStream_t);
@@ -929,6 +926,6 @@ extern "C" ce_status ce_gemm_fp8(int64_t M, int64_t N, int64_t K, const void *A,
     g.bias = bias;
     g.out = D;
     g.ldo = ldd;
-    const cudaError_t e = fp8_gemm(A, lda, B, ldb, g, dtype, FP8_AUTO, reinterpret_cast<cudaStream_t>(stream));
+    const cudaError_t e = fp8_gemm(A, lda, B, ldb, g, dtype, reinterpret_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? CE_OK : cuda_fail(e);
 }

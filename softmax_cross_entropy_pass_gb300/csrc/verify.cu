@@ -61,7 +61,7 @@ struct VfArgs {
     const float *u, *r;              // [B][K], [B]
     const float *temps;              // [B] or NULL
     float temp;
-    int parts, per;                  // parts of a row, elements of a part
+    int parts;                       // of a row
     VfPart *px, *py;                 // [B][K + 1][parts], [B][K][parts]
     int *accepted;
     void *tokens;                    // [B][K + 1]
@@ -1096,7 +1096,7 @@ __global__ void __launch_bounds__(kThreads, 3) vf_seq_kernel(VfArgs a) {
 // without a part), and how many parts a row has wherever it starts.
 constexpr int kStatsWarps = 152 * 3 * kWarps;  // three CTAs an SM
 struct VfCut {
-    int U, per;
+    int U;
     int64_t parts;
 };
 static VfCut vf_cut(int64_t rows, int64_t vocab, int dtype) {
@@ -1104,8 +1104,8 @@ static VfCut vf_cut(int64_t rows, int64_t vocab, int dtype) {
     VfCut c{};
     for (int U = 4; U >= 1; U >>= 1) {
         c.U = U;
-        c.per = U * 32 * N;
-        c.parts = (vocab + N - 1 + c.per - 1) / c.per;
+        const int per = U * 32 * N;
+        c.parts = (vocab + N - 1 + per - 1) / per;
         if (rows * c.parts >= kStatsWarps) break;
     }
     return c;
@@ -1243,7 +1243,6 @@ ce_status ce_verify_drafts(const ce_verify_params *p, const void *logits, const 
     const int64_t rows = p->n_seqs * (p->n_drafts + 1);
     const VfCut cut = vf_cut(rows, p->vocab, p->dtype);
     a.parts = static_cast<int>(cut.parts);
-    a.per = cut.per;
     a.px = reinterpret_cast<VfPart *>(ws);
     a.py = a.px + rows * a.parts;
     a.accepted = accepted;
