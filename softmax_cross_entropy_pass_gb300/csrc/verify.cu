@@ -381,7 +381,8 @@ template <int DT> struct VfStream {
     __device__ inline void drop() { asm volatile("cp.async.wait_all;" ::: "memory"); }
     // every vector without the ring, whose copies have been dropped
     template <typename F> __device__ inline void all(F use) {
-        while (v < v1) slow(use);
+        while (__any_sync(0xffffffffu, v < v1))
+            if (v < v1) slow(use);
     }
     template <typename F> __device__ inline void slow(F use) {
         uint4 ry = make_uint4(0u, 0u, 0u, 0u);
