@@ -371,12 +371,12 @@ fp8_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
 // return shows wherever it is longer than the next block's MMAs. Eight
 // epilogue warps a CTA scale and add a row and 128 columns a thread, with one scale
 // of A (through shared memory, copied half a chunk ahead) and one of the weight.
-// 4096 x 128256 x 4096: 1735 us, 2.48 PFLOP/s. At 2048 rows 833 us; without the adds
-// 699, with them but without the loads 719: each hides behind the MMAs, the two one after
-// the other in a warp do not. Slower there: tiles of 224, 192, 160 (three accumulators)
-// and 128 columns (four), a thread's share loaded whole and given back before it is
-// added, 894, 950, 1046 and 1036 us; sixteen epilogue warps 952; no change: sums that
-// leave through shared memory behind the next tile's, 820.
+// 4096 x 128256 x 4096: 1740 to 1780 us (GPUs differ), 2.4 PFLOP/s. At 2048 rows, on a GPU
+// with 833 us: without the adds 699, with them but without the loads 719: each hides behind
+// the MMAs, the two one after the other in a warp do not. Slower there: tiles of 224, 192,
+// 160 (three accumulators) and 128 columns (four), a thread's share loaded whole and given
+// back before it is added, 894, 950, 1046 and 1036 us; sixteen epilogue warps 952; no change:
+// sums that leave through shared memory behind the next tile's, 820.
 // Barriers as in the bf16 product: `full` in the even CTA counts both CTAs'
 // bytes, `empty` and `tfull` are signalled by multicast commits, `tempty` in the
 // even CTA collects the 16 epilogue warps of the pair (each arrival from the other

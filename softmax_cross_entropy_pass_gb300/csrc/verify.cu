@@ -25,7 +25,7 @@
 // Bound by the chain of dependent steps: a launch, a row's reading, an exchange and
 // the draw where sequences are few (1 of 3 drafts and 128256 bf16 logits with a draft
 // model: 17 us), the longest sequence's positions where they are many (128 of 4
-// drafts: 73 us, of which the rows that decide would take 24 at the copy rate).
+// drafts: 74 us, of which the rows that decide would take 24 at the copy rate).
 // Tried for many sequences and slower (the latter): parts of all rows dealt out
 // position by position, the CTA or warp that completes a row by a counter deciding
 // whether the next ones are read: 108 and 224 us; its fences and atomics took longer
